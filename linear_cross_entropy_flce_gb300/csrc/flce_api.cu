@@ -19,286 +19,179 @@
 // step 1 with global label ids, a merge into the shard's (m, s, zt) and step 3
 // for the label check; flce_backward_shard runs step 3 for the scale and step 4
 // from the caller's combined lse, accumulating its dH part in fp32.
-#include <cuda.h>
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
-#include "../../include/flce.h"
-#include "flce_internal.h"
+#include "flce_host.h"
 
 namespace flce {
-namespace {
 
-constexpr int64_t kDefaultTimeoutNs = 2000000000LL;
-constexpr size_t kGChunkCapBytes = size_t(256) << 20;  // planned bf16 G chunk
-constexpr int kMaxDevices = 64;
+// Backward of a GEMM call, token block outer, vocabulary chunk inner: per chunk the
+// gradient GEMM (G in bf16) and one launch of the dH and / or dW products.
+int launch_backward_products(const Plan& P, const BackwardProducts& b, KernelTrace& trace) {
+  const int64_t N = P.N, D = P.D, V = P.V;
+  const uint16_t* H = b.H;
+  const uint16_t* W = b.W;
+  uint16_t* dH = b.dH;
+  void* dW = b.dW;
+  uint16_t* G = b.G;
+  float* dh_acc = b.dh_acc;
+  float* dw_acc = b.dw_acc;
+  const bool to_f32 = b.dh_f32 != nullptr;   // fp32 dH part of a vocabulary shard
+  const bool want_dh = dH != nullptr || to_f32;
+  const bool dw_bf16 = b.dw_bf16;
+  const int64_t tmo = b.timeout_ns;
+  int32_t* status = b.status;
+  const int sms = b.sms;
+  cudaStream_t st = b.stream;
+  const int cta = P.cta;
+  const int pairs = std::max(1, sms / cta);
+  const int64_t rows_b = ceil_div(P.n_block, P.tile_m) * P.tile_m;
+  // MN-major operands: one 3-D copy per CTA when the MN extent is a multiple of
+  // 64 (always for the G chunk), else 64-wide 2-D boxes.
+  CUtensorMap mH_mn, mW_mn, mG_mn, mG_k, mG_out;
+  const bool d_box3 = D % 64 == 0;
+  const uint32_t b_chunks = static_cast<uint32_t>(BN / cta / 64);
+  const bool ok_h = d_box3 ? encode_bf16_mn3(&mH_mn, H, D, N, D, BK, b_chunks)
+                           : encode_bf16(&mH_mn, H, D, N, D, 64, BK);
+  const bool ok_w = d_box3 ? encode_bf16_mn3(&mW_mn, W, D, V, D, BK, b_chunks)
+                           : encode_bf16(&mW_mn, W, D, V, D, 64, BK);
+  if (!ok_h || !ok_w || !encode_g_chunked(&mG_mn, G, rows_b, P.v_chunk, 64, BK, BM / 64, false) ||
+      !encode_g_chunked(&mG_k, G, rows_b, P.v_chunk, 64, BM, 1, false) ||
+      !encode_g_chunked(&mG_out, G, rows_b, P.v_chunk, 32, 32, 1, true))
+    return FLCE_ERR_CUDA;
+  // dW goes to fp32 dW, to bf16 dW (one token block), or to the fp32 accumulator
+  // that bf16 dW is rounded from after the last token block.
+  const bool dw_direct_bf16 = dw_bf16 && P.n_nblocks == 1;
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+  for (int blk = 0; blk < P.n_nblocks; ++blk) {
+    const int64_t b0 = static_cast<int64_t>(blk) * P.n_block;
+    const int nb_len = static_cast<int>(std::min<int64_t>(P.n_block, N - b0));
+    for (int c = 0; c < P.n_chunks; ++c) {
+      const int64_t c0 = static_cast<int64_t>(c) * P.v_chunk;
+      const int c_len = static_cast<int>(std::min<int64_t>(P.v_chunk, V - c0));
 
-struct DeviceInfo {
-  bool init = false;
-  int status = FLCE_OK;
-  int sms = 0;
-};
+      // G chunk: recompute Z_bc and form (softmax - onehot) * scale in bf16.
+      GemmParams q = b.grad;
+      q.a_mn_major = 0;
+      q.b_mn_major = 0;
+      q.a_mn0 = static_cast<int>(b0);
+      q.b_mn0 = static_cast<int>(c0);
+      q.m_blocks = static_cast<int>(ceil_div(nb_len, P.tile_m));
+      q.n_blocks = static_cast<int>(ceil_div(c_len, BN));
+      q.num_units = q.m_blocks * q.n_blocks;
+      q.group_m = std::min(q.m_blocks, 16);
+      q.timeout_ns = tmo;
+      q.status = status;
+      q.m_valid = nb_len;
+      q.n_valid = c_len;
+      q.row_base = static_cast<int>(b0);
+      q.col_base = static_cast<int>(b.v_base + c0);
+      q.out_row0 = 0;
+      if (b.launch_grad(cta, *b.h_k, *b.w_k, mG_out, q, cta * std::min(q.num_units, pairs), st,
+                        b.fp8) != cudaSuccess ||
+          !trace())
+        return FLCE_ERR_CUDA;
 
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_mu;
+      const bool both = dW != nullptr && want_dh;
+      GemmArgs aw{}, ah{};
+      if (dW != nullptr) {
+        // dW rows [c0, c0 + c_len) (+)= G_bc^T H_b: M = vocabulary, N = hidden, K = tokens.
+        GemmParams& w = aw.p;
+        w.a_mn_major = 1;
+        w.b_mn_major = 1;
+        w.a_box3 = 1;
+        w.b_box3 = d_box3 ? 1 : 0;
+        w.b_k0 = static_cast<int>(b0);
+        w.m_blocks = static_cast<int>(ceil_div(c_len, P.tile_m));
+        w.n_blocks = static_cast<int>(ceil_div(D, kWideDw ? 2 * BN : BN));
+        w.k_blocks = static_cast<int>(ceil_div(nb_len, BK));
+        w.num_units = w.m_blocks * w.n_blocks;
+        w.group_m = std::min(w.m_blocks, 8);
+        // every second tile of a pair walks K backwards, so a wave starts on the K
+        // blocks the previous wave read last (still in L2); on the Llama-3-8B head
+        // (N 8192, D 4096, 16128-id chunks) 19% fewer DRAM reads per launch
+        w.k_serpentine = 1;
+        w.idesc = make_idesc_bf16_f32(P.tile_m, BN, 1, 1);
+        w.timeout_ns = tmo;
+        w.status = status;
+        w.m_valid = c_len;
+        w.n_valid = static_cast<int>(D);
+        // the map holds exactly the chunk's rows, so ragged tiles are clipped
+        const int64_t dw_off = c0 * D;
+        void* dw_base = dw_direct_bf16 ? static_cast<void*>(static_cast<uint16_t*>(dW) + dw_off)
+                        : dw_bf16      ? static_cast<void*>(dw_acc + dw_off)
+                                       : static_cast<void*>(static_cast<float*>(dW) + dw_off);
+        if (!encode_out(&aw.c, dw_base, dw_direct_bf16, D, c_len, D)) return FLCE_ERR_CUDA;
+        aw.a = mG_mn;
+        aw.b = mH_mn;
+        w.out_row0 = 0;
+        w.out_mode = dw_direct_bf16 ? OUT_STORE_BF16 : (blk == 0 ? OUT_STORE_F32 : OUT_ADD_F32);
+      }
 
-int device_info(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FLCE_ERR_CUDA;
-  if (dev < 0 || dev >= kMaxDevices) return FLCE_ERR_DEVICE;
-  std::lock_guard<std::mutex> lk(g_mu);
-  DeviceInfo& d = g_dev[dev];
-  if (!d.init) {
-    int major = 0, minor = 0, count = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      const bool wide_dh = both || kWideDhAlone;
+      if (want_dh) {
+        // dH rows [b0, b0 + nb_len) (+)= G_bc W_c: M = tokens, N = hidden, K = vocabulary.
+        GemmParams& h = ah.p;
+        h.a_mn_major = 0;
+        h.a_kchunk = 1;
+        h.b_mn_major = 1;
+        h.b_box3 = d_box3 ? 1 : 0;
+        h.b_k0 = static_cast<int>(c0);
+        h.m_blocks = static_cast<int>(ceil_div(nb_len, P.tile_m));
+        h.n_blocks = static_cast<int>(ceil_div(D, wide_dh ? 2 * BN : BN));
+        h.k_blocks = static_cast<int>(ceil_div(c_len, BK));
+        h.num_units = h.m_blocks * h.n_blocks;
+        h.group_m = std::min(h.m_blocks, 8);
+        h.k_serpentine = 1;   // as for dW (9% fewer DRAM reads on the same head)
+        h.idesc = make_idesc_bf16_f32(P.tile_m, BN, 0, 1);
+        h.timeout_ns = tmo;
+        h.status = status;
+        h.m_valid = nb_len;
+        h.n_valid = static_cast<int>(D);
+        // one chunk: bf16 dH directly; else an fp32 accumulator of this token
+        // block's rows (stored by chunk 0, reduce-added by the others), rounded
+        // to bf16 after the last chunk. The map holds exactly the block's rows.
+        // A shard accumulates straight into its fp32 dH part.
+        const bool dh_direct = P.n_chunks == 1 && !to_f32;
+        const bool ok_dh = to_f32 ? encode_out(&ah.c, b.dh_f32 + b0 * D, false, D, nb_len, D)
+                           : dh_direct ? encode_out(&ah.c, dH + b0 * D, true, D, nb_len, D)
+                                       : encode_out(&ah.c, dh_acc, false, D, nb_len, D);
+        if (!ok_dh) return FLCE_ERR_CUDA;
+        ah.a = mG_k;
+        ah.b = mW_mn;
+        h.out_row0 = 0;
+        h.out_mode = dh_direct ? OUT_STORE_BF16 : (c == 0 ? OUT_STORE_F32 : OUT_ADD_F32);
+      }
+      // dW and dH both read only G (and H, W), and write different outputs
+      cudaError_t ge = cudaSuccess;
+      if (both) {
+        const int units = ah.p.num_units + aw.p.num_units;
+        ge = launch_gemm_f32_pair(cta, ah, aw, cta * std::min(units, pairs), st);
+      } else if (dW != nullptr) {
+        ge = launch_gemm_f32(cta, aw.a, aw.b, aw.c, aw.p, cta * std::min(aw.p.num_units, pairs),
+                             st, kWideDw ? 1 : 0);
+      } else if (want_dh) {
+        ge = launch_gemm_f32(cta, ah.a, ah.b, ah.c, ah.p, cta * std::min(ah.p.num_units, pairs),
+                             st, wide_dh ? 1 : 0);
+      }
+      if (ge != cudaSuccess || ((dW != nullptr || want_dh) && !trace())) return FLCE_ERR_CUDA;
+    }
+    if (dH != nullptr && P.n_chunks > 1 &&
+        (launch_f32_to_bf16(dh_acc, dH + b0 * D, static_cast<int64_t>(nb_len) * D, sms, st) !=
+             cudaSuccess ||
+         !trace()))
       return FLCE_ERR_CUDA;
-    }
-    d.status = (major == 10 && minor == 3) ? FLCE_OK : FLCE_ERR_DEVICE;
-    d.sms = count;
-    d.init = true;
   }
-  *sms = d.sms;
-  return d.status;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess) {
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-  });
-  return fn;
-}
-
-// bf16 matrix [outer][inner] (inner contiguous, row stride ld elements), read in
-// boxes of box_inner x box_outer with 128-byte swizzle; out-of-range elements
-// read as zero.
-bool encode_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
-                 uint32_t box_inner, uint32_t box_outer) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {ld * 2};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Output map of the GEMM epilogue's TMA stores: [rows][cols] row-major with row
-// stride ld elements, boxes of 32 x 32; fp32 boxes use the 128-byte swizzle and
-// bf16 boxes the 64-byte one (the layouts the epilogue stages in shared memory).
-// Stores outside [rows) x [cols) are dropped, which clips ragged tiles.
-bool encode_out(CUtensorMap* m, const void* base, bool bf16, uint64_t cols, uint64_t rows,
-                uint64_t ld) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  const uint64_t esz = bf16 ? 2 : 4;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {ld * esz};
-  cuuint32_t box[2] = {32, 32};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// The bf16 G chunk is stored chunk-major, [v_chunk/64][rows][64]: the 64 vocabulary
-// ids of one K block of the dH product, or one 64-wide MN chunk of the dW product,
-// are contiguous for a run of rows, so each copy of a consumer reads whole
-// contiguous blocks (8-16 KB) instead of 128-byte pieces of rows v_chunk·2 bytes
-// apart. Three views of it: the gradient epilogue's 32 x 32 store boxes, the
-// K-major A operand of dH (64 ids x 128 rows per box) and the MN-major A operand of
-// dW (64 ids x 64 rows x 2 chunks per box).
-bool encode_g_chunked(CUtensorMap* m, void* G, uint64_t rows, uint64_t v_chunk, uint32_t box_x,
-                      uint32_t box_y, uint32_t box_z, bool sw64) {
-  auto fn = encode_fn();
-  if (fn == nullptr || v_chunk % 64 != 0) return false;
-  cuuint64_t dims[3] = {64, rows, v_chunk / 64};
-  cuuint64_t strides[2] = {128, rows * 128};
-  cuuint32_t box[3] = {box_x, box_y, box_z};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, G, dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  sw64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  sw64 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Tiles are computed by cluster pairs (tcgen05 cta_group::2, 256-row tiles).
-constexpr int kCtaGroup = 2;
-// The dW and dH products (K = the token block / the vocabulary chunk, 8192 and
-// 16032 at the Llama-3-8B head) run 256 x 512 tiles: a quarter fewer operand bytes
-// per flop and fewer distinct operand rows per wave, for an epilogue that no longer
-// overlaps the next tile (about 1% of a tile that long). Requested together they
-// share one launch, dH's tiles first, because dH alone has too few wide tiles to
-// fill the pairs (256 for 76 pairs at the Llama-3-8B head: a last wave 37% full);
-// dH alone keeps 256 x 256 tiles.
-constexpr bool kWideDw = true;
-constexpr bool kWideDhAlone = false;
-
-// MN-major bf16 operand [rows][mn] (mn contiguous, mn % 64 == 0, row stride ld
-// elements) as a 3-D map [mn/64][rows][64] read in boxes of 64 x box_rows x
-// box_chunks with 128-byte swizzle. The view covers exactly the 2-D tensor, so
-// every address it can form lies inside it; rows past the end read as zero.
-bool encode_bf16_mn3(CUtensorMap* m, const void* base, uint64_t mn, uint64_t rows, uint64_t ld,
-                     uint32_t box_rows, uint32_t box_chunks) {
-  auto fn = encode_fn();
-  if (fn == nullptr || mn % 64 != 0) return false;
-  cuuint64_t dims[3] = {64, rows, mn / 64};
-  cuuint64_t strides[2] = {ld * 2, 128};
-  cuuint32_t box[3] = {64, box_rows, box_chunks};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-struct Plan {
-  int64_t N = 0, D = 0, V = 0;
-  int cta = kCtaGroup;  // CTAs per tile
-  int tile_m = BM * kCtaGroup;
-  int m_blocks = 0;     // ceil(N / tile_m): row tiles of the forward pass
-  int part_stride = 0;  // 128-row blocks per vocabulary range in the partials
-  int v_tiles = 0;    // ceil(V / BN)
-  int splits = 0;     // forward vocabulary ranges per token block
-  int64_t n_block = 0, v_chunk = 0;
-  int n_nblocks = 0, n_chunks = 0;
-  bool need_dh_acc = false, need_dw_acc = false;
-  size_t off_part = 0, off_zt = 0, off_nll = 0, off_lse = 0, off_scal = 0, off_gstat = 0,
-         off_g = 0, off_dhacc = 0, off_dwacc = 0, total = 0;
-};
-
-int choose_splits(int m_blocks, int v_tiles, int sms) {
-  // Minimise (waves of units) x (tiles per unit); ties go to fewer splits.
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  const int max_s = std::min(v_tiles, 128);
-  for (int s = 1; s <= max_s; ++s) {
-    const int64_t waves = ceil_div(static_cast<int64_t>(m_blocks) * s, sms);
-    const int64_t cost = waves * ceil_div(v_tiles, s);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
-}
-
-// backward = false: only the forward pieces (partials, target logits, NLL, lse,
-// scalars); the G chunk and the dH / dW accumulators are left out of the total.
-int make_plan(int64_t N, int64_t D, int64_t V, const flce_options& o, int sms, Plan* P,
-              bool backward = true) {
-  Plan p;
-  p.N = N;
-  p.D = D;
-  p.V = V;
-  p.m_blocks = static_cast<int>(ceil_div(N, p.tile_m));
-  p.part_stride = p.m_blocks * p.cta;
-  p.v_tiles = static_cast<int>(ceil_div(V, BN));
-  if (o.v_splits < 0 || o.v_splits > p.v_tiles) return FLCE_ERR_OPTION;
-  p.splits = o.v_splits > 0 ? o.v_splits
-                            : choose_splits(p.m_blocks, p.v_tiles, std::max(1, sms / p.cta));
-
-  const int64_t v_round = ceil_div(V, BN) * BN;
-  if (o.v_chunk < 0 || o.n_block < 0) return FLCE_ERR_OPTION;
-  if (o.v_chunk > 0 && o.v_chunk % BN != 0) return FLCE_ERR_OPTION;
-  if (o.n_block > 0 && o.n_block % BM != 0) return FLCE_ERR_OPTION;
-  // Planned G chunk: vocabulary chunks of at most 16384 ids, balanced in length
-  // (a chunk's dH accumulation and launch ramp are paid per chunk, so fewer,
-  // longer chunks are faster); the tokens form one block unless one chunk of G
-  // would exceed kGChunkCapBytes, in which case they are split into equal
-  // blocks of whole 256-row pair tiles. Measured on GB300: long-sequence head
-  // 99.7 -> 93.9 ms with half the workspace, Llama-2-like head 1.93 -> 1.40 ms.
-  int64_t cv = o.v_chunk, nb = o.n_block;
-  if (cv == 0) {
-    const int64_t chunks = ceil_div(V, 16384);
-    cv = ceil_div(ceil_div(V, chunks), BN) * BN;
-  }
-  if (nb == 0) {
-    const int64_t bytes = ceil_div(N, BM * 2) * (BM * 2) * cv * 2;
-    const int64_t blocks = std::max<int64_t>(1, ceil_div(bytes, static_cast<int64_t>(kGChunkCapBytes)));
-    nb = blocks == 1 ? N : ceil_div(ceil_div(N, blocks), BM * 2) * (BM * 2);
-  }
-  cv = std::min(cv, v_round);
-  nb = std::min(nb, N);
-  p.v_chunk = cv;
-  p.n_block = nb;
-  p.n_chunks = static_cast<int>(ceil_div(V, cv));
-  p.n_nblocks = static_cast<int>(ceil_div(N, nb));
-  p.need_dh_acc = p.n_chunks > 1;
-  p.need_dw_acc = (o.dw_dtype == FLCE_DTYPE_BF16) && p.n_nblocks > 1;
-
-  const int64_t rows_b = ceil_div(nb, p.tile_m) * p.tile_m;
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t at = off;
-    off = align_up(off + bytes, 256);
-    return at;
-  };
-  p.off_part = take(static_cast<size_t>(p.splits) * p.part_stride * BM * sizeof(float2));
-  p.off_zt = take(static_cast<size_t>(N) * 4);
-  p.off_nll = take(static_cast<size_t>(N) * 4);
-  p.off_lse = take(static_cast<size_t>(N) * 4);
-  p.off_scal = take(256);
-  if (backward) {
-    p.off_gstat = take(static_cast<size_t>(N) * 16);   // float4 per token
-    p.off_g = take(static_cast<size_t>(rows_b) * cv * 2);
-    p.off_dhacc = p.need_dh_acc ? take(static_cast<size_t>(rows_b) * D * 4) : off;
-    p.off_dwacc = p.need_dw_acc ? take(static_cast<size_t>(V) * D * 4) : off;
-  } else {
-    p.off_gstat = p.off_g = p.off_dhacc = p.off_dwacc = off;
-  }
-  p.total = off;
-  *P = p;
+  if (dW != nullptr && dw_bf16 && !dw_direct_bf16 &&
+      (launch_f32_to_bf16(dw_acc, static_cast<uint16_t*>(dW), V * D, sms, st) != cudaSuccess ||
+       !trace()))
+    return FLCE_ERR_CUDA;
   return FLCE_OK;
 }
 
-int check_options(const flce_options& o) {
-  if (o.reduction != FLCE_REDUCTION_MEAN && o.reduction != FLCE_REDUCTION_SUM &&
-      o.reduction != FLCE_REDUCTION_NONE)
-    return FLCE_ERR_OPTION;
-  if (o.dw_dtype != FLCE_DTYPE_F32 && o.dw_dtype != FLCE_DTYPE_BF16) return FLCE_ERR_OPTION;
-  if (!(o.normalizer >= 0.f) || !(o.grad_scale == o.grad_scale)) return FLCE_ERR_OPTION;
-  if (o.timeout_ns < 0) return FLCE_ERR_OPTION;
-  if (o.trace_capacity < 0 || (o.trace_capacity > 0 && o.trace_events == nullptr) ||
-      o.reserved != 0)
-    return FLCE_ERR_OPTION;
-  return FLCE_OK;
-}
-
-int check_shape(int64_t N, int64_t D, int64_t V) {
-  if (N < 1 || D < 1 || V < 1) return FLCE_ERR_SHAPE;
-  // int32 coordinates and indices inside the kernels
-  if (N > (int64_t(1) << 30) || V > (int64_t(1) << 30) || D > (int64_t(1) << 20))
-    return FLCE_ERR_SHAPE;
-  if (D % 8 != 0) return FLCE_ERR_ALIGN;
-  return FLCE_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 // Fp8 carries the E4M3 operands of the FP8 variant (null for the bf16 path):
 // they feed the two logits products; H and W (bf16) feed the gradient products.
@@ -322,22 +215,6 @@ struct Shard {
   const float* lse_in = nullptr;
   float* dh_f32 = nullptr;
 };
-
-// uint8 matrix [outer][inner] read in boxes of box_inner x box_outer bytes with
-// 128-byte swizzle; out-of-range elements read as zero.
-bool encode_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
-               uint32_t box_inner, uint32_t box_outer) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {ld};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
 
 int run(const uint16_t* H, const uint16_t* W, const Fp8Operands& f8, const int32_t* labels,
         int64_t N, int64_t D, int64_t V, const flce_options* opt_in, float* loss, float* lse_out,
@@ -420,14 +297,7 @@ int run(const uint16_t* H, const uint16_t* W, const Fp8Operands& f8, const int32
   if (status != nullptr && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess)
     return FLCE_ERR_CUDA;
   // Optional per-kernel trace: event 0 before the first kernel, event k after kernel k.
-  int n_traced = 0;
-  auto trace = [&]() -> bool {
-    if (o.trace_events == nullptr || n_traced >= o.trace_capacity) return true;
-    const bool ok = cudaEventRecord(static_cast<cudaEvent_t>(o.trace_events[n_traced]), st) ==
-                    cudaSuccess;
-    ++n_traced;
-    return ok;
-  };
+  KernelTrace trace{o.trace_events, o.trace_capacity, st};
   if (!trace()) return FLCE_ERR_CUDA;
 
   const int cta = P.cta;
@@ -495,162 +365,35 @@ int run(const uint16_t* H, const uint16_t* W, const Fp8Operands& f8, const int32
       !trace())
     return FLCE_ERR_CUDA;
   if (!want_dh && dW == nullptr) return FLCE_OK;
-  const float* lse_g = shard ? sh.lse_in : lse;   // the lse the gradient is formed from
-
-  // ---- 4. backward, token block outer, vocabulary chunk inner ----
-  const int64_t rows_b = ceil_div(P.n_block, P.tile_m) * P.tile_m;
-  // MN-major operands: one 3-D copy per CTA when the MN extent is a multiple of
-  // 64 (always for the G chunk), else 64-wide 2-D boxes.
-  CUtensorMap mH_mn, mW_mn, mG_mn, mG_k, mG_out;
-  const bool d_box3 = D % 64 == 0;
-  const uint32_t b_chunks = static_cast<uint32_t>(BN / cta / 64);
-  const bool ok_h = d_box3 ? encode_bf16_mn3(&mH_mn, H, D, N, D, BK, b_chunks)
-                           : encode_bf16(&mH_mn, H, D, N, D, 64, BK);
-  const bool ok_w = d_box3 ? encode_bf16_mn3(&mW_mn, W, D, V, D, BK, b_chunks)
-                           : encode_bf16(&mW_mn, W, D, V, D, 64, BK);
-  if (!ok_h || !ok_w || !encode_g_chunked(&mG_mn, G, rows_b, P.v_chunk, 64, BK, BM / 64, false) ||
-      !encode_g_chunked(&mG_k, G, rows_b, P.v_chunk, 64, BM, 1, false) ||
-      !encode_g_chunked(&mG_out, G, rows_b, P.v_chunk, 32, 32, 1, true))
-    return FLCE_ERR_CUDA;
-  const bool dw_bf16 = o.dw_dtype == FLCE_DTYPE_BF16;
-  // dW goes to fp32 dW, to bf16 dW (one token block), or to the fp32 accumulator
-  // that bf16 dW is rounded from after the last token block.
-  const bool dw_direct_bf16 = dw_bf16 && P.n_nblocks == 1;
-
-  for (int b = 0; b < P.n_nblocks; ++b) {
-    const int64_t b0 = static_cast<int64_t>(b) * P.n_block;
-    const int nb_len = static_cast<int>(std::min<int64_t>(P.n_block, N - b0));
-    for (int c = 0; c < P.n_chunks; ++c) {
-      const int64_t c0 = static_cast<int64_t>(c) * P.v_chunk;
-      const int c_len = static_cast<int>(std::min<int64_t>(P.v_chunk, V - c0));
-
-      // G chunk: recompute Z_bc and form (softmax - onehot) * scale in bf16.
-      GemmParams q{};
-      q.a_mn_major = 0;
-      q.b_mn_major = 0;
-      q.a_mn0 = static_cast<int>(b0);
-      q.b_mn0 = static_cast<int>(c0);
-      q.m_blocks = static_cast<int>(ceil_div(nb_len, P.tile_m));
-      q.n_blocks = static_cast<int>(ceil_div(c_len, BN));
-      q.k_blocks = k_blocks_z;
-      q.acc_scale_h = f8.scale_h;
-      q.acc_scale_w = f8.scale_w;
-      q.num_units = q.m_blocks * q.n_blocks;
-      q.group_m = std::min(q.m_blocks, 16);
-      q.idesc = idesc_z;
-      q.timeout_ns = tmo;
-      q.status = status;
-      q.m_valid = nb_len;
-      q.n_valid = c_len;
-      q.labels = labels;
-      q.row_base = static_cast<int>(b0);
-      q.col_base = static_cast<int>(v_base + c0);
-      q.ignore_index = o.ignore_index;
-      q.lse = lse_g;
-      q.gstat = gstat;
-      q.scale = scal;
-      q.out_row0 = 0;
-      if (launch_gemm_grad(cta, mH_k, mW_k, mG_out, q, cta * std::min(q.num_units, pairs), st,
-                           fp8 ? 1 : 0) !=
-              cudaSuccess ||
-          !trace())
-        return FLCE_ERR_CUDA;
-
-      const bool both = dW != nullptr && want_dh;
-      GemmArgs aw{}, ah{};
-      if (dW != nullptr) {
-        // dW rows [c0, c0 + c_len) (+)= G_bc^T H_b: M = vocabulary, N = hidden, K = tokens.
-        GemmParams& w = aw.p;
-        w.a_mn_major = 1;
-        w.b_mn_major = 1;
-        w.a_box3 = 1;
-        w.b_box3 = d_box3 ? 1 : 0;
-        w.b_k0 = static_cast<int>(b0);
-        w.m_blocks = static_cast<int>(ceil_div(c_len, P.tile_m));
-        w.n_blocks = static_cast<int>(ceil_div(D, kWideDw ? 2 * BN : BN));
-        w.k_blocks = static_cast<int>(ceil_div(nb_len, BK));
-        w.num_units = w.m_blocks * w.n_blocks;
-        w.group_m = std::min(w.m_blocks, 8);
-        // every second tile of a pair walks K backwards, so a wave starts on the K
-        // blocks the previous wave read last (still in L2); on the Llama-3-8B head
-        // (N 8192, D 4096, 16128-id chunks) 19% fewer DRAM reads per launch
-        w.k_serpentine = 1;
-        w.idesc = make_idesc_bf16_f32(P.tile_m, BN, 1, 1);
-        w.timeout_ns = tmo;
-        w.status = status;
-        w.m_valid = c_len;
-        w.n_valid = static_cast<int>(D);
-        // the map holds exactly the chunk's rows, so ragged tiles are clipped
-        const int64_t dw_off = c0 * D;
-        void* dw_base = dw_direct_bf16 ? static_cast<void*>(static_cast<uint16_t*>(dW) + dw_off)
-                        : dw_bf16      ? static_cast<void*>(dw_acc + dw_off)
-                                       : static_cast<void*>(static_cast<float*>(dW) + dw_off);
-        if (!encode_out(&aw.c, dw_base, dw_direct_bf16, D, c_len, D)) return FLCE_ERR_CUDA;
-        aw.a = mG_mn;
-        aw.b = mH_mn;
-        w.out_row0 = 0;
-        w.out_mode = dw_direct_bf16 ? OUT_STORE_BF16 : (b == 0 ? OUT_STORE_F32 : OUT_ADD_F32);
-      }
-
-      const bool wide_dh = both || kWideDhAlone;
-      if (want_dh) {
-        // dH rows [b0, b0 + nb_len) (+)= G_bc W_c: M = tokens, N = hidden, K = vocabulary.
-        GemmParams& h = ah.p;
-        h.a_mn_major = 0;
-        h.a_kchunk = 1;
-        h.b_mn_major = 1;
-        h.b_box3 = d_box3 ? 1 : 0;
-        h.b_k0 = static_cast<int>(c0);
-        h.m_blocks = static_cast<int>(ceil_div(nb_len, P.tile_m));
-        h.n_blocks = static_cast<int>(ceil_div(D, wide_dh ? 2 * BN : BN));
-        h.k_blocks = static_cast<int>(ceil_div(c_len, BK));
-        h.num_units = h.m_blocks * h.n_blocks;
-        h.group_m = std::min(h.m_blocks, 8);
-        h.k_serpentine = 1;   // as for dW (9% fewer DRAM reads on the same head)
-        h.idesc = make_idesc_bf16_f32(P.tile_m, BN, 0, 1);
-        h.timeout_ns = tmo;
-        h.status = status;
-        h.m_valid = nb_len;
-        h.n_valid = static_cast<int>(D);
-        // one chunk: bf16 dH directly; else an fp32 accumulator of this token
-        // block's rows (stored by chunk 0, reduce-added by the others), rounded
-        // to bf16 after the last chunk. The map holds exactly the block's rows.
-        // A shard accumulates straight into its fp32 dH part.
-        const bool dh_direct = P.n_chunks == 1 && !shard;
-        const bool ok_dh = shard ? encode_out(&ah.c, sh.dh_f32 + b0 * D, false, D, nb_len, D)
-                           : dh_direct ? encode_out(&ah.c, dH + b0 * D, true, D, nb_len, D)
-                                       : encode_out(&ah.c, dh_acc, false, D, nb_len, D);
-        if (!ok_dh) return FLCE_ERR_CUDA;
-        ah.a = mG_k;
-        ah.b = mW_mn;
-        h.out_row0 = 0;
-        h.out_mode = dh_direct ? OUT_STORE_BF16 : (c == 0 ? OUT_STORE_F32 : OUT_ADD_F32);
-      }
-      // dW and dH both read only G (and H, W), and write different outputs
-      cudaError_t ge = cudaSuccess;
-      if (both) {
-        const int units = ah.p.num_units + aw.p.num_units;
-        ge = launch_gemm_f32_pair(cta, ah, aw, cta * std::min(units, pairs), st);
-      } else if (dW != nullptr) {
-        ge = launch_gemm_f32(cta, aw.a, aw.b, aw.c, aw.p, cta * std::min(aw.p.num_units, pairs),
-                             st, kWideDw ? 1 : 0);
-      } else if (want_dh) {
-        ge = launch_gemm_f32(cta, ah.a, ah.b, ah.c, ah.p, cta * std::min(ah.p.num_units, pairs),
-                             st, wide_dh ? 1 : 0);
-      }
-      if (ge != cudaSuccess || ((dW != nullptr || want_dh) && !trace())) return FLCE_ERR_CUDA;
-    }
-    if (dH != nullptr && !shard && P.n_chunks > 1 &&
-        (launch_f32_to_bf16(dh_acc, dH + b0 * D, static_cast<int64_t>(nb_len) * D, sms, st) !=
-             cudaSuccess ||
-         !trace()))
-      return FLCE_ERR_CUDA;
-  }
-  if (dW != nullptr && dw_bf16 && !dw_direct_bf16 &&
-      (launch_f32_to_bf16(dw_acc, static_cast<uint16_t*>(dW), V * D, sms, st) != cudaSuccess ||
-       !trace()))
-    return FLCE_ERR_CUDA;
-  return FLCE_OK;
+  BackwardProducts bp{};
+  bp.H = H;
+  bp.W = W;
+  bp.h_k = &mH_k;
+  bp.w_k = &mW_k;
+  bp.launch_grad = launch_gemm_grad;
+  bp.fp8 = fp8 ? 1 : 0;
+  bp.grad.k_blocks = k_blocks_z;
+  bp.grad.acc_scale_h = f8.scale_h;
+  bp.grad.acc_scale_w = f8.scale_w;
+  bp.grad.idesc = idesc_z;
+  bp.grad.labels = labels;
+  bp.grad.ignore_index = o.ignore_index;
+  bp.grad.lse = shard ? sh.lse_in : lse;   // the lse the gradient is formed from
+  bp.grad.gstat = gstat;
+  bp.grad.scale = scal;
+  bp.v_base = v_base;
+  bp.dH = shard ? nullptr : dH;
+  bp.dh_f32 = shard ? sh.dh_f32 : nullptr;
+  bp.dW = dW;
+  bp.dw_bf16 = o.dw_dtype == FLCE_DTYPE_BF16;
+  bp.G = G;
+  bp.dh_acc = dh_acc;
+  bp.dw_acc = dw_acc;
+  bp.timeout_ns = tmo;
+  bp.status = status;
+  bp.sms = sms;
+  bp.stream = st;
+  return launch_backward_products(P, bp, trace);
 }
 
 int workspace_bytes(int64_t N, int64_t D, int64_t V, const flce_options* opt, bool backward,
@@ -792,14 +535,7 @@ int flce_ce_logits(const void* logits, int32_t dtype, int64_t ld, const int32_t*
   float* loss_scalar = per_token ? reinterpret_cast<float*>(ws + 2 * nb + 8) : loss;
   if (status != nullptr && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess)
     return FLCE_ERR_CUDA;
-  int n_traced = 0;
-  auto trace = [&]() -> bool {
-    if (o.trace_events == nullptr || n_traced >= o.trace_capacity) return true;
-    const bool ok = cudaEventRecord(static_cast<cudaEvent_t>(o.trace_events[n_traced]), st) ==
-                    cudaSuccess;
-    ++n_traced;
-    return ok;
-  };
+  flce::KernelTrace trace{o.trace_events, o.trace_capacity, st};
   if (!trace()) return FLCE_ERR_CUDA;
   const int Ni = static_cast<int>(N), Vi = static_cast<int>(V);
   if (dlogits != nullptr &&
