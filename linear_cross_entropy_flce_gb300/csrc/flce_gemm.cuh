@@ -1,4 +1,4 @@
-// Persistent, warp-specialised tcgen05 GEMM for sm_103a with three fused
+// Persistent, warp-specialised tcgen05 GEMM for sm_103a with five fused
 // epilogues. Every product of fused linear cross-entropy runs through it:
 //
 //   LSE  : Z = H W^T tile by tile, accumulated in TMEM; the epilogue keeps a
@@ -12,6 +12,10 @@
 //          sum off the target and -scale * (1 - p) at it, and writes one chunk of
 //          G, stored chunk-major (same page, 2. In-Kernel Gradient Computation:
 //          recompute the tile logits from the saved LSE, derive dL/dz in the kernel).
+//   LOGP : as LSE, with the sum that the entropy needs and each token's largest
+//          logits ranked on the fly (log probabilities of given tokens).
+//   LOGP_GRAD : as GRAD, with G = p (A - B (log p + entropy)) from per-token upstream
+//          gradients, and the token's own entry given.
 //   F32  : plain product whose tile is stored as fp32, added to fp32 already in
 //          memory, or stored as bf16 — used for dW = G^T H and dH = G W (same
 //          page, 2.).
@@ -43,6 +47,8 @@
 #include <cstdint>
 
 #include "flce_gemm_params.h"
+#include "flce_rowstat.cuh"
+#include "flce_topk.cuh"
 #include "ptx.cuh"
 
 namespace flce {
@@ -54,7 +60,7 @@ namespace flce {
 template <int kEpi>
 __device__ __forceinline__ int unit_tiles(const GemmParams& p, int u, int& m_blk, int& n_begin,
                                           int& n_end) {
-  const int n_units_per_row = (kEpi == EPI_LSE) ? p.splits : p.n_blocks;
+  const int n_units_per_row = epi_sums_rows(kEpi) ? p.splits : p.n_blocks;
   const int per_group = p.group_m * n_units_per_row;
   const int g = u / per_group;
   const int first_m = g * p.group_m;
@@ -62,7 +68,7 @@ __device__ __forceinline__ int unit_tiles(const GemmParams& p, int u, int& m_blk
   const int r = u - g * per_group;
   const int col = r / gm;
   m_blk = first_m + (r - col * gm);
-  if constexpr (kEpi == EPI_LSE) {
+  if constexpr (epi_sums_rows(kEpi)) {
     n_begin = static_cast<int>((static_cast<int64_t>(col) * p.n_blocks) / p.splits);
     n_end = static_cast<int>((static_cast<int64_t>(col + 1) * p.n_blocks) / p.splits);
   } else {
@@ -127,6 +133,115 @@ __device__ __forceinline__ void lse_chunk(const float (&v)[32], int col_local, i
   }
   st.s = st.s * ex2_approx((st.m - mn) * kLog2e) + ((s0 + s1) + (s2 + s3));
   st.m = mn;
+}
+
+// A token's ranking within its vocabulary range: the top_k largest logits so far, in
+// descending order, in shared memory (entry j of the CTA's 128 rows is contiguous, so
+// the lanes of a warp never conflict), the smallest of them in a register. A thread
+// only touches it when a logit beats that one, about top_k ln(range / top_k) times.
+struct RankState {
+  float last;      // the smallest value of a full list; -inf before
+  float* value;    // [kMaxTopK][BM], this row's column
+  int* id;
+};
+
+// Ids come in ascending order, so an equal value goes behind the ones before it.
+__device__ __forceinline__ void rank_insert(RankState& r, int top_k, float v, int id) {
+  int j = top_k - 1;
+  for (; j > 0; --j) {
+    const float o = r.value[(j - 1) * BM];
+    if (o >= v) break;
+    r.value[j * BM] = o;
+    r.id[j * BM] = r.id[(j - 1) * BM];
+  }
+  r.value[j * BM] = v;
+  r.id[j * BM] = id;
+  r.last = r.value[(top_k - 1) * BM];
+}
+
+// lse_chunk with the entropy's sum and, for top_k > 0, the columns that beat the
+// ranking's last value as a bit mask. The logits are raw: c = log2(e) / temperature
+// is applied in the exponent.
+struct LogpState {
+  RowPart p;   // running max, sum 2^d, sum 2^d d (flce_rowstat.cuh), the token's term left out
+  float zt;
+  bool found;
+};
+
+__device__ __forceinline__ uint32_t logp_chunk(const float (&v)[32], int col_local, int n_valid,
+                                               int rel_target, float c, bool ranked, float last,
+                                               LogpState& st) {
+  float x[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] = v[k];
+  if (col_local + 32 > n_valid) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (col_local + k >= n_valid) x[k] = -INFINITY;
+  }
+  float c0 = max_nan(x[0], x[1]), c1 = max_nan(x[2], x[3]);
+#pragma unroll
+  for (int k = 4; k < 32; k += 4) {
+    c0 = max_nan(c0, max_nan(x[k], x[k + 1]));
+    c1 = max_nan(c1, max_nan(x[k + 2], x[k + 3]));
+  }
+  const float cm = max_nan(c0, c1);
+  uint32_t beats = 0;
+  if (ranked && __any_sync(0xffffffffu, cm > last)) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) beats |= (x[k] > last ? 1u : 0u) << k;
+  }
+  const float mn = max_nan(st.p.m, cm);
+  if (static_cast<unsigned>(rel_target) < 32u) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (k == rel_target) {
+        st.zt = v[k];
+        x[k] = -INFINITY;   // in the max above, not in the sums below
+      }
+    st.found = true;
+  }
+  if (mn == -INFINITY) return beats;
+  const float ms = mn * c;
+  float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const float d0 = fmaxf(fmaf(x[k], c, -ms), kMinExponent);
+    const float d1 = fmaxf(fmaf(x[k + 1], c, -ms), kMinExponent);
+    const float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
+    s0 += e0;
+    s1 += e1;
+    t0 = fmaf(e0, d0, t0);
+    t1 = fmaf(e1, d1, t1);
+  }
+  const float dm = fmaxf((st.p.m - mn) * c, kMinExponent);
+  const float f = exp2_approx(dm);
+  st.p.t = fmaf(fmaf(st.p.s, dm, st.p.t), f, t0 + t1);
+  st.p.s = fmaf(st.p.s, f, s0 + s1);
+  st.p.m = mn;
+  return beats;
+}
+
+// G for one 32-column chunk of the log-probability gradient: l = log p,
+// p (A - B (l + entropy)) off the token and `target` at it, 0 past n_valid.
+__device__ __forceinline__ void logp_grad_chunk(const float (&v)[32], int col_local, int n_valid,
+                                                int rel_target, float inv_t, const float4& k4,
+                                                float target, float (&g)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float l = fmaf(v[k], inv_t, -k4.x);
+    g[k] = ex2_approx(l * kLog2e) * fmaf(-k4.z, l + k4.w, k4.y);
+  }
+  if (static_cast<unsigned>(rel_target) < 32u) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (k == rel_target) g[k] = target;
+  }
+  if (col_local + 32 > n_valid) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (col_local + k >= n_valid) g[k] = 0.f;
+  }
 }
 
 // Epilogue staging. Each epilogue warp writes its 32 rows x 32 columns into a
@@ -243,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&g0.a);
     tma_prefetch_desc(&g0.b);
-    if constexpr (kEpi != EPI_LSE) tma_prefetch_desc(&g0.c);
+    if constexpr (!epi_sums_rows(kEpi)) tma_prefetch_desc(&g0.c);
     if constexpr (kProducts == 2) {
       tma_prefetch_desc(&g1.a);
       tma_prefetch_desc(&g1.b);
@@ -501,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = prow < p.m_valid;
       int y = -1;
       if constexpr (kEpi != EPI_F32) {
-        if (row_ok) {
+        // the log-probability epilogues may run without tokens
+        if (row_ok && (kEpi == EPI_LSE || kEpi == EPI_GRAD || p.labels != nullptr)) {
           const int lab = p.labels[p.row_base + prow];
           y = (lab == p.ignore_index) ? -1 : lab;
         }
@@ -510,6 +626,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Rows past the product (or of another token block) take zmax = +inf, so
       // their G is exactly 0 whatever logits the tile holds for them.
       float zmax = INFINITY, a = 0.f, sc = 0.f, q = -1.f;
+      LogpState lst{{-INFINITY, 0.f, 0.f}, 0.f, false};
+      RankState ranking{-INFINITY, nullptr, nullptr};
+      if constexpr (kEpi == EPI_LOGP) {
+        // the staging boxes' 32 KB, which this epilogue does not use otherwise
+        ranking.value = reinterpret_cast<float*>(smem + Cfg::kRingBytes) + row;
+        ranking.id = reinterpret_cast<int*>(smem + Cfg::kRingBytes + kMaxTopK * BM * 4) + row;
+        for (int j = 0; j < p.top_k; ++j) {
+          ranking.value[j * BM] = -INFINITY;
+          ranking.id[j * BM] = -1;
+        }
+      }
+      // Rows past the product: log p = -3e38, so p and G are 0.
+      float4 k4 = make_float4(3.0e38f, 0.f, 0.f, 0.f);
+      float target = 0.f;
+      if constexpr (kEpi == EPI_LOGP_GRAD) {
+        if (row_ok) {
+          k4 = p.coef[p.row_base + prow];
+          target = p.target[p.row_base + prow];
+        }
+      }
       if constexpr (kEpi == EPI_GRAD) {
         if (row_ok) {
           sc = (y >= 0) ? scale_v : 0.f;
@@ -561,6 +697,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = n_blk * Cfg::kTileN + c * 32;  // product column
           if constexpr (kEpi == EPI_LSE) {
             lse_chunk(v, col, p.n_valid, y - (p.col_base + col), st);
+          } else if constexpr (kEpi == EPI_LOGP) {
+            const uint32_t beats = logp_chunk(v, col, p.n_valid, y - (p.col_base + col),
+                                              p.exp_scale, p.top_k > 0, ranking.last, lst);
+            // the columns that beat some row's ranking, re-read one at a time
+            for (uint32_t u = __reduce_or_sync(0xffffffffu, beats); u != 0; u &= u - 1) {
+              const int k = __ffs(u) - 1;
+              const float z = __uint_as_float(tmem_read_column(taddr + c * 32 + k));
+              if ((beats >> k & 1u) && z > ranking.last)
+                rank_insert(ranking, p.top_k, z, p.col_base + col + k);
+              __syncwarp();
+            }
           } else {
             const uint32_t box = stg + (nbox & 1u) * Cfg::kStgBytes;
             // the store issued two boxes ago from this buffer has read it
@@ -569,6 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kEpi == EPI_GRAD) {
               float g[32];
               grad_chunk(v, col, p.n_valid, y - (p.col_base + col), zmax, a, sc, q, g);
+              stage_bf16_row(box, lane, g);
+            } else if constexpr (kEpi == EPI_LOGP_GRAD) {
+              float g[32];
+              logp_grad_chunk(v, col, p.n_valid, y - (p.col_base + col), p.inv_t, k4, target, g);
               stage_bf16_row(box, lane, g);
             } else if (p.out_mode == OUT_STORE_BF16) {
               stage_bf16_row(box, lane, v);
@@ -581,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // rows and columns outside the map are dropped by the store
               const int oy = p.out_row0 + m_blk * Cfg::kTileM + static_cast<int>(rank) * BM +
                              quarter * 32;
-              if constexpr (kEpi == EPI_GRAD) tma_store_3d(&G.c, box, col & 63, oy, col >> 6);
+              if constexpr (epi_writes_g(kEpi)) tma_store_3d(&G.c, box, col & 63, oy, col >> 6);
               else if (p.out_mode == OUT_ADD_F32) tma_reduce_add_2d(&G.c, box, col, oy);
               else tma_store_2d(&G.c, box, col, oy);
               bulk_commit_group();
@@ -609,13 +760,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_ok && st.found) p.zt[p.row_base + prow] = st.zt;
         }
       }
+      if constexpr (kEpi == EPI_LOGP) {
+        if (ok) {
+          const int blk128 = m_blk * kCta + static_cast<int>(rank);
+          const int64_t slot = (static_cast<int64_t>(col_unit) * p.part_stride + blk128) * BM + row;
+          p.part4[slot] = make_float4(lst.p.m, lst.p.s, lst.p.t, 0.f);
+          if (row_ok && lst.found) p.zt[p.row_base + prow] = lst.zt;
+          for (int j = 0; j < p.top_k; ++j) {
+            const int id = ranking.id[j * BM];
+            p.lists[slot * p.top_k + j] = id < 0 ? 0 : rank_key(ranking.value[j * BM], id);
+          }
+        }
+      }
     }
     if (!ok) {
       if (lane == 0) record_status(p0.status, kStatusTimeout);
       *abort_flag = 1;
     }
     // every store of this warp has landed before the CTA can exit
-    if constexpr (kEpi != EPI_LSE) {
+    if constexpr (!epi_sums_rows(kEpi)) {
       if (lane == 0) bulk_wait_group_all();
       __syncwarp();
     }

@@ -59,7 +59,12 @@ struct TileCfg {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum EpiKind { EPI_LSE = 0, EPI_GRAD = 1, EPI_F32 = 2 };
+// EPI_LOGP is EPI_LSE with the entropy's sum and the ranking of the largest logits;
+// EPI_LOGP_GRAD is EPI_GRAD for per-token upstream gradients of log probability,
+// entropy and log-sum-exp.
+enum EpiKind { EPI_LSE = 0, EPI_GRAD = 1, EPI_F32 = 2, EPI_LOGP = 3, EPI_LOGP_GRAD = 4 };
+__host__ __device__ constexpr bool epi_sums_rows(int epi) { return epi == EPI_LSE || epi == EPI_LOGP; }
+__host__ __device__ constexpr bool epi_writes_g(int epi) { return epi == EPI_GRAD || epi == EPI_LOGP_GRAD; }
 // Output of the fp32 epilogue through the output tensor map: store fp32, add fp32
 // to what is there (TMA reduce-add), or store rounded to bf16.
 enum OutMode { OUT_STORE_F32 = 0, OUT_ADD_F32 = 1, OUT_STORE_BF16 = 2 };
@@ -124,6 +129,18 @@ struct GemmParams {
   // it is, with no difference of nearly equal numbers when p is close to 1
   const float4* gstat;
   const float* scale;     // EPI_GRAD: device scalar grad_scale / n
+  // EPI_LOGP / EPI_LOGP_GRAD: 1 / temperature of the logits, and that times log2(e)
+  float inv_t, exp_scale;
+  int top_k;              // EPI_LOGP: length of each token's ranking (0: none)
+  // EPI_LOGP: per (vocabulary range, token) (max of the raw logits, sum 2^d,
+  // sum 2^d d, 0) without the token's own term, [splits][part_stride][BM], and the
+  // ranking of the range, [splits][part_stride][BM][top_k] keys in descending order
+  float4* part4;
+  uint64_t* lists;
+  // EPI_LOGP_GRAD: per token (lse, A, B, entropy) with G = p (A - B (log p + entropy)),
+  // and the entry at the token
+  const float4* coef;
+  const float* target;
   // EPI_F32: the output map (third tensor map) holds product row r at map row
   // out_row0 + r, product column c at map column c; boxes of 32 x 32. EPI_GRAD: the
   // map is the chunk-major G, [columns/64][rows][64], boxes of 32 x 32 x 1.

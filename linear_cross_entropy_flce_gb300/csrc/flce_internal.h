@@ -81,4 +81,51 @@ cudaError_t launch_quantize_e4m3(const uint16_t* x, int64_t n, uint8_t* q, float
 cudaError_t launch_scale(void* x, int64_t bytes, int bf16, const float* scale, int sms,
                          cudaStream_t stream);
 
+// The log-probability GEMMs (cluster pairs, bf16): row sums and rankings of each
+// vocabulary range (p.part4, p.lists, p.zt), and G from p.coef / p.target.
+cudaError_t launch_gemm_logp(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
+                             int grid, cudaStream_t stream);
+cudaError_t launch_gemm_logp_grad(int cta_group, const CUtensorMap& a, const CUtensorMap& b,
+                                  const CUtensorMap& c, const GemmParams& p, int grid,
+                                  cudaStream_t stream, int fp8);
+
+// Joins the vocabulary ranges of launch_gemm_logp into the outputs (any may be null;
+// top_lp and top_id are [N, top_k]).
+cudaError_t launch_logprob_merge(const float4* part, const float* zt, const uint64_t* lists,
+                                 const int32_t* tokens, int N, int V, int part_stride, int splits,
+                                 int ignore_index, int top_k, float inv_t, float* logprob,
+                                 float* entropy, float* lse, float* top_lp, int32_t* top_id,
+                                 int32_t* status, cudaStream_t stream);
+
+// Per token (lse, A, B, entropy) and the token's own entry for launch_gemm_logp_grad.
+cudaError_t launch_logprob_coef(const int32_t* tokens, int N, int V, int ignore_index, float inv_t,
+                                const float* logprob, const float* entropy, const float* lse,
+                                const float* dlogprob, const float* dentropy, const float* dlse,
+                                float4* coef, float* target, cudaStream_t stream);
+
+// Log probabilities over given logits (bf16 = 1: bf16, else fp32), and their gradient
+// in the logits (g may be z).
+cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const int32_t* tokens,
+                                int N, int V, int ignore_index, int top_k, float inv_t,
+                                float* logprob, float* entropy, float* lse, float* top_lp,
+                                int32_t* top_id, int32_t* status, int sms, cudaStream_t stream);
+cudaError_t launch_logprob_grad(int bf16, const void* z, int64_t ld_bytes, const int32_t* tokens,
+                                int N, int V, int ignore_index, float inv_t, const float* logprob,
+                                const float* entropy, const float* lse, const float* dlogprob,
+                                const float* dentropy, const float* dlse, void* g,
+                                int64_t gld_bytes, cudaStream_t stream);
+
+// Layer norm (bf16 / wbf16: types of the rows / of weight, bias and their gradients;
+// strides in elements). part: kNormRanges * 2 * D floats.
+constexpr int kNormRanges = 304;
+cudaError_t launch_layer_norm(const void* x, int bf16, int64_t ldx, const void* weight,
+                              const void* bias, int wbf16, int N, int D, float eps, void* y,
+                              int64_t ldy, float* mean, float* rstd, int sms,
+                              cudaStream_t stream);
+cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int bf16,
+                                       int64_t ldx, const void* weight, int wbf16,
+                                       const float* mean, const float* rstd, int N, int D,
+                                       void* dx, int64_t lddx, void* dweight, void* dbias,
+                                       float* part, int sms, cudaStream_t stream);
+
 }  // namespace flce

@@ -1,0 +1,130 @@
+// The statistics of a softmax row that log probabilities and entropies are formed
+// from, kept in the base-2 domain the hardware exponential works in.
+//
+// With d_v = (z_v - m) c, c = log2(e) / temperature, a part of a row is
+//   m = max z (raw logits), s = sum 2^d, t = sum 2^d d
+// and parts join by rescaling to the larger maximum. The token's own term is left out
+// of s and t and added at the end, so that 1 - p of a confident token, and its log
+// probability -log1p(others / its term), are no differences of nearly equal numbers.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+namespace flce {
+
+constexpr float kLn2 = 0.6931471805599453f;
+// A 2^d below 2^-200 is 0 in fp32 however d is rounded; the floor keeps d finite for
+// logits of -inf, whose 2^d d would otherwise be 0 * -inf.
+constexpr float kMinExponent = -200.f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Maximum that keeps a NaN (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// A log-sum-exp below this comes from a row whose every id is masked, with -inf or with
+// the type's lowest value. Its gradient is 0: p = exp(x - lse) has no digits there.
+constexpr float kMaskedLse = -1.0e30f;
+
+struct RowPart {
+  float m, s, t;
+};
+
+// Joins b into a (either may be empty: m = -inf, s = t = 0). A NaN or +inf maximum
+// stays one; s and t then have no meaning.
+__device__ __forceinline__ void row_join(RowPart& a, const RowPart& b, float c) {
+  const float M = max_nan(a.m, b.m);
+  if (M == -INFINITY) return;
+  const float da = fmaxf((a.m - M) * c, kMinExponent), db = fmaxf((b.m - M) * c, kMinExponent);
+  const float fa = exp2_approx(da), fb = exp2_approx(db);
+  a.t = fmaf(a.s, da, a.t) * fa + fmaf(b.s, db, b.t) * fb;
+  a.s = a.s * fa + b.s * fb;
+  a.m = M;
+}
+
+struct RowOut {
+  float logprob, entropy, lse;
+  float m, log_s;   // lse = m / temperature + log_s, kept apart for id_logprob
+};
+
+// Log probability of an id from its raw logit: no difference with lse, in which log S
+// drowns when the logits are far from 0. NaN in a row without a softmax.
+__device__ __forceinline__ float id_logprob(const RowOut& r, float z, float inv_t) {
+  return fmaf(z - r.m, inv_t, -r.log_s);
+}
+
+// The row's outputs from its joined part (the token's term left out), the raw logit zt
+// of the token, and whether it has one. `inv_t` = 1 / temperature, c = log2(e) inv_t.
+__device__ __forceinline__ RowOut row_finish(const RowPart& p, float zt, bool has_token,
+                                             float inv_t, float c) {
+  RowOut o;
+  o.m = p.m;
+  o.log_s = 0.f;
+  if (!(p.m < INFINITY)) {   // NaN or +inf among the logits
+    o.entropy = o.lse = o.log_s = __uint_as_float(0x7FC00000u);
+    o.logprob = has_token ? o.lse : 0.f;
+    return o;
+  }
+  if (p.m == -INFINITY) {    // every id is masked
+    o.lse = -INFINITY;
+    o.entropy = 0.f;
+    o.logprob = has_token ? -INFINITY : 0.f;
+    return o;
+  }
+  float dt = kMinExponent, et = 0.f;
+  if (has_token) {
+    dt = fmaxf((zt - p.m) * c, kMinExponent);
+    et = exp2_approx(dt);
+  }
+  const float S = p.s + et, T = fmaf(et, dt, p.t);
+  const float log_s = logf(S);
+  o.log_s = log_s;
+  o.lse = fmaf(p.m, inv_t, log_s);
+  const float h = fmaf(-kLn2, T / S, log_s);
+  o.entropy = h < 0.f ? 0.f : h;
+  // e_t < 2^-60: x_y - lse has no cancellation, and the quotient could overflow
+  o.logprob = !has_token ? 0.f : (et >= 0x1p-60f ? -log1pf(p.s / et) : id_logprob(o, zt, inv_t));
+  return o;
+}
+
+// A row's gradient coefficients: dL/dz_v = p_v (A - B (log p_v + entropy)) off the
+// token and `target` at it, everything divided by the temperature.
+struct RowCoef {
+  float lse, A, B, entropy, target;
+};
+
+__device__ __forceinline__ RowCoef row_coef(float lse, float entropy, float logprob, float a,
+                                            float b, float c, bool has_token, float inv_t) {
+  RowCoef r;
+  if (!has_token) a = 0.f;
+  r.lse = lse;
+  r.entropy = b != 0.f ? entropy : 0.f;
+  r.A = (c - a) * inv_t;
+  r.B = b * inv_t;
+  r.target = 0.f;
+  if (lse != lse) r.A = lse;   // NaN in the row: NaN everywhere, also where p is 0
+  if (lse < kMaskedLse) {   // every id is masked: no gradient
+    r.lse = 3.0e38f;        // p = 0 for every finite logit
+    r.A = r.B = r.entropy = 0.f;
+    return r;
+  }
+  if (has_token) {
+    const float lp = fmaxf(logprob, -1.0e4f);   // p log p of a masked token is 0
+    const float p = expf(lp);
+    r.target = (-expm1f(lp) * a + p * (c - b * (lp + r.entropy))) * inv_t;
+    if (logprob != logprob) r.target = logprob;
+    if (logprob == -INFINITY) r.target = 0.f;   // a -inf logit has no gradient
+  }
+  return r;
+}
+
+}  // namespace flce
