@@ -5,10 +5,18 @@
 //   g = dy weight, dx = rstd (g - mean(g) - h mean(g h)),
 //   dweight = sum_rows dy h, dbias = sum_rows dy
 //
-// One row per CTA; the row is read again (from the caches) for each of its passes. The
-// sums over rows go through one fp32 partial per range of rows, joined in a fixed order.
+// Forward: a group of R threads holds a row in registers, so it is read once; the variance
+// is taken from centred values. Backward: the groups of a persistent grid walk the rows,
+// each thread owning the same columns of every row, so that dweight and dbias accumulate
+// in its registers while dx is formed from the same loads; the next row is loaded before
+// the current one is reduced. One fp32 partial per CTA is left, joined in a fixed order.
+//
+// Accesses are as wide as the hidden size, the strides and the addresses allow (VW
+// elements, 2 to 16 bytes). Rows longer than 1024 threads can hold take the looped
+// kernels, which read a row again for each of its passes.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "flce_internal.h"
 
@@ -126,17 +134,377 @@ __global__ void __launch_bounds__(kColumnThreads)
   part[(static_cast<int64_t>(range) * 2 + 1) * D + i] = db;
 }
 
-__global__ void layer_norm_join_kernel(const float* __restrict__ part, int ranges, int D,
-                                       void* dweight, void* dbias, int wbf16) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= D) return;
-  float dw = 0.f, db = 0.f;
-  for (int r = 0; r < ranges; ++r) {
-    dw += part[(static_cast<int64_t>(r) * 2) * D + i];
-    db += part[(static_cast<int64_t>(r) * 2 + 1) * D + i];
+// Adds up the partials: 32 columns of dweight and dbias per block, eight warps each
+// taking every eighth partial, in a fixed order.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    layer_norm_join_kernel(const float* __restrict__ part, int ranges, int D, void* dweight,
+                           void* dbias, int wbf16) {
+  __shared__ float2 s_sum[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + lane;
+  float2 s = make_float2(0.f, 0.f);
+  if (i < D) {
+#pragma unroll 4
+    for (int r = warp; r < ranges; r += kJoinWarps) {
+      s.x += part[static_cast<int64_t>(r) * 2 * D + i];
+      s.y += part[static_cast<int64_t>(r) * 2 * D + D + i];
+    }
   }
-  if (dweight != nullptr) store_from_f32(dweight, i, dw, wbf16);
-  if (dbias != nullptr) store_from_f32(dbias, i, db, wbf16);
+  s_sum[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && i < D) {
+#pragma unroll
+    for (int q = 1; q < kJoinWarps; ++q) {
+      s.x += s_sum[q][lane].x;
+      s.y += s_sum[q][lane].y;
+    }
+    if (dweight != nullptr) store_from_f32(dweight, i, s.x, wbf16);
+    if (dbias != nullptr) store_from_f32(dbias, i, s.y, wbf16);
+  }
+}
+
+// ---- rows held in registers ---------------------------------------------------------
+
+template <int kBytes>
+struct RawOf;
+template <> struct RawOf<16> { using type = uint4; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<2> { using type = uint16_t; };
+
+// VW consecutive elements, loaded and stored as one access.
+template <int kBf16, int VW>
+struct Pack {
+  static constexpr int kBytes = VW * (kBf16 ? 2 : 4);
+  using Raw = typename RawOf<kBytes>::type;
+  __device__ static Raw load(const void* p, int64_t i) {
+    return *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p) + i * (kBf16 ? 2 : 4));
+  }
+  __device__ static void widen(Raw raw, float (&x)[VW]) {
+    if constexpr (!kBf16) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) x[e] = __uint_as_float(w[e]);
+    } else if constexpr (VW == 1) {
+      x[0] = __uint_as_float(static_cast<uint32_t>(raw) << 16);
+    } else {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+      for (int e = 0; e < VW; e += 2) {
+        x[e] = __uint_as_float(w[e / 2] << 16);
+        x[e + 1] = __uint_as_float(w[e / 2] & 0xFFFF0000u);
+      }
+    }
+  }
+  __device__ static void store(void* p, int64_t i, const float (&x)[VW]) {
+    Raw raw;
+    if constexpr (!kBf16) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) w[e] = __float_as_uint(x[e]);
+    } else if constexpr (VW == 1) {
+      uint32_t r;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(x[0]));
+      raw = static_cast<uint16_t>(r & 0xFFFFu);
+    } else {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
+#pragma unroll
+      for (int e = 0; e < VW; e += 2)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e / 2]) : "f"(x[e + 1]), "f"(x[e]));
+    }
+    *reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + i * (kBf16 ? 2 : 4)) = raw;
+  }
+};
+
+// VW values of weight or bias from element i, or `none` without one.
+template <int VW>
+__device__ __forceinline__ void load_param(const void* p, int i, int wbf16, float none,
+                                           float (&v)[VW]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = none;
+  } else if (wbf16) {
+    Pack<1, VW>::widen(Pack<1, VW>::load(p, i), v);
+  } else {
+    constexpr int W4 = VW < 4 ? VW : 4;
+#pragma unroll
+    for (int k = 0; k < VW; k += W4) {
+      float q[W4];
+      Pack<0, W4>::widen(Pack<0, W4>::load(p, i + k), q);
+#pragma unroll
+      for (int e = 0; e < W4; ++e) v[k + e] = q[e];
+    }
+  }
+}
+
+// Sum of a pair over the R threads of a group (R a multiple of 32, at most the block);
+// the same value in all of them. `slots` are the block's warps' slots, not read by any
+// warp that has not passed a block barrier since the call before last.
+__device__ __forceinline__ float2 group_sum2(float2 v, int R, float2* slots) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  if (R == 32) return v;
+  if (lane == 0) slots[warp] = v;
+  __syncthreads();
+  const int per = R >> 5, base = warp - warp % per;
+  v = lane < per ? slots[base + lane] : make_float2(0.f, 0.f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  return v;
+}
+
+template <int kBf16, int VW, int kNv>
+__global__ void __launch_bounds__(1024)
+    layer_norm_rows_kernel(const void* x, int64_t ldx, const void* weight, const void* bias,
+                           int wbf16, int N, int D, float eps, void* y, int64_t ldy,
+                           float* mean_out, float* rstd_out, int R) {
+  using P = Pack<kBf16, VW>;
+  __shared__ float2 s_slots[2][32];
+  const int group = threadIdx.x / R, t = threadIdx.x % R;
+  const int row = blockIdx.x * (blockDim.x / R) + group;
+  const int nvec = row < N ? D / VW : 0;
+  const int64_t xr = static_cast<int64_t>(row) * ldx, yr = static_cast<int64_t>(row) * ldy;
+  float v[kNv][VW];
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kNv; ++k) {
+    const int i = t + k * R;
+    if (i < nvec) {
+      P::widen(P::load(x, xr + static_cast<int64_t>(i) * VW), v[k]);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) sum += v[k][e];
+    }
+  }
+  const float inv_d = 1.f / static_cast<float>(D);
+  const float mean = group_sum2(make_float2(sum, 0.f), R, s_slots[0]).x * inv_d;
+  float sq = 0.f;
+#pragma unroll
+  for (int k = 0; k < kNv; ++k)
+    if (t + k * R < nvec) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        const float d = v[k][e] - mean;
+        sq = fmaf(d, d, sq);
+      }
+    }
+  const float rstd = 1.f / sqrtf(group_sum2(make_float2(sq, 0.f), R, s_slots[1]).x * inv_d + eps);
+#pragma unroll
+  for (int k = 0; k < kNv; ++k) {
+    const int i = t + k * R;
+    if (i < nvec) {
+      float w[VW], b[VW];
+      load_param<VW>(weight, i * VW, wbf16, 1.f, w);
+      load_param<VW>(bias, i * VW, wbf16, 0.f, b);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) v[k][e] = fmaf((v[k][e] - mean) * rstd, w[e], b[e]);
+      P::store(y, yr + static_cast<int64_t>(i) * VW, v[k]);
+    }
+  }
+  if (t == 0 && row < N) {
+    if (mean_out != nullptr) mean_out[row] = mean;
+    if (rstd_out != nullptr) rstd_out[row] = rstd;
+  }
+}
+
+// dx and, in part (not null), this CTA's sums over its rows: part[blockIdx.x][0][i] of dy h
+// and [1][i] of dy.
+template <int kBf16, int VW, int kNv>
+__global__ void __launch_bounds__(512, kNv * VW <= 8 && VW > 1 ? 2 : 1)
+    layer_norm_grad_kernel(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                           const void* weight, int wbf16, const float* __restrict__ mean_in,
+                           const float* __restrict__ rstd_in, int N, int D, void* dx,
+                           int64_t lddx, float* part, int R) {
+  using P = Pack<kBf16, VW>;
+  using Raw = typename P::Raw;
+  __shared__ float2 s_slots[2][16];
+  extern __shared__ float s_cols[];   // [groups][2 * D] when several groups share a block
+  const int groups = blockDim.x / R;
+  const int group = threadIdx.x / R, t = threadIdx.x % R;
+  const int nvec = D / VW;
+  const int step = gridDim.x * groups;
+  const float inv_d = 1.f / static_cast<float>(D);
+  float dw[kNv][VW], db[kNv][VW], w[kNv][VW];
+#pragma unroll
+  for (int k = 0; k < kNv; ++k) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) dw[k][e] = db[k][e] = 0.f;
+    if (t + k * R < nvec) load_param<VW>(weight, (t + k * R) * VW, wbf16, 1.f, w[k]);
+  }
+  Raw rx[kNv], rg[kNv];
+  float mean = 0.f, rstd = 0.f;
+  auto fetch = [&](int row) {
+    if (row < N) {
+#pragma unroll
+      for (int k = 0; k < kNv; ++k) {
+        const int i = t + k * R;
+        if (i < nvec) {
+          rx[k] = P::load(x, static_cast<int64_t>(row) * ldx + static_cast<int64_t>(i) * VW);
+          rg[k] = P::load(dy, static_cast<int64_t>(row) * lddy + static_cast<int64_t>(i) * VW);
+        }
+      }
+      mean = mean_in[row];
+      rstd = rstd_in[row];
+    }
+  };
+  int row = blockIdx.x * groups + group;
+  fetch(row);
+  // every group of the grid takes as many turns, for the block barriers of the sums
+  const int turns = (N + step - 1) / step;
+  for (int turn = 0; turn < turns; ++turn, row += step) {
+    const bool live = row < N;
+    const float r = rstd;
+    float g[kNv][VW], h[kNv][VW];
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kNv; ++k)
+      if (live && t + k * R < nvec) {
+        P::widen(rx[k], h[k]);
+        P::widen(rg[k], g[k]);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          h[k][e] = (h[k][e] - mean) * r;
+          dw[k][e] = fmaf(g[k][e], h[k][e], dw[k][e]);
+          db[k][e] += g[k][e];
+          g[k][e] *= w[k][e];
+          sum.x += g[k][e];
+          sum.y = fmaf(g[k][e], h[k][e], sum.y);
+        }
+      }
+    fetch(row + step);
+    if (dx != nullptr) {
+      sum = group_sum2(sum, R, s_slots[turn & 1]);
+      const float mg = sum.x * inv_d, mgh = sum.y * inv_d;
+#pragma unroll
+      for (int k = 0; k < kNv; ++k) {
+        const int i = t + k * R;
+        if (live && i < nvec) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) g[k][e] = r * (g[k][e] - mg - h[k][e] * mgh);
+          P::store(dx, static_cast<int64_t>(row) * lddx + static_cast<int64_t>(i) * VW, g[k]);
+        }
+      }
+    }
+  }
+  if (part == nullptr) return;
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * D;
+  if (groups > 1) out = s_cols + static_cast<int64_t>(group) * 2 * D;
+#pragma unroll
+  for (int k = 0; k < kNv; ++k) {
+    const int i = t + k * R;
+    if (i < nvec) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        out[i * VW + e] = dw[k][e];
+        out[D + i * VW + e] = db[k][e];
+      }
+    }
+  }
+  if (groups > 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+      float s = 0.f;
+      for (int q = 0; q < groups; ++q) s += s_cols[q * 2 * D + i];
+      part[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = s;
+    }
+  }
+}
+
+}  // namespace
+
+namespace {
+
+// The widest access (elements) that D, the row strides and the addresses allow.
+int access_width(int bf16, int D, std::initializer_list<int64_t> strides,
+                 std::initializer_list<const void*> rows, std::initializer_list<const void*> params,
+                 int wbf16) {
+  const int elt = bf16 ? 2 : 4, welt = wbf16 ? 2 : 4;
+  int vw = 16 / elt;
+  auto fits = [&](int v) {
+    if (D % v != 0) return false;
+    for (int64_t s : strides)
+      if (s % v != 0) return false;
+    for (const void* p : rows)
+      if (reinterpret_cast<uintptr_t>(p) % static_cast<unsigned>(v * elt) != 0) return false;
+    for (const void* p : params) {
+      const unsigned a = static_cast<unsigned>(v * welt < 16 ? v * welt : 16);
+      if (reinterpret_cast<uintptr_t>(p) % a != 0) return false;
+    }
+    return true;
+  };
+  while (vw > 1 && !fits(vw)) vw /= 2;
+  return vw;
+}
+
+// Threads per row: enough for nvec vectors at `most` per thread, and then more, down to
+// one vector per thread, while the rows alone do not fill the GPU (a quarter of its 2048
+// threads per SM).
+int row_threads(int nvec, int most, int limit, int64_t N, int sms) {
+  int R = 32;
+  while (R * most < nvec) R *= 2;
+  while (R < nvec && R < limit && N * R < static_cast<int64_t>(sms) * 512) R *= 2;
+  return R;
+}
+
+// Vectors of a row that a thread of the forward kernel holds at most.
+constexpr int norm_vectors(int vw) { return vw == 8 ? 2 : 4; }
+
+template <int kBf16, int VW>
+cudaError_t norm_rows(const void* x, int64_t ldx, const void* weight, const void* bias, int wbf16,
+                      int N, int D, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                      int sms, cudaStream_t stream) {
+  constexpr int kMost = norm_vectors(VW);
+  const int nvec = D / VW;
+  const int R = row_threads(nvec, kMost, 1024, N, sms);
+  const int block = R < 128 ? 128 : R;
+  const int rows = block / R;
+  auto go = [&](auto kern) {
+    kern<<<(N + rows - 1) / rows, block, 0, stream>>>(x, ldx, weight, bias, wbf16, N, D, eps, y,
+                                                      ldy, mean, rstd, R);
+    return cudaGetLastError();
+  };
+  const int per = (nvec + R - 1) / R;
+  if (per <= 1) return go(layer_norm_rows_kernel<kBf16, VW, 1>);
+  if (per <= 2) return go(layer_norm_rows_kernel<kBf16, VW, 2>);
+  return go(layer_norm_rows_kernel<kBf16, VW, kMost>);
+}
+
+// The backward kernel: 512 threads per CTA, several rows at a time where a row needs fewer,
+// each thread holding 8 elements of a row (two CTAs per SM by registers), or 16 for rows
+// of more than 4096 (one CTA).
+constexpr int kGradBlock = 512;
+constexpr int grad_elems(int vw) { return vw == 1 ? 8 : 16; }
+
+template <int kBf16, int VW>
+cudaError_t norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                      int wbf16, const float* mean, const float* rstd, int N, int D, void* dx,
+                      int64_t lddx, float* part, int* ranges, int sms, cudaStream_t stream) {
+  constexpr int kMost = grad_elems(VW) / VW;
+  const int nvec = D / VW;
+  const int R = row_threads(nvec, nvec <= kGradBlock * 8 / VW ? 8 / VW : kMost, kGradBlock, N, sms);
+  const int groups = kGradBlock / R;
+  const size_t smem = groups > 1 ? static_cast<size_t>(groups) * 2 * D * 4 : 0;   // at most 32 KB
+  int grid = (N + groups - 1) / groups;
+  if (grid > kNormRanges) grid = kNormRanges;
+  *ranges = grid;
+  auto go = [&](auto kern) {
+    kern<<<grid, kGradBlock, smem, stream>>>(dy, lddy, x, ldx, weight, wbf16, mean, rstd, N, D,
+                                             dx, lddx, part, R);
+    return cudaGetLastError();
+  };
+  const int per = (nvec + R - 1) / R;
+  if (per <= 1) return go(layer_norm_grad_kernel<kBf16, VW, 1>);
+  if (per <= 2) return go(layer_norm_grad_kernel<kBf16, VW, 2>);
+  if constexpr (kMost >= 4)
+    if (per <= 4) return go(layer_norm_grad_kernel<kBf16, VW, 4>);
+  return go(layer_norm_grad_kernel<kBf16, VW, kMost>);
 }
 
 }  // namespace
@@ -145,6 +513,25 @@ cudaError_t launch_layer_norm(const void* x, int bf16, int64_t ldx, const void* 
                               const void* bias, int wbf16, int N, int D, float eps, void* y,
                               int64_t ldy, float* mean, float* rstd, int sms,
                               cudaStream_t stream) {
+  const int vw = access_width(bf16, D, {ldx, ldy}, {x, y}, {weight, bias}, wbf16);
+  if (D / vw <= 1024 * norm_vectors(vw)) {
+    auto go = [&](auto f) {
+      return f(x, ldx, weight, bias, wbf16, N, D, eps, y, ldy, mean, rstd, sms, stream);
+    };
+    if (bf16) {
+      switch (vw) {
+        case 8: return go(norm_rows<1, 8>);
+        case 4: return go(norm_rows<1, 4>);
+        case 2: return go(norm_rows<1, 2>);
+        default: return go(norm_rows<1, 1>);
+      }
+    }
+    switch (vw) {
+      case 4: return go(norm_rows<0, 4>);
+      case 2: return go(norm_rows<0, 2>);
+      default: return go(norm_rows<0, 1>);
+    }
+  }
   const int grid = N < sms * 8 ? N : sms * 8;
   layer_norm_kernel<<<grid, kNormThreads, 0, stream>>>(x, bf16, ldx, weight, bias, wbf16, N, D,
                                                        eps, y, ldy, mean, rstd);
@@ -157,28 +544,51 @@ cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void*
                                        void* dx, int64_t lddx, void* dweight, void* dbias,
                                        float* part, int sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  // the column sums first: dx may overwrite dy
-  if (dweight != nullptr || dbias != nullptr) {
-    const int ranges = N < kNormRanges ? N : kNormRanges;
-    const dim3 grid(static_cast<unsigned>((D + kColumnThreads - 1) / kColumnThreads),
-                    static_cast<unsigned>(ranges));
-    if (ranges > 0)
+  const bool columns = dweight != nullptr || dbias != nullptr;
+  int ranges = 0;
+  const int vw = access_width(bf16, D, {lddy, ldx, dx != nullptr ? lddx : 0}, {dy, x, dx}, {weight},
+                              wbf16);
+  if (N > 0 && D <= grad_elems(vw) * kGradBlock) {
+    auto go = [&](auto f) {
+      return f(dy, lddy, x, ldx, weight, wbf16, mean, rstd, N, D, dx, lddx,
+               columns ? part : nullptr, &ranges, sms, stream);
+    };
+    if (bf16) {
+      switch (vw) {
+        case 8: e = go(norm_grad<1, 8>); break;
+        case 4: e = go(norm_grad<1, 4>); break;
+        case 2: e = go(norm_grad<1, 2>); break;
+        default: e = go(norm_grad<1, 1>); break;
+      }
+    } else {
+      switch (vw) {
+        case 4: e = go(norm_grad<0, 4>); break;
+        case 2: e = go(norm_grad<0, 2>); break;
+        default: e = go(norm_grad<0, 1>); break;
+      }
+    }
+  } else if (N > 0) {
+    // the column sums first: dx may overwrite dy
+    if (columns) {
+      ranges = N < kNormRanges ? N : kNormRanges;
+      const dim3 grid(static_cast<unsigned>((D + kColumnThreads - 1) / kColumnThreads),
+                      static_cast<unsigned>(ranges));
       layer_norm_columns_kernel<<<grid, kColumnThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, mean,
                                                                      rstd, N, D, ranges, part);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    layer_norm_join_kernel<<<(D + 127) / 128, 128, 0, stream>>>(part, ranges, D, dweight, dbias,
-                                                                wbf16);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    if (dx != nullptr) {
+      const int grid = N < sms * 8 ? N : sms * 8;
+      layer_norm_dx_kernel<<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, weight,
+                                                              wbf16, mean, rstd, N, D, dx, lddx);
+      e = cudaGetLastError();
+    }
   }
-  if (dx != nullptr && N > 0) {
-    const int grid = N < sms * 8 ? N : sms * 8;
-    layer_norm_dx_kernel<<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, weight, wbf16,
-                                                            mean, rstd, N, D, dx, lddx);
-    e = cudaGetLastError();
-  }
-  return e;
+  if (e != cudaSuccess || !columns) return e;
+  layer_norm_join_kernel<<<(D + 31) / 32, 32 * kJoinWarps, 0, stream>>>(part, ranges, D, dweight,
+                                                                        dbias, wbf16);
+  return cudaGetLastError();
 }
 
 }  // namespace flce
