@@ -262,7 +262,7 @@ __device__ __forceinline__ float2 group_sum2(float2 v, int R, float2* slots) {
 }
 
 template <int kBf16, int VW, int kNv>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, kNv * (Pack<kBf16, VW>::kBytes + 3) / 4 <= 8 && VW > 1 ? 2 : 1)
     layer_norm_rows_kernel(const void* x, int64_t ldx, const void* weight, const void* bias,
                            int wbf16, int N, int D, float eps, void* y, int64_t ldy,
                            float* mean_out, float* rstd_out, int R) {
@@ -272,40 +272,42 @@ __global__ void __launch_bounds__(1024)
   const int row = blockIdx.x * (blockDim.x / R) + group;
   const int nvec = row < N ? D / VW : 0;
   const int64_t xr = static_cast<int64_t>(row) * ldx, yr = static_cast<int64_t>(row) * ldy;
-  float v[kNv][VW];
+  typename P::Raw raw[kNv];   // as loaded: half the registers of widened bf16
   float sum = 0.f;
 #pragma unroll
-  for (int k = 0; k < kNv; ++k) {
-    const int i = t + k * R;
-    if (i < nvec) {
-      P::widen(P::load(x, xr + static_cast<int64_t>(i) * VW), v[k]);
+  for (int k = 0; k < kNv; ++k)
+    if (t + k * R < nvec) raw[k] = P::load(x, xr + static_cast<int64_t>(t + k * R) * VW);
 #pragma unroll
-      for (int e = 0; e < VW; ++e) sum += v[k][e];
+  for (int k = 0; k < kNv; ++k)
+    if (t + k * R < nvec) {
+      float v[VW];
+      P::widen(raw[k], v);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) sum += v[e];
     }
-  }
   const float inv_d = 1.f / static_cast<float>(D);
   const float mean = group_sum2(make_float2(sum, 0.f), R, s_slots[0]).x * inv_d;
   float sq = 0.f;
 #pragma unroll
   for (int k = 0; k < kNv; ++k)
     if (t + k * R < nvec) {
+      float v[VW];
+      P::widen(raw[k], v);
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        const float d = v[k][e] - mean;
-        sq = fmaf(d, d, sq);
-      }
+      for (int e = 0; e < VW; ++e) sq = fmaf(v[e] - mean, v[e] - mean, sq);
     }
   const float rstd = 1.f / sqrtf(group_sum2(make_float2(sq, 0.f), R, s_slots[1]).x * inv_d + eps);
 #pragma unroll
   for (int k = 0; k < kNv; ++k) {
     const int i = t + k * R;
     if (i < nvec) {
-      float w[VW], b[VW];
+      float v[VW], w[VW], b[VW];
+      P::widen(raw[k], v);
       load_param<VW>(weight, i * VW, wbf16, 1.f, w);
       load_param<VW>(bias, i * VW, wbf16, 0.f, b);
 #pragma unroll
-      for (int e = 0; e < VW; ++e) v[k][e] = fmaf((v[k][e] - mean) * rstd, w[e], b[e]);
-      P::store(y, yr + static_cast<int64_t>(i) * VW, v[k]);
+      for (int e = 0; e < VW; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+      P::store(y, yr + static_cast<int64_t>(i) * VW, v);
     }
   }
   if (t == 0 && row < N) {
@@ -453,8 +455,8 @@ int row_threads(int nvec, int most, int limit, int64_t N, int sms) {
   return R;
 }
 
-// Vectors of a row that a thread of the forward kernel holds at most.
-constexpr int norm_vectors(int vw) { return vw == 8 ? 2 : 4; }
+// Vectors of a row that a thread of the forward kernel holds at most: 16 elements.
+constexpr int norm_vectors(int vw) { return 16 / vw; }
 
 template <int kBf16, int VW>
 cudaError_t norm_rows(const void* x, int64_t ldx, const void* weight, const void* bias, int wbf16,
@@ -473,6 +475,10 @@ cudaError_t norm_rows(const void* x, int64_t ldx, const void* weight, const void
   const int per = (nvec + R - 1) / R;
   if (per <= 1) return go(layer_norm_rows_kernel<kBf16, VW, 1>);
   if (per <= 2) return go(layer_norm_rows_kernel<kBf16, VW, 2>);
+  if constexpr (kMost >= 4)
+    if (per <= 4) return go(layer_norm_rows_kernel<kBf16, VW, 4>);
+  if constexpr (kMost >= 8)
+    if (per <= 8) return go(layer_norm_rows_kernel<kBf16, VW, 8>);
   return go(layer_norm_rows_kernel<kBf16, VW, kMost>);
 }
 
