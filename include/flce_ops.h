@@ -31,7 +31,7 @@ enum { FLCE_MAX_TOP_K = 32 };
 typedef struct flce_logprob_options {
   int32_t ignore_index; /* token id that marks a row without a token; default -100 */
   int32_t top_k;        /* alternatives per row, 0 (default) to min(FLCE_MAX_TOP_K, V) */
-  float temperature;    /* > 0 and finite: the logits are divided by it; default 1 */
+  float temperature;    /* the logits are divided by it: 1e-6 to 1e6, default 1 */
   int32_t dw_dtype;     /* linear form: dW element type, FLCE_DTYPE_F32 (default) or _BF16 */
   int64_t timeout_ns;   /* limit of every device-side wait; 0 = 2 s */
 } flce_logprob_options;

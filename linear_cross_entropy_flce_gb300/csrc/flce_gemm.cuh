@@ -135,49 +135,79 @@ __device__ __forceinline__ void lse_chunk(const float (&v)[32], int col_local, i
   st.m = mn;
 }
 
-// A token's ranking within its vocabulary range: the top_k largest logits so far, in
-// descending order, in shared memory (entry j of the CTA's 128 rows is contiguous, so
-// the lanes of a warp never conflict), the smallest of them in a register. A thread
-// only touches it when a logit beats that one, about top_k ln(range / top_k) times.
+// A token's ranking within its vocabulary range. The thread that owns the row appends the
+// logits that beat the smallest of its top_k so far to a buffer of kBeat entries in shared
+// memory (two instructions each); when some row's buffer could not take another eight
+// columns, the warp joins the fuller buffers with their rows' lists, one row at a time with
+// a key per lane, which also raises the bound. The lists live in the output array (one
+// 8-byte key per lane, L2), so that shared memory holds only the buffers. Inserting each
+// candidate into a sorted list by its own thread, the first form of this, cost the other 31
+// lanes its whole latency: 8192 x 4096 x 128256 with 20 alternatives took 37.4 ms that way,
+// with 5 alternatives 7.6 ms, without any 5.0 ms.
+constexpr int kBeat = 32;
+
 struct RankState {
-  float last;      // the smallest value of a full list; -inf before
-  float* value;    // [kMaxTopK][BM], this row's column
-  int* id;
+  float bound;       // the smallest value of a full list; -inf before, +inf for no row
+  int count;         // entries in this row's buffer
+  uint32_t listed;   // rows of the warp whose list has been written (the same in all lanes)
 };
 
-// Ids come in ascending order, so an equal value goes behind the ones before it.
-__device__ __forceinline__ void rank_insert(RankState& r, int top_k, float v, int id) {
-  int j = top_k - 1;
-  for (; j > 0; --j) {
-    const float o = r.value[(j - 1) * BM];
-    if (o >= v) break;
-    r.value[j * BM] = o;
-    r.id[j * BM] = r.id[(j - 1) * BM];
+// Entry e of a row's buffer: the rotation by the row keeps a warp's accesses, by row or by
+// entry, on different banks.
+__device__ __forceinline__ int beat_slot(int row, int e) { return row * kBeat + ((e + row) & (kBeat - 1)); }
+
+// Joins the buffers that hold more than `keep` entries (-1: all rows, and rows without a list
+// get an empty one) with their lists. `buffer` is the CTA's, `row0` the warp's first row in
+// it, `lists` the warp's first list, `rows` the warp's rows that exist.
+__device__ __forceinline__ void rank_join(RankState& r, uint2* buffer, int row0, int lane,
+                                          uint64_t* lists, int top_k, int keep, int rows) {
+  __syncwarp();
+  const bool mine = lane < rows && r.count > keep && (r.count > 0 || !(r.listed >> lane & 1u));
+  for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo != 0;
+       todo &= todo - 1) {
+    const int i = __ffs(todo) - 1;
+    const int n = __shfl_sync(0xffffffffu, r.count, i);
+    uint64_t* list = lists + static_cast<int64_t>(i) * top_k;
+    uint64_t old = 0, key = 0;
+    if ((r.listed >> i & 1u) && lane < top_k) old = list[lane];
+    if (lane < n) {
+      const uint2 e = buffer[beat_slot(row0 + i, lane)];
+      key = rank_key(__uint_as_float(e.x), static_cast<int>(e.y));
+    }
+    key = warp_merge_desc(warp_sort_desc(key, lane), old, lane);
+    if (lane < top_k) list[lane] = key;
+    const uint64_t last = __shfl_sync(0xffffffffu, key, top_k - 1);
+    r.listed |= 1u << i;
+    if (lane == i) {
+      r.count = 0;
+      r.bound = last != 0 ? key_value(last) : -INFINITY;
+    }
   }
-  r.value[j * BM] = v;
-  r.id[j * BM] = id;
-  r.last = r.value[(top_k - 1) * BM];
+  __syncwarp();
 }
 
-// lse_chunk with the entropy's sum and, for top_k > 0, the columns that beat the
-// ranking's last value as a bit mask. The logits are raw: c = log2(e) / temperature
-// is applied in the exponent.
+// Running row state of the log-probability epilogue. The logits are raw: c = log2(e) /
+// temperature is applied in the exponent.
 struct LogpState {
   RowPart p;   // running max, sum 2^d, sum 2^d d (flce_rowstat.cuh), the token's term left out
   float zt;
   bool found;
 };
 
-__device__ __forceinline__ uint32_t logp_chunk(const float (&v)[32], int col_local, int n_valid,
-                                               int rel_target, float c, bool ranked, float last,
-                                               LogpState& st) {
+// What takes the place of a column that is not summed: 2^d = 0 and d finite, so that
+// 2^d d is 0 too (temperatures are at least 1e-6).
+constexpr float kNoLogit = -1.0e30f;
+
+// lse_chunk with the entropy's sum. Returns the chunk's largest logit.
+__device__ __forceinline__ float logp_chunk(const float (&v)[32], int col_local, int n_valid,
+                                            int rel_target, float c, LogpState& st) {
   float x[32];
 #pragma unroll
   for (int k = 0; k < 32; ++k) x[k] = v[k];
   if (col_local + 32 > n_valid) {
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-      if (col_local + k >= n_valid) x[k] = -INFINITY;
+      if (col_local + k >= n_valid) x[k] = kNoLogit;
   }
   float c0 = max_nan(x[0], x[1]), c1 = max_nan(x[2], x[3]);
 #pragma unroll
@@ -186,28 +216,21 @@ __device__ __forceinline__ uint32_t logp_chunk(const float (&v)[32], int col_loc
     c1 = max_nan(c1, max_nan(x[k + 2], x[k + 3]));
   }
   const float cm = max_nan(c0, c1);
-  uint32_t beats = 0;
-  if (ranked && __any_sync(0xffffffffu, cm > last)) {
-#pragma unroll
-    for (int k = 0; k < 32; ++k) beats |= (x[k] > last ? 1u : 0u) << k;
-  }
   const float mn = max_nan(st.p.m, cm);
   if (static_cast<unsigned>(rel_target) < 32u) {
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       if (k == rel_target) {
         st.zt = v[k];
-        x[k] = -INFINITY;   // in the max above, not in the sums below
+        x[k] = kNoLogit;   // in the max above, not in the sums below
       }
     st.found = true;
   }
-  if (mn == -INFINITY) return beats;
   const float ms = mn * c;
   float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
-    const float d0 = fmaxf(fmaf(x[k], c, -ms), kMinExponent);
-    const float d1 = fmaxf(fmaf(x[k + 1], c, -ms), kMinExponent);
+    const float d0 = fmaf(x[k], c, -ms), d1 = fmaf(x[k + 1], c, -ms);
     const float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
     s0 += e0;
     s1 += e1;
@@ -219,7 +242,7 @@ __device__ __forceinline__ uint32_t logp_chunk(const float (&v)[32], int col_loc
   st.p.t = fmaf(fmaf(st.p.s, dm, st.p.t), f, t0 + t1);
   st.p.s = fmaf(st.p.s, f, s0 + s1);
   st.p.m = mn;
-  return beats;
+  return cm;
 }
 
 // G for one 32-column chunk of the log-probability gradient: l = log p,
@@ -627,15 +650,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // their G is exactly 0 whatever logits the tile holds for them.
       float zmax = INFINITY, a = 0.f, sc = 0.f, q = -1.f;
       LogpState lst{{-INFINITY, 0.f, 0.f}, 0.f, false};
-      RankState ranking{-INFINITY, nullptr, nullptr};
+      RankState ranking{row_ok ? -INFINITY : INFINITY, 0, 0u};
+      uint2* const beaten = reinterpret_cast<uint2*>(smem + Cfg::kRingBytes);
+      uint64_t* lists = nullptr;
+      int warp_rows = 0;   // rows of this warp that exist
       if constexpr (kEpi == EPI_LOGP) {
-        // the staging boxes' 32 KB, which this epilogue does not use otherwise
-        ranking.value = reinterpret_cast<float*>(smem + Cfg::kRingBytes) + row;
-        ranking.id = reinterpret_cast<int*>(smem + Cfg::kRingBytes + kMaxTopK * BM * 4) + row;
-        for (int j = 0; j < p.top_k; ++j) {
-          ranking.value[j * BM] = -INFINITY;
-          ranking.id[j * BM] = -1;
-        }
+        const int blk128 = m_blk * kCta + static_cast<int>(rank);
+        lists = p.lists + ((static_cast<int64_t>(col_unit) * p.part_stride + blk128) * BM +
+                           quarter * 32) * p.top_k;
+        warp_rows = min(32, p.m_valid - (blk128 * BM + quarter * 32));
       }
       // Rows past the product: log p = -3e38, so p and G are 0.
       float4 k4 = make_float4(3.0e38f, 0.f, 0.f, 0.f);
@@ -698,15 +721,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kEpi == EPI_LSE) {
             lse_chunk(v, col, p.n_valid, y - (p.col_base + col), st);
           } else if constexpr (kEpi == EPI_LOGP) {
-            const uint32_t beats = logp_chunk(v, col, p.n_valid, y - (p.col_base + col),
-                                              p.exp_scale, p.top_k > 0, ranking.last, lst);
-            // the columns that beat some row's ranking, re-read one at a time
-            for (uint32_t u = __reduce_or_sync(0xffffffffu, beats); u != 0; u &= u - 1) {
-              const int k = __ffs(u) - 1;
-              const float z = __uint_as_float(tmem_read_column(taddr + c * 32 + k));
-              if ((beats >> k & 1u) && z > ranking.last)
-                rank_insert(ranking, p.top_k, z, p.col_base + col + k);
-              __syncwarp();
+            const float top = logp_chunk(v, col, p.n_valid, y - (p.col_base + col), p.exp_scale, lst);
+            if (p.top_k > 0 && __any_sync(0xffffffffu, top > ranking.bound)) {
+              const int left = p.n_valid - col;   // columns of the chunk that exist
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                if (k % 8 == 0 && __any_sync(0xffffffffu, ranking.count > kBeat - 8))
+                  rank_join(ranking, beaten, quarter * 32, lane, lists, p.top_k, kBeat / 2, warp_rows);
+                if (v[k] > ranking.bound && k < left) {
+                  beaten[beat_slot(row, ranking.count)] =
+                      make_uint2(__float_as_uint(v[k]), static_cast<uint32_t>(p.col_base + col + k));
+                  ++ranking.count;
+                }
+              }
             }
           } else {
             const uint32_t box = stg + (nbox & 1u) * Cfg::kStgBytes;
@@ -766,10 +793,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t slot = (static_cast<int64_t>(col_unit) * p.part_stride + blk128) * BM + row;
           p.part4[slot] = make_float4(lst.p.m, lst.p.s, lst.p.t, 0.f);
           if (row_ok && lst.found) p.zt[p.row_base + prow] = lst.zt;
-          for (int j = 0; j < p.top_k; ++j) {
-            const int id = ranking.id[j * BM];
-            p.lists[slot * p.top_k + j] = id < 0 ? 0 : rank_key(ranking.value[j * BM], id);
-          }
+          // every row's list, empty ones too
+          if (p.top_k > 0)
+            rank_join(ranking, beaten, quarter * 32, lane, lists, p.top_k, -1, warp_rows);
         }
       }
     }

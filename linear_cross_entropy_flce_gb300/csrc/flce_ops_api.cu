@@ -30,9 +30,7 @@ bool known_dtype(int32_t dtype) { return dtype == FLCE_DTYPE_F32 || dtype == FLC
 
 int check_logprob_options(const flce_logprob_options& o, int64_t V) {
   if (o.top_k < 0 || o.top_k > FLCE_MAX_TOP_K || o.top_k > V) return FLCE_ERR_OPTION;
-  if (!(o.temperature > 0.f) || std::isinf(o.temperature)) return FLCE_ERR_OPTION;
-  const float inv = 1.f / o.temperature;
-  if (std::isinf(inv) || !(inv > 0.f)) return FLCE_ERR_OPTION;
+  if (!(o.temperature >= 1e-6f && o.temperature <= 1e6f)) return FLCE_ERR_OPTION;
   if (!known_dtype(o.dw_dtype) || o.timeout_ns < 0) return FLCE_ERR_OPTION;
   return FLCE_OK;
 }

@@ -353,18 +353,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-// One 32-bit column of the warp's 32 lanes, loaded and waited for.
-__device__ __forceinline__ uint32_t tmem_read_column(uint32_t taddr) {
-  uint32_t r;
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r)
-      : "r"(taddr)
-      : "memory");
-  return r;
-}
-
 // ---- UMMA descriptors -------------------------------------------------------------
 //
 // Shared-memory matrix descriptor (64 bit) for the 128-byte swizzled canonical
