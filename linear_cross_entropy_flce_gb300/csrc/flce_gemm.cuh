@@ -1,4 +1,4 @@
-// Persistent, warp-specialised tcgen05 GEMM for sm_103a with five fused
+// Persistent, warp-specialised tcgen05 GEMM for sm_103a with six fused
 // epilogues. Every product of fused linear cross-entropy runs through it:
 //
 //   LSE  : Z = H W^T tile by tile, accumulated in TMEM; the epilogue keeps a
@@ -12,8 +12,8 @@
 //          sum off the target and -scale * (1 - p) at it, and writes one chunk of
 //          G, stored chunk-major (same page, 2. In-Kernel Gradient Computation:
 //          recompute the tile logits from the saved LSE, derive dL/dz in the kernel).
-//   LOGP : as LSE, with the sum that the entropy needs and each token's largest
-//          logits ranked on the fly (log probabilities of given tokens).
+//   LOGP : as LSE, with the sum that the entropy needs (log probabilities of given
+//          tokens); LOGP_TOP also ranks each token's largest logits on the fly.
 //   LOGP_GRAD : as GRAD, with G = p (A - B (log p + entropy)) from per-token upstream
 //          gradients, and the token's own entry given.
 //   F32  : plain product whose tile is stored as fp32, added to fp32 already in
@@ -136,54 +136,96 @@ __device__ __forceinline__ void lse_chunk(const float (&v)[32], int col_local, i
 }
 
 // A token's ranking within its vocabulary range. The thread that owns the row appends the
-// logits that beat the smallest of its top_k so far to a buffer of kBeat entries in shared
-// memory (two instructions each); when some row's buffer could not take another eight
-// columns, the warp joins the fuller buffers with their rows' lists, one row at a time with
-// a key per lane, which also raises the bound. The lists live in the output array (one
-// 8-byte key per lane, L2), so that shared memory holds only the buffers. Inserting each
-// candidate into a sorted list by its own thread, the first form of this, cost the other 31
-// lanes its whole latency: 8192 x 4096 x 128256 with 20 alternatives took 37.4 ms that way,
-// with 5 alternatives 7.6 ms, without any 5.0 ms.
-constexpr int kBeat = 32;
+// logits that beat its bound, the smallest of its top_k so far, to kBeat entries in shared
+// memory; when some row of the warp could not take another eight columns, every thread cuts
+// its entries down to its top_k: a sorting network over their values gives the top_k-th, and
+// one pass keeps what reaches it. All 32 rows of the warp do that at once, about 1000
+// instructions for the warp, ln(range / top_k) or so times per range and token.
+// Measured at 8192 x 4096 x 128256 with 20 alternatives (4.75 ms without any): inserting
+// each candidate into a sorted list by its own thread 37.4 ms, joining buffers and lists row
+// by row with a key per lane 7.6 ms, this 5.3 ms (5.0 ms with 5).
+//
+// An entry is the logit and its column within the range (16 bits: the ranges are planned to
+// have at most 65536 columns), entry e of the CTA's 128 rows contiguous, so that the threads
+// of a warp never conflict.
+constexpr int kBeat = 40;
 
-struct RankState {
-  float bound;       // the smallest value of a full list; -inf before, +inf for no row
-  int count;         // entries in this row's buffer
-  uint32_t listed;   // rows of the warp whose list has been written (the same in all lanes)
+// Compare-exchange, the larger value first.
+__device__ __forceinline__ void order_desc(float& a, float& b) {
+  const float hi = fmaxf(a, b);
+  b = fminf(a, b);
+  a = hi;
+}
+
+// Steps kJ, kJ / 2, ... 1 of a bitonic network over x[0, 32): blocks of kSize in alternating
+// order (kSize = 32: descending).
+template <int kSize, int kJ>
+__device__ __forceinline__ void bitonic_steps(float (&x)[kBeat]) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if ((e & kJ) == 0) {
+      if ((e & kSize) == 0) order_desc(x[e], x[e | kJ]);
+      else order_desc(x[e | kJ], x[e]);
+    }
+  if constexpr (kJ > 1) bitonic_steps<kSize, kJ / 2>(x);
+}
+template <int kSize>
+__device__ __forceinline__ void bitonic_sort(float (&x)[kBeat]) {
+  if constexpr (kSize > 2) bitonic_sort<kSize / 2>(x);
+  bitonic_steps<kSize, kSize / 2>(x);
+}
+// One step of odd-even transposition over x[32, 40), smaller values first.
+template <int kStep>
+__device__ __forceinline__ void transpose_steps(float (&x)[kBeat]) {
+#pragma unroll
+  for (int e = kStep & 1; e + 1 < 8; e += 2) order_desc(x[32 + e + 1], x[32 + e]);
+  if constexpr (kStep < 7) transpose_steps<kStep + 1>(x);
+}
+
+struct RankCut {
+  float bound;
+  int count;
 };
 
-// Entry e of a row's buffer: the rotation by the row keeps a warp's accesses, by row or by
-// entry, on different banks.
-__device__ __forceinline__ int beat_slot(int row, int e) { return row * kBeat + ((e + row) & (kBeat - 1)); }
-
-// Joins the buffers that hold more than `keep` entries (-1: all rows, and rows without a list
-// get an empty one) with their lists. `buffer` is the CTA's, `row0` the warp's first row in
-// it, `lists` the warp's first list, `rows` the warp's rows that exist.
-__device__ __forceinline__ void rank_join(RankState& r, uint2* buffer, int row0, int lane,
-                                          uint64_t* lists, int top_k, int keep, int rows) {
-  __syncwarp();
-  const bool mine = lane < rows && r.count > keep && (r.count > 0 || !(r.listed >> lane & 1u));
-  for (uint32_t todo = __ballot_sync(0xffffffffu, mine); todo != 0;
-       todo &= todo - 1) {
-    const int i = __ffs(todo) - 1;
-    const int n = __shfl_sync(0xffffffffu, r.count, i);
-    uint64_t* list = lists + static_cast<int64_t>(i) * top_k;
-    uint64_t old = 0, key = 0;
-    if ((r.listed >> i & 1u) && lane < top_k) old = list[lane];
-    if (lane < n) {
-      const uint2 e = buffer[beat_slot(row0 + i, lane)];
-      key = rank_key(__uint_as_float(e.x), static_cast<int>(e.y));
+// Cuts a row's entries down to the top_k largest, in the order they came (ascending ids);
+// the new bound is the smallest of them. `values` and `columns` are the shared-memory
+// addresses of the row's entries. Not inlined: its 1000 instructions four times over in
+// the loop over the tile's columns evict the loop from the instruction cache.
+static __device__ __noinline__ RankCut rank_cut(uint32_t values, uint32_t columns, int count, int top_k) {
+  if (count < top_k) return RankCut{-INFINITY, count};
+  float x[kBeat];
+#pragma unroll
+  for (int e = 0; e < kBeat; ++e) {
+    x[e] = -INFINITY;
+    if (e < count) x[e] = ld_shared_f32(values + e * (BM * 4));
+  }
+  bitonic_sort<32>(x);
+  transpose_steps<0>(x);
+  // the 32 largest of both: the maxima of the smallest 8 of one with the other are bitonic
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[24 + e] = fmaxf(x[24 + e], x[32 + e]);
+  bitonic_steps<32, 16>(x);
+  float bound = x[0];
+  int equal = 1;   // entries at the bound that stay
+#pragma unroll
+  for (int e = 1; e < 32; ++e)
+    if (e < top_k) {
+      equal = x[e] == bound ? equal + 1 : 1;
+      bound = x[e];
     }
-    key = warp_merge_desc(warp_sort_desc(key, lane), old, lane);
-    if (lane < top_k) list[lane] = key;
-    const uint64_t last = __shfl_sync(0xffffffffu, key, top_k - 1);
-    r.listed |= 1u << i;
-    if (lane == i) {
-      r.count = 0;
-      r.bound = last != 0 ? key_value(last) : -INFINITY;
+  int kept = 0;
+#pragma unroll 8
+  for (int e = 0; e < kBeat; ++e) {
+    const float v = ld_shared_f32(values + e * (BM * 4));
+    const uint32_t c = ld_shared_u16(columns + e * (BM * 2));
+    if (e < count && (v > bound || (v == bound && equal > 0))) {
+      if (v == bound) --equal;
+      st_shared_f32(values + kept * (BM * 4), v);
+      st_shared_u16(columns + kept * (BM * 2), c);
+      ++kept;
     }
   }
-  __syncwarp();
+  return RankCut{bound, kept};
 }
 
 // Running row state of the log-probability epilogue. The logits are raw: c = log2(e) /
@@ -650,16 +692,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // their G is exactly 0 whatever logits the tile holds for them.
       float zmax = INFINITY, a = 0.f, sc = 0.f, q = -1.f;
       LogpState lst{{-INFINITY, 0.f, 0.f}, 0.f, false};
-      RankState ranking{row_ok ? -INFINITY : INFINITY, 0, 0u};
-      uint2* const beaten = reinterpret_cast<uint2*>(smem + Cfg::kRingBytes);
-      uint64_t* lists = nullptr;
-      int warp_rows = 0;   // rows of this warp that exist
-      if constexpr (kEpi == EPI_LOGP) {
-        const int blk128 = m_blk * kCta + static_cast<int>(rank);
-        lists = p.lists + ((static_cast<int64_t>(col_unit) * p.part_stride + blk128) * BM +
-                           quarter * 32) * p.top_k;
-        warp_rows = min(32, p.m_valid - (blk128 * BM + quarter * 32));
-      }
+      // the ranking's entries are in the staging boxes' 32 KB, which this epilogue does not
+      // use otherwise
+      const uint32_t rank_values = stage0 + Cfg::kRingBytes + static_cast<uint32_t>(row) * 4u;
+      const uint32_t rank_columns =
+          stage0 + Cfg::kRingBytes + kBeat * BM * 4u + static_cast<uint32_t>(row) * 2u;
+      // -inf until there are top_k entries, +inf for a row that does not exist
+      RankCut ranking{row_ok ? -INFINITY : INFINITY, 0};
       // Rows past the product: log p = -3e38, so p and G are 0.
       float4 k4 = make_float4(3.0e38f, 0.f, 0.f, 0.f);
       float target = 0.f;
@@ -720,17 +759,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = n_blk * Cfg::kTileN + c * 32;  // product column
           if constexpr (kEpi == EPI_LSE) {
             lse_chunk(v, col, p.n_valid, y - (p.col_base + col), st);
-          } else if constexpr (kEpi == EPI_LOGP) {
+          } else if constexpr (kEpi == EPI_LOGP || kEpi == EPI_LOGP_TOP) {
             const float top = logp_chunk(v, col, p.n_valid, y - (p.col_base + col), p.exp_scale, lst);
-            if (p.top_k > 0 && __any_sync(0xffffffffu, top > ranking.bound)) {
+            if (kEpi == EPI_LOGP_TOP && __any_sync(0xffffffffu, top > ranking.bound)) {
               const int left = p.n_valid - col;   // columns of the chunk that exist
+              const int first = col - n_begin * Cfg::kTileN;
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
-                if (k % 8 == 0 && __any_sync(0xffffffffu, ranking.count > kBeat - 8))
-                  rank_join(ranking, beaten, quarter * 32, lane, lists, p.top_k, kBeat / 2, warp_rows);
+                if (k % 8 == 0 && __any_sync(0xffffffffu, ranking.count > kBeat - 8)) {
+                  const RankCut cut = rank_cut(rank_values, rank_columns, ranking.count, p.top_k);
+                  if (row_ok) ranking = cut;
+                }
                 if (v[k] > ranking.bound && k < left) {
-                  beaten[beat_slot(row, ranking.count)] =
-                      make_uint2(__float_as_uint(v[k]), static_cast<uint32_t>(p.col_base + col + k));
+                  st_shared_f32(rank_values + ranking.count * (BM * 4), v[k]);
+                  st_shared_u16(rank_columns + ranking.count * (BM * 2),
+                                static_cast<uint32_t>(first + k));
                   ++ranking.count;
                 }
               }
@@ -787,15 +830,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_ok && st.found) p.zt[p.row_base + prow] = st.zt;
         }
       }
-      if constexpr (kEpi == EPI_LOGP) {
+      if constexpr (kEpi == EPI_LOGP || kEpi == EPI_LOGP_TOP) {
         if (ok) {
           const int blk128 = m_blk * kCta + static_cast<int>(rank);
           const int64_t slot = (static_cast<int64_t>(col_unit) * p.part_stride + blk128) * BM + row;
           p.part4[slot] = make_float4(lst.p.m, lst.p.s, lst.p.t, 0.f);
           if (row_ok && lst.found) p.zt[p.row_base + prow] = lst.zt;
-          // every row's list, empty ones too
-          if (p.top_k > 0)
-            rank_join(ranking, beaten, quarter * 32, lane, lists, p.top_k, -1, warp_rows);
+          if constexpr (kEpi == EPI_LOGP_TOP) {   // in no order: the join sorts them
+            const int n = rank_cut(rank_values, rank_columns, ranking.count, p.top_k).count;
+            const int id0 = p.col_base + n_begin * Cfg::kTileN;
+            for (int j = 0; j < p.top_k; ++j)
+              p.lists[slot * p.top_k + j] =
+                  j < n ? rank_key(ld_shared_f32(rank_values + j * (BM * 4)),
+                                   id0 + static_cast<int>(ld_shared_u16(rank_columns + j * (BM * 2))))
+                        : 0;
+          }
         }
       }
     }

@@ -11,7 +11,8 @@ cudaError_t launch_gemm_logp(const CUtensorMap& a, const CUtensorMap& b, const G
   g.a = a;
   g.b = b;
   g.p = p;
-  return launch_gemm<EPI_LOGP, 2, 0, 0>(g, g, grid, stream);
+  return p.top_k > 0 ? launch_gemm<EPI_LOGP_TOP, 2, 0, 0>(g, g, grid, stream)
+                     : launch_gemm<EPI_LOGP, 2, 0, 0>(g, g, grid, stream);
 }
 
 cudaError_t launch_gemm_logp_grad(int cta_group, const CUtensorMap& a, const CUtensorMap& b,

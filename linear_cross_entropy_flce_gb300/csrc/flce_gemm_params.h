@@ -59,11 +59,19 @@ struct TileCfg {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// EPI_LOGP is EPI_LSE with the entropy's sum and the ranking of the largest logits;
+// Column tiles of a vocabulary range at most, where its columns are kept in 16 bits
+// (EPI_LOGP).
+constexpr int kMaxRangeTiles = 65536 / BN;
+
+// EPI_LOGP is EPI_LSE with the entropy's sum, EPI_LOGP_TOP adds the ranking of the largest
+// logits;
 // EPI_LOGP_GRAD is EPI_GRAD for per-token upstream gradients of log probability,
 // entropy and log-sum-exp.
-enum EpiKind { EPI_LSE = 0, EPI_GRAD = 1, EPI_F32 = 2, EPI_LOGP = 3, EPI_LOGP_GRAD = 4 };
-__host__ __device__ constexpr bool epi_sums_rows(int epi) { return epi == EPI_LSE || epi == EPI_LOGP; }
+enum EpiKind { EPI_LSE = 0, EPI_GRAD = 1, EPI_F32 = 2, EPI_LOGP = 3, EPI_LOGP_GRAD = 4,
+               EPI_LOGP_TOP = 5 };
+__host__ __device__ constexpr bool epi_sums_rows(int epi) {
+  return epi == EPI_LSE || epi == EPI_LOGP || epi == EPI_LOGP_TOP;
+}
 __host__ __device__ constexpr bool epi_writes_g(int epi) { return epi == EPI_GRAD || epi == EPI_LOGP_GRAD; }
 // Output of the fp32 epilogue through the output tensor map: store fp32, add fp32
 // to what is there (TMA reduce-add), or store rounded to bf16.
@@ -134,7 +142,7 @@ struct GemmParams {
   int top_k;              // EPI_LOGP: length of each token's ranking (0: none)
   // EPI_LOGP: per (vocabulary range, token) (max of the raw logits, sum 2^d,
   // sum 2^d d, 0) without the token's own term, [splits][part_stride][BM], and the
-  // ranking of the range, [splits][part_stride][BM][top_k] keys in descending order
+  // ranking of the range, [splits][part_stride][BM][top_k] keys in no order, 0 for none
   float4* part4;
   uint64_t* lists;
   // EPI_LOGP_GRAD: per token (lse, A, B, entropy) with G = p (A - B (log p + entropy)),

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   uint64_t list = 0;
   if (top_k > 0) {
     for (int s = first; s < splits; s += kStep) {
-      const uint64_t k = lane < top_k ? lists[slot(s) * top_k + lane] : 0;
+      const uint64_t k = warp_sort_desc(lane < top_k ? lists[slot(s) * top_k + lane] : 0, lane);
       list = s == first ? k : warp_merge_desc(list, k, lane);
     }
   }

@@ -68,8 +68,10 @@ int make_logp_plan(int64_t N, int64_t D, int64_t V, const flce_logprob_options& 
     return FLCE_OK;
   }
   if (!backward)
-    fo.v_splits = choose_splits(static_cast<int>(ceil_div(N, BM * kCtaGroup)),
-                                static_cast<int>(ceil_div(V, BN)), kPlanPairs);
+    // a ranking's entries hold 16 bits of column
+    fo.v_splits = std::max(choose_splits(static_cast<int>(ceil_div(N, BM * kCtaGroup)),
+                                         static_cast<int>(ceil_div(V, BN)), kPlanPairs),
+                           static_cast<int>(ceil_div(ceil_div(V, BN), kMaxRangeTiles)));
   const int rc = make_plan(N, D, V, fo, 2 * kPlanPairs, &L.P, backward);
   if (rc != FLCE_OK) return rc;
   size_t off = backward ? L.P.total : 0;
