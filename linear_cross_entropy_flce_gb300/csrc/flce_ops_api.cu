@@ -19,6 +19,7 @@
 
 #include "../../include/flce_ops.h"
 #include "flce_clip.h"
+#include "flce_gemm_few.h"
 #include "flce_host.h"
 
 namespace flce {
@@ -51,8 +52,15 @@ int check_rows(int64_t N, int64_t V) {
 // that the workspace does not depend on a device being there.
 constexpr int kPlanPairs = 76;
 
+// Up to this many tokens the forward pass takes the logits of all of them (the kernel for few
+// tokens) and then their rows; above it the large GEMM, which does not store them.
+constexpr int64_t kFewTokens = 128;
+
 struct LogpPlan {
   Plan P;
+  bool few = false;
+  int64_t ldz = 0;
+  size_t off_pad = 0, off_z = 0;
   size_t off_part = 0, off_zt = 0, off_lists = 0, off_coef = 0, off_target = 0, total = 0;
 };
 
@@ -64,6 +72,15 @@ int make_logp_plan(int64_t N, int64_t D, int64_t V, const flce_logprob_options& 
   fo.dw_dtype = o.dw_dtype;
   fo.v_splits = 1;
   if (N == 0) {
+    *out = L;
+    return FLCE_OK;
+  }
+  if (!backward && N <= kFewTokens) {
+    L.few = true;
+    L.ldz = static_cast<int64_t>(align_up(static_cast<size_t>(V), 4));
+    L.off_pad = 0;
+    L.off_z = align_up(static_cast<size_t>(kFewPadRows) * D * 2, 256);
+    L.total = L.off_z + static_cast<size_t>(N) * L.ldz * 4;
     *out = L;
     return FLCE_OK;
   }
@@ -92,6 +109,39 @@ int make_logp_plan(int64_t N, int64_t D, int64_t V, const flce_logprob_options& 
   L.total = off;
   *out = L;
   return FLCE_OK;
+}
+
+int few_token_logprobs(const LogpPlan& L, const uint16_t* H, const uint16_t* W,
+                       const int32_t* tokens, int64_t N, int64_t D, int64_t V,
+                       const flce_logprob_options& o, float* logprob, float* entropy, float* lse,
+                       float* top_logprob, int32_t* top_id, uint8_t* ws, int32_t* status, int sms,
+                       cudaStream_t st) {
+  const int kn = few_tile(N);
+  uint16_t* pad = reinterpret_cast<uint16_t*>(ws + L.off_pad);
+  FewParams p{};
+  p.N = static_cast<int>(N);
+  p.V = static_cast<int>(V);
+  p.k_blocks = static_cast<int>(ceil_div(D, BK));
+  p.z = reinterpret_cast<float*>(ws + L.off_z);
+  p.ldz = L.ldz;
+  p.timeout_ns = o.timeout_ns > 0 ? o.timeout_ns : kDefaultTimeoutNs;
+  p.status = status;
+  // more than 64 tokens are read as they are (rows past N read as zero)
+  const bool direct = kn == kFewPadRows;
+  p.copies = kFewPadRows / kn;
+  CUtensorMap mW, mW16, mH;
+  if (!encode_bf16(&mW, W, D, V, D, BK, BM) || !encode_bf16(&mW16, W, D, V, D, BK, 16) ||
+      !encode_bf16(&mH, direct ? H : pad, D, direct ? N : kFewPadRows, D, BK,
+                   static_cast<uint32_t>(kn)))
+    return FLCE_ERR_CUDA;
+  if (!direct && launch_pad_tokens(H, p.N, static_cast<int>(D), kn, pad, st) != cudaSuccess)
+    return FLCE_ERR_CUDA;
+  if (launch_few_logits(kn, mW, mW16, mH, p, sms, st) != cudaSuccess) return FLCE_ERR_CUDA;
+  return launch_logprob_rows(0, p.z, p.ldz * 4, tokens, p.N, p.V, o.ignore_index, o.top_k,
+                             1.f / o.temperature, logprob, entropy, lse, top_logprob, top_id,
+                             status, sms, st) == cudaSuccess
+             ? FLCE_OK
+             : FLCE_ERR_CUDA;
 }
 
 int linear_shape(int64_t N, int64_t D, int64_t V) {
@@ -234,9 +284,12 @@ int flce_linear_token_logprobs(const uint16_t* H, const uint16_t* W, const int32
   int sms = 0;
   rc = device_info(&sms);
   if (rc != FLCE_OK) return rc;
-  const Plan& P = L.P;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (L.few)
+    return few_token_logprobs(L, H, W, tokens, N, D, V, o, logprob, entropy, lse, top_logprob,
+                              top_id, ws, status, sms, st);
+  const Plan& P = L.P;
   const int cta = P.cta;
   CUtensorMap mH, mW;
   if (!encode_bf16(&mH, H, D, N, D, BK, BM) ||

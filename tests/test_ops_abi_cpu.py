@@ -107,7 +107,7 @@ def test_linear_workspace_size():
     # far below the logits, with and without rankings and gradients
     for N, D, V in ((1, 4096, 128256), (8192, 4096, 128256), (4096, 2048, 32000)):
         small, ranked = _linear_ws(N, D, V)[1], _linear_ws(N, D, V, top_k=20)[1]
-        assert 0 < small < ranked
+        assert 0 < small <= ranked   # equal for a few tokens, whose logits are held either way
         if N > 1:
             assert ranked < N * V * 4 // 10
             assert _linear_ws(N, D, V, backward=1)[1] < N * V * 4 // 2
