@@ -108,7 +108,8 @@ cudaError_t launch_logprob_coef(const int32_t* tokens, int N, int V, int ignore_
 cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const int32_t* tokens,
                                 int N, int V, int ignore_index, int top_k, float inv_t,
                                 float* logprob, float* entropy, float* lse, float* top_lp,
-                                int32_t* top_id, int32_t* status, int sms, cudaStream_t stream);
+                                int32_t* top_id, int32_t* status, int sms, int64_t timeout_ns,
+                                cudaStream_t stream);
 cudaError_t launch_logprob_grad(int bf16, const void* z, int64_t ld_bytes, const int32_t* tokens,
                                 int N, int V, int ignore_index, float inv_t, const float* logprob,
                                 const float* entropy, const float* lse, const float* dlogprob,

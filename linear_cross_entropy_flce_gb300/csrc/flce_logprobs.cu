@@ -1,23 +1,34 @@
 // Log probabilities of given tokens over a logits matrix Z [N, V] (fp32 or bf16), with
 // each row's entropy and most likely ids, and their gradient in the logits.
 //
-// Forward, one row per CTA: pass 1 takes the maximum, pass 2 sums 2^d and 2^d d against
-// it (flce_rowstat.cuh) and collects the candidates of the ranking. Any element of the
-// top k is at least as large as the k-th largest of 32 maxima over disjoint groups of
-// threads, since those k groups hold k elements that large; pass 1 gives those maxima,
-// so pass 2 only keeps the elements that reach that threshold, about 2 k of them on
-// logits without many equal values. One warp sorts them. A row where too many reach it
-// (most of its logits equal) is ranked by k passes instead, each the largest key below
-// the one before.
+// Forward, two passes over each row: pass 1 takes the maximum, pass 2 sums 2^d and 2^d d
+// against it (flce_rowstat.cuh) and collects the candidates of the ranking. Any element of
+// the top k is at least as large as the k-th largest of 32 maxima over disjoint groups of
+// threads, since those k groups hold k elements that large; pass 1 gives those maxima, so
+// pass 2 only keeps the elements that reach that threshold, a few more than k on most
+// logits. One warp sorts them. A row where too many reach it is ranked by k passes
+// instead, each the largest key below the one before.
+//
+//   logprob_stream_kernel : rows of up to 880 KB. Persistent clusters of 1-8 CTAs, one row
+//       at a time; each CTA's slice is copied into shared memory by the bulk-copy engine,
+//       double-buffered, so both passes read shared memory and every logit leaves DRAM
+//       once. All but one of the CTA's warps do the passes; the last warp sorts the
+//       candidates of the row before, joins the cluster's parts (each CTA sends its sums
+//       and its ranking to the first one) and starts the copies, so that none of it holds
+//       the passes up.
+//   logprob_rows_kernel : longer rows; one CTA each, read twice from global memory.
 //
 // Backward, elementwise: every entry of dZ from its logit and five numbers of its row.
 //
 // Rows may start at any element: the elements before the first 16-byte boundary and
 // after the last one are read singly.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "flce_internal.h"
+#include "ptx.cuh"
 #include "flce_rowstat.cuh"
 #include "flce_topk.cuh"
 
@@ -26,7 +37,8 @@ namespace flce {
 namespace {
 
 constexpr int kRowThreads = 512;
-constexpr int kCandidates = 1024;
+constexpr int kCandidates = 384;
+constexpr int kMaxRowCluster = 8;
 
 template <int kBf16>
 struct Logit;
@@ -289,6 +301,535 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// ---- rows through shared memory ----------------------------------------------------------
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+// (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1)
+__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                      float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Running maximum over 16-byte vectors, bf16 two at a time.
+template <int kBf16>
+struct VecMax;
+template <>
+struct VecMax<1> {
+  uint32_t a = 0xFF80FF80u, b = 0xFF80FF80u;   // -inf
+  __device__ void take(const uint4& w) {
+    a = max2_nan(a, max2_nan(w.x, w.y));
+    b = max2_nan(b, max2_nan(w.z, w.w));
+  }
+  __device__ float value() const {
+    const uint32_t m = max2_nan(a, b);
+    return max_nan(lo_of(m), hi_of(m));
+  }
+};
+template <>
+struct VecMax<0> {
+  float a = -INFINITY, b = -INFINITY;
+  __device__ void take(const uint4& w) {
+    a = max_nan(a, max_nan(__uint_as_float(w.x), __uint_as_float(w.y)));
+    b = max_nan(b, max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+  __device__ float value() const { return max_nan(a, b); }
+};
+
+// What a CTA knows of a row: maximum, sums, the token's logit if it is in its slice (0
+// otherwise), and its ranking.
+struct __align__(16) RowMsg {
+  float4 part;   // m, s, t, zt
+  uint64_t list[kMaxTopK];
+};
+
+template <int kBf16, bool kTop, int kWarps, int kSlice, int kMinBlocks>
+__global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
+    logprob_stream_kernel(const uint8_t* __restrict__ z, int64_t ld_bytes,
+                          const int32_t* __restrict__ tokens, int N, int V, int ignore_index,
+                          int top_k, float inv_t, float* __restrict__ logprob,
+                          float* __restrict__ entropy, float* __restrict__ lse,
+                          float* __restrict__ top_lp, int32_t* __restrict__ top_id,
+                          int32_t* status, uint64_t timeout_ns) {
+  using L = Logit<kBf16>;
+  constexpr int E = L::E;
+  constexpr int kData = kWarps * 32;          // threads that do the passes
+  constexpr int kAll = kData + 32;
+  constexpr int kBarMax = 1, kBarDone = 2, kBarFree = 4;   // named barriers; the last two in pairs
+  extern __shared__ __align__(128) uint8_t s_rows[];       // two slices
+  __shared__ __align__(8) uint64_t s_full[2];   // a slice's copy has landed
+  __shared__ __align__(8) uint64_t s_got[2];    // first CTA: every CTA's message is here
+  __shared__ __align__(8) uint64_t s_used[2];   // the first CTA has read this CTA's message
+  __shared__ RowMsg s_msg[2][kMaxRowCluster];   // first CTA
+  __shared__ float s_max[2][kWarps][32];
+  __shared__ float2 s_sum[2][kWarps];
+  __shared__ float s_m[2], s_zt[2];
+  __shared__ int s_count[2];
+  __shared__ uint64_t s_cand[kTop ? 2 : 1][kTop ? kCandidates : 1];
+  __shared__ volatile int s_late;               // a wait ran out of time
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int crank = static_cast<int>(cluster_ctarank()), csize = static_cast<int>(cluster_size());
+  const int first = static_cast<int>(blockIdx.x) / csize, step = static_cast<int>(gridDim.x) / csize;
+  const float c = kLog2e * inv_t;
+  if (tid == 0) {
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&s_full[k]), 1);
+      mbar_init(smem_u32(&s_got[k]), static_cast<uint32_t>(csize));
+      mbar_init(smem_u32(&s_used[k]), 1);
+      s_count[k] = 0;
+      s_zt[k] = 0.f;
+    }
+    s_late = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (csize > 1) cluster_sync();   // the barriers exist before a peer arrives on them
+
+  const volatile int never = 0;
+  int begun[2] = {0, 0};   // lane 0 of the last warp: turns of s_full begun
+
+  // This CTA's slice of a row: vectors [v0, v0 + nv) of those between the row's first and
+  // last 16-byte boundary; the first CTA has the elements before them, the last those after.
+  struct Slice {
+    const uint8_t* row;
+    int head, tail, v0, nv;
+  };
+  auto slice_of = [&](int row) {
+    Slice q;
+    q.row = z + static_cast<int64_t>(row) * ld_bytes;
+    q.head = row_head<kBf16>(q.row, V);
+    const int nvec = (V - q.head) / E;
+    q.tail = q.head + nvec * E;
+    const int per = (nvec + csize - 1) / csize;
+    q.v0 = min(nvec, crank * per);
+    q.nv = min(nvec, q.v0 + per) - q.v0;
+    return q;
+  };
+  // single element number i of this CTA (a few at most): its id, or -1
+  auto single_of = [&](const Slice& q, int i) {
+    const int n_head = crank == 0 ? q.head : 0, n_tail = crank == csize - 1 ? V - q.tail : 0;
+    return i < n_head ? i : i < n_head + n_tail ? q.tail + i - n_head : -1;
+  };
+
+  if (warp < kWarps) {
+    int it = 0;
+    for (int row = first; row < N; row += step, ++it) {
+      const int k = it & 1;
+      const Slice q = slice_of(row);
+      const int y = tokens != nullptr ? tokens[row] : ignore_index;
+      const int yt = (y == ignore_index || y < 0 || y >= V) ? -1 : y;
+      const int ie = tid < 16 ? single_of(q, tid) : -1;
+      const float xe = ie >= 0 ? L::load1(q.row + static_cast<int64_t>(ie) * L::kBytes) : -INFINITY;
+      uint8_t* const buf = s_rows + k * kSlice;
+      const uint4* const vec = reinterpret_cast<const uint4*>(buf);
+      if (!mbar_wait_bounded(smem_u32(&s_full[k]), static_cast<uint32_t>((it >> 1) & 1), timeout_ns,
+                             &s_late))
+        s_late = 1;
+      // pass 1
+      VecMax<kBf16> vm;
+#pragma unroll 4
+      for (int v = tid; v < q.nv; v += kData) vm.take(vec[v]);
+      const float mine = max_nan(vm.value(), xe);
+      s_max[k][warp][lane] = mine;
+      // the token's element: its thread keeps the value and takes it out of the sums
+      const int id0 = q.head + q.v0 * E;   // id of the slice's first vector element
+      float zt = 0.f;
+      const bool taken = yt >= id0 && yt < id0 + q.nv * E && (yt - id0) / E % kData == tid;
+      const bool own = taken || (ie >= 0 && ie == yt);
+      if (own) zt = xe;
+      if (taken) {
+        uint8_t* at = buf + static_cast<int64_t>(yt - id0) * L::kBytes;
+        zt = L::load1(at);
+        if (kBf16) *reinterpret_cast<uint16_t*>(at) = 0xFF80u;   // -inf
+        else *reinterpret_cast<float*>(at) = -INFINITY;
+      }
+      bar_sync(kBarMax, kData);
+      float gm = s_max[k][0][lane];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) gm = max_nan(gm, s_max[k][w][lane]);
+      float M = gm;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+      // the last warp has taken what this slot held
+      if (it >= 2) bar_sync(kBarFree + k, kAll);
+      float thr = INFINITY;
+      if constexpr (kTop) {
+        // the top_k-th largest of the maxima over the threads of equal lane
+        int rank = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float o = __shfl_sync(0xffffffffu, gm, j);
+          rank += (o > gm || (o == gm && j < lane)) ? 1 : 0;
+        }
+        const unsigned at = __ballot_sync(0xffffffffu, rank == top_k - 1);
+        thr = at ? __shfl_sync(0xffffffffu, gm, __ffs(at) - 1) : -INFINITY;
+      }
+      if (own) s_zt[k] = zt;
+      float s = 0.f, t = 0.f;
+      if (M > -INFINITY && M < INFINITY) {
+        int equal = 0;   // elements at the threshold that this warp has offered: top_k do
+        // Offers this lane's elements x[0, n) of ids id, id + 1, ...; the whole warp calls.
+        auto offer = [&](const float* x, int n, int id) {
+          uint32_t gt = 0, eq = 0;
+          for (int e = 0; e < n; ++e) {
+            gt |= (x[e] > thr ? 1u : 0u) << e;
+            eq |= (x[e] == thr && x[e] > -INFINITY ? 1u : 0u) << e;
+          }
+          int before = __popc(eq);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int p = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += p;
+          }
+          const int all = __shfl_sync(0xffffffffu, before, 31);
+          int room = top_k - equal - (before - __popc(eq));   // of this lane's equal ones
+          room = room < 0 ? 0 : room;
+          equal += all;
+          const int take = __popc(gt) + min(room, __popc(eq));
+          if (take > 0) {
+            int at = atomicAdd(&s_count[k], take);
+            for (int e = 0; e < n; ++e) {
+              const bool g = gt >> e & 1u;
+              if (g || ((eq >> e & 1u) && room-- > 0)) {
+                if (at < kCandidates) s_cand[kTop ? k : 0][at] = rank_key(x[e], id + e);
+                ++at;
+              }
+            }
+          }
+        };
+        // what smaller logits (and -inf) are raised to: far enough below M that their 2^d is
+        // 0, near enough that d is finite. Rows where rounding leaves no such value (logits
+        // of 1e5 in bf16) or that are that far from 0 clamp the exponent of each element.
+        const float below = M - 200.f / c;
+        uint32_t lo2;
+        asm("cvt.rz.bf16x2.f32 %0, %1, %1;" : "=r"(lo2) : "f"(below));
+        const float lo = kBf16 ? lo_of(lo2) : below;
+        const bool safe = !(fabsf(M) < 1.0e30f) || !((lo - M) * c < -150.f);
+        const bool hot = kTop && __any_sync(0xffffffffu, mine >= thr);
+        float s2 = 0.f, t2 = 0.f;
+#pragma unroll 2
+        for (int vw = warp * 32; vw < q.nv; vw += kData) {
+          const int v = vw + lane;
+          uint4 w;
+          if (v < q.nv) {
+            w = vec[v];
+          } else {
+            const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+            w = make_uint4(none, none, none, none);
+          }
+          if (kTop && hot) {
+            VecMax<kBf16> top;
+            top.take(w);
+            if (__any_sync(0xffffffffu, top.value() >= thr)) {
+              float x[E];
+              L::widen(w, x);
+              offer(x, E, id0 + v * E);
+            }
+          }
+          float x[E];
+          if (!safe) {
+            if constexpr (kBf16) {
+              w.x = max2_nan(w.x, lo2);
+              w.y = max2_nan(w.y, lo2);
+              w.z = max2_nan(w.z, lo2);
+              w.w = max2_nan(w.w, lo2);
+            }
+            L::widen(w, x);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              if constexpr (!kBf16) {
+                x[e] = fmaxf(x[e], lo);
+                x[e + 1] = fmaxf(x[e + 1], lo);
+              }
+              // the difference first: exact near M, however far M is from 0
+              fadd2(x[e], x[e + 1], -M, -M);
+              fmul2(x[e], x[e + 1], c, c);
+            }
+          } else {
+            L::widen(w, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = fmaxf((x[e] - M) * c, kMinExponent);
+          }
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float e0 = exp2_approx(x[e]), e1 = exp2_approx(x[e + 1]);
+            fadd2(s, s2, e0, e1);
+            ffma2(t, t2, e0, e1, x[e], x[e + 1], t, t2);
+          }
+        }
+        s += s2;
+        t += t2;
+        if (ie >= 0 && ie != yt) {
+          const float d = fmaxf((xe - M) * c, kMinExponent);
+          const float e = exp2_approx(d);
+          s += e;
+          t = fmaf(e, d, t);
+        }
+        // the single elements, and the token's that the slice no longer holds, are candidates
+        // as they are
+        if constexpr (kTop) {
+          auto offer_one = [&](float x, int id) {
+            if (x >= thr && x > -INFINITY) {
+              const int at = atomicAdd(&s_count[k], 1);
+              if (at < kCandidates) s_cand[k][at] = rank_key(x, id);
+            }
+          };
+          if (ie >= 0) offer_one(xe, ie);
+          if (taken) offer_one(zt, yt);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+      }
+      if (lane == 0) s_sum[k][warp] = make_float2(s, t);
+      if (tid == 0) s_m[k] = M;
+      bar_arrive(kBarDone + k, kAll);
+    }
+  } else {
+    auto copy = [&](int row, int k) {
+      const Slice q = slice_of(row);
+      const uint32_t bytes = static_cast<uint32_t>(q.nv) * 16u, bar = smem_u32(&s_full[k]);
+      ++begun[k];
+      if (bytes == 0) {   // the row has no vector here: its turn of the barrier passes all the same
+        mbar_arrive(bar);
+        return;
+      }
+      const uint8_t* src = q.row + static_cast<int64_t>(q.head) * L::kBytes + static_cast<int64_t>(q.v0) * 16;
+      const uint32_t dst = smem_u32(s_rows + k * kSlice);
+      // the passes' reads and writes of the buffer come before the copy's
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive_expect_tx(bar, bytes);
+      for (uint32_t off = 0; off < bytes; off += 16384u) {
+        const uint32_t n = min(16384u, bytes - off);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                dst + off),
+            "l"(src + off), "r"(n), "r"(bar)
+            : "memory");
+      }
+    };
+    if (lane == 0) {
+      if (first < N) copy(first, 0);
+      if (first + step < N) copy(first + step, 1);
+    }
+    int it = 0;
+    for (int row = first; row < N; row += step, ++it) {
+      const int k = it & 1;
+      const bool more = row + 2 * static_cast<int64_t>(step) < N;
+      bar_sync(kBarDone + k, kAll);
+      const int y = tokens != nullptr ? tokens[row] : ignore_index;
+      const bool bad = y != ignore_index && (y < 0 || y >= V);
+      const bool has = y != ignore_index && !bad;
+      float2 sums = lane < kWarps ? s_sum[k][lane] : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
+        sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
+      }
+      RowPart part{s_m[k], sums.x, sums.y};
+      float zt = s_zt[k];
+      uint64_t list = 0;
+      if constexpr (kTop) {
+        const int count = s_count[k];
+        if (count <= kCandidates) {
+          for (int b = 0; b < count; b += 32) {
+            const uint64_t key = warp_sort_desc(b + lane < count ? s_cand[k][b + lane] : 0, lane);
+            list = b == 0 ? key : warp_merge_desc(list, key, lane);
+          }
+        } else {
+          // too many reach the threshold: the largest key below the one before, top_k times.
+          // The token's element was taken out of the slice: it joins from its value.
+          const Slice q = slice_of(row);
+          const uint4* vec = reinterpret_cast<const uint4*>(s_rows + k * kSlice);
+          const int id0 = q.head + q.v0 * E;
+          const int ie = lane < 16 ? single_of(q, lane) : -1;
+          const float xe = ie >= 0 ? L::load1(q.row + static_cast<int64_t>(ie) * L::kBytes) : -INFINITY;
+          const bool mine = has && y >= id0 && y < id0 + q.nv * E;
+          uint64_t below = ~0ull;
+          for (int i = 0; i < top_k && below != 0; ++i) {
+            uint64_t best = 0;
+            auto look = [&](float x, int id) {
+              if (x > -INFINITY) {
+                const uint64_t key = rank_key(x, id);
+                if (key < below && key > best) best = key;
+              }
+            };
+            for (int v = lane; v < q.nv; v += 32) {
+              float x[E];
+              L::widen(vec[v], x);
+#pragma unroll
+              for (int e = 0; e < E; ++e) look(x[e], id0 + v * E + e);
+            }
+            if (ie >= 0) look(xe, ie);
+            if (mine && lane == 31) look(zt, y);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              const uint64_t key = __shfl_xor_sync(0xffffffffu, best, o);
+              best = key > best ? key : best;
+            }
+            below = best;
+            if (lane == i) list = best;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        s_count[k] = 0;
+        s_zt[k] = 0.f;
+        if (more) copy(row + 2 * step, k);
+      }
+      __syncwarp();
+      if (more) bar_arrive(kBarFree + k, kAll);
+
+      bool late = s_late != 0;
+      if (csize > 1) {
+        // to the first CTA, once it has read the message two rows before
+        if (it >= 2 && !mbar_wait_bounded<true>(smem_u32(&s_used[k]), static_cast<uint32_t>(((it >> 1) - 1) & 1),
+                                                timeout_ns, &never))
+          late = true;
+        const uint32_t msg = mapa_shared(smem_u32(&s_msg[k][crank]), 0);
+        if (lane == 0)
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(msg), "f"(part.m),
+                       "f"(part.s), "f"(part.t), "f"(zt)
+                       : "memory");
+        if (kTop && lane < top_k)
+          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(msg + 16u + 8u * lane), "l"(list)
+                       : "memory");
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_got[k]), 0));
+        if (crank == 0) {
+          if (!mbar_wait_bounded<true>(smem_u32(&s_got[k]), static_cast<uint32_t>((it >> 1) & 1), timeout_ns,
+                                       &never))
+            late = true;
+          part = RowPart{-INFINITY, 0.f, 0.f};
+          zt = 0.f;
+          list = 0;
+          for (int r = 0; r < csize; ++r) {
+            const float4 p = s_msg[k][r].part;
+            row_join(part, RowPart{p.x, p.y, p.z}, c);
+            zt += p.w;
+            if (kTop) {
+              const uint64_t key = lane < top_k ? s_msg[k][r].list[lane] : 0;
+              list = r == 0 ? key : warp_merge_desc(list, key, lane);
+            }
+          }
+          __syncwarp();
+          if (lane < csize) mbar_arrive_cluster(mapa_shared(smem_u32(&s_used[k]), static_cast<uint32_t>(lane)));
+        }
+      }
+      if (late) s_late = 1;
+      late = __any_sync(0xffffffffu, late);
+      if (crank == 0) {
+        RowOut r = row_finish(part, zt, has, inv_t, c);
+        const float nan = __uint_as_float(0x7FC00000u);
+        if (late) r.logprob = r.entropy = r.lse = nan;
+        if (lane == 0) {
+          if (logprob != nullptr) logprob[row] = bad ? nan : r.logprob;
+          if (entropy != nullptr) entropy[row] = r.entropy;
+          if (lse != nullptr) lse[row] = r.lse;
+          if (bad) record_error(status, 8);
+          if (late) record_error(status, kStatusTimeout);
+        }
+        if (kTop && lane < top_k) {
+          const int64_t at = static_cast<int64_t>(row) * top_k + lane;
+          const bool none = list == 0;
+          top_id[at] = none || late ? -1 : key_id(list);
+          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t);
+        }
+      }
+    }
+  }
+  // copies that nobody waited for land before the memory is given back (only after a timeout)
+  if (warp == kWarps && lane == 0 && s_late) {
+    for (int k = 0; k < 2; ++k)
+      if (begun[k] > 0)
+        mbar_wait_bounded(smem_u32(&s_full[k]), static_cast<uint32_t>((begun[k] - 1) & 1), 1000000000ull, &never);
+  }
+  __syncwarp();
+  // no CTA leaves while a peer may still write to it or arrive on its barriers
+  if (csize > 1) cluster_sync();
+}
+
+template <int kBf16, bool kTop, int kWarps, int kSlice, int kMinBlocks>
+cudaError_t launch_stream(int cluster, int N, int sms, const uint8_t* z, int64_t ld_bytes,
+                          const int32_t* tokens, int V, int ignore_index, int top_k, float inv_t,
+                          float* logprob, float* entropy, float* lse, float* top_lp,
+                          int32_t* top_id, int32_t* status, int64_t timeout_ns,
+                          cudaStream_t stream) {
+  auto kern = logprob_stream_kernel<kBf16, kTop, kWarps, kSlice, kMinBlocks>;
+  constexpr int smem = 2 * kSlice;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  int clusters = sms * kMinBlocks / cluster;
+  if (clusters < 1) clusters = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3((kWarps + 1) * 32, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (N < clusters) {
+    clusters = N;
+  } else if (cluster > 1) {
+    // persistent: no more clusters than can be resident at once (asked once per size)
+    static std::atomic<int> resident[kMaxRowCluster + 1];
+    int active = resident[cluster].load(std::memory_order_relaxed);
+    if (active == 0) {
+      cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster), 1, 1);
+      if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) != cudaSuccess || active < 1)
+        active = clusters;
+      resident[cluster].store(active, std::memory_order_relaxed);
+    }
+    if (active < clusters) clusters = active;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, z, ld_bytes, tokens, N, V, ignore_index, top_k, inv_t,
+                            logprob, entropy, lse, top_lp, top_id, status,
+                            static_cast<uint64_t>(timeout_ns));
+}
+
 // dZ: 16-byte vectors where the row of dZ starts at the same offset from a 16-byte
 // boundary as the row of Z, single elements otherwise. A -inf logit gets 0.
 constexpr int kGradThreads = 256;
@@ -360,16 +901,51 @@ __global__ void __launch_bounds__(kGradThreads)
 cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const int32_t* tokens,
                                 int N, int V, int ignore_index, int top_k, float inv_t,
                                 float* logprob, float* entropy, float* lse, float* top_lp,
-                                int32_t* top_id, int32_t* status, int sms, cudaStream_t stream) {
+                                int32_t* top_id, int32_t* status, int sms, int64_t timeout_ns,
+                                cudaStream_t stream) {
   const uint8_t* zp = static_cast<const uint8_t*>(z);
-  const int grid = N < sms * 4 ? N : sms * 4;
-  auto go = [&](auto kern) {
-    kern<<<grid, kRowThreads, 0, stream>>>(zp, ld_bytes, tokens, N, V, ignore_index, top_k, inv_t,
-                                           logprob, entropy, lse, top_lp, top_id, status);
+  const int64_t row_bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
+  // Slices: small rows whole in CTAs of 128 + 32 threads (16 KB, five per SM), others in
+  // slices of at most 49 KB (two CTAs per SM), or, when eight of those do not hold the row,
+  // 104 KB (one).
+  constexpr int kSmall = 16 << 10, kTwo = 49 << 10, kOne = 104 << 10;
+  auto cluster_for = [&](int64_t slice) {
+    // whole 16-byte vectors per CTA: leave one vector for the rounding up
+    return static_cast<int>((row_bytes + slice - 17) / (slice - 16));
+  };
+  auto go = [&](auto b, auto t) {
+    auto run = [&](auto warps, auto slice, auto blocks, int cluster) {
+      return launch_stream<b(), t(), warps(), slice(), blocks()>(
+          cluster, N, sms, zp, ld_bytes, tokens, V, ignore_index, top_k, inv_t, logprob, entropy,
+          lse, top_lp, top_id, status, timeout_ns, stream);
+    };
+    using std::integral_constant;
+    // few rows: more CTAs for each, down to 8 KB, until every SM has one
+    int spread = sms / N;
+    const int most = static_cast<int>((row_bytes + (8 << 10) - 1) / (8 << 10));
+    spread = spread < most ? spread : most;
+    spread = spread < kMaxRowCluster ? spread : kMaxRowCluster;
+    int cl = cluster_for(kSmall);
+    if (cl <= 1 && spread <= 1)
+      return run(integral_constant<int, 4>{}, integral_constant<int, kSmall>{}, integral_constant<int, 5>{}, 1);
+    cl = cluster_for(kTwo);
+    if (cl <= kMaxRowCluster)
+      return run(integral_constant<int, 16>{}, integral_constant<int, kTwo>{}, integral_constant<int, 2>{},
+                 cl > spread ? cl : spread);
+    cl = cluster_for(kOne);
+    if (cl <= kMaxRowCluster)
+      return run(integral_constant<int, 16>{}, integral_constant<int, kOne>{}, integral_constant<int, 1>{},
+                 cl > spread ? cl : spread);
+    const int grid = N < sms * 4 ? N : sms * 4;
+    logprob_rows_kernel<b(), t()><<<grid, kRowThreads, 0, stream>>>(
+        zp, ld_bytes, tokens, N, V, ignore_index, top_k, inv_t, logprob, entropy, lse, top_lp,
+        top_id, status);
     return cudaGetLastError();
   };
-  if (bf16) return top_k ? go(logprob_rows_kernel<1, true>) : go(logprob_rows_kernel<1, false>);
-  return top_k ? go(logprob_rows_kernel<0, true>) : go(logprob_rows_kernel<0, false>);
+  if (bf16) return top_k ? go(std::integral_constant<int, 1>{}, std::true_type{})
+                         : go(std::integral_constant<int, 1>{}, std::false_type{});
+  return top_k ? go(std::integral_constant<int, 0>{}, std::true_type{})
+               : go(std::integral_constant<int, 0>{}, std::false_type{});
 }
 
 cudaError_t launch_logprob_grad(int bf16, const void* z, int64_t ld_bytes, const int32_t* tokens,

@@ -139,7 +139,7 @@ int few_token_logprobs(const LogpPlan& L, const uint16_t* H, const uint16_t* W,
   if (launch_few_logits(kn, mW, mW16, mH, p, sms, st) != cudaSuccess) return FLCE_ERR_CUDA;
   return launch_logprob_rows(0, p.z, p.ldz * 4, tokens, p.N, p.V, o.ignore_index, o.top_k,
                              1.f / o.temperature, logprob, entropy, lse, top_logprob, top_id,
-                             status, sms, st) == cudaSuccess
+                             status, sms, p.timeout_ns, st) == cudaSuccess
              ? FLCE_OK
              : FLCE_ERR_CUDA;
 }
@@ -189,7 +189,8 @@ int flce_token_logprobs(const void* logits, int32_t dtype, int64_t ld, const int
   return launch_logprob_rows(dtype == FLCE_DTYPE_BF16, logits, ld * elt, tokens,
                              static_cast<int>(N), static_cast<int>(V), o.ignore_index, o.top_k,
                              1.f / o.temperature, logprob, entropy, lse, top_logprob, top_id,
-                             status, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                             status, sms, o.timeout_ns > 0 ? o.timeout_ns : kDefaultTimeoutNs,
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FLCE_OK
              : FLCE_ERR_CUDA;
 }
