@@ -268,18 +268,27 @@ __device__ __forceinline__ float logp_chunk(const float (&v)[32], int col_local,
       }
     st.found = true;
   }
-  const float ms = mn * c;
   float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+  auto sums = [&](auto exponent) {
 #pragma unroll
-  for (int k = 0; k < 32; k += 2) {
-    const float d0 = fmaf(x[k], c, -ms), d1 = fmaf(x[k + 1], c, -ms);
-    const float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
-    s0 += e0;
-    s1 += e1;
-    t0 = fmaf(e0, d0, t0);
-    t1 = fmaf(e1, d1, t1);
+    for (int k = 0; k < 32; k += 2) {
+      const float d0 = exponent(x[k]), d1 = exponent(x[k + 1]);
+      const float e0 = exp2_approx(d0), e1 = exp2_approx(d1);
+      s0 += e0;
+      s1 += e1;
+      t0 = fmaf(e0, d0, t0);
+      t1 = fmaf(e1, d1, t1);
+    }
+  };
+  const float ref = row_ref(mn, c);
+  float dm;
+  if (__all_sync(0xffffffffu, has_ref(mn, c))) {
+    sums([&](float z) { return fmaf(z, c, -ref); });
+    dm = fmaxf(row_ref(st.p.m, c) - ref, kMinExponent);
+  } else {   // very low temperatures, or no finite logits
+    sums([&](float z) { return row_exponent(z, mn, c); });
+    dm = row_shift(st.p.m, mn, c);
   }
-  const float dm = fmaxf((st.p.m - mn) * c, kMinExponent);
   const float f = exp2_approx(dm);
   st.p.t = fmaf(fmaf(st.p.s, dm, st.p.t), f, t0 + t1);
   st.p.s = fmaf(st.p.s, f, s0 + s1);

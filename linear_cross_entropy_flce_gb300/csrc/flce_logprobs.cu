@@ -14,8 +14,9 @@
 //       double-buffered, so both passes read shared memory and every logit leaves DRAM
 //       once. All but one of the CTA's warps do the passes; the last warp sorts the
 //       candidates of the row before, joins the cluster's parts (each CTA sends its sums
-//       and its ranking to the first one) and starts the copies, so that none of it holds
-//       the passes up.
+//       and its ranking to one of them, another one for each row) and starts the copies,
+//       so that none of it holds the passes up.
+//   logprob_warp_kernel : rows of up to 8 KB, one warp each.
 //   logprob_rows_kernel : longer rows; one CTA each, read twice from global memory.
 //
 // Backward, elementwise: every entry of dZ from its logit and five numbers of its row.
@@ -172,8 +173,7 @@ __global__ void __launch_bounds__(kRowThreads)
     // pass 2
     float s = 0.f, t = 0.f;
     auto add = [&](float x) {
-      // the difference first: x c alone overflows for a mask of the type's lowest value
-      const float d = fmaxf((x - M) * c, kMinExponent);
+      const float d = row_exponent(x, M, c);
       const float e = exp2_approx(d);
       s += e;
       t = fmaf(e, d, t);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kRowThreads)
           const int64_t at = static_cast<int64_t>(row) * top_k + lane;
           const bool none = list == 0;
           top_id[at] = none ? -1 : key_id(list);
-          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t);
+          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
         }
       }
     }
@@ -319,12 +319,6 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1) {
   asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
       "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a0), "f"(a1));
-}
-__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "+f"(d0), "+f"(d1)
       : "f"(a0), "f"(a1));
 }
@@ -370,6 +364,272 @@ struct VecMax<0> {
   __device__ float value() const { return max_nan(a, b); }
 };
 
+// 32 values in descending order over the warp.
+__device__ __forceinline__ float warp_sort_values(float v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+    const bool desc = (lane & size) == 0 || size == 32;
+#pragma unroll
+    for (int j = size >> 1; j > 0; j >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, v, j);
+      v = ((lane & j) == 0) == desc ? fmaxf(v, o) : fminf(v, o);
+    }
+  }
+  return v;
+}
+
+// Whether a 16-byte vector has an element that reaches thr (a value of the row's type).
+template <int kBf16>
+struct Reaches;
+template <>
+struct Reaches<1> {
+  uint32_t below;   // the bf16 value before thr, in both halves (-inf for -inf)
+  __device__ explicit Reaches(float thr) {
+    const uint32_t b = __float_as_uint(thr) >> 16;
+    const uint32_t p = b == 0xFF80u ? b : (b & 0x7FFFu) == 0 ? 0x8001u : (b & 0x8000u) ? b + 1 : b - 1;
+    below = p | (p << 16);
+  }
+  __device__ bool operator()(const uint4& w) const {
+    return max2_nan(max2_nan(max2_nan(w.x, w.y), max2_nan(w.z, w.w)), below) != below;
+  }
+};
+template <>
+struct Reaches<0> {
+  float thr;
+  __device__ explicit Reaches(float t) : thr(t) {}
+  __device__ bool operator()(const uint4& w) const {
+    const float m = fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
+                          fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    return m >= thr && m > -INFINITY;
+  }
+};
+
+// Sums 2^d and 2^d d over 16-byte vectors of a row with maximum M.
+template <int kBf16>
+struct RowSums {
+  float M, c, ref, lo;
+  uint32_t lo2;
+  bool clamp;   // element by element, without a reference or a floor
+  float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+  // Smaller logits (and -inf) are raised to a floor: far enough below M that their 2^d is 0,
+  // near enough that d is finite. In bf16 rows of logits of 1e4 or more rounding may leave
+  // no such value: those clamp the exponents.
+  __device__ RowSums(float m, float cc) : M(m), c(cc), ref(row_ref(m, cc)) {
+    const float below = m - 200.f / cc;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %1;" : "=r"(lo2) : "f"(below));
+    lo = kBf16 ? lo_of(lo2) : below;
+    clamp = !has_ref(m, cc) || !(fmaf(lo, cc, -ref) < -150.f);
+  }
+  __device__ void add(uint4 w) {
+    constexpr int E = Logit<kBf16>::E;
+    float x[E];
+    if (!clamp) {
+      if constexpr (kBf16) {
+        w.x = max2_nan(w.x, lo2);
+        w.y = max2_nan(w.y, lo2);
+        w.z = max2_nan(w.z, lo2);
+        w.w = max2_nan(w.w, lo2);
+      }
+      Logit<kBf16>::widen(w, x);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        if constexpr (!kBf16) {
+          x[e] = fmaxf(x[e], lo);
+          x[e + 1] = fmaxf(x[e + 1], lo);
+        }
+        ffma2(x[e], x[e + 1], x[e], x[e + 1], c, c, -ref, -ref);
+      }
+    } else {
+      Logit<kBf16>::widen(w, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = row_exponent(x[e], M, c);
+    }
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float e0 = exp2_approx(x[e]), e1 = exp2_approx(x[e + 1]);
+      fadd2(s0, s1, e0, e1);
+      ffma2(t0, t1, e0, e1, x[e], x[e + 1], t0, t1);
+    }
+  }
+  __device__ void add_one(float z) {
+    const float d = row_exponent(z, M, c), e = exp2_approx(d);
+    s0 += e;
+    t0 = fmaf(e, d, t0);
+  }
+};
+
+template <int kBf16>
+__device__ __forceinline__ uint4 no_logits() {
+  const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+  return make_uint4(none, none, none, none);
+}
+
+// ---- short rows: one warp each -----------------------------------------------------------
+//
+// The row stays in the warp's registers for both passes: no barriers, and the lanes' maxima
+// are the 32 groups of the ranking's threshold.
+constexpr int kWarpRowWarps = 4;
+constexpr int kWarpCandidates = 96;
+
+template <int kBf16, bool kTop, int kNv>
+__global__ void __launch_bounds__(kWarpRowWarps * 32)
+    logprob_warp_kernel(const uint8_t* __restrict__ z, int64_t ld_bytes,
+                        const int32_t* __restrict__ tokens, int N, int V, int ignore_index,
+                        int top_k, float inv_t, float* __restrict__ logprob,
+                        float* __restrict__ entropy, float* __restrict__ lse,
+                        float* __restrict__ top_lp, int32_t* __restrict__ top_id,
+                        int32_t* status) {
+  using L = Logit<kBf16>;
+  constexpr int E = L::E;
+  __shared__ uint64_t s_cand[kTop ? kWarpRowWarps : 1][kTop ? kWarpCandidates : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * kWarpRowWarps + warp;
+  if (row >= N) return;
+  const float c = kLog2e * inv_t;
+  const uint8_t* zr = z + static_cast<int64_t>(row) * ld_bytes;
+  const int head = row_head<kBf16>(zr, V);
+  const int nvec = (V - head) / E;
+  const int tail = head + nvec * E;
+  const uint4* vec = reinterpret_cast<const uint4*>(zr + static_cast<int64_t>(head) * L::kBytes);
+  uint4 w[kNv];
+#pragma unroll
+  for (int j = 0; j < kNv; ++j) w[j] = lane + 32 * j < nvec ? __ldg(vec + lane + 32 * j) : no_logits<kBf16>();
+  const int ie = lane < head ? lane : lane < head + V - tail ? tail + lane - head : -1;
+  const float xe = ie >= 0 ? L::load1(zr + static_cast<int64_t>(ie) * L::kBytes) : -INFINITY;
+  const int y = tokens != nullptr ? tokens[row] : ignore_index;
+  const bool bad = y != ignore_index && (y < 0 || y >= V);
+  const int yt = (y == ignore_index || bad) ? -1 : y;
+  VecMax<kBf16> vm;
+#pragma unroll
+  for (int j = 0; j < kNv; ++j) vm.take(w[j]);
+  const float mine = max_nan(vm.value(), xe);
+  float M = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+  RowPart part{M, 0.f, 0.f};
+  float zt = 0.f;
+  uint64_t list = 0;
+  if (M > -INFINITY && M < INFINITY) {
+    if constexpr (kTop) {
+      const float thr = __shfl_sync(0xffffffffu, warp_sort_values(mine, lane), top_k - 1);
+      const Reaches<kBf16> reaches(thr);
+      int count = 0;
+      // the elements x[0, n) of every lane that reach thr, of ids id, id + 1, ...
+      auto offer = [&](const float (&x)[E], int n, int id) {
+        uint32_t in = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) in |= (e < n && x[e] >= thr && x[e] > -INFINITY ? 1u : 0u) << e;
+        int before = __popc(in);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int p = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += p;
+        }
+        const int all = __shfl_sync(0xffffffffu, before, 31);
+        int at = count + before - __popc(in);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (in >> e & 1u) {
+            if (at < kWarpCandidates) s_cand[warp][at] = rank_key(x[e], id + e);
+            ++at;
+          }
+        count += all;
+      };
+#pragma unroll
+      for (int j = 0; j < kNv; ++j)
+        if (__any_sync(0xffffffffu, reaches(w[j]))) {
+          float x[E];
+          L::widen(w[j], x);
+          offer(x, E, head + (lane + 32 * j) * E);
+        }
+      if (__any_sync(0xffffffffu, ie >= 0)) {
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = xe;
+        offer(x, ie >= 0 ? 1 : 0, ie);
+      }
+      __syncwarp();
+      if (count <= kWarpCandidates) {
+        for (int b = 0; b < count; b += 32) {
+          const uint64_t key = warp_sort_desc(b + lane < count ? s_cand[warp][b + lane] : 0, lane);
+          list = b == 0 ? key : warp_merge_desc(list, key, lane);
+        }
+      } else {
+        // too many equal ones: the largest key below the one before, top_k times
+        uint64_t below = ~0ull;
+        for (int i = 0; i < top_k && below != 0; ++i) {
+          uint64_t best = 0;
+          auto look = [&](float x, int id) {
+            const uint64_t key = x > -INFINITY ? rank_key(x, id) : 0;
+            if (key < below && key > best) best = key;
+          };
+#pragma unroll
+          for (int j = 0; j < kNv; ++j) {
+            float x[E];
+            L::widen(w[j], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) look(x[e], head + (lane + 32 * j) * E + e);
+          }
+          if (ie >= 0) look(xe, ie);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t key = __shfl_xor_sync(0xffffffffu, best, o);
+            best = key > best ? key : best;
+          }
+          below = best;
+          if (lane == i) list = best;
+        }
+      }
+    }
+    // the token's element leaves the sums
+    bool own = ie >= 0 && ie == yt;
+    if (own) zt = xe;
+    RowSums<kBf16> sums(M, c);
+#pragma unroll
+    for (int j = 0; j < kNv; ++j) {
+      const int base = head + (lane + 32 * j) * E;
+      if (yt >= 0 && static_cast<unsigned>(yt - base) < static_cast<unsigned>(E) && yt < tail) {
+        float x[E];
+        L::widen(w[j], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (base + e == yt) {
+            zt = x[e];
+            x[e] = -INFINITY;
+          }
+        w[j] = L::narrow(x);
+        own = true;
+      }
+      sums.add(w[j]);
+    }
+    if (ie >= 0 && ie != yt) sums.add_one(xe);
+    const unsigned who = __ballot_sync(0xffffffffu, own);
+    zt = who ? __shfl_sync(0xffffffffu, zt, __ffs(who) - 1) : 0.f;
+    part.s = sums.s0 + sums.s1;
+    part.t = sums.t0 + sums.t1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      part.s += __shfl_xor_sync(0xffffffffu, part.s, o);
+      part.t += __shfl_xor_sync(0xffffffffu, part.t, o);
+    }
+  }
+  const RowOut r = row_finish(part, zt, yt >= 0, inv_t, c);
+  if (lane == 0) {
+    if (logprob != nullptr) logprob[row] = bad ? __uint_as_float(0x7FC00000u) : r.logprob;
+    if (entropy != nullptr) entropy[row] = r.entropy;
+    if (lse != nullptr) lse[row] = r.lse;
+    if (bad) record_error(status, 8);
+  }
+  if (kTop && lane < top_k) {
+    const int64_t at = static_cast<int64_t>(row) * top_k + lane;
+    const bool none = list == 0;
+    top_id[at] = none ? -1 : key_id(list);
+    top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
+  }
+}
+
+// ---- longer rows: clusters, through shared memory -------------------------------------------
+
 // What a CTA knows of a row: maximum, sums, the token's logit if it is in its slice (0
 // otherwise), and its ranking.
 struct __align__(16) RowMsg {
@@ -392,10 +652,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
   constexpr int kBarMax = 1, kBarDone = 2, kBarFree = 4;   // named barriers; the last two in pairs
   extern __shared__ __align__(128) uint8_t s_rows[];       // two slices
   __shared__ __align__(8) uint64_t s_full[2];   // a slice's copy has landed
-  __shared__ __align__(8) uint64_t s_got[2];    // first CTA: every CTA's message is here
-  __shared__ __align__(8) uint64_t s_used[2];   // the first CTA has read this CTA's message
-  __shared__ RowMsg s_msg[2][kMaxRowCluster];   // first CTA
-  __shared__ float s_max[2][kWarps][32];
+  // A row's parts meet in one CTA, each in turn (row it of the cluster in CTA it % csize, its
+  // turn u = it / csize): messages and their barriers alternate between turns.
+  __shared__ __align__(8) uint64_t s_got[2];                    // every CTA's message is here
+  __shared__ __align__(8) uint64_t s_used[kMaxRowCluster][2];   // CTA r has read this one's message
+  __shared__ RowMsg s_msg[2][kMaxRowCluster];
+  __shared__ float s_max[2][kWarps][kTop ? 32 : 1];
   __shared__ float2 s_sum[2][kWarps];
   __shared__ float s_m[2], s_zt[2];
   __shared__ int s_count[2];
@@ -409,7 +671,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&s_full[k]), 1);
       mbar_init(smem_u32(&s_got[k]), static_cast<uint32_t>(csize));
-      mbar_init(smem_u32(&s_used[k]), 1);
+      for (int r = 0; r < kMaxRowCluster; ++r) mbar_init(smem_u32(&s_used[r][k]), 1);
       s_count[k] = 0;
       s_zt[k] = 0.f;
     }
@@ -464,7 +726,14 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
 #pragma unroll 4
       for (int v = tid; v < q.nv; v += kData) vm.take(vec[v]);
       const float mine = max_nan(vm.value(), xe);
-      s_max[k][warp][lane] = mine;
+      if constexpr (kTop) {
+        s_max[k][warp][lane] = mine;
+      } else {
+        float wm = mine;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) wm = max_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+        if (lane == 0) s_max[k][warp][0] = wm;
+      }
       // the token's element: its thread keeps the value and takes it out of the sums
       const int id0 = q.head + q.v0 * E;   // id of the slice's first vector element
       float zt = 0.f;
@@ -478,34 +747,34 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
         else *reinterpret_cast<float*>(at) = -INFINITY;
       }
       bar_sync(kBarMax, kData);
-      float gm = s_max[k][0][lane];
+      float gm;   // the maximum over the threads of equal lane, or one of the warps' maxima
+      if constexpr (kTop) {
+        gm = s_max[k][0][lane];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) gm = max_nan(gm, s_max[k][w][lane]);
+        for (int w = 1; w < kWarps; ++w) gm = max_nan(gm, s_max[k][w][lane]);
+      } else {
+        gm = s_max[k][lane % kWarps][0];
+      }
       float M = gm;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+      for (int o = kTop ? 16 : kWarps / 2; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
       // the last warp has taken what this slot held
       if (it >= 2) bar_sync(kBarFree + k, kAll);
-      float thr = INFINITY;
-      if constexpr (kTop) {
-        // the top_k-th largest of the maxima over the threads of equal lane
-        int rank = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float o = __shfl_sync(0xffffffffu, gm, j);
-          rank += (o > gm || (o == gm && j < lane)) ? 1 : 0;
-        }
-        const unsigned at = __ballot_sync(0xffffffffu, rank == top_k - 1);
-        thr = at ? __shfl_sync(0xffffffffu, gm, __ffs(at) - 1) : -INFINITY;
-      }
       if (own) s_zt[k] = zt;
       float s = 0.f, t = 0.f;
       if (M > -INFINITY && M < INFINITY) {
+        RowSums<kBf16> sums(M, c);
+        // the top_k-th largest of the 32 maxima
+        float thr = 0.f;
+        if constexpr (kTop) thr = __shfl_sync(0xffffffffu, warp_sort_values(gm, lane), top_k - 1);
         int equal = 0;   // elements at the threshold that this warp has offered: top_k do
-        // Offers this lane's elements x[0, n) of ids id, id + 1, ...; the whole warp calls.
-        auto offer = [&](const float* x, int n, int id) {
+        // Offers this lane's elements of ids id, id + 1, ...; the whole warp calls.
+        auto offer = [&](const uint4& w, int id) {
+          float x[E];
+          L::widen(w, x);
           uint32_t gt = 0, eq = 0;
-          for (int e = 0; e < n; ++e) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
             gt |= (x[e] > thr ? 1u : 0u) << e;
             eq |= (x[e] == thr && x[e] > -INFINITY ? 1u : 0u) << e;
           }
@@ -516,89 +785,35 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
             if (lane >= o) before += p;
           }
           const int all = __shfl_sync(0xffffffffu, before, 31);
-          int room = top_k - equal - (before - __popc(eq));   // of this lane's equal ones
-          room = room < 0 ? 0 : room;
+          int room = max(top_k - equal - (before - __popc(eq)), 0);   // of this lane's equal ones
           equal += all;
           const int take = __popc(gt) + min(room, __popc(eq));
           if (take > 0) {
             int at = atomicAdd(&s_count[k], take);
-            for (int e = 0; e < n; ++e) {
-              const bool g = gt >> e & 1u;
-              if (g || ((eq >> e & 1u) && room-- > 0)) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              bool in = gt >> e & 1u;
+              if (!in && (eq >> e & 1u)) in = room-- > 0;
+              if (in) {
                 if (at < kCandidates) s_cand[kTop ? k : 0][at] = rank_key(x[e], id + e);
                 ++at;
               }
             }
           }
         };
-        // what smaller logits (and -inf) are raised to: far enough below M that their 2^d is
-        // 0, near enough that d is finite. Rows where rounding leaves no such value (logits
-        // of 1e5 in bf16) or that are that far from 0 clamp the exponent of each element.
-        const float below = M - 200.f / c;
-        uint32_t lo2;
-        asm("cvt.rz.bf16x2.f32 %0, %1, %1;" : "=r"(lo2) : "f"(below));
-        const float lo = kBf16 ? lo_of(lo2) : below;
-        const bool safe = !(fabsf(M) < 1.0e30f) || !((lo - M) * c < -150.f);
-        const bool hot = kTop && __any_sync(0xffffffffu, mine >= thr);
-        float s2 = 0.f, t2 = 0.f;
+        const Reaches<kBf16> reaches(thr);
+        if (kTop && __any_sync(0xffffffffu, mine >= thr)) {
+          for (int vw = warp * 32; vw < q.nv; vw += kData) {
+            const int v = vw + lane;
+            const uint4 w = v < q.nv ? vec[v] : no_logits<kBf16>();
+            if (__any_sync(0xffffffffu, reaches(w))) offer(w, id0 + v * E);
+            sums.add(w);   // (-inf adds nothing)
+          }
+        } else {
 #pragma unroll 2
-        for (int vw = warp * 32; vw < q.nv; vw += kData) {
-          const int v = vw + lane;
-          uint4 w;
-          if (v < q.nv) {
-            w = vec[v];
-          } else {
-            const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;   // -inf
-            w = make_uint4(none, none, none, none);
-          }
-          if (kTop && hot) {
-            VecMax<kBf16> top;
-            top.take(w);
-            if (__any_sync(0xffffffffu, top.value() >= thr)) {
-              float x[E];
-              L::widen(w, x);
-              offer(x, E, id0 + v * E);
-            }
-          }
-          float x[E];
-          if (!safe) {
-            if constexpr (kBf16) {
-              w.x = max2_nan(w.x, lo2);
-              w.y = max2_nan(w.y, lo2);
-              w.z = max2_nan(w.z, lo2);
-              w.w = max2_nan(w.w, lo2);
-            }
-            L::widen(w, x);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              if constexpr (!kBf16) {
-                x[e] = fmaxf(x[e], lo);
-                x[e + 1] = fmaxf(x[e + 1], lo);
-              }
-              // the difference first: exact near M, however far M is from 0
-              fadd2(x[e], x[e + 1], -M, -M);
-              fmul2(x[e], x[e + 1], c, c);
-            }
-          } else {
-            L::widen(w, x);
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = fmaxf((x[e] - M) * c, kMinExponent);
-          }
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float e0 = exp2_approx(x[e]), e1 = exp2_approx(x[e + 1]);
-            fadd2(s, s2, e0, e1);
-            ffma2(t, t2, e0, e1, x[e], x[e + 1], t, t2);
-          }
+          for (int v = tid; v < q.nv; v += kData) sums.add(vec[v]);
         }
-        s += s2;
-        t += t2;
-        if (ie >= 0 && ie != yt) {
-          const float d = fmaxf((xe - M) * c, kMinExponent);
-          const float e = exp2_approx(d);
-          s += e;
-          t = fmaf(e, d, t);
-        }
+        if (ie >= 0 && ie != yt) sums.add_one(xe);
         // the single elements, and the token's that the slice no longer holds, are candidates
         // as they are
         if constexpr (kTop) {
@@ -611,6 +826,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
           if (ie >= 0) offer_one(xe, ie);
           if (taken) offer_one(zt, yt);
         }
+        s = sums.s0 + sums.s1;
+        t = sums.t0 + sums.t1;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -718,12 +935,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
       if (more) bar_arrive(kBarFree + k, kAll);
 
       bool late = s_late != 0;
+      const int leader = it % csize, u = it / csize, slot = u & 1;
       if (csize > 1) {
-        // to the first CTA, once it has read the message two rows before
-        if (it >= 2 && !mbar_wait_bounded<true>(smem_u32(&s_used[k]), static_cast<uint32_t>(((it >> 1) - 1) & 1),
-                                                timeout_ns, &never))
+        // to this row's CTA, once it has read the message of two turns before
+        if (u >= 2 && !mbar_wait_bounded<true>(smem_u32(&s_used[leader][slot]),
+                                               static_cast<uint32_t>(((u >> 1) - 1) & 1), timeout_ns, &never))
           late = true;
-        const uint32_t msg = mapa_shared(smem_u32(&s_msg[k][crank]), 0);
+        const uint32_t msg = mapa_shared(smem_u32(&s_msg[slot][crank]), static_cast<uint32_t>(leader));
         if (lane == 0)
           asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(msg), "f"(part.m),
                        "f"(part.s), "f"(part.t), "f"(zt)
@@ -733,30 +951,41 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
                        : "memory");
         asm volatile("fence.acq_rel.cluster;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_got[k]), 0));
-        if (crank == 0) {
-          if (!mbar_wait_bounded<true>(smem_u32(&s_got[k]), static_cast<uint32_t>((it >> 1) & 1), timeout_ns,
+        if (lane == 0)
+          mbar_arrive_cluster(mapa_shared(smem_u32(&s_got[slot]), static_cast<uint32_t>(leader)));
+        if (crank == leader) {
+          if (!mbar_wait_bounded<true>(smem_u32(&s_got[slot]), static_cast<uint32_t>((u >> 1) & 1), timeout_ns,
                                        &never))
             late = true;
-          part = RowPart{-INFINITY, 0.f, 0.f};
-          zt = 0.f;
-          list = 0;
-          for (int r = 0; r < csize; ++r) {
-            const float4 p = s_msg[k][r].part;
-            row_join(part, RowPart{p.x, p.y, p.z}, c);
-            zt += p.w;
-            if (kTop) {
-              const uint64_t key = lane < top_k ? s_msg[k][r].list[lane] : 0;
+          // lane r joins CTA r's sums; the rankings one after the other
+          const float4 p = lane < csize ? s_msg[slot][lane].part : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+          part = RowPart{p.x, p.y, p.z};
+          zt = p.w;
+#pragma unroll
+          for (int o = kMaxRowCluster / 2; o > 0; o >>= 1) {
+            const RowPart q{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o),
+                            __shfl_xor_sync(0xffffffffu, part.t, o)};
+            row_join(part, q, c);
+            zt += __shfl_xor_sync(0xffffffffu, zt, o);
+          }
+          part = RowPart{__shfl_sync(0xffffffffu, part.m, 0), __shfl_sync(0xffffffffu, part.s, 0),
+                         __shfl_sync(0xffffffffu, part.t, 0)};
+          zt = __shfl_sync(0xffffffffu, zt, 0);
+          if constexpr (kTop) {
+            list = 0;
+            for (int r = 0; r < csize; ++r) {
+              const uint64_t key = lane < top_k ? s_msg[slot][r].list[lane] : 0;
               list = r == 0 ? key : warp_merge_desc(list, key, lane);
             }
           }
           __syncwarp();
-          if (lane < csize) mbar_arrive_cluster(mapa_shared(smem_u32(&s_used[k]), static_cast<uint32_t>(lane)));
+          if (lane < csize)
+            mbar_arrive_cluster(mapa_shared(smem_u32(&s_used[crank][slot]), static_cast<uint32_t>(lane)));
         }
       }
       if (late) s_late = 1;
       late = __any_sync(0xffffffffu, late);
-      if (crank == 0) {
+      if (crank == leader) {
         RowOut r = row_finish(part, zt, has, inv_t, c);
         const float nan = __uint_as_float(0x7FC00000u);
         if (late) r.logprob = r.entropy = r.lse = nan;
@@ -771,7 +1000,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
           const int64_t at = static_cast<int64_t>(row) * top_k + lane;
           const bool none = list == 0;
           top_id[at] = none || late ? -1 : key_id(list);
-          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t);
+          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
         }
       }
     }
@@ -905,21 +1134,31 @@ cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const
                                 cudaStream_t stream) {
   const uint8_t* zp = static_cast<const uint8_t*>(z);
   const int64_t row_bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
-  // Slices: small rows whole in CTAs of 128 + 32 threads (16 KB, five per SM), others in
-  // slices of at most 49 KB (two CTAs per SM), or, when eight of those do not hold the row,
-  // 104 KB (one).
-  constexpr int kSmall = 16 << 10, kTwo = 49 << 10, kOne = 104 << 10;
+  // Slices: rows of up to 20 KB whole in CTAs of 4 + 1 warps (four per SM), others in slices
+  // of at most 49 KB in CTAs of 8 + 1 warps (two per SM), or, when eight of those do not hold
+  // the row, 104 KB in CTAs of 16 + 1 (one).
+  constexpr int kWarpRow = 8 << 10, kSmall = 20 << 10, kTwo = 49 << 10, kOne = 104 << 10;
   auto cluster_for = [&](int64_t slice) {
     // whole 16-byte vectors per CTA: leave one vector for the rounding up
     return static_cast<int>((row_bytes + slice - 17) / (slice - 16));
   };
   auto go = [&](auto b, auto t) {
+    using std::integral_constant;
+    auto warp_rows = [&](auto nv) {
+      logprob_warp_kernel<b(), t(), nv()>
+          <<<(N + kWarpRowWarps - 1) / kWarpRowWarps, kWarpRowWarps * 32, 0, stream>>>(
+              zp, ld_bytes, tokens, N, V, ignore_index, top_k, inv_t, logprob, entropy, lse,
+              top_lp, top_id, status);
+      return cudaGetLastError();
+    };
+    if (row_bytes <= kWarpRow / 4) return warp_rows(integral_constant<int, 4>{});
+    if (row_bytes <= kWarpRow / 2) return warp_rows(integral_constant<int, 8>{});
+    if (row_bytes <= kWarpRow) return warp_rows(integral_constant<int, 16>{});
     auto run = [&](auto warps, auto slice, auto blocks, int cluster) {
       return launch_stream<b(), t(), warps(), slice(), blocks()>(
           cluster, N, sms, zp, ld_bytes, tokens, V, ignore_index, top_k, inv_t, logprob, entropy,
           lse, top_lp, top_id, status, timeout_ns, stream);
     };
-    using std::integral_constant;
     // few rows: more CTAs for each, down to 8 KB, until every SM has one
     int spread = sms / N;
     const int most = static_cast<int>((row_bytes + (8 << 10) - 1) / (8 << 10));
@@ -927,10 +1166,10 @@ cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const
     spread = spread < kMaxRowCluster ? spread : kMaxRowCluster;
     int cl = cluster_for(kSmall);
     if (cl <= 1 && spread <= 1)
-      return run(integral_constant<int, 4>{}, integral_constant<int, kSmall>{}, integral_constant<int, 5>{}, 1);
+      return run(integral_constant<int, 4>{}, integral_constant<int, kSmall>{}, integral_constant<int, 4>{}, 1);
     cl = cluster_for(kTwo);
     if (cl <= kMaxRowCluster)
-      return run(integral_constant<int, 16>{}, integral_constant<int, kTwo>{}, integral_constant<int, 2>{},
+      return run(integral_constant<int, 8>{}, integral_constant<int, kTwo>{}, integral_constant<int, 2>{},
                  cl > spread ? cl : spread);
     cl = cluster_for(kOne);
     if (cl <= kMaxRowCluster)

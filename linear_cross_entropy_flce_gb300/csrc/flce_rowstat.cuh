@@ -1,11 +1,13 @@
-// The statistics of a softmax row that log probabilities and entropies are formed
-// from, kept in the base-2 domain the hardware exponential works in.
+// The statistics of a softmax row that log probabilities and entropies are formed from,
+// kept in the base-2 domain the hardware exponential works in.
 //
-// With d_v = (z_v - m) c, c = log2(e) / temperature, a part of a row is
-//   m = max z (raw logits), s = sum 2^d, t = sum 2^d d
-// and parts join by rescaling to the larger maximum. The token's own term is left out
-// of s and t and added at the end, so that 1 - p of a confident token, and its log
-// probability -log1p(others / its term), are no differences of nearly equal numbers.
+// With c = log2(e) / temperature, a part of a row is
+//   m = max z (raw logits), s = sum 2^d, t = sum 2^d d,  d_v = z_v c - r,
+// with r = row_ref(m, c) a whole number next to m c: it is exact in fp32, so one FMA gives
+// d with a single rounding of its own size, however far the logits are from 0, and parts
+// join by factors 2^(r - r'). The token's own term is left out of s and t and added at the
+// end, so that 1 - p of a confident token, and its log probability -log1p(others / its
+// term), are no differences of nearly equal numbers.
 #pragma once
 
 #include <cmath>
@@ -31,6 +33,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Logits whose m c leaves the range in which fp32 holds every whole number (a row of a type's
+// lowest values, for one) have no such r: there d = (z - m) c.
+constexpr float kMaxRef = 4194304.f;
+__device__ __forceinline__ bool has_ref(float m, float c) { return fabsf(m * c) < kMaxRef; }
+__device__ __forceinline__ float row_ref(float m, float c) { return rintf(m * c); }
+
 // A log-sum-exp below this comes from a row whose every id is masked, with -inf or with
 // the type's lowest value. Its gradient is 0: p = exp(x - lse) has no digits there.
 constexpr float kMaskedLse = -1.0e30f;
@@ -39,12 +47,30 @@ struct RowPart {
   float m, s, t;
 };
 
+// d of a logit against the maximum m of its part.
+__device__ __forceinline__ float row_exponent(float z, float m, float c) {
+  return fmaxf(has_ref(m, c) ? fmaf(z, c, -row_ref(m, c)) : (z - m) * c, kMinExponent);
+}
+
+// What d of a part with maximum m becomes less by when the maximum becomes M >= m.
+__device__ __forceinline__ float row_shift(float m, float M, float c) {
+  float d;
+  if (has_ref(m, c) && has_ref(M, c)) {
+    d = row_ref(m, c) - row_ref(M, c);
+  } else {   // r in place of m c on one side at most
+    const float om = has_ref(m, c) ? fmaf(-m, c, row_ref(m, c)) : 0.f;
+    const float oM = has_ref(M, c) ? fmaf(-M, c, row_ref(M, c)) : 0.f;
+    d = (m - M) * c + (om - oM);
+  }
+  return fmaxf(d, kMinExponent);
+}
+
 // Joins b into a (either may be empty: m = -inf, s = t = 0). A NaN or +inf maximum
 // stays one; s and t then have no meaning.
 __device__ __forceinline__ void row_join(RowPart& a, const RowPart& b, float c) {
   const float M = max_nan(a.m, b.m);
   if (M == -INFINITY) return;
-  const float da = fmaxf((a.m - M) * c, kMinExponent), db = fmaxf((b.m - M) * c, kMinExponent);
+  const float da = row_shift(a.m, M, c), db = row_shift(b.m, M, c);
   const float fa = exp2_approx(da), fb = exp2_approx(db);
   a.t = fmaf(a.s, da, a.t) * fa + fmaf(b.s, db, b.t) * fb;
   a.s = a.s * fa + b.s * fb;
@@ -53,13 +79,15 @@ __device__ __forceinline__ void row_join(RowPart& a, const RowPart& b, float c) 
 
 struct RowOut {
   float logprob, entropy, lse;
-  float m, log_s;   // lse = m / temperature + log_s, kept apart for id_logprob
+  float m, log_s;   // lse = r ln 2 + log_s (m / temperature + log_s without an r), for id_logprob
 };
 
 // Log probability of an id from its raw logit: no difference with lse, in which log S
 // drowns when the logits are far from 0. NaN in a row without a softmax.
-__device__ __forceinline__ float id_logprob(const RowOut& r, float z, float inv_t) {
-  return fmaf(z - r.m, inv_t, -r.log_s);
+__device__ __forceinline__ float id_logprob(const RowOut& r, float z, float inv_t, float c) {
+  // (for a logit beyond the reference's range r against m c, half a unit, is below rounding)
+  return has_ref(r.m, c) && has_ref(z, c) ? fmaf(fmaf(z, c, -row_ref(r.m, c)), kLn2, -r.log_s)
+                                          : fmaf(z - r.m, inv_t, -r.log_s);
 }
 
 // The row's outputs from its joined part (the token's term left out), the raw logit zt
@@ -82,17 +110,17 @@ __device__ __forceinline__ RowOut row_finish(const RowPart& p, float zt, bool ha
   }
   float dt = kMinExponent, et = 0.f;
   if (has_token) {
-    dt = fmaxf((zt - p.m) * c, kMinExponent);
+    dt = row_exponent(zt, p.m, c);
     et = exp2_approx(dt);
   }
   const float S = p.s + et, T = fmaf(et, dt, p.t);
   const float log_s = logf(S);
   o.log_s = log_s;
-  o.lse = fmaf(p.m, inv_t, log_s);
+  o.lse = has_ref(p.m, c) ? fmaf(row_ref(p.m, c), kLn2, log_s) : fmaf(p.m, inv_t, log_s);
   const float h = fmaf(-kLn2, T / S, log_s);
   o.entropy = h < 0.f ? 0.f : h;
   // e_t < 2^-60: x_y - lse has no cancellation, and the quotient could overflow
-  o.logprob = !has_token ? 0.f : (et >= 0x1p-60f ? -log1pf(p.s / et) : id_logprob(o, zt, inv_t));
+  o.logprob = !has_token ? 0.f : (et >= 0x1p-60f ? -log1pf(p.s / et) : id_logprob(o, zt, inv_t, c));
   return o;
 }
 
