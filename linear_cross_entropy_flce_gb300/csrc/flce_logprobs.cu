@@ -38,8 +38,11 @@ namespace flce {
 namespace {
 
 constexpr int kRowThreads = 512;
-constexpr int kCandidates = 384;
+constexpr int kCandidates = 512;
 constexpr int kMaxRowCluster = 8;
+// Elements that a warp offers to the ranking, all together or at once, before it counts the
+// equal ones: with top_k of those, eight warps stay within kCandidates.
+constexpr int kManyHits = 16;
 
 template <int kBf16>
 struct Logit;
@@ -458,6 +461,15 @@ struct RowSums {
   }
 };
 
+// Element e of a 16-byte vector.
+template <int kBf16>
+__device__ __forceinline__ float element_of(const uint4& w, int e) {
+  const int i = kBf16 ? e >> 1 : e;
+  const uint32_t a = i & 1 ? w.y : w.x, b = i & 1 ? w.w : w.z;
+  const uint32_t v = i & 2 ? b : a;
+  return kBf16 ? (e & 1 ? hi_of(v) : lo_of(v)) : __uint_as_float(v);
+}
+
 template <int kBf16>
 __device__ __forceinline__ uint4 no_logits() {
   const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;   // -inf
@@ -670,7 +682,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
   if (tid == 0) {
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&s_full[k]), 1);
-      mbar_init(smem_u32(&s_got[k]), static_cast<uint32_t>(csize));
+      mbar_init(smem_u32(&s_got[k]), 1);
       for (int r = 0; r < kMaxRowCluster; ++r) mbar_init(smem_u32(&s_used[r][k]), 1);
       s_count[k] = 0;
       s_zt[k] = 0.f;
@@ -708,11 +720,16 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
   };
 
   if (warp < kWarps) {
+    auto token_of = [&](int64_t row) {
+      return tokens != nullptr && row < N ? tokens[row] : ignore_index;
+    };
+    int y_next = token_of(first);   // read a row ahead
     int it = 0;
     for (int row = first; row < N; row += step, ++it) {
       const int k = it & 1;
       const Slice q = slice_of(row);
-      const int y = tokens != nullptr ? tokens[row] : ignore_index;
+      const int y = y_next;
+      y_next = token_of(static_cast<int64_t>(row) + step);
       const int yt = (y == ignore_index || y < 0 || y >= V) ? -1 : y;
       const int ie = tid < 16 ? single_of(q, tid) : -1;
       const float xe = ie >= 0 ? L::load1(q.row + static_cast<int64_t>(ie) * L::kBytes) : -INFINITY;
@@ -767,37 +784,41 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
         // the top_k-th largest of the 32 maxima
         float thr = 0.f;
         if constexpr (kTop) thr = __shfl_sync(0xffffffffu, warp_sort_values(gm, lane), top_k - 1);
-        int equal = 0;   // elements at the threshold that this warp has offered: top_k do
-        // Offers this lane's elements of ids id, id + 1, ...; the whole warp calls.
+        int hits = 0, equal = 0;   // of this warp: offered so far; equal to the threshold
+        // Offers this lane's elements of ids id, id + 1, ...; the whole warp calls. On rows
+        // with many elements equal to the threshold only the first top_k of them count.
         auto offer = [&](const uint4& w, int id) {
           float x[E];
           L::widen(w, x);
-          uint32_t gt = 0, eq = 0;
+          uint32_t in = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            gt |= (x[e] > thr ? 1u : 0u) << e;
-            eq |= (x[e] == thr && x[e] > -INFINITY ? 1u : 0u) << e;
+          for (int e = 0; e < E; ++e) in |= (x[e] >= thr ? 1u : 0u) << e;
+          if (thr == -INFINITY)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (x[e] == -INFINITY) in &= ~(1u << e);
+          const int here = __reduce_add_sync(0xffffffffu, __popc(in));
+          hits += here;
+          if (hits > kManyHits || here > kManyHits) {
+            uint32_t eq = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) eq |= (x[e] == thr ? 1u : 0u) << e;
+            eq &= in;
+            int before = __popc(eq);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int p = __shfl_up_sync(0xffffffffu, before, o);
+              if (lane >= o) before += p;
+            }
+            int room = max(top_k - equal - (before - __popc(eq)), 0);   // of this lane's equal ones
+            equal += __shfl_sync(0xffffffffu, before, 31);
+            for (; __popc(eq) > room; eq &= ~(0x80000000u >> __clz(eq))) in &= ~(0x80000000u >> __clz(eq));
           }
-          int before = __popc(eq);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int p = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += p;
-          }
-          const int all = __shfl_sync(0xffffffffu, before, 31);
-          int room = max(top_k - equal - (before - __popc(eq)), 0);   // of this lane's equal ones
-          equal += all;
-          const int take = __popc(gt) + min(room, __popc(eq));
-          if (take > 0) {
-            int at = atomicAdd(&s_count[k], take);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              bool in = gt >> e & 1u;
-              if (!in && (eq >> e & 1u)) in = room-- > 0;
-              if (in) {
-                if (at < kCandidates) s_cand[kTop ? k : 0][at] = rank_key(x[e], id + e);
-                ++at;
-              }
+          if (in != 0) {
+            int at = atomicAdd(&s_count[k], __popc(in));
+            for (; in != 0; in &= in - 1, ++at) {
+              const int e = __ffs(in) - 1;
+              if (at < kCandidates) s_cand[kTop ? k : 0][at] = rank_key(element_of<kBf16>(w, e), id + e);
             }
           }
         };
@@ -869,70 +890,88 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
     for (int row = first; row < N; row += step, ++it) {
       const int k = it & 1;
       const bool more = row + 2 * static_cast<int64_t>(step) < N;
-      bar_sync(kBarDone + k, kAll);
       const int y = tokens != nullptr ? tokens[row] : ignore_index;
       const bool bad = y != ignore_index && (y < 0 || y >= V);
       const bool has = y != ignore_index && !bad;
+      bar_sync(kBarDone + k, kAll);
+      // take what the slot holds, start the copy into it and give it back, then sort
+      const int count = kTop ? s_count[k] : 0;
       float2 sums = lane < kWarps ? s_sum[k][lane] : make_float2(0.f, 0.f);
+      RowPart part{s_m[k], 0.f, 0.f};
+      float zt = s_zt[k];
+      uint64_t list = 0;
+      auto give_back = [&]() {
+        __syncwarp();
+        if (lane == 0) {
+          s_count[k] = 0;
+          s_zt[k] = 0.f;
+          if (more) copy(row + 2 * step, k);
+        }
+        __syncwarp();
+        if (more) bar_arrive(kBarFree + k, kAll);
+      };
+      if (count <= 64) {
+        uint64_t a = 0, b = 0;
+        if constexpr (kTop) {
+          if (lane < count) a = s_cand[k][lane];
+          if (lane + 32 < count) b = s_cand[k][lane + 32];
+        }
+        give_back();
+        if constexpr (kTop) {
+          list = warp_sort_desc(a, lane);
+          if (count > 32) list = warp_merge_desc(list, warp_sort_desc(b, lane), lane);
+        }
+      } else if (count <= kCandidates) {
+        if constexpr (kTop) {
+          for (int b = 0; b < count; b += 32) {
+            const uint64_t key = warp_sort_desc(b + lane < count ? s_cand[k][b + lane] : 0, lane);
+            list = b == 0 ? key : warp_merge_desc(list, key, lane);
+          }
+        }
+        give_back();
+      } else {
+        // too many reach the threshold: the largest key below the one before, top_k times.
+        // The token's element was taken out of the slice: it joins from its value.
+        const Slice q = slice_of(row);
+        const uint4* vec = reinterpret_cast<const uint4*>(s_rows + k * kSlice);
+        const int id0 = q.head + q.v0 * E;
+        const int ie = lane < 16 ? single_of(q, lane) : -1;
+        const float xe = ie >= 0 ? L::load1(q.row + static_cast<int64_t>(ie) * L::kBytes) : -INFINITY;
+        const bool mine = has && y >= id0 && y < id0 + q.nv * E;
+        uint64_t below = ~0ull;
+        for (int i = 0; i < top_k && below != 0; ++i) {
+          uint64_t best = 0;
+          auto look = [&](float x, int id) {
+            if (x > -INFINITY) {
+              const uint64_t key = rank_key(x, id);
+              if (key < below && key > best) best = key;
+            }
+          };
+          for (int v = lane; v < q.nv; v += 32) {
+            float x[E];
+            L::widen(vec[v], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) look(x[e], id0 + v * E + e);
+          }
+          if (ie >= 0) look(xe, ie);
+          if (mine && lane == 31) look(zt, y);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t key = __shfl_xor_sync(0xffffffffu, best, o);
+            best = key > best ? key : best;
+          }
+          below = best;
+          if (lane == i) list = best;
+        }
+        give_back();
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
         sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
       }
-      RowPart part{s_m[k], sums.x, sums.y};
-      float zt = s_zt[k];
-      uint64_t list = 0;
-      if constexpr (kTop) {
-        const int count = s_count[k];
-        if (count <= kCandidates) {
-          for (int b = 0; b < count; b += 32) {
-            const uint64_t key = warp_sort_desc(b + lane < count ? s_cand[k][b + lane] : 0, lane);
-            list = b == 0 ? key : warp_merge_desc(list, key, lane);
-          }
-        } else {
-          // too many reach the threshold: the largest key below the one before, top_k times.
-          // The token's element was taken out of the slice: it joins from its value.
-          const Slice q = slice_of(row);
-          const uint4* vec = reinterpret_cast<const uint4*>(s_rows + k * kSlice);
-          const int id0 = q.head + q.v0 * E;
-          const int ie = lane < 16 ? single_of(q, lane) : -1;
-          const float xe = ie >= 0 ? L::load1(q.row + static_cast<int64_t>(ie) * L::kBytes) : -INFINITY;
-          const bool mine = has && y >= id0 && y < id0 + q.nv * E;
-          uint64_t below = ~0ull;
-          for (int i = 0; i < top_k && below != 0; ++i) {
-            uint64_t best = 0;
-            auto look = [&](float x, int id) {
-              if (x > -INFINITY) {
-                const uint64_t key = rank_key(x, id);
-                if (key < below && key > best) best = key;
-              }
-            };
-            for (int v = lane; v < q.nv; v += 32) {
-              float x[E];
-              L::widen(vec[v], x);
-#pragma unroll
-              for (int e = 0; e < E; ++e) look(x[e], id0 + v * E + e);
-            }
-            if (ie >= 0) look(xe, ie);
-            if (mine && lane == 31) look(zt, y);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const uint64_t key = __shfl_xor_sync(0xffffffffu, best, o);
-              best = key > best ? key : best;
-            }
-            below = best;
-            if (lane == i) list = best;
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        s_count[k] = 0;
-        s_zt[k] = 0.f;
-        if (more) copy(row + 2 * step, k);
-      }
-      __syncwarp();
-      if (more) bar_arrive(kBarFree + k, kAll);
+      part.s = sums.x;
+      part.t = sums.y;
 
       bool late = s_late != 0;
       const int leader = it % csize, u = it / csize, slot = u & 1;
@@ -941,19 +980,24 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
         if (u >= 2 && !mbar_wait_bounded<true>(smem_u32(&s_used[leader][slot]),
                                                static_cast<uint32_t>(((u >> 1) - 1) & 1), timeout_ns, &never))
           late = true;
+        // asynchronous stores, counted in bytes on the receiver's barrier: no fence
         const uint32_t msg = mapa_shared(smem_u32(&s_msg[slot][crank]), static_cast<uint32_t>(leader));
+        const uint32_t bar = mapa_shared(smem_u32(&s_got[slot]), static_cast<uint32_t>(leader));
         if (lane == 0)
-          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(msg), "f"(part.m),
-                       "f"(part.s), "f"(part.t), "f"(zt)
-                       : "memory");
+          asm volatile(
+              "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(msg),
+              "f"(part.m), "f"(part.s), "f"(part.t), "f"(zt), "r"(bar)
+              : "memory");
         if (kTop && lane < top_k)
-          asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(msg + 16u + 8u * lane), "l"(list)
+          asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                           msg + 16u + 8u * lane),
+                       "l"(list), "r"(bar)
                        : "memory");
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-        __syncwarp();
-        if (lane == 0)
-          mbar_arrive_cluster(mapa_shared(smem_u32(&s_got[slot]), static_cast<uint32_t>(leader)));
         if (crank == leader) {
+          if (lane == 0)
+            mbar_arrive_expect_tx(smem_u32(&s_got[slot]),
+                                  static_cast<uint32_t>(csize) * (16u + (kTop ? 8u * top_k : 0u)));
+          __syncwarp();
           if (!mbar_wait_bounded<true>(smem_u32(&s_got[slot]), static_cast<uint32_t>((u >> 1) & 1), timeout_ns,
                                        &never))
             late = true;
