@@ -12,10 +12,10 @@
 //   logprob_stream_kernel : rows of up to 880 KB. Persistent clusters of 1-8 CTAs, one row
 //       at a time; each CTA's slice is copied into shared memory by the bulk-copy engine,
 //       double-buffered, so both passes read shared memory and every logit leaves DRAM
-//       once. All but one of the CTA's warps do the passes; the last warp sorts the
-//       candidates of the row before, joins the cluster's parts (each CTA sends its sums
-//       and its ranking to one of them, another one for each row) and starts the copies,
-//       so that none of it holds the passes up.
+//       once. Most of the CTA's warps do the passes; one sorts the candidates of the row
+//       before, sends the CTA's part of it and starts the copies; one joins the parts of
+//       the rows that are this CTA's (each row's meet in another CTA of the cluster), so
+//       that none of it holds the passes up.
 //   logprob_warp_kernel : rows of up to 8 KB, one warp each.
 //   logprob_rows_kernel : longer rows; one CTA each, read twice from global memory.
 //
@@ -417,8 +417,9 @@ struct RowSums {
   // Smaller logits (and -inf) are raised to a floor: far enough below M that their 2^d is 0,
   // near enough that d is finite. In bf16 rows of logits of 1e4 or more rounding may leave
   // no such value: those clamp the exponents.
-  __device__ RowSums(float m, float cc) : M(m), c(cc), ref(row_ref(m, cc)) {
-    const float below = m - 200.f / cc;
+  // reach: 200 / c
+  __device__ RowSums(float m, float cc, float reach) : M(m), c(cc), ref(row_ref(m, cc)) {
+    const float below = m - reach;
     asm("cvt.rz.bf16x2.f32 %0, %1, %1;" : "=r"(lo2) : "f"(below));
     lo = kBf16 ? lo_of(lo2) : below;
     clamp = !has_ref(m, cc) || !(fmaf(lo, cc, -ref) < -150.f);
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
     // the token's element leaves the sums
     bool own = ie >= 0 && ie == yt;
     if (own) zt = xe;
-    RowSums<kBf16> sums(M, c);
+    RowSums<kBf16> sums(M, c, 200.f / c);
 #pragma unroll
     for (int j = 0; j < kNv; ++j) {
       const int base = head + (lane + 32 * j) * E;
@@ -650,7 +651,7 @@ struct __align__(16) RowMsg {
 };
 
 template <int kBf16, bool kTop, int kWarps, int kSlice, int kMinBlocks>
-__global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
+__global__ void __launch_bounds__((kWarps + 2) * 32, kMinBlocks)
     logprob_stream_kernel(const uint8_t* __restrict__ z, int64_t ld_bytes,
                           const int32_t* __restrict__ tokens, int N, int V, int ignore_index,
                           int top_k, float inv_t, float* __restrict__ logprob,
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
   using L = Logit<kBf16>;
   constexpr int E = L::E;
   constexpr int kData = kWarps * 32;          // threads that do the passes
-  constexpr int kAll = kData + 32;
+  constexpr int kAll = kData + 32;            // and the warp that ranks
   constexpr int kBarMax = 1, kBarDone = 2, kBarFree = 4;   // named barriers; the last two in pairs
   extern __shared__ __align__(128) uint8_t s_rows[];       // two slices
   __shared__ __align__(8) uint64_t s_full[2];   // a slice's copy has landed
@@ -702,15 +703,24 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
     const uint8_t* row;
     int head, tail, v0, nv;
   };
-  auto slice_of = [&](int row) {
+  auto slice_at = [&](const uint8_t* at) {
     Slice q;
-    q.row = z + static_cast<int64_t>(row) * ld_bytes;
-    q.head = row_head<kBf16>(q.row, V);
+    q.row = at;
+    q.head = row_head<kBf16>(at, V);
     const int nvec = (V - q.head) / E;
     q.tail = q.head + nvec * E;
     const int per = (nvec + csize - 1) / csize;
     q.v0 = min(nvec, crank * per);
     q.nv = min(nvec, q.v0 + per) - q.v0;
+    return q;
+  };
+  const Slice q_first = slice_at(z);
+  const bool alike = ld_bytes % 16 == 0;   // every row starts as the first does
+  auto slice_of = [&](int row) {
+    const uint8_t* at = z + static_cast<int64_t>(row) * ld_bytes;
+    if (!alike) return slice_at(at);
+    Slice q = q_first;
+    q.row = at;
     return q;
   };
   // single element number i of this CTA (a few at most): its id, or -1
@@ -719,7 +729,29 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
     return i < n_head ? i : i < n_head + n_tail ? q.tail + i - n_head : -1;
   };
 
+  // Writes a row's outputs from its joined part; the whole warp calls.
+  auto finish = [&](int row, int y, const RowPart& part, float zt, uint64_t list, bool late) {
+    const bool bad = y != ignore_index && (y < 0 || y >= V);
+    RowOut r = row_finish(part, zt, y != ignore_index && !bad, inv_t, c);
+    const float nan = __uint_as_float(0x7FC00000u);
+    if (late) r.logprob = r.entropy = r.lse = nan;
+    if (lane == 0) {
+      if (logprob != nullptr) logprob[row] = bad ? nan : r.logprob;
+      if (entropy != nullptr) entropy[row] = r.entropy;
+      if (lse != nullptr) lse[row] = r.lse;
+      if (bad) record_error(status, 8);
+      if (late) record_error(status, kStatusTimeout);
+    }
+    if (kTop && lane < top_k) {
+      const int64_t at = static_cast<int64_t>(row) * top_k + lane;
+      const bool none = list == 0;
+      top_id[at] = none || late ? -1 : key_id(list);
+      top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
+    }
+  };
+
   if (warp < kWarps) {
+    const float reach = 200.f / c;
     auto token_of = [&](int64_t row) {
       return tokens != nullptr && row < N ? tokens[row] : ignore_index;
     };
@@ -780,7 +812,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
       if (own) s_zt[k] = zt;
       float s = 0.f, t = 0.f;
       if (M > -INFINITY && M < INFINITY) {
-        RowSums<kBf16> sums(M, c);
+        RowSums<kBf16> sums(M, c, reach);
         // the top_k-th largest of the 32 maxima
         float thr = 0.f;
         if constexpr (kTop) thr = __shfl_sync(0xffffffffu, warp_sort_values(gm, lane), top_k - 1);
@@ -859,7 +891,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
       if (tid == 0) s_m[k] = M;
       bar_arrive(kBarDone + k, kAll);
     }
-  } else {
+  } else if (warp == kWarps) {
     auto copy = [&](int row, int k) {
       const Slice q = slice_of(row);
       const uint32_t bytes = static_cast<uint32_t>(q.nv) * 16u, bar = smem_u32(&s_full[k]);
@@ -891,8 +923,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
       const int k = it & 1;
       const bool more = row + 2 * static_cast<int64_t>(step) < N;
       const int y = tokens != nullptr ? tokens[row] : ignore_index;
-      const bool bad = y != ignore_index && (y < 0 || y >= V);
-      const bool has = y != ignore_index && !bad;
       bar_sync(kBarDone + k, kAll);
       // take what the slot holds, start the copy into it and give it back, then sort
       const int count = kTop ? s_count[k] : 0;
@@ -937,7 +967,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
         const int id0 = q.head + q.v0 * E;
         const int ie = lane < 16 ? single_of(q, lane) : -1;
         const float xe = ie >= 0 ? L::load1(q.row + static_cast<int64_t>(ie) * L::kBytes) : -INFINITY;
-        const bool mine = has && y >= id0 && y < id0 + q.nv * E;
+        const bool mine = y != ignore_index && y >= id0 && y < id0 + q.nv * E;
         uint64_t below = ~0ull;
         for (int i = 0; i < top_k && below != 0; ++i) {
           uint64_t best = 0;
@@ -973,16 +1003,18 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
       part.s = sums.x;
       part.t = sums.y;
 
-      bool late = s_late != 0;
-      const int leader = it % csize, u = it / csize, slot = u & 1;
-      if (csize > 1) {
+      if (csize == 1) {
+        finish(row, y, part, zt, list, s_late != 0);
+      } else {
         // to this row's CTA, once it has read the message of two turns before
+        const int leader = it % csize, u = it / csize, slot = u & 1;
         if (u >= 2 && !mbar_wait_bounded<true>(smem_u32(&s_used[leader][slot]),
                                                static_cast<uint32_t>(((u >> 1) - 1) & 1), timeout_ns, &never))
-          late = true;
+          s_late = 1;
         // asynchronous stores, counted in bytes on the receiver's barrier: no fence
         const uint32_t msg = mapa_shared(smem_u32(&s_msg[slot][crank]), static_cast<uint32_t>(leader));
         const uint32_t bar = mapa_shared(smem_u32(&s_got[slot]), static_cast<uint32_t>(leader));
+        if (s_late) part.m = __uint_as_float(0x7FC00000u);   // a row that came to nothing
         if (lane == 0)
           asm volatile(
               "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(msg),
@@ -993,60 +1025,48 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kMinBlocks)
                            msg + 16u + 8u * lane),
                        "l"(list), "r"(bar)
                        : "memory");
-        if (crank == leader) {
-          if (lane == 0)
-            mbar_arrive_expect_tx(smem_u32(&s_got[slot]),
-                                  static_cast<uint32_t>(csize) * (16u + (kTop ? 8u * top_k : 0u)));
-          __syncwarp();
-          if (!mbar_wait_bounded<true>(smem_u32(&s_got[slot]), static_cast<uint32_t>((u >> 1) & 1), timeout_ns,
-                                       &never))
-            late = true;
-          // lane r joins CTA r's sums; the rankings one after the other
-          const float4 p = lane < csize ? s_msg[slot][lane].part : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-          part = RowPart{p.x, p.y, p.z};
-          zt = p.w;
+      }
+    }
+  } else if (csize > 1) {
+    // joins the rows whose turn this CTA is
+    int u = 0;
+    for (int64_t row = first + static_cast<int64_t>(crank) * step; row < N;
+         row += static_cast<int64_t>(csize) * step, ++u) {
+      const int slot = u & 1;
+      const int y = tokens != nullptr ? tokens[row] : ignore_index;
+      if (lane == 0)
+        mbar_arrive_expect_tx(smem_u32(&s_got[slot]),
+                              static_cast<uint32_t>(csize) * (16u + (kTop ? 8u * top_k : 0u)));
+      __syncwarp();
+      bool late = !mbar_wait_bounded<true>(smem_u32(&s_got[slot]), static_cast<uint32_t>((u >> 1) & 1),
+                                           timeout_ns, &never);
+      late = __any_sync(0xffffffffu, late) || s_late != 0;
+      // lane r joins CTA r's sums; the rankings one after the other
+      const float4 p = lane < csize ? s_msg[slot][lane].part : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      RowPart part{p.x, p.y, p.z};
+      float zt = p.w;
 #pragma unroll
-          for (int o = kMaxRowCluster / 2; o > 0; o >>= 1) {
-            const RowPart q{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o),
-                            __shfl_xor_sync(0xffffffffu, part.t, o)};
-            row_join(part, q, c);
-            zt += __shfl_xor_sync(0xffffffffu, zt, o);
-          }
-          part = RowPart{__shfl_sync(0xffffffffu, part.m, 0), __shfl_sync(0xffffffffu, part.s, 0),
-                         __shfl_sync(0xffffffffu, part.t, 0)};
-          zt = __shfl_sync(0xffffffffu, zt, 0);
-          if constexpr (kTop) {
-            list = 0;
-            for (int r = 0; r < csize; ++r) {
-              const uint64_t key = lane < top_k ? s_msg[slot][r].list[lane] : 0;
-              list = r == 0 ? key : warp_merge_desc(list, key, lane);
-            }
-          }
-          __syncwarp();
-          if (lane < csize)
-            mbar_arrive_cluster(mapa_shared(smem_u32(&s_used[crank][slot]), static_cast<uint32_t>(lane)));
+      for (int o = kMaxRowCluster / 2; o > 0; o >>= 1) {
+        const RowPart q{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o),
+                        __shfl_xor_sync(0xffffffffu, part.t, o)};
+        row_join(part, q, c);
+        zt += __shfl_xor_sync(0xffffffffu, zt, o);
+      }
+      part = RowPart{__shfl_sync(0xffffffffu, part.m, 0), __shfl_sync(0xffffffffu, part.s, 0),
+                     __shfl_sync(0xffffffffu, part.t, 0)};
+      zt = __shfl_sync(0xffffffffu, zt, 0);
+      uint64_t list = 0;
+      if constexpr (kTop) {
+        for (int r = 0; r < csize; ++r) {
+          const uint64_t key = lane < top_k ? s_msg[slot][r].list[lane] : 0;
+          list = r == 0 ? key : warp_merge_desc(list, key, lane);
         }
       }
+      __syncwarp();
+      if (lane < csize)
+        mbar_arrive_cluster(mapa_shared(smem_u32(&s_used[crank][slot]), static_cast<uint32_t>(lane)));
       if (late) s_late = 1;
-      late = __any_sync(0xffffffffu, late);
-      if (crank == leader) {
-        RowOut r = row_finish(part, zt, has, inv_t, c);
-        const float nan = __uint_as_float(0x7FC00000u);
-        if (late) r.logprob = r.entropy = r.lse = nan;
-        if (lane == 0) {
-          if (logprob != nullptr) logprob[row] = bad ? nan : r.logprob;
-          if (entropy != nullptr) entropy[row] = r.entropy;
-          if (lse != nullptr) lse[row] = r.lse;
-          if (bad) record_error(status, 8);
-          if (late) record_error(status, kStatusTimeout);
-        }
-        if (kTop && lane < top_k) {
-          const int64_t at = static_cast<int64_t>(row) * top_k + lane;
-          const bool none = list == 0;
-          top_id[at] = none || late ? -1 : key_id(list);
-          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
-        }
-      }
+      finish(static_cast<int>(row), y, part, zt, list, late);
     }
   }
   // copies that nobody waited for land before the memory is given back (only after a timeout)
@@ -1073,7 +1093,7 @@ cudaError_t launch_stream(int cluster, int N, int sms, const uint8_t* z, int64_t
   int clusters = sms * kMinBlocks / cluster;
   if (clusters < 1) clusters = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3((kWarps + 1) * 32, 1, 1);
+  cfg.blockDim = dim3((kWarps + 2) * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1178,9 +1198,9 @@ cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const
                                 cudaStream_t stream) {
   const uint8_t* zp = static_cast<const uint8_t*>(z);
   const int64_t row_bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
-  // Slices: rows of up to 20 KB whole in CTAs of 4 + 1 warps (four per SM), others in slices
-  // of at most 49 KB in CTAs of 8 + 1 warps (two per SM), or, when eight of those do not hold
-  // the row, 104 KB in CTAs of 16 + 1 (one).
+  // Slices: rows of up to 20 KB whole in CTAs of 4 + 2 warps (four per SM), others in slices
+  // of at most 49 KB in CTAs of 8 + 2 warps (two per SM), or, when eight of those do not hold
+  // the row, 104 KB in CTAs of 16 + 2 (one).
   constexpr int kWarpRow = 8 << 10, kSmall = 20 << 10, kTwo = 49 << 10, kOne = 104 << 10;
   auto cluster_for = [&](int64_t slice) {
     // whole 16-byte vectors per CTA: leave one vector for the rounding up
