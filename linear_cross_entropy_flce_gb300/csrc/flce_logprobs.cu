@@ -13,7 +13,8 @@
 //       at a time; each CTA's slice is copied into shared memory by the bulk-copy engine,
 //       double-buffered, so both passes read shared memory and every logit leaves DRAM
 //       once. Most of the CTA's warps do the passes; one sorts the candidates of the row
-//       before, sends the CTA's part of it and starts the copies; one joins the parts of
+//       before, sends the CTA's part of it and starts the copies; one finds the ranking's
+//       threshold while the sums are taken; one joins the parts of
 //       the rows that are this CTA's (each row's meet in another CTA of the cluster), so
 //       that none of it holds the passes up.
 //   logprob_warp_kernel : rows of up to 8 KB, one warp each.
@@ -40,9 +41,6 @@ namespace {
 constexpr int kRowThreads = 512;
 constexpr int kCandidates = 512;
 constexpr int kMaxRowCluster = 8;
-// Elements that a warp offers to the ranking, all together or at once, before it counts the
-// equal ones: with top_k of those, eight warps stay within kCandidates.
-constexpr int kManyHits = 16;
 
 template <int kBf16>
 struct Logit;
@@ -367,6 +365,13 @@ struct VecMax<0> {
   __device__ float value() const { return max_nan(a, b); }
 };
 
+// Maximum over the warp that keeps a NaN, in one instruction.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // 32 values in descending order over the warp.
 __device__ __forceinline__ float warp_sort_values(float v, int lane) {
 #pragma unroll
@@ -495,6 +500,7 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
   using L = Logit<kBf16>;
   constexpr int E = L::E;
   __shared__ uint64_t s_cand[kTop ? kWarpRowWarps : 1][kTop ? kWarpCandidates : 1];
+  __shared__ int s_count[kWarpRowWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * kWarpRowWarps + warp;
   if (row >= N) return;
@@ -516,9 +522,7 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
 #pragma unroll
   for (int j = 0; j < kNv; ++j) vm.take(w[j]);
   const float mine = max_nan(vm.value(), xe);
-  float M = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float M = warp_max_nan(mine);
   RowPart part{M, 0.f, 0.f};
   float zt = 0.f;
   uint64_t list = 0;
@@ -526,42 +530,28 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
     if constexpr (kTop) {
       const float thr = __shfl_sync(0xffffffffu, warp_sort_values(mine, lane), top_k - 1);
       const Reaches<kBf16> reaches(thr);
-      int count = 0;
-      // the elements x[0, n) of every lane that reach thr, of ids id, id + 1, ...
-      auto offer = [&](const float (&x)[E], int n, int id) {
-        uint32_t in = 0;
+      uint32_t hit = 0;   // this lane's vectors that reach the threshold: a few in the warp
 #pragma unroll
-        for (int e = 0; e < E; ++e) in |= (e < n && x[e] >= thr && x[e] > -INFINITY ? 1u : 0u) << e;
-        int before = __popc(in);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int p = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += p;
-        }
-        const int all = __shfl_sync(0xffffffffu, before, 31);
-        int at = count + before - __popc(in);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (in >> e & 1u) {
-            if (at < kWarpCandidates) s_cand[warp][at] = rank_key(x[e], id + e);
-            ++at;
-          }
-        count += all;
-      };
-#pragma unroll
-      for (int j = 0; j < kNv; ++j)
-        if (__any_sync(0xffffffffu, reaches(w[j]))) {
-          float x[E];
-          L::widen(w[j], x);
-          offer(x, E, head + (lane + 32 * j) * E);
-        }
-      if (__any_sync(0xffffffffu, ie >= 0)) {
-        float x[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = xe;
-        offer(x, ie >= 0 ? 1 : 0, ie);
-      }
+      for (int j = 0; j < kNv; ++j) hit |= (reaches(w[j]) ? 1u : 0u) << j;
+      if (lane == 0) s_count[warp] = 0;
       __syncwarp();
+      auto offer = [&](float x, int id) {
+        if (x >= thr && x > -INFINITY) {
+          const int at = atomicAdd(&s_count[warp], 1);
+          if (at < kWarpCandidates) s_cand[warp][at] = rank_key(x, id);
+        }
+      };
+      for (; hit != 0; hit &= hit - 1) {
+        const int v = lane + 32 * (__ffs(hit) - 1);
+        const uint4 again = __ldg(vec + v);   // (indexing the registers would move them to memory)
+        float x[E];
+        L::widen(again, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) offer(x[e], head + v * E + e);
+      }
+      if (ie >= 0) offer(xe, ie);
+      __syncwarp();
+      const int count = s_count[warp];
       if (count <= kWarpCandidates) {
         for (int b = 0; b < count; b += 32) {
           const uint64_t key = warp_sort_desc(b + lane < count ? s_cand[warp][b + lane] : 0, lane);
@@ -651,7 +641,7 @@ struct __align__(16) RowMsg {
 };
 
 template <int kBf16, bool kTop, int kWarps, int kSlice, int kMinBlocks>
-__global__ void __launch_bounds__((kWarps + 2) * 32, kMinBlocks)
+__global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
     logprob_stream_kernel(const uint8_t* __restrict__ z, int64_t ld_bytes,
                           const int32_t* __restrict__ tokens, int N, int V, int ignore_index,
                           int top_k, float inv_t, float* __restrict__ logprob,
@@ -662,7 +652,8 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, kMinBlocks)
   constexpr int E = L::E;
   constexpr int kData = kWarps * 32;          // threads that do the passes
   constexpr int kAll = kData + 32;            // and the warp that ranks
-  constexpr int kBarMax = 1, kBarDone = 2, kBarFree = 4;   // named barriers; the last two in pairs
+  constexpr int kBarMax = 1;   // named barriers; the others in pairs
+  constexpr int kBarDone = 2, kBarFree = 4, kBarLanes = 6, kBarThr = 8;
   extern __shared__ __align__(128) uint8_t s_rows[];       // two slices
   __shared__ __align__(8) uint64_t s_full[2];   // a slice's copy has landed
   // A row's parts meet in one CTA, each in turn (row it of the cluster in CTA it % csize, its
@@ -670,7 +661,10 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, kMinBlocks)
   __shared__ __align__(8) uint64_t s_got[2];                    // every CTA's message is here
   __shared__ __align__(8) uint64_t s_used[kMaxRowCluster][2];   // CTA r has read this one's message
   __shared__ RowMsg s_msg[2][kMaxRowCluster];
-  __shared__ float s_max[2][kWarps][kTop ? 32 : 1];
+  __shared__ float s_max[2][kWarps];            // each warp's maximum
+  __shared__ float s_lanes[kTop ? 2 : 1][kWarps][kTop ? 32 : 1];   // each thread's
+  __shared__ float s_thr[2];                    // the ranking's threshold
+  __shared__ int s_ties[2];                     // whether many elements may be equal to it
   __shared__ float2 s_sum[2][kWarps];
   __shared__ float s_m[2], s_zt[2];
   __shared__ int s_count[2];
@@ -776,13 +770,12 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, kMinBlocks)
       for (int v = tid; v < q.nv; v += kData) vm.take(vec[v]);
       const float mine = max_nan(vm.value(), xe);
       if constexpr (kTop) {
-        s_max[k][warp][lane] = mine;
-      } else {
-        float wm = mine;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) wm = max_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-        if (lane == 0) s_max[k][warp][0] = wm;
+        s_lanes[k][warp][lane] = mine;
+        __syncwarp();
+        bar_arrive(kBarLanes + k, kAll);
       }
+      const float wm = warp_max_nan(mine);
+      if (lane == 0) s_max[k][warp] = wm;
       // the token's element: its thread keeps the value and takes it out of the sums
       const int id0 = q.head + q.v0 * E;   // id of the slice's first vector element
       float zt = 0.f;
@@ -796,91 +789,80 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, kMinBlocks)
         else *reinterpret_cast<float*>(at) = -INFINITY;
       }
       bar_sync(kBarMax, kData);
-      float gm;   // the maximum over the threads of equal lane, or one of the warps' maxima
-      if constexpr (kTop) {
-        gm = s_max[k][0][lane];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) gm = max_nan(gm, s_max[k][w][lane]);
-      } else {
-        gm = s_max[k][lane % kWarps][0];
-      }
-      float M = gm;
-#pragma unroll
-      for (int o = kTop ? 16 : kWarps / 2; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float M = warp_max_nan(s_max[k][lane % kWarps]);
       // the last warp has taken what this slot held
       if (it >= 2) bar_sync(kBarFree + k, kAll);
       if (own) s_zt[k] = zt;
       float s = 0.f, t = 0.f;
       if (M > -INFINITY && M < INFINITY) {
         RowSums<kBf16> sums(M, c, reach);
-        // the top_k-th largest of the 32 maxima
-        float thr = 0.f;
-        if constexpr (kTop) thr = __shfl_sync(0xffffffffu, warp_sort_values(gm, lane), top_k - 1);
-        int hits = 0, equal = 0;   // of this warp: offered so far; equal to the threshold
-        // Offers this lane's elements of ids id, id + 1, ...; the whole warp calls. On rows
-        // with many elements equal to the threshold only the first top_k of them count.
-        auto offer = [&](const uint4& w, int id) {
-          float x[E];
-          L::widen(w, x);
-          uint32_t in = 0;
-#pragma unroll
-          for (int e = 0; e < E; ++e) in |= (x[e] >= thr ? 1u : 0u) << e;
-          if (thr == -INFINITY)
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              if (x[e] == -INFINITY) in &= ~(1u << e);
-          const int here = __reduce_add_sync(0xffffffffu, __popc(in));
-          hits += here;
-          if (hits > kManyHits || here > kManyHits) {
-            uint32_t eq = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) eq |= (x[e] == thr ? 1u : 0u) << e;
-            eq &= in;
-            int before = __popc(eq);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const int p = __shfl_up_sync(0xffffffffu, before, o);
-              if (lane >= o) before += p;
-            }
-            int room = max(top_k - equal - (before - __popc(eq)), 0);   // of this lane's equal ones
-            equal += __shfl_sync(0xffffffffu, before, 31);
-            for (; __popc(eq) > room; eq &= ~(0x80000000u >> __clz(eq))) in &= ~(0x80000000u >> __clz(eq));
-          }
-          if (in != 0) {
-            int at = atomicAdd(&s_count[k], __popc(in));
-            for (; in != 0; in &= in - 1, ++at) {
-              const int e = __ffs(in) - 1;
-              if (at < kCandidates) s_cand[kTop ? k : 0][at] = rank_key(element_of<kBf16>(w, e), id + e);
-            }
+#pragma unroll 2
+        for (int v = tid; v < q.nv; v += kData) sums.add(vec[v]);
+        if (ie >= 0 && ie != yt) sums.add_one(xe);
+        s = sums.s0 + sums.s1;
+        t = sums.t0 + sums.t1;
+      }
+      if constexpr (kTop) {
+        // the candidates: from the threads whose maximum reaches the threshold
+        bar_sync(kBarThr + k, kAll);
+        const float thr = s_thr[k];
+        const bool live = M > -INFINITY && M < INFINITY;
+        auto offer_one = [&](float x, int id) {
+          if (x >= thr && x > -INFINITY) {
+            const int at = atomicAdd(&s_count[k], 1);
+            if (at < kCandidates) s_cand[k][at] = rank_key(x, id);
           }
         };
-        const Reaches<kBf16> reaches(thr);
-        if (kTop && __any_sync(0xffffffffu, mine >= thr)) {
-          for (int vw = warp * 32; vw < q.nv; vw += kData) {
-            const int v = vw + lane;
-            const uint4 w = v < q.nv ? vec[v] : no_logits<kBf16>();
-            if (__any_sync(0xffffffffu, reaches(w))) offer(w, id0 + v * E);
-            sums.add(w);   // (-inf adds nothing)
+        int equal = 0;   // of this warp: elements equal to the threshold so far
+        // Many equal ones: only the first top_k of them count, of this warp too, so that the
+        // list holds what eight warps offer. The whole warp calls.
+        auto offer_first = [&](const uint4& w, int id) {
+          float x[E];
+          L::widen(w, x);
+          uint32_t gt = 0, eq = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            gt |= (x[e] > thr ? 1u : 0u) << e;
+            eq |= (x[e] == thr && x[e] > -INFINITY ? 1u : 0u) << e;
           }
-        } else {
-#pragma unroll 2
-          for (int v = tid; v < q.nv; v += kData) sums.add(vec[v]);
-        }
-        if (ie >= 0 && ie != yt) sums.add_one(xe);
-        // the single elements, and the token's that the slice no longer holds, are candidates
-        // as they are
-        if constexpr (kTop) {
-          auto offer_one = [&](float x, int id) {
-            if (x >= thr && x > -INFINITY) {
-              const int at = atomicAdd(&s_count[k], 1);
-              if (at < kCandidates) s_cand[k][at] = rank_key(x, id);
+          int before = __popc(eq);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int p = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += p;
+          }
+          const int room = max(top_k - equal - (before - __popc(eq)), 0);   // of this lane's
+          equal += __shfl_sync(0xffffffffu, before, 31);
+          while (__popc(eq) > room) eq &= ~(0x80000000u >> __clz(eq));
+          for (uint32_t in = gt | eq; in != 0; in &= in - 1) {
+            const int e = __ffs(in) - 1;
+            offer_one(element_of<kBf16>(w, e), id + e);
+          }
+        };
+        if (live && __any_sync(0xffffffffu, mine >= thr)) {
+          const Reaches<kBf16> reaches(thr);
+          if (s_ties[k]) {
+            for (int vw = warp * 32; vw < q.nv; vw += kData) {
+              const uint4 w = vw + lane < q.nv ? vec[vw + lane] : no_logits<kBf16>();
+              if (__any_sync(0xffffffffu, reaches(w))) offer_first(w, id0 + (vw + lane) * E);
             }
-          };
+          } else if (mine >= thr) {
+#pragma unroll 2
+            for (int v = tid; v < q.nv; v += kData) {
+              const uint4 w = vec[v];
+              if (reaches(w)) {
+                float x[E];
+                L::widen(w, x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) offer_one(x[e], id0 + v * E + e);
+              }
+            }
+          }
+          // the single elements, and the token's that the slice no longer holds
           if (ie >= 0) offer_one(xe, ie);
           if (taken) offer_one(zt, yt);
         }
-        s = sums.s0 + sums.s1;
-        t = sums.t0 + sums.t1;
+        __syncwarp();
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -1027,6 +1009,24 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, kMinBlocks)
                        : "memory");
       }
     }
+  } else if (kTop && warp == kWarps + 1) {
+    // the top_k-th largest of the maxima over the threads of equal lane
+    int it = 0;
+    for (int64_t row = first; row < N; row += step, ++it) {
+      const int k = it & 1;
+      bar_sync(kBarLanes + k, kAll);
+      float m = s_lanes[k][0][lane];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_lanes[k][w][lane]);
+      const float thr = __shfl_sync(0xffffffffu, warp_sort_values(m, lane), top_k - 1);
+      const int same = __popc(__ballot_sync(0xffffffffu, m == thr && thr > -INFINITY));
+      if (lane == 0) {
+        s_thr[k] = thr;
+        s_ties[k] = same > 4;
+      }
+      __syncwarp();
+      bar_arrive(kBarThr + k, kAll);
+    }
   } else if (csize > 1) {
     // joins the rows whose turn this CTA is
     int u = 0;
@@ -1093,7 +1093,7 @@ cudaError_t launch_stream(int cluster, int N, int sms, const uint8_t* z, int64_t
   int clusters = sms * kMinBlocks / cluster;
   if (clusters < 1) clusters = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3((kWarps + 2) * 32, 1, 1);
+  cfg.blockDim = dim3((kTop ? kWarps + 3 : kWarps + 2) * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
