@@ -39,7 +39,7 @@ namespace flce {
 namespace {
 
 constexpr int kRowThreads = 512;
-constexpr int kCandidates = 512;
+constexpr int kCandidates = 448;
 constexpr int kMaxRowCluster = 8;
 
 template <int kBf16>
@@ -546,8 +546,14 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
         const uint4 again = __ldg(vec + v);   // (indexing the registers would move them to memory)
         float x[E];
         L::widen(again, x);
+        uint32_t in = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) offer(x[e], head + v * E + e);
+        for (int e = 0; e < E; ++e) in |= (x[e] >= thr && x[e] > -INFINITY ? 1u : 0u) << e;
+        int at = atomicAdd(&s_count[warp], __popc(in));
+        for (; in != 0; in &= in - 1, ++at) {
+          const int e = __ffs(in) - 1;
+          if (at < kWarpCandidates) s_cand[warp][at] = rank_key(element_of<kBf16>(again, e), head + v * E + e);
+        }
       }
       if (ie >= 0) offer(xe, ie);
       __syncwarp();
@@ -566,12 +572,9 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
             const uint64_t key = x > -INFINITY ? rank_key(x, id) : 0;
             if (key < below && key > best) best = key;
           };
-#pragma unroll
-          for (int j = 0; j < kNv; ++j) {
-            float x[E];
-            L::widen(w[j], x);
-#pragma unroll
-            for (int e = 0; e < E; ++e) look(x[e], head + (lane + 32 * j) * E + e);
+          for (int v = lane; v < nvec; v += 32) {
+            const uint4 again = __ldg(vec + v);
+            for (int e = 0; e < E; ++e) look(element_of<kBf16>(again, e), head + v * E + e);
           }
           if (ie >= 0) look(xe, ie);
 #pragma unroll
@@ -664,6 +667,8 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
   __shared__ float s_max[2][kWarps];            // each warp's maximum
   __shared__ float s_lanes[kTop ? 2 : 1][kWarps][kTop ? 32 : 1];   // each thread's
   __shared__ float s_thr[2];                    // the ranking's threshold
+  __shared__ uint16_t s_hot[kTop ? 2 : 1][kTop ? kData : 1];   // the threads whose maximum reaches it
+  __shared__ int s_nhot[2];
   __shared__ int s_ties[2];                     // whether many elements may be equal to it
   __shared__ float2 s_sum[2][kWarps];
   __shared__ float s_m[2], s_zt[2];
@@ -839,7 +844,7 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
             offer_one(element_of<kBf16>(w, e), id + e);
           }
         };
-        if (live && __any_sync(0xffffffffu, mine >= thr)) {
+        if (live) {
           const Reaches<kBf16> reaches(thr);
           if (s_ties[k]) {
             for (int vw = warp * 32; vw < q.nv; vw += kData) {
@@ -847,27 +852,26 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
               if (__any_sync(0xffffffffu, reaches(w))) offer_first(w, id0 + (vw + lane) * E);
             }
           } else {
-            // the threads whose maximum reaches it, a few in the CTA: their vectors are looked
-            // through by 8, 16 or 32 lanes each, not by the thread itself, whose chain of loads
-            // would hold up the whole CTA (165 of 577 us at 8192 x 128256 bf16)
+            // the vectors of the threads whose maximum reaches it, dealt to the whole CTA: left
+            // to those threads (or their warps) their chain of loads holds up the others
+            const int hot = s_nhot[k];
+            const int shift = hot > 1 ? 32 - __clz(hot - 1) : 0;
             const int rounds = (q.nv + kData - 1) / kData;
-            const int width = rounds <= 8 ? 8 : rounds <= 16 ? 16 : 32;
-            for (uint32_t hot = __ballot_sync(0xffffffffu, mine >= thr); hot != 0;) {
-              int src = -1;
-              for (int g = 0; g < 32; g += width) {
-                if (lane >= g && hot != 0) src = __ffs(hot) - 1;
-                else if (lane >= g) src = -1;
-                hot &= hot - 1;
-              }
-              for (int r = lane % width; r < rounds; r += 32) {
-                const int v = warp * 32 + src + r * kData;
-                if (src >= 0 && v < q.nv) {
-                  const uint4 w = vec[v];
-                  if (reaches(w)) {
-                    float x[E];
-                    L::widen(w, x);
+            for (int i = tid; i < rounds << shift; i += kData) {
+              const int h = i & ((1 << shift) - 1);
+              const int v = h < hot ? s_hot[k][h] + (i >> shift) * kData : q.nv;
+              if (v < q.nv) {
+                const uint4 w = vec[v];
+                if (reaches(w)) {   // one reservation for all of the vector's
+                  float x[E];
+                  L::widen(w, x);
+                  uint32_t in = 0;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) offer_one(x[e], id0 + v * E + e);
+                  for (int e = 0; e < E; ++e) in |= (x[e] >= thr && x[e] > -INFINITY ? 1u : 0u) << e;
+                  int at = atomicAdd(&s_count[k], __popc(in));
+                  for (; in != 0; in &= in - 1, ++at) {
+                    const int e = __ffs(in) - 1;
+                    if (at < kCandidates) s_cand[k][at] = rank_key(element_of<kBf16>(w, e), id0 + v * E + e);
                   }
                 }
               }
@@ -1030,14 +1034,26 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
     for (int64_t row = first; row < N; row += step, ++it) {
       const int k = it & 1;
       bar_sync(kBarLanes + k, kAll);
-      float m = s_lanes[k][0][lane];
+      float each[kWarps], m = -INFINITY;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_lanes[k][w][lane]);
+      for (int w = 0; w < kWarps; ++w) {
+        each[w] = s_lanes[k][w][lane];
+        m = fmaxf(m, each[w]);
+      }
       const float thr = __shfl_sync(0xffffffffu, warp_sort_values(m, lane), top_k - 1);
       const int same = __popc(__ballot_sync(0xffffffffu, m == thr && thr > -INFINITY));
+      int hot = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const unsigned in = __ballot_sync(0xffffffffu, each[w] >= thr && each[w] > -INFINITY);
+        if (in >> lane & 1u)
+          s_hot[k][hot + __popc(in & ((1u << lane) - 1u))] = static_cast<uint16_t>(w * 32 + lane);
+        hot += __popc(in);
+      }
       if (lane == 0) {
         s_thr[k] = thr;
         s_ties[k] = same > 4;
+        s_nhot[k] = hot;
       }
       __syncwarp();
       bar_arrive(kBarThr + k, kAll);
