@@ -1,4 +1,5 @@
-"""In-tree build of libflce.so (the C-ABI library) for sm_103a.
+"""In-tree build of libflce.so (the C-ABI library) for sm_103a, and of _flce_ops.so, the
+Python extension that makes the ordinary calls of include/flce_ops.h.
 
 Each .cu translation unit is compiled in parallel with nvcc and linked into
 linear_cross_entropy_flce_gb300/libflce.so. No cmake; CUDA's runtime is linked
@@ -8,10 +9,12 @@ library loads on a machine without a GPU driver.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -37,6 +40,36 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+EXT = os.path.join(PKG, "_flce_ops.so")
+
+
+def _compile_ext() -> str:
+    """Compile py_ops.cpp against the installed PyTorch's headers (not imported for it)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    obj = os.path.join(BUILD, "py_ops.o")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(torch, "include"),
+           "-I" + os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), "-c", os.path.join(CSRC, "py_ops.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for py_ops.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_ext(obj: str) -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = EXT + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libflce.so",
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,--no-as-needed"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _flce_ops.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def _compile(src: str, extra) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -47,10 +80,11 @@ def _compile(src: str, extra) -> str:
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libflce.so; return its path."""
+    """Compile and link libflce.so (whose path is returned) and _flce_ops.so."""
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext_obj = ex.submit(_compile_ext)
         logs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
     if verbose or ptxas_info:
         for s, log in zip(SOURCES, logs):
@@ -63,6 +97,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext_obj.result())
     return LIB
 
 
