@@ -30,6 +30,7 @@ SOURCES = ["flce_api.cu", "flce_reduce.cu", "flce_gemm_lse.cu", "flce_gemm_grad.
            "flce_gemm_f32.cu", "flce_gemm_logp.cu", "flce_gemm_few.cu",
            "flce_noalloc.cu", "flce_ce.cu",
            "flce_ops_api.cu", "flce_logprobs.cu", "flce_logprob_merge.cu", "flce_norm.cu",
+           "flce_norm_stream.cu", "flce_norm_stream_grad.cu",
            "flce_clip.cu"]
 
 

@@ -11,14 +11,18 @@
 // in its registers while dx is formed from the same loads; the next row is loaded before
 // the current one is reduced. One fp32 partial per CTA is left, joined in a fixed order.
 //
+// Many rows of 1 KB or more on 16-byte boundaries go through the kernels of
+// flce_norm_stream*.cu instead.
+//
 // Accesses are as wide as the hidden size, the strides and the addresses allow (VW
 // elements, 2 to 16 bytes). Rows longer than 1024 threads can hold take the looped
 // kernels, which read a row again for each of its passes.
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 
 #include "flce_internal.h"
+#include "flce_norm.cuh"
+#include "flce_norm_stream.h"
 
 namespace flce {
 
@@ -26,21 +30,6 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kColumnThreads = 128;
-
-__device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int bf16) {
-  return bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16)
-              : static_cast<const float*>(p)[i];
-}
-
-__device__ __forceinline__ void store_from_f32(void* p, int64_t i, float v, int bf16) {
-  if (bf16) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(v));
-    static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(r & 0xFFFFu);
-  } else {
-    static_cast<float*>(p)[i] = v;
-  }
-}
 
 // Sum of a pair over the block, the same value in every thread.
 __device__ __forceinline__ float2 block_sum2(float2 v, float2* s_part) {
@@ -165,78 +154,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 }
 
 // ---- rows held in registers ---------------------------------------------------------
-
-template <int kBytes>
-struct RawOf;
-template <> struct RawOf<16> { using type = uint4; };
-template <> struct RawOf<8> { using type = uint2; };
-template <> struct RawOf<4> { using type = uint32_t; };
-template <> struct RawOf<2> { using type = uint16_t; };
-
-// VW consecutive elements, loaded and stored as one access.
-template <int kBf16, int VW>
-struct Pack {
-  static constexpr int kBytes = VW * (kBf16 ? 2 : 4);
-  using Raw = typename RawOf<kBytes>::type;
-  __device__ static Raw load(const void* p, int64_t i) {
-    return *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p) + i * (kBf16 ? 2 : 4));
-  }
-  __device__ static void widen(Raw raw, float (&x)[VW]) {
-    if constexpr (!kBf16) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) x[e] = __uint_as_float(w[e]);
-    } else if constexpr (VW == 1) {
-      x[0] = __uint_as_float(static_cast<uint32_t>(raw) << 16);
-    } else {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
-#pragma unroll
-      for (int e = 0; e < VW; e += 2) {
-        x[e] = __uint_as_float(w[e / 2] << 16);
-        x[e + 1] = __uint_as_float(w[e / 2] & 0xFFFF0000u);
-      }
-    }
-  }
-  __device__ static void store(void* p, int64_t i, const float (&x)[VW]) {
-    Raw raw;
-    if constexpr (!kBf16) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) w[e] = __float_as_uint(x[e]);
-    } else if constexpr (VW == 1) {
-      uint32_t r;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(x[0]));
-      raw = static_cast<uint16_t>(r & 0xFFFFu);
-    } else {
-      uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
-#pragma unroll
-      for (int e = 0; e < VW; e += 2)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e / 2]) : "f"(x[e + 1]), "f"(x[e]));
-    }
-    *reinterpret_cast<Raw*>(static_cast<uint8_t*>(p) + i * (kBf16 ? 2 : 4)) = raw;
-  }
-};
-
-// VW values of weight or bias from element i, or `none` without one.
-template <int VW>
-__device__ __forceinline__ void load_param(const void* p, int i, int wbf16, float none,
-                                           float (&v)[VW]) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) v[e] = none;
-  } else if (wbf16) {
-    Pack<1, VW>::widen(Pack<1, VW>::load(p, i), v);
-  } else {
-    constexpr int W4 = VW < 4 ? VW : 4;
-#pragma unroll
-    for (int k = 0; k < VW; k += W4) {
-      float q[W4];
-      Pack<0, W4>::widen(Pack<0, W4>::load(p, i + k), q);
-#pragma unroll
-      for (int e = 0; e < W4; ++e) v[k + e] = q[e];
-    }
-  }
-}
 
 // Sum of a pair over the R threads of a group (R a multiple of 32, at most the block);
 // the same value in all of them. `slots` are the block's warps' slots, not read by any
@@ -423,28 +340,6 @@ __global__ void __launch_bounds__(512, kNv * VW <= 8 && VW > 1 ? 2 : 1)
 
 namespace {
 
-// The widest access (elements) that D, the row strides and the addresses allow.
-int access_width(int bf16, int D, std::initializer_list<int64_t> strides,
-                 std::initializer_list<const void*> rows, std::initializer_list<const void*> params,
-                 int wbf16) {
-  const int elt = bf16 ? 2 : 4, welt = wbf16 ? 2 : 4;
-  int vw = 16 / elt;
-  auto fits = [&](int v) {
-    if (D % v != 0) return false;
-    for (int64_t s : strides)
-      if (s % v != 0) return false;
-    for (const void* p : rows)
-      if (reinterpret_cast<uintptr_t>(p) % static_cast<unsigned>(v * elt) != 0) return false;
-    for (const void* p : params) {
-      const unsigned a = static_cast<unsigned>(v * welt < 16 ? v * welt : 16);
-      if (reinterpret_cast<uintptr_t>(p) % a != 0) return false;
-    }
-    return true;
-  };
-  while (vw > 1 && !fits(vw)) vw /= 2;
-  return vw;
-}
-
 // Threads per row: enough for nvec vectors at `most` per thread, and then more, down to
 // one vector per thread, while the rows alone do not fill the GPU (a quarter of its 2048
 // threads per SM).
@@ -513,12 +408,24 @@ cudaError_t norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   return go(layer_norm_grad_kernel<kBf16, VW, kMost>);
 }
 
+cudaError_t join_columns(const float* part, int ranges, int D, void* dweight, void* dbias,
+                         int wbf16, cudaStream_t stream) {
+  layer_norm_join_kernel<<<(D + 31) / 32, 32 * kJoinWarps, 0, stream>>>(part, ranges, D, dweight,
+                                                                        dbias, wbf16);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_layer_norm(const void* x, int bf16, int64_t ldx, const void* weight,
                               const void* bias, int wbf16, int N, int D, float eps, void* y,
                               int64_t ldy, float* mean, float* rstd, int sms,
                               cudaStream_t stream) {
+  if (norm_stream_fits(D, bf16 ? 2 : 4)) {
+    const cudaError_t e = launch_norm_stream(x, bf16, ldx, weight, bias, wbf16, N, D, eps, y, ldy,
+                                             mean, rstd, sms, stream);
+    if (e != cudaErrorNotSupported) return e;   // few rows: the kernel below
+  }
   const int vw = access_width(bf16, D, {ldx, ldy}, {x, y}, {weight, bias}, wbf16);
   if (D / vw <= 1024 * norm_vectors(vw)) {
     auto go = [&](auto f) {
@@ -552,6 +459,15 @@ cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void*
   cudaError_t e = cudaSuccess;
   const bool columns = dweight != nullptr || dbias != nullptr;
   int ranges = 0;
+  if (N > 0 && norm_stream_fits(D, bf16 ? 2 : 4)) {
+    e = launch_norm_stream_backward(dy, lddy, x, bf16, ldx, weight, wbf16, mean, rstd, N, D, dx,
+                                    lddx, dweight, dbias, columns ? part : nullptr, &ranges, sms,
+                                    stream);
+    if (e == cudaSuccess && columns && ranges > 1)
+      return join_columns(part, ranges, D, dweight, dbias, wbf16, stream);
+    if (e != cudaErrorNotSupported) return e;
+    e = cudaSuccess;
+  }
   const int vw = access_width(bf16, D, {lddy, ldx, dx != nullptr ? lddx : 0}, {dy, x, dx}, {weight},
                               wbf16);
   if (N > 0 && D <= grad_elems(vw) * kGradBlock) {
@@ -592,9 +508,7 @@ cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void*
     }
   }
   if (e != cudaSuccess || !columns) return e;
-  layer_norm_join_kernel<<<(D + 31) / 32, 32 * kJoinWarps, 0, stream>>>(part, ranges, D, dweight,
-                                                                        dbias, wbf16);
-  return cudaGetLastError();
+  return join_columns(part, ranges, D, dweight, dbias, wbf16, stream);
 }
 
 }  // namespace flce

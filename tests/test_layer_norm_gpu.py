@@ -107,6 +107,40 @@ def test_strides_and_alignments(dtype, N, D, pad, shift):
     _run(x, dy, w, b, dtype, "f32", pad=pad, shift=shift)
 
 
+@pytest.mark.parametrize("dtype,wdtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("N,D,pad", [
+    (2001, 512, 0), (4000, 512, 24), (1501, 1032, 0), (1203, 2728, 8), (701, 4096, 0), (305, 8192, 0),
+    (153, 12288, 0), (160, 16384, 8), (2000, 511, 0), (1501, 1030, 0), (1203, 2731, 5), (701, 4095, 0),
+    (303, 8190, 2)])
+def test_many_rows(dtype, wdtype, N, D, pad):
+    x, dy, w, b = _draw(N, D, N + D)
+    _run(x, dy, w, b, dtype, wdtype, pad=pad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,pad,shift", [(1024, 0, 0), (1000, 3, 1), (1029, 0, 2), (1111, 5, 0), (1031, 8, 3)])
+def test_many_rows_in_place_and_in_parts(dtype, D, pad, shift):
+    N = 2501
+    x, dy, w, b = _draw(N, D, D)
+    xt, dyt = (_put(a, dtype, pad, shift)[0] for a in (x, dy))
+    wt, bt = (_put(a, "f32")[0] for a in (w, b))
+    r = flce.layer_norm(xt, wt, bt)
+    want = flce.layer_norm_backward(dyt, xt, wt, r)
+    for k in range(3):
+        need = [i == k for i in range(3)]
+        got = flce.layer_norm_backward(dyt, xt, wt, r, need_dx=need[0], need_dweight=need[1], need_dbias=need[2])
+        assert torch.equal(got[k], want[k])
+    if pad == 0:   # outputs are contiguous
+        g = _put(dy, dtype, pad, shift)[0]
+        assert torch.equal(flce.layer_norm_backward(g, xt, wt, r, out={"dx": g})[0], want[0])
+        y = _put(x, dtype, pad, shift)[0]
+        assert torch.equal(flce.layer_norm(y, wt, bt, out={"y": y}).y, r.y)
+    for got in (flce.layer_norm(xt, wt).y, flce.layer_norm(xt, None, bt).y, flce.layer_norm(xt).y):
+        assert got.shape == (N, D) and bool(torch.isfinite(got).all())
+    _run(x, dy, w, None, dtype, "f32", pad=pad, shift=shift)
+    _run(x, dy, None, b, dtype, "bf16", pad=pad, shift=shift)
+
+
 @pytest.mark.parametrize("with_w,with_b", [(True, False), (False, True), (False, False)])
 def test_without_weight_or_bias(with_w, with_b):
     x, dy, w, b = _draw(50, 320, 3)
