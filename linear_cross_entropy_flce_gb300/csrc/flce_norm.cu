@@ -11,8 +11,7 @@
 // in its registers while dx is formed from the same loads; the next row is loaded before
 // the current one is reduced. One fp32 partial per CTA is left, joined in a fixed order.
 //
-// Many rows of 1 KB or more on 16-byte boundaries go through the kernels of
-// flce_norm_stream*.cu instead.
+// Many rows of 1 KB or more go through the kernels of flce_norm_stream*.cu instead.
 //
 // Accesses are as wide as the hidden size, the strides and the addresses allow (VW
 // elements, 2 to 16 bytes). Rows longer than 1024 threads can hold take the looped
