@@ -14,6 +14,7 @@
 
 #include "flce_clip.h"
 #include "flce_internal.h"
+#include "flce_launch.cuh"
 
 namespace flce {
 
@@ -22,19 +23,28 @@ namespace {
 constexpr int kClipThreads = 512;
 constexpr int kPieceBytes = 32 << 10;
 
-__device__ __forceinline__ double block_sum(double v, double* s_part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sum over the CTA, valid in warp 0. The fp64 units add two lanes a cycle: warp 0 adds up
+// 16 values per lane, then the lanes (500 cycles against the 1300 of shuffles in every warp).
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) s_part[warp] = v;
+  return v;
+}
+__device__ __forceinline__ double block_sum(double v, double* s_all) {
+  s_all[threadIdx.x] = v;
   __syncthreads();
-  double r = 0.0;
-  for (int w = 0; w < kClipThreads / 32; ++w) r += s_part[w];
-  return r;
+  if (threadIdx.x >= 32) return 0.0;
+  double r = s_all[threadIdx.x];
+#pragma unroll
+  for (int j = 1; j < kClipThreads / 32; ++j) r += s_all[threadIdx.x + 32 * j];
+  return warp_sum(r);
 }
 
-// The tensor that holds piece `p`: the last whose first piece is at most p.
+// The tensor that holds piece `p`: the last whose first piece is at most p. Tensors of one
+// size are found at once, others by halving.
 __device__ __forceinline__ int tensor_of(const ClipTable& tab, int p) {
+  const int guess = min(static_cast<int>(static_cast<float>(p) * tab.density), tab.count - 1);
+  if (tab.first[guess] <= p && (guess + 1 == tab.count || tab.first[guess + 1] > p)) return guess;
   int lo = 0, hi = tab.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -136,9 +146,10 @@ __device__ __forceinline__ Piece piece_of(const ClipTable& tab, int t, int p) {
   return r;
 }
 
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, 4)
     grad_squares_kernel(const __grid_constant__ ClipTable tab, double* part) {
-  __shared__ double s_part[kClipThreads / 32];
+  __shared__ double s_all[kClipThreads];
+  start_next_launch();
   double sum = 0.0;
   for (int p = blockIdx.x; p < tab.pieces; p += gridDim.x) {
     const int t = tensor_of(tab, p);
@@ -146,17 +157,22 @@ __global__ void __launch_bounds__(kClipThreads)
     const int elt = tab.bf16[t] ? 2 : 4;
     sum += static_cast<double>(squares(static_cast<const uint8_t*>(tab.src[t]) + c.at * elt, c.n, tab.bf16[t]));
   }
-  const double total = block_sum(sum, s_part);
+  const double total = block_sum(sum, s_all);
   if (threadIdx.x == 0) part[blockIdx.x] = total;
 }
 
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, 4)
     grad_scale_kernel(const __grid_constant__ ClipTable tab, const double* __restrict__ part,
                       int parts, float max_norm, float* norm_out) {
-  __shared__ double s_part[kClipThreads / 32];
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kClipThreads) sum += part[i];
-  const float norm = static_cast<float>(sqrt(block_sum(sum, s_part)));
+  __shared__ float s_norm;
+  wait_for_launch_before();   // the partials, and the last reads of what may be overwritten
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 32) sum += part[i];
+    s_norm = static_cast<float>(sqrt(warp_sum(sum)));
+  }
+  __syncthreads();
+  const float norm = s_norm;
   if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float ratio = max_norm / (norm + 1e-6f);
   const float c = ratio > 1.f ? 1.f : ratio;   // NaN stays
@@ -183,8 +199,8 @@ cudaError_t launch_grad_squares(const ClipTable& tab, double* part, int grid, cu
 
 cudaError_t launch_grad_scale(const ClipTable& tab, const double* part, int parts, float max_norm,
                               float* norm, int grid, cudaStream_t stream) {
-  grad_scale_kernel<<<grid, kClipThreads, 0, stream>>>(tab, part, parts, max_norm, norm);
-  return cudaGetLastError();
+  return launch_after(grad_scale_kernel, dim3(static_cast<unsigned>(grid)), dim3(kClipThreads), 0, stream,
+                      tab, part, parts, max_norm, norm);
 }
 
 }  // namespace flce

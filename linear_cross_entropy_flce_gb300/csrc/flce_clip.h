@@ -18,6 +18,7 @@ struct ClipTable {
   uint8_t bf16[kTableTensors];
   int count;
   int pieces;                      // of all tensors of the table
+  float density;                   // count / pieces
 };
 
 int clip_piece_bytes();

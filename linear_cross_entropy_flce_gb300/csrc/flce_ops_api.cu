@@ -536,6 +536,7 @@ int flce_clip_grads(const void* const* grads, void* const* outs, const int64_t* 
       pieces += n;
     }
     t->pieces = static_cast<int>(pieces);
+    t->density = static_cast<float>(t->count) / static_cast<float>(std::max<int64_t>(pieces, 1));
     return t->count > 0;
   };
 
