@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kClipThreads, 4)
 }
 
 __global__ void __launch_bounds__(kClipThreads, 4)
-    grad_scale_kernel(const __grid_constant__ ClipTable tab, const double* __restrict__ part,
+    grad_scale_kernel(const __grid_constant__ ClipTable tab, const double* part,
                       int parts, float max_norm, float* norm_out) {
   __shared__ float s_norm;
   wait_for_launch_before();   // the partials, and the last reads of what may be overwritten

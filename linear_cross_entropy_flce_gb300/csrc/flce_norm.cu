@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "flce_internal.h"
+#include "flce_launch.cuh"
 #include "flce_norm.cuh"
 #include "flce_norm_stream.h"
 
@@ -122,18 +123,20 @@ __global__ void __launch_bounds__(kColumnThreads)
   part[(static_cast<int64_t>(range) * 2 + 1) * D + i] = db;
 }
 
-// Adds up the partials: 32 columns of dweight and dbias per block, eight warps each
-// taking every eighth partial, in a fixed order.
-constexpr int kJoinWarps = 8;
+// Adds up the partials: 32 columns of dweight and dbias per block, sixteen warps each
+// taking every sixteenth partial, in a fixed order. (part is not __restrict__: its loads stay
+// behind the wait for the launch that writes it.)
+constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    layer_norm_join_kernel(const float* __restrict__ part, int ranges, int D, void* dweight,
+    layer_norm_join_kernel(const float* part, int ranges, int D, void* dweight,
                            void* dbias, int wbf16) {
   __shared__ float2 s_sum[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   float2 s = make_float2(0.f, 0.f);
+  wait_for_launch_before();
   if (i < D) {
-#pragma unroll 4
+#pragma unroll 10
     for (int r = warp; r < ranges; r += kJoinWarps) {
       s.x += part[static_cast<int64_t>(r) * 2 * D + i];
       s.y += part[static_cast<int64_t>(r) * 2 * D + D + i];
@@ -244,6 +247,7 @@ __global__ void __launch_bounds__(512, kNv * VW <= 8 && VW > 1 ? 2 : 1)
   using Raw = typename P::Raw;
   __shared__ float2 s_slots[2][16];
   extern __shared__ float s_cols[];   // [groups][2 * D] when several groups share a block
+  start_next_launch();
   const int groups = blockDim.x / R;
   const int group = threadIdx.x / R, t = threadIdx.x % R;
   const int nvec = D / VW;
@@ -409,9 +413,8 @@ cudaError_t norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
 
 cudaError_t join_columns(const float* part, int ranges, int D, void* dweight, void* dbias,
                          int wbf16, cudaStream_t stream) {
-  layer_norm_join_kernel<<<(D + 31) / 32, 32 * kJoinWarps, 0, stream>>>(part, ranges, D, dweight,
-                                                                        dbias, wbf16);
-  return cudaGetLastError();
+  return launch_after(layer_norm_join_kernel, dim3(static_cast<unsigned>((D + 31) / 32)),
+                      dim3(32 * kJoinWarps), 0, stream, part, ranges, D, dweight, dbias, wbf16);
 }
 
 }  // namespace

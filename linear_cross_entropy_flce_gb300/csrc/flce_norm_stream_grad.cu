@@ -8,11 +8,14 @@
 //
 // One row of a turn, as the accumulators leave no registers for a second. With the join of
 // the partials 8192 x 4096 bf16 takes 42.5 us (4.7 TB/s), 16384 x 8192 148 us (5.5 TB/s), 4000
-// x 4096 fp32 38.4 us (5.1 TB/s); the rows' loads in registers instead of the ring 55, 175, 46.
+// x 4096 fp32 38.4 us (5.1 TB/s), 2000 x 8000 39.6 us; the rows' loads in registers instead of
+// the ring 55, 175, 46, 50. Bound by its instructions (23 per element, 12 warps per SM): reading
+// the slot again for dx, to hold less and run 16 warps, took 53 us.
 // Ragged rows (loads in registers in brackets): 3001 x 1111 fp32 18.1 us (25.2), 16384 x 2730
 // bf16 77 (109), 16000 x 4001 bf16 102 (179).
 #include <cstdint>
 
+#include "flce_launch.cuh"
 #include "flce_norm_stream.cuh"
 #include "flce_norm_stream.h"
 
@@ -20,12 +23,13 @@ namespace flce {
 
 namespace {
 
-// 64 accumulators and 64 values of the row: 168 registers a thread.
-constexpr int kBackwardBlock = 384;
+// bf16: 64 accumulators and 64 values of the row, 168 registers a thread. fp32: half of both.
+constexpr int kMostBlock = 512;
+constexpr int backward_block(int bf16) { return bf16 ? 384 : kMostBlock; }
 constexpr int kRing = 3;   // turns of a group in the ring, of one row of x and dy each
 
 template <int kBf16, int kWbf16, int kRagged, int kNv>
-__global__ void __launch_bounds__(kBackwardBlock, 1)
+__global__ void __launch_bounds__(backward_block(kBf16), 1)
     norm_stream_grad_kernel(const void* dy, int64_t lddy, const void* x, int64_t ldx,
                             const void* weight, const float* __restrict__ mean_in,
                             const float* __restrict__ rstd_in, int N, int D, void* dx,
@@ -37,8 +41,9 @@ __global__ void __launch_bounds__(kBackwardBlock, 1)
   using Raw = typename P::Raw;
   using W = Param<kWbf16, VW>;
   extern __shared__ uint4 s_dyn[];
-  __shared__ __align__(8) uint64_t s_full[kBackwardBlock / 32][kRing];
-  __shared__ float2 s_sum[2][kBackwardBlock / 32];
+  __shared__ __align__(8) uint64_t s_full[kMostBlock / 32][kRing];
+  __shared__ float2 s_sum[2][kMostBlock / 32];
+  start_next_launch();   // the join's CTAs come as these go
   const int groups = static_cast<int>(blockDim.x) / R;
   const int group = threadIdx.x / R, t = threadIdx.x % R;
   const float inv_d = 1.f / static_cast<float>(D);
@@ -216,7 +221,7 @@ cudaError_t launch_norm_stream_backward(const void* dy, int64_t lddy, const void
   const size_t params =
       weight != nullptr ? static_cast<size_t>(slot / elt) * (wbf16 ? 2 : 4) : 0;
   const int most = sms / 8 * 8;
-  const StreamShape s = stream_shape(chunks, N, kBackwardBlock,
+  const StreamShape s = stream_shape(chunks, N, backward_block(bf16),
                                      static_cast<size_t>(slot) * (2 * kRing + (lay.apart ? 1 : 0)),
                                      params, most);
   // Streaming pays from 1.5 MB, or for long rows. bf16, streamed / by the kernel of rows in
