@@ -1229,9 +1229,9 @@ cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const
                                 cudaStream_t stream) {
   const uint8_t* zp = static_cast<const uint8_t*>(z);
   const int64_t row_bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
-  // Slices: rows of up to 20 KB whole in CTAs of 4 + 2 warps (four per SM), others in slices
-  // of at most 49 KB in CTAs of 8 + 2 warps (two per SM), or, when eight of those do not hold
-  // the row, 104 KB in CTAs of 16 + 2 (one).
+  // Slices: rows of up to 20 KB whole in CTAs of 4 warps for the passes (four per SM), others in
+  // slices of at most 49 KB in CTAs of 8 (two per SM), or, when eight of those do not hold the
+  // row, 104 KB in CTAs of 16 (one); and two more warps each, three with a ranking.
   constexpr int kWarpRow = 8 << 10, kSmall = 20 << 10, kTwo = 49 << 10, kOne = 104 << 10;
   auto cluster_for = [&](int64_t slice) {
     // whole 16-byte vectors per CTA: leave one vector for the rounding up

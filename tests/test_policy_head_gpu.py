@@ -73,3 +73,32 @@ def test_it_learns():
     _, _, _, rewards = policy_head.train(steps=60, tokens=1024, vocab=500, hidden=128)
     first, last = sum(rewards[:5]) / 5, sum(rewards[-5:]) / 5
     assert last > first
+
+
+def test_a_captured_step_repeats_the_eager_one():
+    torch.manual_seed(5)
+    N, D, V = 300, 128, 777
+    head = policy_head.PolicyHead(D, V)
+    x = torch.randn(N, D, device="cuda:0").bfloat16()
+    tokens = torch.randint(0, V, (N,), device="cuda:0").int()
+    sampled = head.score(x, tokens).logprob
+    advantage = torch.randn(N, device="cuda:0")
+    start = {n: t.detach().clone() for n, t in head.named_parameters()}
+    want = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):   # no eager graph of the leaves is left when the capture begins
+        for _ in range(3):
+            loss, norm = policy_head.policy_step(head, x, tokens, sampled, advantage, max_norm=0.1)
+            want.append((float(loss), float(norm)))
+    torch.cuda.current_stream().wait_stream(side)
+    eager = {n: t.detach().clone() for n, t in head.named_parameters()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, norm = policy_head.policy_step(head, x, tokens, sampled, advantage, max_norm=0.1)
+    head.load_state_dict(start)
+    for k in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (float(loss), float(norm)) == want[k]
+    assert all(torch.equal(t.detach(), eager[n]) for n, t in head.named_parameters())
