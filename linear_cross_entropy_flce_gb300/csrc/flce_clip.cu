@@ -9,6 +9,10 @@
 // Squares are summed in fp32 within a piece and thread (32 at most) and joined in fp64 in
 // a fixed order, one partial per CTA and launch. Each CTA of the scaling launch adds up
 // the partials itself: the same sum in the same order, with no third launch between.
+//
+// Bound by HBM: a read for the norm, then a read and a write. 1.8 GB of bf16 gradients in 49
+// tensors 828 us, 790 at the copy rate; 64 small fp32 tensors (1.5 MB) 10.3 us a call, of which
+// the host spends 10.
 #include <cmath>
 #include <cstdint>
 

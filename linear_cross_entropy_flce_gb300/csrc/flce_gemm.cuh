@@ -137,13 +137,15 @@ __device__ __forceinline__ void lse_chunk(const float (&v)[32], int col_local, i
 
 // A token's ranking within its vocabulary range. The thread that owns the row appends the
 // logits that beat its bound, the smallest of its top_k so far, to kBeat entries in shared
-// memory; when some row of the warp could not take another eight columns, every thread cuts
+// memory; when some row of the warp could not take another four columns, every thread cuts
 // its entries down to its top_k: a sorting network over their values gives the top_k-th, and
 // one pass keeps what reaches it. All 32 rows of the warp do that at once, about 1000
 // instructions for the warp, ln(range / top_k) or so times per range and token.
 // Measured at 8192 x 4096 x 128256 with 20 alternatives (4.75 ms without any): inserting
 // each candidate into a sorted list by its own thread 37.4 ms, joining buffers and lists row
-// by row with a key per lane 7.6 ms, this 5.3 ms (5.0 ms with 5).
+// by row with a key per lane 7.6 ms, this 5.3 ms (5.0 ms with 5). Looking every four columns
+// leaves five entries of room with 32 alternatives: 2048 tokens 1.55 ms (1.12 with 5); every
+// eight, one entry, 4.99 ms; every two, 1.48 but 1% more with 16 or fewer.
 //
 // An entry is the logit and its column within the range (16 bits: the ranges are planned to
 // have at most 65536 columns), entry e of the CTA's 128 rows contiguous, so that the threads
@@ -775,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int first = col - n_begin * Cfg::kTileN;
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
-                if (k % 8 == 0 && __any_sync(0xffffffffu, ranking.count > kBeat - 8)) {
+                if (k % 4 == 0 && __any_sync(0xffffffffu, ranking.count > kBeat - 4)) {
                   const RankCut cut = rank_cut(rank_values, rank_columns, ranking.count, p.top_k);
                   if (row_ok) ranking = cut;
                 }

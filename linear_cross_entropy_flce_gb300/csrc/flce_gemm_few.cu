@@ -14,6 +14,9 @@
 // reads one of the copies.
 //
 // Z goes to the workspace (N rows; it stays in L2) for the row kernel to read.
+//
+// Bound by the reads of W: D = 4096, V = 128256 (1.05 GB, 155 us at the copy rate) takes 166 us
+// with the row kernel for 1 token, 173 for 64, 192 for 128.
 #include <cstdint>
 
 #include "flce_gemm_few.h"

@@ -1,5 +1,6 @@
 // Per-token work around the log-probability GEMMs: joining the vocabulary ranges'
-// partial sums and rankings into the outputs, and the gradient's row coefficients.
+// partial sums and rankings into the outputs, and the gradient's row coefficients. A few
+// microseconds beside products of 190 us and more.
 #include <cstdint>
 
 #include "flce_internal.h"
@@ -45,9 +46,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
   uint64_t list = 0;
   if (top_k > 0) {
-    for (int s = first; s < splits; s += kStep) {
-      const uint64_t k = warp_sort_desc(lane < top_k ? lists[slot(s) * top_k + lane] : 0, lane);
-      list = s == first ? k : warp_merge_desc(list, k, lane);
+    // 32 keys at a time, of as many ranges as they are
+    for (int b = first * 32; b < splits * top_k; b += 32 * kStep) {
+      const int s = (b + lane) / top_k, j = b + lane - s * top_k;
+      const uint64_t k = warp_sort_desc(s < splits ? lists[slot(s) * top_k + j] : 0, lane);
+      list = b == first * 32 ? k : warp_merge_desc(list, k, lane);
     }
   }
   if (kWide) {
@@ -118,8 +121,11 @@ cudaError_t launch_logprob_merge(const float4* part, const float* zt, const uint
                                                 top_lp, top_id, status);
     return cudaGetLastError();
   };
-  return splits > kMergeWarps ? go(logprob_merge_kernel<1>, N)
-                              : go(logprob_merge_kernel<0>, (N + kMergeWarps - 1) / kMergeWarps);
+  // Many ranges come with few tokens. D = 4096, V = 128256, 20 alternatives, the call with a block
+  // / a warp per token: 129 tokens (76 ranges) 210 / 241 us, 768 (25) 538 / 571, 2048 (9) 1277 / 1259.
+  return splits > 2 * kMergeWarps
+             ? go(logprob_merge_kernel<1>, N)
+             : go(logprob_merge_kernel<0>, (N + kMergeWarps - 1) / kMergeWarps);
 }
 
 cudaError_t launch_logprob_coef(const int32_t* tokens, int N, int V, int ignore_index, float inv_t,

@@ -17,10 +17,15 @@
 //       threshold while the sums are taken; one joins the parts of
 //       the rows that are this CTA's (each row's meet in another CTA of the cluster), so
 //       that none of it holds the passes up.
-//   logprob_warp_kernel : rows of up to 8 KB, one warp each.
+//       8192 x 128256 bf16 (2.1 GB, 309 us at the copy rate): 370 us (5.7 TB/s), with 5 alternatives
+//       494, with 20 585; 4096 x 128256 fp32 295, 355, 381. Bound by the exponentials and maxima
+//       beside the reads (two packed instructions for each pair of logits and pass), and with
+//       alternatives by the second look at the threads whose maximum reaches the threshold.
+//   logprob_warp_kernel : rows of up to 8 KB, one warp each: 16384 x 2000 bf16 17.4 us (3.8 TB/s).
 //   logprob_rows_kernel : longer rows; one CTA each, read twice from global memory.
 //
-// Backward, elementwise: every entry of dZ from its logit and five numbers of its row.
+// Backward, elementwise: every entry of dZ from its logit and five numbers of its row. Bound by
+// HBM: 8192 x 128256 bf16 662 us (6.3 TB/s), 4096 x 128256 fp32 592 us (7.1 TB/s).
 //
 // Rows may start at any element: the elements before the first 16-byte boundary and
 // after the last one are read singly.
@@ -1231,7 +1236,13 @@ cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const
   const int64_t row_bytes = static_cast<int64_t>(V) * (bf16 ? 2 : 4);
   // Slices: rows of up to 20 KB whole in CTAs of 4 warps for the passes (four per SM), others in
   // slices of at most 49 KB in CTAs of 8 (two per SM), or, when eight of those do not hold the
-  // row, 104 KB in CTAs of 16 (one); and two more warps each, three with a ranking.
+  // row, 104 KB in CTAs of 16 (one); and two more warps each, three with a ranking. In us without
+  // and with 5 alternatives, the kernel taken / the next one up:
+  //   a warp per row to 8 KB : 16384 x 2000 bf16 17.4, 26.0 / 37.0, 55.0; 8192 x 4000 19.8, 29.4 /
+  //                            23.7, 31.9
+  //   20 KB, four per SM     : 4096 x 8000 bf16 18.6, 23.5 / 21.6, 31.6
+  //   49 KB, two per SM      : 8192 x 128256 bf16 370, 494 / 390, 502; 4096 x 20000 35, 44 / 45, 69
+  //   104 KB, one per SM     : 512 x 180000 fp32 72, 91 / 125, 128 (rows read twice)
   constexpr int kWarpRow = 8 << 10, kSmall = 20 << 10, kTwo = 49 << 10, kOne = 104 << 10;
   auto cluster_for = [&](int64_t slice) {
     // whole 16-byte vectors per CTA: leave one vector for the rounding up
@@ -1254,15 +1265,17 @@ cudaError_t launch_logprob_rows(int bf16, const void* z, int64_t ld_bytes, const
           cluster, N, sms, zp, ld_bytes, tokens, V, ignore_index, top_k, inv_t, logprob, entropy,
           lse, top_lp, top_id, status, timeout_ns, stream);
     };
-    // few rows: more CTAs for each, down to 8 KB, until every SM has one
-    int spread = sms / N;
+    int cl = cluster_for(kSmall);
+    if (cl <= 1)
+      return run(integral_constant<int, 4>{}, integral_constant<int, kSmall>{}, integral_constant<int, 4>{}, 1);
+    cl = cluster_for(kTwo);
+    // few rows of several CTAs: more for each, down to 8 KB, until half of the SMs have one. One
+    // row of 128256 fp32 logits 5.6 us on 8 CTAs, 6.5 on 6; 16 rows of bf16 6.2 on 8, 5.9 on 6;
+    // one row of 24 KB 4.7 on 3 against 3.7 on one.
+    int spread = cl > 1 ? sms / (2 * N) : 1;
     const int most = static_cast<int>((row_bytes + (8 << 10) - 1) / (8 << 10));
     spread = spread < most ? spread : most;
     spread = spread < kMaxRowCluster ? spread : kMaxRowCluster;
-    int cl = cluster_for(kSmall);
-    if (cl <= 1 && spread <= 1)
-      return run(integral_constant<int, 4>{}, integral_constant<int, kSmall>{}, integral_constant<int, 4>{}, 1);
-    cl = cluster_for(kTwo);
     if (cl <= kMaxRowCluster)
       return run(integral_constant<int, 8>{}, integral_constant<int, kTwo>{}, integral_constant<int, 2>{},
                  cl > spread ? cl : spread);

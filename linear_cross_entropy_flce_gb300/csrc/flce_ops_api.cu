@@ -53,7 +53,9 @@ int check_rows(int64_t N, int64_t V) {
 constexpr int kPlanPairs = 76;
 
 // Up to this many tokens the forward pass takes the logits of all of them (the kernel for few
-// tokens) and then their rows; above it the large GEMM, which does not store them.
+// tokens) and then their rows; above it the large GEMM, which does not store them. D = 4096, V =
+// 128256, with 5 alternatives: 1 token 167 us / 961 by the GEMM, 64 176 / 205, 128 197 / 206 (without
+// alternatives 192 / 190), 129 207.
 constexpr int64_t kFewTokens = 128;
 
 struct LogpPlan {
