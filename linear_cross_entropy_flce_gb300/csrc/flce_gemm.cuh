@@ -141,11 +141,11 @@ __device__ __forceinline__ void lse_chunk(const float (&v)[32], int col_local, i
 // its entries down to its top_k: a sorting network over their values gives the top_k-th, and
 // one pass keeps what reaches it. All 32 rows of the warp do that at once, about 1000
 // instructions for the warp, ln(range / top_k) or so times per range and token.
-// Measured at 8192 x 4096 x 128256 with 20 alternatives (4.75 ms without any): inserting
-// each candidate into a sorted list by its own thread 37.4 ms, joining buffers and lists row
-// by row with a key per lane 7.6 ms, this 5.3 ms (5.0 ms with 5). Looking every four columns
-// leaves five entries of room with 32 alternatives: 2048 tokens 1.55 ms (1.12 with 5); every
-// eight, one entry, 4.99 ms; every two, 1.48 but 1% more with 16 or fewer.
+// Measured at 8192 x 4096 x 128256 (4.28 ms without alternatives) with 5, 20 and 32: 4.33, 4.46,
+// 4.77 ms; with a bound per range alone, below, 4.37, 4.72, 10.0. Earlier, against 4.75 ms without,
+// with 20: inserting each candidate into a sorted list by its own thread 37.4 ms, joining buffers
+// and lists row by row with a key per lane 7.6. Looking every eight columns leaves one entry of
+// room with 32: 2048 tokens 4.99 ms against 1.55; every two took 1% more with 16 or fewer.
 //
 // An entry is the logit and its column within the range (16 bits: the ranges are planned to
 // have at most 65536 columns), entry e of the CTA's 128 rows contiguous, so that the threads
@@ -188,6 +188,20 @@ struct RankCut {
   float bound;
   int count;
 };
+
+// A token's ranges, in whatever order they run, tell each other their bounds: the top_k-th of
+// some of the row is no more than that of the whole, so logits below it need not be kept.
+// Those equal to it must, as they may have lower ids: the bound taken over is a little less.
+// (Which entries are kept on the way depends on the order, the top_k of them all do not.)
+__device__ __forceinline__ float just_below(uint32_t bits) {
+  const float v = bits == 0 ? -INFINITY : ordered_value(bits);
+  return fabsf(v) < INFINITY ? v - (fabsf(v) * 2.4e-7f + 1e-37f) : -INFINITY;
+}
+__device__ __forceinline__ uint32_t ld_relaxed_u32(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // Cuts a row's entries down to the top_k largest, in the order they came (ascending ids);
 // the new bound is the smallest of them. `values` and `columns` are the shared-memory
@@ -710,6 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage0 + Cfg::kRingBytes + kBeat * BM * 4u + static_cast<uint32_t>(row) * 2u;
       // -inf until there are top_k entries, +inf for a row that does not exist
       RankCut ranking{row_ok ? -INFINITY : INFINITY, 0};
+      uint32_t* const bound_at = p.bounds + prow;
+      uint32_t shared_bound = 0;
+      if (kEpi == EPI_LOGP_TOP && row_ok) shared_bound = ld_relaxed_u32(bound_at);
       // Rows past the product: log p = -3e38, so p and G are 0.
       float4 k4 = make_float4(3.0e38f, 0.f, 0.f, 0.f);
       float target = 0.f;
@@ -755,6 +772,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t taddr = tmem_base + lane_addr + static_cast<uint32_t>(acc * Cfg::kTileN);
+        if constexpr (kEpi == EPI_LOGP_TOP) {
+          if (row_ok) {   // what the tile before asked for
+            ranking.bound = fmaxf(ranking.bound, just_below(shared_bound));
+            shared_bound = ld_relaxed_u32(bound_at);
+          }
+        }
 #pragma unroll 1
         for (int c = 0; c < Cfg::kTileN / 32; ++c) {
           uint32_t r[32];
@@ -779,7 +802,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 32; ++k) {
                 if (k % 4 == 0 && __any_sync(0xffffffffu, ranking.count > kBeat - 4)) {
                   const RankCut cut = rank_cut(rank_values, rank_columns, ranking.count, p.top_k);
-                  if (row_ok) ranking = cut;
+                  if (row_ok) {
+                    ranking.count = cut.count;
+                    ranking.bound = fmaxf(ranking.bound, cut.bound);
+                    if (cut.bound > -INFINITY) atomicMax(bound_at, ordered_bits(cut.bound));
+                  }
                 }
                 if (v[k] > ranking.bound && k < left) {
                   st_shared_f32(rank_values + ranking.count * (BM * 4), v[k]);
@@ -848,7 +875,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part4[slot] = make_float4(lst.p.m, lst.p.s, lst.p.t, 0.f);
           if (row_ok && lst.found) p.zt[p.row_base + prow] = lst.zt;
           if constexpr (kEpi == EPI_LOGP_TOP) {   // in no order: the join sorts them
-            const int n = rank_cut(rank_values, rank_columns, ranking.count, p.top_k).count;
+            const RankCut cut = rank_cut(rank_values, rank_columns, ranking.count, p.top_k);
+            if (row_ok && cut.bound > -INFINITY) atomicMax(bound_at, ordered_bits(cut.bound));
+            const int n = cut.count;
             const int id0 = p.col_base + n_begin * Cfg::kTileN;
             for (int j = 0; j < p.top_k; ++j)
               p.lists[slot * p.top_k + j] =

@@ -145,6 +145,8 @@ struct GemmParams {
   // ranking of the range, [splits][part_stride][BM][top_k] keys in no order, 0 for none
   float4* part4;
   uint64_t* lists;
+  uint32_t* bounds;   // per token, shared by its ranges: ordered_bits of a lower bound of the
+                      // ranking's last entry, 0 for none (EPI_LOGP_TOP)
   // EPI_LOGP_GRAD: per token (lse, A, B, entropy) with G = p (A - B (log p + entropy)),
   // and the entry at the token
   const float4* coef;

@@ -63,7 +63,7 @@ struct LogpPlan {
   bool few = false;
   int64_t ldz = 0;
   size_t off_pad = 0, off_z = 0;
-  size_t off_part = 0, off_zt = 0, off_lists = 0, off_coef = 0, off_target = 0, total = 0;
+  size_t off_part = 0, off_zt = 0, off_lists = 0, off_bounds = 0, off_coef = 0, off_target = 0, total = 0;
 };
 
 int make_logp_plan(int64_t N, int64_t D, int64_t V, const flce_logprob_options& o, bool backward,
@@ -107,6 +107,7 @@ int make_logp_plan(int64_t N, int64_t D, int64_t V, const flce_logprob_options& 
     L.off_part = take(slots * 16);
     L.off_zt = take(static_cast<size_t>(N) * 4);
     L.off_lists = take(slots * static_cast<size_t>(o.top_k) * 8);
+    L.off_bounds = take(o.top_k > 0 ? static_cast<size_t>(N) * 4 : 0);
   }
   L.total = off;
   *out = L;
@@ -319,6 +320,10 @@ int flce_linear_token_logprobs(const uint16_t* H, const uint16_t* W, const int32
   g.part4 = reinterpret_cast<float4*>(ws + L.off_part);
   g.zt = reinterpret_cast<float*>(ws + L.off_zt);
   g.lists = reinterpret_cast<uint64_t*>(ws + L.off_lists);
+  g.bounds = reinterpret_cast<uint32_t*>(ws + L.off_bounds);
+  if (o.top_k > 0 &&
+      cudaMemsetAsync(g.bounds, 0, static_cast<size_t>(N) * 4, st) != cudaSuccess)
+    return FLCE_ERR_CUDA;
   const int pairs = std::max(1, sms / cta);
   if (launch_gemm_logp(mH, mW, g, cta * std::min(g.num_units, pairs), st) != cudaSuccess)
     return FLCE_ERR_CUDA;

@@ -18,15 +18,21 @@ namespace flce {
 
 constexpr int kMaxTopK = 32;
 
-__device__ __forceinline__ uint64_t rank_key(float v, int id) {
+// Bits that order as the values do.
+__device__ __forceinline__ uint32_t ordered_bits(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);   // -0 ranks as +0
-  const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float ordered_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+
+__device__ __forceinline__ uint64_t rank_key(float v, int id) {
+  return (static_cast<uint64_t>(ordered_bits(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(id));
 }
 
 __device__ __forceinline__ float key_value(uint64_t k) {
-  const uint32_t o = static_cast<uint32_t>(k >> 32);
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+  return ordered_value(static_cast<uint32_t>(k >> 32));
 }
 
 __device__ __forceinline__ int key_id(uint64_t k) {

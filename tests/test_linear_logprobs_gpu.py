@@ -220,3 +220,22 @@ def test_autograd():
     (lp.sum() + 0.1 * ent.sum()).backward()
     _check_grads(H, W, y, (np.ones(24), np.full(24, np.float32(0.1)), None), 1.0,
                  Hd.grad.view(24, 128), Wd.grad)
+
+
+@pytest.mark.parametrize("top_k", [1, 7, 32])
+@pytest.mark.parametrize("N,V,high", [(300, 20000, 2), (700, 9000, 3), (129, 50000, 1), (2500, 70000, 2)])
+def test_equal_logits_of_many_tokens_rank_by_id(N, V, high, top_k):
+    # whole-number products, exact in fp32: rows full of ties, over and around 0
+    g = np.random.Generator(np.random.Philox(np.random.SeedSequence([N + V, 64])))
+    H = g.integers(-high, high + 1, (N, 16)).astype(np.float64)
+    W = g.integers(-high, high + 1, (V, 16)).astype(np.float64)
+    H[5] = 0.0
+    H[6] = np.abs(H[6]) * -40
+    W[V // 2:] = W[:V - V // 2]   # every logit comes twice
+    Z = H @ W.T
+    order = np.argsort(-Z, axis=1, kind="stable")[:, :top_k]
+    runs = []
+    for _ in range(3):
+        r = flce.linear_token_logprobs(_dev(H), _dev(W), None, top_k=top_k)
+        runs.append(r.top_id.cpu().numpy())
+        assert np.array_equal(runs[-1], order)
