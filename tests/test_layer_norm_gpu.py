@@ -141,6 +141,28 @@ def test_many_rows_in_place_and_in_parts(dtype, D, pad, shift):
     _run(x, dy, None, b, dtype, "bf16", pad=pad, shift=shift)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,xpad,gpad", [(1000, 3, 0), (1024, 0, 5), (1111, 1, 0), (2048, 8, 16)])
+def test_rows_and_upstream_gradients_in_different_strides(dtype, D, xpad, gpad):
+    N = 1501
+    x, dy, w, b = _draw(N, D, D + xpad)
+    wt = _put(w, "f32")[0]
+    same = _put(x, dtype)[0], _put(dy, dtype)[0]
+    want = flce.layer_norm_backward(same[1], same[0], wt, flce.layer_norm(same[0], wt))
+    xt, gt = _put(x, dtype, xpad)[0], _put(dy, dtype, gpad)[0]
+    r = flce.layer_norm(xt, wt)
+    assert r.y.is_contiguous()
+    got = flce.layer_norm_backward(gt, xt, wt, r)
+    # the same values in another order of sums: by twice their bound of test_shapes_and_types
+    e = U * (D / 64 + 24)
+    scale = [float(t.double().abs().max()) for t in want]
+    n = U * (N / 16 + 400)
+    for k, (g, t) in enumerate(zip(got, want)):
+        bound = 2 * (8 * e if k == 0 else n * float(np.abs(dy).sum(0).max()) * 8 / max(scale[k], 1e-30)) * scale[k]
+        bound += 2 * half_step(t.dtype) * scale[k]
+        assert float((g.double() - t.double()).abs().max()) <= bound, k
+
+
 @pytest.mark.parametrize("with_w,with_b", [(True, False), (False, True), (False, False)])
 def test_without_weight_or_bias(with_w, with_b):
     x, dy, w, b = _draw(50, 320, 3)
