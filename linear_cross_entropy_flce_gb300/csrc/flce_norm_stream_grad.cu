@@ -7,7 +7,7 @@
 // groups' sums meet in shared memory at the end, one partial per CTA.
 //
 // One row of a turn, as the accumulators leave no registers for a second. With the join of
-// the partials 8192 x 4096 bf16 takes 42.5 us (4.7 TB/s), 16384 x 8192 148 us (5.5 TB/s), 4000
+// the partials (4 us, and their writing 2) 8192 x 4096 bf16 takes 40.8 us (4.9 TB/s), 16384 x 8192 148 us (5.5 TB/s), 4000
 // x 4096 fp32 38.4 us (5.1 TB/s), 2000 x 8000 39.6 us; the rows' loads in registers instead of
 // the ring 55, 175, 46, 50. Bound by its instructions (23 per element, 12 warps per SM): reading
 // the slot again for dx, to hold less and run 16 warps, took 53 us.
@@ -192,6 +192,19 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
       }
     }
   __syncthreads();
+  if (!kRagged && gridDim.x > 1) {   // four columns at a time
+#pragma unroll 4
+    for (int i = 4 * threadIdx.x; i < 2 * D; i += 4 * blockDim.x) {
+      float4 s = *reinterpret_cast<const float4*>(cols + i);
+      for (int q = 1; q < groups; ++q) {
+        const float4 o = *reinterpret_cast<const float4*>(cols + q * 2 * D + i);
+        s = make_float4(s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w);
+      }
+      *reinterpret_cast<float4*>(part + static_cast<int64_t>(blockIdx.x) * 2 * D + i) = s;
+    }
+    return;
+  }
+#pragma unroll 4
   for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
     const int j = place.s + (i < D ? i : i - D + width);
     float s = cols[j];
