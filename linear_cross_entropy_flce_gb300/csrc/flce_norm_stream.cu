@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
     float nan = 0.f;   // a copy that never came makes its row NaN
     if (!mbar_wait_bounded(smem_u32(&s_full[group][slot]), phase, limit, &never)) {
       nan = __uint_as_float(0x7FC00000u);
+      if (t == 0 && limit != 0) drain_ring(s_full[group], kRing, slot, phase, row, step, N);
       limit = 0;
     }
     const uint8_t* in = ring + slot * 2 * slot_bytes;
@@ -125,10 +126,10 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
       }
       part[r] = sum_n(acc);
     }
-    const float2 sum = stream_sum2(make_float2(part[0], part[1]), group, R, s_sum);
-    const float mean[2] = {sum.x * inv_d + nan, sum.y * inv_d + nan};
+    const float2 sum = stream_sum2(make_float2(part[0] + nan, part[1] + nan), group, R, s_sum);
+    const float mean[2] = {sum.x * inv_d, sum.y * inv_d};
     if (R == 32) __syncwarp();
-    if (t < kFetchers) {   // everyone has read the slot; those reads come before the copies' writes
+    if (t < kFetchers && limit != 0) {   // everyone has read the slot; those reads come before the copies' writes
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       fetch(row + kRing * step, slot, single[0]);
     }

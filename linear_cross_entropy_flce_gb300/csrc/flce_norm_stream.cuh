@@ -146,6 +146,18 @@ struct RowPlace {
   }
 };
 
+// After a copy that did not come in time: waits, again with a limit, for those of a group's
+// ring (turns `turn_row`, `turn_row` + step, ... from `slot` on), so that none is in flight
+// when the memory is given back. No further one is started.
+static __device__ __noinline__ void drain_ring(uint64_t* full, int ring, int slot, uint32_t phase,
+                                        int64_t turn_row, int64_t step, int N) {
+  const volatile int never = 0;
+  for (int d = 0; d < ring && turn_row + d * step < N; ++d) {
+    const int at = slot + d;
+    mbar_wait_bounded(smem_u32(full + at % ring), phase ^ (at >= ring ? 1u : 0u), 1000000000ull, &never);
+  }
+}
+
 // weight and bias (either may be null) to shared memory, in the places of the rows' chunks
 // (zeros beside the row)
 template <int kWbf16, int VW, bool kRagged>

@@ -6,11 +6,11 @@
 // formed from the same copy of the row, so x and dy are read once for all three. The
 // groups' sums meet in shared memory at the end, one partial per CTA.
 //
-// One row of a turn, as the accumulators leave no registers for a second. With the join of
-// the partials (4 us, and their writing 2) 8192 x 4096 bf16 takes 40.8 us (4.9 TB/s), 16384 x 8192 148 us (5.5 TB/s), 4000
-// x 4096 fp32 38.4 us (5.1 TB/s), 2000 x 8000 39.6 us; the rows' loads in registers instead of
-// the ring 55, 175, 46, 50. Bound by its instructions (23 per element, 12 warps per SM): reading
-// the slot again for dx, to hold less and run 16 warps, took 53 us.
+// One row of a turn, as the accumulators leave no registers for a second. 8192 x 4096 bf16 takes
+// 40.8 us (4.9 TB/s) with the partials (their join 4, their writing 2), 16384 x 8192 148 us (5.5
+// TB/s), 4000 x 4096 fp32 38.4 us (5.1 TB/s), 2000 x 8000 39.6 us; the rows' loads in registers
+// instead of the ring 55, 175, 46, 50. Bound by its instructions (23 per element, 12 warps per
+// SM): reading the slot again for dx, to hold less and run 16 warps, took 53 us.
 // Ragged rows (loads in registers in brackets): 3001 x 1111 fp32 18.1 us (25.2), 16384 x 2730
 // bf16 77 (109), 16000 x 4001 bf16 102 (179).
 #include <cstdint>
@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
     // a copy that never came makes its row, and the sums, NaN
     if (!mbar_wait_bounded(smem_u32(&s_full[group][slot]), phase, limit, &never)) {
       rstd = __uint_as_float(0x7FC00000u);
+      if (t == 0 && limit != 0) drain_ring(s_full[group], kRing, slot, phase, row, step, N);
       limit = 0;
     }
     const uint8_t* in_x = ring + slot * 2 * slot_bytes;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
     const float2 sum =
         stream_sum2(make_float2(sum_n(s0), sum_n(s1)), group, R, s_sum[turn & 1]);
     if (R == 32) __syncwarp();
-    if (t < kFetchers) {   // everyone has read the slot; those reads come before the copies' writes
+    if (t < kFetchers && limit != 0) {   // everyone has read the slot; those reads come before the copies' writes
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       fetch(row + kRing * step, slot, single[0]);
     }
