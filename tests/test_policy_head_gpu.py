@@ -25,7 +25,7 @@ def _plain(head, x, tokens, sampled, advantage, beta):
     entropy = -(lp.exp() * lp).sum(1)
     loss = -((logprob - sampled.double()).exp() * advantage.double()).mean() - beta * entropy.mean()
     loss.backward()
-    size = (h.abs() @ p["weight"].abs().T).max()
+    size = (h.detach().abs() @ p["weight"].detach().abs().T).max()
     return float(loss.detach()), {n: t.grad for n, t in p.items()}, float(size)
 
 
