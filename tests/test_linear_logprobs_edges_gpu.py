@@ -1,0 +1,73 @@
+"""Log probabilities from hidden states at the edges of their kernels. Bounds count roundings as
+in head_ops_testlib, u = 2^-24."""
+import math
+
+import numpy as np
+import pytest
+
+from head_ops_testlib import U
+from oracle import head_ops as ho
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import linear_cross_entropy_flce_gb300 as flce
+
+DEV = "cuda:0"
+
+
+@pytest.mark.parametrize("N", [5, 100, 200, 700])
+@pytest.mark.parametrize("top_k", [0, 6])
+def test_ids_masked_through_the_weight(N, top_k):
+    """The last hidden value is 1 and the weight's last column 0, or -inf for ids that cannot
+    come: logits of -inf, as over given logits. One row's ids are all masked."""
+    D, V = 64, 3001
+    g = np.random.Generator(np.random.Philox(np.random.SeedSequence([N, 68])))
+    H = np.clip(np.round(g.standard_normal((N, D)) * 32), -255, 255) / 32
+    W = np.clip(np.round(g.standard_normal((V, D)) * 300), -255, 255) / 2048
+    H[:, -1], W[:, -1] = 1.0, 0.0
+    dead = g.random(V) < 0.3
+    dead[:300] = True
+    dead[-40:] = True
+    y = g.integers(0, V, N).astype(np.int32)
+    y[:2] = 5                       # a masked token
+    Z = H @ W.T
+    Z[:, dead] = -np.inf
+    W[dead, -1] = -np.inf
+    Hd, Wd = torch.from_numpy(H).to(DEV).bfloat16(), torch.from_numpy(W).to(DEV).bfloat16()
+    yd = torch.from_numpy(y).to(DEV)
+    r = flce.linear_token_logprobs(Hd, Wd, yd, top_k=top_k)
+    ref = ho.token_logprobs(Z, y, top_k=top_k)
+    for name in ("logprob", "entropy", "lse"):
+        got, want = getattr(r, name).double().cpu().numpy(), ref[name]
+        inf = np.isinf(want)
+        assert np.array_equal(got[inf], want[inf]), name
+        assert np.all(np.abs(got[~inf] - want[~inf]) <= 4 * (2.0 ** -22 + U * 200) * 10), name
+    if top_k:
+        assert np.array_equal(r.top_id.cpu().numpy(), ref["top_id"])
+    a = g.standard_normal((3, N)).astype(np.float32)
+    up = [torch.from_numpy(t).to(DEV) for t in a]
+    dH, dW = flce.linear_token_logprobs_backward(Hd, Wd, yd, r, dlogprob=up[0], dentropy=up[1], dlse=up[2])
+    G = ho.token_logprobs_grad(Z, y, *a)
+    rho = 2.0 ** -8 + 1e-4
+    want, size = G.T @ H, np.abs(G).T @ np.abs(H)
+    assert np.all(np.abs(dW.double().cpu().numpy() - want) <= (rho + 2.0 ** -20) * size + 1e-30)
+    Wf = W[:, :-1]
+    want, size = G @ Wf, np.abs(G) @ np.abs(Wf)     # the last column meets -inf
+    got = dH.double().cpu().numpy()[:, :-1]
+    assert np.all(np.abs(got - want) <= (rho + 2.0 ** -20) * size + 2.0 ** -8 * np.abs(want) + 1e-30)
+
+
+def test_rows_whose_every_id_is_masked():
+    for N in (3, 150):
+        H = torch.zeros(N, 64, device=DEV)
+        H[:, -1] = 1.0
+        W = torch.zeros(1001, 64, device=DEV)
+        W[:, -1] = -math.inf
+        y = torch.arange(N, dtype=torch.int32, device=DEV)
+        y[0] = -100
+        r = flce.linear_token_logprobs(H.bfloat16(), W.bfloat16(), y, top_k=3)
+        assert bool((r.lse == -math.inf).all()) and torch.count_nonzero(r.entropy) == 0
+        assert bool((r.logprob[1:] == -math.inf).all()) and float(r.logprob[0]) == 0
+        assert bool((r.top_id == -1).all()) and bool((r.top_logprob == -math.inf).all())
