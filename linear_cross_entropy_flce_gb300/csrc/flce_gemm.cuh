@@ -336,7 +336,7 @@ __device__ __forceinline__ void logp_grad_chunk(const float (&v)[32], int col_lo
   if (static_cast<unsigned>(rel_target) < 32u) {
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-      if (k == rel_target) g[k] = target;
+      if (k == rel_target) g[k] = target_entry(target, v[k]);
   }
   if (col_local + 32 > n_valid) {
 #pragma unroll

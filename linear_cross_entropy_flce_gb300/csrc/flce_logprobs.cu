@@ -1187,7 +1187,7 @@ __global__ void __launch_bounds__(kGradThreads)
                                dentropy != nullptr ? dentropy[row] : 0.f,
                                dlse != nullptr ? dlse[row] : 0.f, yt >= 0, inv_t);
     auto entry = [&](float x, int id) {
-      if (id == yt) return k.target;
+      if (id == yt) return target_entry(k.target, x);
       const float lp = fmaxf(fmaf(x, inv_t, -k.lse), -1.0e4f);
       const float p = exp2_approx(lp * kLog2e);
       return p * fmaf(-k.B, lp + k.entropy, k.A);

@@ -150,9 +150,14 @@ __device__ __forceinline__ RowCoef row_coef(float lse, float entropy, float logp
     const float p = expf(lp);
     r.target = (-expm1f(lp) * a + p * (c - b * (lp + r.entropy))) * inv_t;
     if (logprob != logprob) r.target = logprob;
-    if (logprob == -INFINITY) r.target = 0.f;   // a -inf logit has no gradient
   }
   return r;
+}
+
+// The token's own entry, given its logit: none at -inf. (The log probability does not tell: that
+// of a token with the type's lowest value is -inf too, at temperatures below 1.)
+__device__ __forceinline__ float target_entry(float target, float z) {
+  return z == -INFINITY && target == target ? 0.f : target;
 }
 
 }  // namespace flce
