@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     top_id[at] = list == 0 ? -1 : key_id(list);
     top_lp[at] = r.lse != r.lse ? r.lse
                  : list == 0    ? -INFINITY
-                                : id_logprob(r, key_value(list), inv_t, c);
+                                : id_logprob(r, key_value(list), inv_t);
   }
 }
 

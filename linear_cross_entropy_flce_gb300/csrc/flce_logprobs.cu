@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kRowThreads)
           const int64_t at = static_cast<int64_t>(row) * top_k + lane;
           const bool none = list == 0;
           top_id[at] = none ? -1 : key_id(list);
-          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
+          top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t);
         }
       }
     }
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
     const int64_t at = static_cast<int64_t>(row) * top_k + lane;
     const bool none = list == 0;
     top_id[at] = none ? -1 : key_id(list);
-    top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
+    top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t);
   }
 }
 
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
       const int64_t at = static_cast<int64_t>(row) * top_k + lane;
       const bool none = list == 0;
       top_id[at] = none || late ? -1 : key_id(list);
-      top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t, c);
+      top_lp[at] = r.lse != r.lse ? r.lse : none ? -INFINITY : id_logprob(r, key_value(list), inv_t);
     }
   };
 

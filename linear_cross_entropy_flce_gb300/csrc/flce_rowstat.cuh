@@ -79,19 +79,21 @@ __device__ __forceinline__ void row_join(RowPart& a, const RowPart& b, float c) 
 
 struct RowOut {
   float logprob, entropy, lse;
-  float m, log_s;   // lse = r ln 2 + log_s (m / temperature + log_s without an r), for id_logprob
+  float m, log_s;   // lse = m / temperature + log_s, for id_logprob
 };
 
-// Log probability of an id from its raw logit: no difference with lse, in which log S
+// Log probability of an id from its raw logit: no difference with lse, in which log_s
 // drowns when the logits are far from 0. NaN in a row without a softmax.
-__device__ __forceinline__ float id_logprob(const RowOut& r, float z, float inv_t, float c) {
-  // (for a logit beyond the reference's range r against m c, half a unit, is below rounding)
-  return has_ref(r.m, c) && has_ref(z, c) ? fmaf(fmaf(z, c, -row_ref(r.m, c)), kLn2, -r.log_s)
-                                          : fmaf(z - r.m, inv_t, -r.log_s);
+__device__ __forceinline__ float id_logprob(const RowOut& r, float z, float inv_t) {
+  return fmaf(z - r.m, inv_t, -r.log_s);
 }
 
 // The row's outputs from its joined part (the token's term left out), the raw logit zt
 // of the token, and whether it has one. `inv_t` = 1 / temperature, c = log2(e) inv_t.
+//
+// Logarithms are of sums relative to the largest term e_m = 2^d_m, formed here as it was for the
+// sums: where the others are 0 the logarithm and the entropy are 0, not the difference of two
+// rounded numbers, log_s is never negative, and the largest id's log probability is the token's.
 __device__ __forceinline__ RowOut row_finish(const RowPart& p, float zt, bool has_token,
                                              float inv_t, float c) {
   RowOut o;
@@ -113,14 +115,18 @@ __device__ __forceinline__ RowOut row_finish(const RowPart& p, float zt, bool ha
     dt = row_exponent(zt, p.m, c);
     et = exp2_approx(dt);
   }
-  const float S = p.s + et, T = fmaf(et, dt, p.t);
-  const float log_s = logf(S);
-  o.log_s = log_s;
-  o.lse = has_ref(p.m, c) ? fmaf(row_ref(p.m, c), kLn2, log_s) : fmaf(p.m, inv_t, log_s);
-  const float h = fmaf(-kLn2, T / S, log_s);
+  const float dm = row_exponent(p.m, p.m, c), em = exp2_approx(dm);
+  // sums over the ids but the largest (the token, if it is that) of e and of e (d - d_m)
+  const bool top = has_token && zt == p.m;
+  const float s = top ? p.s : fmaxf(p.s + et - em, 0.f);
+  const float t = top ? fmaf(-dm, p.s, p.t)
+                      : fmaf(-dm, s, fmaf(et, dt, p.t) - __fmul_rn(em, dm));
+  o.log_s = log1pf(s / em);
+  o.lse = fmaf(p.m, inv_t, o.log_s);
+  const float h = fmaf(-kLn2, t / (s + em), o.log_s);
   o.entropy = h < 0.f ? 0.f : h;
   // e_t < 2^-60: x_y - lse has no cancellation, and the quotient could overflow
-  o.logprob = !has_token ? 0.f : (et >= 0x1p-60f ? -log1pf(p.s / et) : id_logprob(o, zt, inv_t, c));
+  o.logprob = !has_token ? 0.f : (et >= 0x1p-60f ? -log1pf(p.s / et) : id_logprob(o, zt, inv_t));
   return o;
 }
 

@@ -71,3 +71,25 @@ def test_rows_whose_every_id_is_masked():
         assert bool((r.lse == -math.inf).all()) and torch.count_nonzero(r.entropy) == 0
         assert bool((r.logprob[1:] == -math.inf).all()) and float(r.logprob[0]) == 0
         assert bool((r.top_id == -1).all()) and bool((r.top_logprob == -math.inf).all())
+
+
+@pytest.mark.parametrize("N", [7, 300])
+def test_rows_with_one_likely_id(N):
+    """A token far above the others: its log probability as an alternative is the token's, and
+    with the others below 2^-150 of it both are 0, and so is the entropy."""
+    D, V = 64, 5000
+    H = torch.zeros(N, D, device=DEV)
+    H[torch.arange(N), torch.arange(N) % 32] = 1.0
+    W = torch.zeros(V, D, device=DEV)
+    ids = torch.arange(32, device=DEV) * 150 + 3
+    W[ids, torch.arange(32, device=DEV)] = torch.arange(32, device=DEV) * 8.0 + 11.0
+    H, W = H.bfloat16(), W.bfloat16()
+    y = ids[torch.arange(N, device=DEV) % 32].int()
+    for tok in (y, None):
+        r = flce.linear_token_logprobs(H, W, tok, top_k=3, temperature=0.75)
+        far = (torch.arange(N, device=DEV) % 32) * 8 + 11 > 120
+        assert torch.equal(r.top_id[:, 0], y)
+        assert bool((r.top_logprob <= 0).all()) and torch.count_nonzero(r.top_logprob[far, 0]) == 0
+        assert torch.count_nonzero(r.entropy[far]) == 0
+        if tok is not None:
+            assert torch.equal(r.logprob, r.top_logprob[:, 0])

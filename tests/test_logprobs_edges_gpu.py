@@ -38,3 +38,32 @@ def test_gradient_at_a_token_with_the_types_lowest_logit(dtype, T):
     g = flce.token_logprobs_backward(z, y, r, dlogprob=a, dentropy=a, dlse=a, temperature=T)
     want = torch.tensor([0.75 / T, 0.0, 0.75 / T], device=DEV)
     assert float((g[:, 7].float() - want).abs().max()) <= 4 * U   # 0.75 / T is a number of each type
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5, 900, 6000, 50000, 240007])
+@pytest.mark.parametrize("T", [1.0, 0.7])
+def test_rows_with_one_likely_id(dtype, V, T):
+    """Where all but one id are masked its log probability is 0 and so is the entropy; where
+    the others are merely unlikely, the alternative's log probability is the token's."""
+    g = _rng(V)
+    top = g.integers(0, V, 40)
+    level = (g.standard_normal(40) * 30).astype(np.float32)
+    z = torch.full((40, V), -math.inf, device=DEV)
+    z[20:] = 0.0
+    z += torch.where(torch.isinf(z), 0.0, torch.from_numpy(level).to(DEV)[:, None])
+    gap = torch.from_numpy((1 + g.random(40) * 60).astype(np.float32)).to(DEV)
+    rows = torch.arange(40, device=DEV)
+    z[rows, torch.from_numpy(top).to(DEV)] = torch.from_numpy(level).to(DEV) + gap
+    z = z.to(TYPES[dtype])
+    tok = torch.from_numpy(top.astype(np.int32)).to(DEV)
+    for y in (tok, None):
+        r = flce.token_logprobs(z, y, top_k=2, temperature=T)
+        assert torch.equal(r.top_id[:, 0], tok)
+        assert torch.count_nonzero(r.entropy[:20]) == 0 and bool((r.entropy >= 0).all())
+        assert torch.count_nonzero(r.top_logprob[:20, 0]) == 0 and bool((r.top_logprob <= 0).all())
+        x = z[rows, tok.long()].double() / T
+        assert bool(((r.lse[:20].double() - x[:20]).abs() <= 3 * U * x[:20].abs()).all())
+        if y is not None:
+            assert torch.count_nonzero(r.logprob[:20]) == 0
+            assert torch.equal(r.logprob, r.top_logprob[:, 0])
