@@ -1165,7 +1165,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;   // vectors per thread
 
 template <int kBf16>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(kGradThreads, 6)
     logprob_grad_kernel(const uint8_t* z, int64_t ld_bytes,   // may alias g (in place)
                         const int32_t* __restrict__ tokens, int N, int V, int ignore_index,
                         float inv_t, const float* __restrict__ logprob,
@@ -1186,8 +1186,7 @@ __global__ void __launch_bounds__(kGradThreads)
                                dlogprob != nullptr ? dlogprob[row] : 0.f,
                                dentropy != nullptr ? dentropy[row] : 0.f,
                                dlse != nullptr ? dlse[row] : 0.f, yt >= 0, inv_t);
-    auto entry = [&](float x, int id) {
-      if (id == yt) return target_entry(k.target, x);
+    auto entry = [&](float x) {   // off the token
       const float lp = fmaxf(fmaf(x, inv_t, -k.lse), -1.0e4f);
       const float p = exp2_approx(lp * kLog2e);
       return p * fmaf(-k.B, lp + k.entropy, k.A);
@@ -1210,7 +1209,14 @@ __global__ void __launch_bounds__(kGradThreads)
         float x[E];
         L::widen(w[u], x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = entry(x[e], head + v * E + e);
+        for (int e = 0; e < E; ++e) x[e] = entry(x[e]);
+        const int at = yt - (head + v * E);
+        if (static_cast<unsigned>(at) < static_cast<unsigned>(E)) {   // the token's vector
+          const float target = target_entry(k.target, element_of<kBf16>(w[u], at));
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (e == at) x[e] = target;
+        }
         __stcs(reinterpret_cast<uint4*>(gv) + v, L::narrow(x));
       }
     }
@@ -1220,7 +1226,7 @@ __global__ void __launch_bounds__(kGradThreads)
     for (int i = blockIdx.x * kGradThreads + tid; i < singles; i += gridDim.x * kGradThreads) {
       const int id = i < head ? i : tail + i - head;
       const float x = L::load1(zr + static_cast<int64_t>(id) * L::kBytes);
-      L::store1(gr + static_cast<int64_t>(id) * L::kBytes, entry(x, id));
+      L::store1(gr + static_cast<int64_t>(id) * L::kBytes, id == yt ? target_entry(k.target, x) : entry(x));
     }
   }
 }
