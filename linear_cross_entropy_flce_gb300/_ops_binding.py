@@ -261,7 +261,7 @@ def token_logprobs_backward(logits, tokens, result, *, dlogprob=None, dentropy=N
     """Gradient in the logits of a token_logprobs call (`result`), from the upstream
     gradients of its logprob, entropy and lse (fp32 [N], None for 0), via
     flce_token_logprobs_backward. Returns dlogits, of the logits' dtype: `out`, or the
-    logits themselves (in_place), or a new tensor with the logits' row stride."""
+    logits themselves (in_place), or a new tensor, whose rows are at most 15 bytes apart."""
     if out is None and not in_place and stream is None:
         g = _fast.token_logprobs_backward(logits, tokens, result.logprob, result.entropy, result.lse,
                                           dlogprob, dentropy, dlse, temperature, ignore_index)
@@ -281,7 +281,9 @@ def token_logprobs_backward(logits, tokens, result, *, dlogprob=None, dentropy=N
                 raise ValueError("out must match the logits' device, dtype and shape")
             grad = out
         else:
-            grad = torch.empty_strided((N, V), (ld, 1), dtype=logits.dtype, device=dev)
+            # rows that start relative to 16 bytes as the logits' do, however far apart those are
+            vec = 16 // logits.element_size()
+            grad = torch.empty_strided((N, V), (V + (ld - V) % vec, 1), dtype=logits.dtype, device=dev)
     _, _, dld = _logits(grad, "out")
     _check(_token_logprobs_backward(logits.data_ptr(), dtype, ld, tok, N, V,
                                     _options(ignore_index, 0, temperature), *map(_ptr, vecs),

@@ -202,9 +202,11 @@ FUNCTION(token_logprobs_backward) {
     const float* v[6];
     for (int i = 0; i < 6; ++i) v[i] = vector_of(a[2 + i], N, h.device);
     const flce_logprob_options o = options(a[9], 0, a[8]);
-    const Tensor g = h.strided({N, V}, {ld, 1}, z.scalar_type());
+    // rows that start relative to 16 bytes as the logits' do, however far apart those are
+    const int64_t vec = 16 / static_cast<int64_t>(z.element_size()), dld = V + (ld - V) % vec;
+    const Tensor g = h.strided({N, V}, {dld, 1}, z.scalar_type());
     check(flce_token_logprobs_backward(z.const_data_ptr(), dtype, ld, y, N, V, &o, v[0], v[1], v[2], v[3],
-                                       v[4], v[5], g.data_ptr(), ld, h.stream) == FLCE_OK);
+                                       v[4], v[5], g.data_ptr(), dld, h.stream) == FLCE_OK);
     return THPVariable_Wrap(g);
   });
 }

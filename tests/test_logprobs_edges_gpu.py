@@ -67,3 +67,26 @@ def test_rows_with_one_likely_id(dtype, V, T):
         if y is not None:
             assert torch.count_nonzero(r.logprob[:20]) == 0
             assert torch.equal(r.logprob, r.top_logprob[:, 0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1000, 1003])
+def test_the_gradient_takes_no_more_memory_than_its_rows(dtype, V):
+    """The last position of each sequence: rows of logits that lie T V elements apart."""
+    z = torch.randn(8, 50, V, device=DEV).to(TYPES[dtype])
+    y = torch.arange(8, dtype=torch.int32, device=DEV)
+    rows = z[:, -1]
+    r = flce.token_logprobs(rows, y)
+    want = flce.token_logprobs_backward(rows.contiguous(), y, r, dlogprob=r.lse)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = flce.token_logprobs_backward(rows, y, r, dlogprob=r.lse)
+    h = flce.token_logprobs_backward(rows, y, r, dlogprob=r.lse, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    for t in (g, h):
+        assert t.shape == rows.shape and torch.equal(t, want)
+        assert t.untyped_storage().nbytes() <= 8 * (V + 8) * t.element_size() + 16
+    leaf = rows.detach().requires_grad_(True)
+    lp, _, lse = flce.fused_token_logprobs(leaf, y)
+    lp.backward(lse.detach())
+    assert torch.equal(leaf.grad, want)
