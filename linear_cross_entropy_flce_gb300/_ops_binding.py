@@ -281,9 +281,12 @@ def token_logprobs_backward(logits, tokens, result, *, dlogprob=None, dentropy=N
                 raise ValueError("out must match the logits' device, dtype and shape")
             grad = out
         else:
-            # rows that start relative to 16 bytes as the logits' do, however far apart those are
-            vec = 16 // logits.element_size()
-            grad = torch.empty_strided((N, V), (V + (ld - V) % vec, 1), dtype=logits.dtype, device=dev)
+            # rows that start relative to 16 bytes as the logits' do (the first one too), however
+            # far apart those are
+            elt = logits.element_size()
+            dld, off = V + (ld - V) % (16 // elt), logits.data_ptr() % 16 // elt
+            flat = torch.empty(off + (N - 1) * dld + V if N else 0, dtype=logits.dtype, device=dev)
+            grad = flat.as_strided((N, V), (dld, 1), off if N else 0)
     _, _, dld = _logits(grad, "out")
     _check(_token_logprobs_backward(logits.data_ptr(), dtype, ld, tok, N, V,
                                     _options(ignore_index, 0, temperature), *map(_ptr, vecs),

@@ -80,10 +80,6 @@ struct Here {
     return at::detail::empty_cuda(size, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device)),
                                   std::nullopt);
   }
-  Tensor strided(at::IntArrayRef size, at::IntArrayRef stride, at::ScalarType type) const {
-    return at::detail::empty_strided_cuda(size, stride, type,
-                                          at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
-  }
 };
 
 // int32 [N] tokens, or null.
@@ -202,9 +198,13 @@ FUNCTION(token_logprobs_backward) {
     const float* v[6];
     for (int i = 0; i < 6; ++i) v[i] = vector_of(a[2 + i], N, h.device);
     const flce_logprob_options o = options(a[9], 0, a[8]);
-    // rows that start relative to 16 bytes as the logits' do, however far apart those are
-    const int64_t vec = 16 / static_cast<int64_t>(z.element_size()), dld = V + (ld - V) % vec;
-    const Tensor g = h.strided({N, V}, {dld, 1}, z.scalar_type());
+    // rows that start relative to 16 bytes as the logits' do (the first one too), however far
+    // apart those are
+    const int64_t elt = static_cast<int64_t>(z.element_size()), dld = V + (ld - V) % (16 / elt);
+    const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(z.const_data_ptr()) & 15u) / elt;
+    const Tensor g = h.empty({N > 0 ? off + (N - 1) * dld + V : 0}, z.scalar_type());
+    g.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({N, V}), at::IntArrayRef({dld, 1}),
+                                                   N > 0 ? off : 0);
     check(flce_token_logprobs_backward(z.const_data_ptr(), dtype, ld, y, N, V, &o, v[0], v[1], v[2], v[3],
                                        v[4], v[5], g.data_ptr(), dld, h.stream) == FLCE_OK);
     return THPVariable_Wrap(g);

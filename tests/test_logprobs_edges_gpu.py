@@ -90,3 +90,24 @@ def test_the_gradient_takes_no_more_memory_than_its_rows(dtype, V):
     lp, _, lse = flce.fused_token_logprobs(leaf, y)
     lp.backward(lse.detach())
     assert torch.equal(leaf.grad, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,pad,skip", [(1003, 0, 1), (1001, 0, 3), (1000, 4, 1), (1002, 3, 2)])
+def test_the_gradients_rows_start_as_the_logits_do(dtype, V, pad, skip):
+    """Relative to 16 bytes, so that both are accessed 16 bytes at a time."""
+    z = torch.randn(9, V + pad, device=DEV).to(TYPES[dtype])[skip:, :V]
+    y = torch.arange(9 - skip, dtype=torch.int32, device=DEV)
+    r = flce.token_logprobs(z, y)
+    g = flce.token_logprobs_backward(z, y, r, dlogprob=r.lse, dentropy=r.lse)
+    out = torch.empty(9 - skip, V, dtype=z.dtype, device=DEV)
+    flce.token_logprobs_backward(z, y, r, dlogprob=r.lse, dentropy=r.lse, out=out)
+    assert torch.equal(g, out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    h = flce.token_logprobs_backward(z, y, r, dlogprob=r.lse, dentropy=r.lse, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(g, h)
+    for t in (g, h):
+        for i in range(9 - skip):
+            assert (t[i].data_ptr() - z[i].data_ptr()) % 16 == 0
