@@ -29,20 +29,68 @@ def _flat_grad(g):
     return None if g is None else g.detach().reshape(-1).to(torch.float32)
 
 
+class _Places:
+    """Where the rows of a [..., V] view are among the R equally spaced rows that enclose it."""
+
+    def __init__(self, sizes, steps, rows):
+        self.sizes, self.steps, self.rows = sizes, steps, rows
+
+    def spread(self, t, fill):
+        """t, one value for each row of the view, as a vector of R: `fill` in the other places."""
+        e = t.new_full((self.rows,), fill)
+        e.as_strided(self.sizes, self.steps).copy_(t.reshape(self.sizes))
+        return e
+
+    def pick(self, t):
+        """The view's values of a vector of R, in the view's shape."""
+        return t.as_strided(self.sizes, self.steps).contiguous()
+
+    def pick_rows(self, t):
+        """The view's rows of a [R, V] matrix, as a view of it."""
+        ld = t.stride(0)
+        return t.as_strided((*self.sizes, t.shape[1]), (*(n * ld for n in self.steps), 1))
+
+
+def _rows(logits):
+    """logits [..., V] as (z [R, V] of unit column stride, places). Without places, z has the
+    rows in order. A view that leaves out some rows of an evenly spaced whole, as the shifted
+    logits[:, :-1] does, would have to be copied for that; where they are few (an eighth of the
+    others at most: a row is read once and a copy writes and reads it as well) z is the whole,
+    and the operators run over the rows between too, whose results count nowhere."""
+    V = logits.shape[-1]
+    sizes, strides = logits.shape[:-1], logits.stride()[:-1]
+    dims = [(n, st) for n, st in zip(sizes, strides) if n > 1]
+    if len(dims) > 1 and logits.numel() > 0 and (V == 1 or logits.stride(-1) == 1):
+        ld = dims[-1][1]
+        if ld >= V and all(st % ld == 0 and st >= n * inner
+                           for (_, st), (n, inner) in zip(dims, dims[1:])):
+            whole = 1 + sum((n - 1) * (st // ld) for n, st in dims)
+            rows = logits.numel() // V
+            if whole > rows and 8 * whole <= 9 * rows:
+                steps = [st // ld if n > 1 else 1 for n, st in zip(sizes, strides)]
+                return logits.as_strided((whole, V), (ld, 1)), _Places(sizes, steps, whole)
+    z = logits.reshape(-1, V)
+    if V > 1 and z.stride(1) != 1 or z.shape[0] > 1 and z.stride(0) < V:
+        z = z.contiguous()
+    return z, None
+
+
 class TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, temperature: float, ignore_index: int):
-        V = logits.shape[-1]
-        z = logits.reshape(-1, V)
-        if V > 1 and z.stride(1) != 1 or z.shape[0] > 1 and z.stride(0) < V:
-            z = z.contiguous()
+        z, places = _rows(logits)
         y = _flat_tokens(tokens)
+        rows = logits.shape[:-1]
+        if places is not None and y is not None:
+            if y.numel() != rows.numel():
+                raise ValueError("tokens must have one id for each row of logits")
+            y = places.spread(y, ignore_index)
         r = B.token_logprobs(z, y, temperature=temperature, ignore_index=ignore_index)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(z, y, r.logprob, r.entropy, r.lse)
-        ctx.shape, ctx.options = logits.shape, (temperature, ignore_index)
-        rows = logits.shape[:-1]
-        return r.logprob.reshape(rows), r.entropy.reshape(rows), r.lse.reshape(rows)
+        ctx.shape, ctx.options, ctx.places = logits.shape, (temperature, ignore_index), places
+        outputs = r.logprob, r.entropy, r.lse
+        return tuple(t.reshape(rows) if places is None else places.pick(t) for t in outputs)
 
     @staticmethod
     @once_differentiable
@@ -51,10 +99,13 @@ class TokenLogprobsFunction(torch.autograd.Function):
             return None, None, None, None
         z, y, *saved = ctx.saved_tensors
         temperature, ignore_index = ctx.options
-        dz = B.token_logprobs_backward(z, y, B.TokenLogprobs(*saved), dlogprob=_flat_grad(dlogprob),
-                                       dentropy=_flat_grad(dentropy), dlse=_flat_grad(dlse),
-                                       temperature=temperature, ignore_index=ignore_index)
-        return dz.reshape(ctx.shape), None, None, None
+        places = ctx.places
+        up = [_flat_grad(g) for g in (dlogprob, dentropy, dlse)]
+        if places is not None:
+            up = [g if g is None else places.spread(g, 0) for g in up]
+        dz = B.token_logprobs_backward(z, y, B.TokenLogprobs(*saved), dlogprob=up[0], dentropy=up[1],
+                                       dlse=up[2], temperature=temperature, ignore_index=ignore_index)
+        return dz.reshape(ctx.shape) if places is None else places.pick_rows(dz), None, None, None
 
 
 class LinearTokenLogprobsFunction(torch.autograd.Function):

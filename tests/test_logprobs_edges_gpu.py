@@ -111,3 +111,52 @@ def test_the_gradients_rows_start_as_the_logits_do(dtype, V, pad, skip):
     for t in (g, h):
         for i in range(9 - skip):
             assert (t[i].data_ptr() - z[i].data_ptr()) % 16 == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,V", [(3, 40, 1000), (2, 100, 64), (5, 4, 504), (1, 20, 304), (4, 1, 80)])
+def test_a_shifted_sequence(dtype, B, T, V):
+    """logits[:, :-1] with tokens[:, 1:]: the values of a contiguous copy, without making one
+    of a long sequence. (Rows start at whole 16 bytes, so that both add up in one order.)"""
+    z = torch.randn(B, T + 1, V, device=DEV).to(TYPES[dtype])
+    z[:, -1] = math.nan          # the position that is left out counts nowhere
+    y = torch.randint(0, V, (B, T + 1), device=DEV)
+    y[0, 1] = -100
+    up = torch.randn(3, B, T, device=DEV)
+    got = []
+    for copy in (True, False):
+        leaf = z.detach().clone().requires_grad_(True)
+        rows = leaf[:, :-1].contiguous() if copy else leaf[:, :-1]
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        out = flce.fused_token_logprobs(rows, y[:, 1:], temperature=0.8)
+        spent = torch.cuda.max_memory_allocated() - before
+        assert all(t.shape == (B, T) and t.is_contiguous() for t in out)
+        if T == 40:
+            assert copy or spent < rows.numel() * rows.element_size() // 4
+        sum((t * u).sum() for t, u in zip(out, up)).backward()
+        got.append([*out, leaf.grad])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    lp, _, _ = flce.fused_token_logprobs(z[:, :-1], None)
+    assert torch.count_nonzero(lp) == 0
+    with pytest.raises(ValueError):
+        flce.fused_token_logprobs(z[:, :-1], y[:, :1].expand(B, T + 1))
+
+
+def test_other_views_of_logits():
+    z = torch.randn(4, 3, 25, 132, device=DEV)
+    y = torch.randint(0, 132, (4, 3, 25), device=DEV)
+    for cut in (lambda t: t[:, :, 1:], lambda t: t[1:, :2], lambda t: t[:, :, ::2], lambda t: t.transpose(0, 1),
+                lambda t: t[:1].expand(4, 3, 25, *t.shape[3:]), lambda t: t[:, :, :24], lambda t: t[:0],
+                lambda t: t[:, 1:2, 1:], lambda t: t[:, :, 3], lambda t: t[2, 1, :]):
+        got = []
+        for copy in (True, False):
+            leaf = z.clone().requires_grad_(True)
+            rows = cut(leaf)
+            lp, ent, lse = flce.fused_token_logprobs(rows.contiguous() if copy else rows, cut(y))
+            (lp * 2 + ent - lse * 0.5).sum().backward()
+            got.append((lp, ent, lse, leaf.grad))
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
