@@ -7,7 +7,7 @@ library's CUDA kernels; PyTorch provides device memory and streams.
 The plain form of a call (nothing preallocated, the current stream) is made by the
 extension _flce_ops, which takes a third of the time on the host; it returns None, with
 nothing enqueued, for what it does not take, and the general form below then serves the
-call or says what is wrong with it.
+call or says what is wrong with it. A CUDA error, which may come after a launch, is raised.
 
 Each call takes an optional `stream` (a torch.cuda.Stream or a raw cudaStream_t; the
 current stream by default). What a call allocates for itself belongs to that stream.
@@ -25,6 +25,8 @@ import torch
 from ._binding import FLCE_OK, FLCEError, lib
 
 from . import _flce_ops as _fast  # built with libflce.so, which _binding has checked for
+
+_fast.set_error_type(FLCEError)
 
 MAX_TOP_K = 32
 

@@ -6,7 +6,8 @@
 // preallocated outputs, workspace, status word or stream given). Where an argument is not of
 // the expected kind, or the library refuses the call, it returns None without having
 // enqueued anything, and the caller goes on to the general form in _ops_binding.py, which
-// says what is wrong.
+// says what is wrong. A CUDA error may come after a launch, so it is raised here and not tried
+// again.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -66,6 +67,18 @@ double number(PyObject* o) {
 void check(bool ok) {
   if (!ok) throw Refused{};
 }
+
+struct Failed {
+  const char* where;
+};
+
+// The library's answer to call `where`: only what it refuses has enqueued nothing.
+void check(int rc, const char* where) {
+  if (rc == FLCE_ERR_CUDA) throw Failed{where};
+  check(rc == FLCE_OK);
+}
+
+PyObject* error_type = nullptr;   // FLCEError
 
 // Allocations and launches of one call: the current device and its current stream.
 struct Here {
@@ -144,6 +157,17 @@ PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, F&& f) {
     return f();
   } catch (const Refused&) {
     Py_RETURN_NONE;
+  } catch (const Failed& f) {
+    if (error_type == nullptr) {
+      PyErr_SetString(PyExc_RuntimeError, f.where);
+      return nullptr;
+    }
+    PyObject* const error = PyObject_CallFunction(error_type, "is", FLCE_ERR_CUDA, f.where);
+    if (error != nullptr) {
+      PyErr_SetObject(error_type, error);
+      Py_DECREF(error);
+    }
+    return nullptr;
   } catch (const std::exception& e) {   // out of memory and the like
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;
@@ -182,7 +206,7 @@ FUNCTION(token_logprobs) {
     const LogprobOutputs out(h, N, k);
     check(flce_token_logprobs(z.const_data_ptr(), dtype, ld, y, N, V, &o, out.logprob.data_ptr<float>(),
                               out.entropy.data_ptr<float>(), out.lse.data_ptr<float>(), out.top_lp(),
-                              out.ids(), nullptr, h.stream) == FLCE_OK);
+                              out.ids(), nullptr, h.stream), "flce_token_logprobs");
     return out.tuple();
   });
 }
@@ -206,7 +230,8 @@ FUNCTION(token_logprobs_backward) {
     g.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({N, V}), at::IntArrayRef({dld, 1}),
                                                    N > 0 ? off : 0);
     check(flce_token_logprobs_backward(z.const_data_ptr(), dtype, ld, y, N, V, &o, v[0], v[1], v[2], v[3],
-                                       v[4], v[5], g.data_ptr(), dld, h.stream) == FLCE_OK);
+                                       v[4], v[5], g.data_ptr(), dld, h.stream),
+          "flce_token_logprobs_backward");
     return THPVariable_Wrap(g);
   });
 }
@@ -225,7 +250,8 @@ struct Linear {
   const uint16_t* h() const { return static_cast<const uint16_t*>(H.const_data_ptr()); }
   const uint16_t* w() const { return static_cast<const uint16_t*>(W.const_data_ptr()); }
   Tensor workspace(const Here& here, const flce_logprob_options& o, int backward, size_t* bytes) const {
-    check(flce_linear_logprobs_workspace_size(N, D, V, &o, backward, bytes) == FLCE_OK);
+    check(flce_linear_logprobs_workspace_size(N, D, V, &o, backward, bytes),
+          "flce_linear_logprobs_workspace_size");
     return here.empty({static_cast<int64_t>(*bytes < 16 ? 16 : *bytes)}, at::kByte);
   }
 };
@@ -244,7 +270,8 @@ FUNCTION(linear_token_logprobs) {
     const Tensor ws = p.workspace(h, o, 0, &bytes);
     check(flce_linear_token_logprobs(p.h(), p.w(), y, p.N, p.D, p.V, &o, out.logprob.data_ptr<float>(),
                                      out.entropy.data_ptr<float>(), out.lse.data_ptr<float>(), out.top_lp(),
-                                     out.ids(), ws.data_ptr(), bytes, nullptr, h.stream) == FLCE_OK);
+                                     out.ids(), ws.data_ptr(), bytes, nullptr, h.stream),
+          "flce_linear_token_logprobs");
     return out.tuple();
   });
 }
@@ -268,7 +295,8 @@ FUNCTION(linear_token_logprobs_backward) {
     check(flce_linear_token_logprobs_backward(
               p.h(), p.w(), y, p.N, p.D, p.V, &o, v[0], v[1], v[2], v[3], v[4], v[5],
               dH.defined() ? static_cast<uint16_t*>(dH.data_ptr()) : nullptr,
-              dW.defined() ? dW.data_ptr() : nullptr, ws.data_ptr(), bytes, nullptr, h.stream) == FLCE_OK);
+              dW.defined() ? dW.data_ptr() : nullptr, ws.data_ptr(), bytes, nullptr, h.stream),
+          "flce_linear_token_logprobs_backward");
     return tuple({dH, dW});
   });
 }
@@ -313,7 +341,7 @@ FUNCTION(layer_norm) {
     const Tensor mean = h.empty({r.N}, at::kFloat), rstd = h.empty({r.N}, at::kFloat);
     check(flce_layer_norm(x.const_data_ptr(), dtype, r.ld, w, b, wcode < 0 ? FLCE_DTYPE_F32 : wcode, r.N,
                           r.D, static_cast<float>(number(a[3])), y.data_ptr(), r.D,
-                          mean.data_ptr<float>(), rstd.data_ptr<float>(), h.stream) == FLCE_OK);
+                          mean.data_ptr<float>(), rstd.data_ptr<float>(), h.stream), "flce_layer_norm");
     return tuple({y, mean, rstd});
   });
 }
@@ -336,13 +364,14 @@ FUNCTION(layer_norm_backward) {
     if (integer(a[7])) db = h.empty({r.D}, wtype);
     size_t bytes = 0;
     if (dw.defined() || db.defined()) {
-      check(flce_layer_norm_workspace_size(r.N, r.D, &bytes) == FLCE_OK);
+      check(flce_layer_norm_workspace_size(r.N, r.D, &bytes), "flce_layer_norm_workspace_size");
       ws = h.empty({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, at::kByte);
     }
     auto at_of = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
     check(flce_layer_norm_backward(dy.const_data_ptr(), g.ld, x.const_data_ptr(), dtype, r.ld, w,
                                    wcode < 0 ? FLCE_DTYPE_F32 : wcode, mean, rstd, r.N, r.D, at_of(dx),
-                                   r.D, at_of(dw), at_of(db), at_of(ws), bytes, h.stream) == FLCE_OK);
+                                   r.D, at_of(dw), at_of(db), at_of(ws), bytes, h.stream),
+          "flce_layer_norm_backward");
     return tuple({dx, dw, db});
   });
 }
@@ -372,13 +401,22 @@ FUNCTION(clip_grads) {
       }
     }
     size_t bytes = 0;
-    check(flce_clip_grads_workspace_size(count, &bytes) == FLCE_OK);
+    check(flce_clip_grads_workspace_size(count, &bytes), "flce_clip_grads_workspace_size");
     const Tensor norm = h.empty({1}, at::kFloat);
     const Tensor ws = h.empty({static_cast<int64_t>(bytes)}, at::kByte);
     check(flce_clip_grads(src.data(), a[1] == Py_None ? nullptr : dst.data(), numel.data(), codes.data(),
                           count, static_cast<float>(number(a[2])), norm.data_ptr<float>(), ws.data_ptr(),
-                          bytes, h.stream) == FLCE_OK);
+                          bytes, h.stream), "flce_clip_grads");
     return THPVariable_Wrap(norm);
+  });
+}
+
+// (FLCEError): the type of the errors raised here.
+FUNCTION(set_error_type) {
+  return guarded(n, 1, [&]() -> PyObject* {
+    Py_INCREF(a[0]);
+    Py_XSETREF(error_type, a[0]);
+    Py_RETURN_NONE;
   });
 }
 
@@ -386,7 +424,8 @@ FUNCTION(clip_grads) {
 PyMethodDef methods[] = {METHOD(token_logprobs),        METHOD(token_logprobs_backward),
                          METHOD(linear_token_logprobs), METHOD(linear_token_logprobs_backward),
                          METHOD(layer_norm),            METHOD(layer_norm_backward),
-                         METHOD(clip_grads),            {nullptr, nullptr, 0, nullptr}};
+                         METHOD(clip_grads),            METHOD(set_error_type),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_flce_ops", nullptr, -1, methods,
                       nullptr,               nullptr,     nullptr, nullptr};
 
