@@ -14,9 +14,11 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <exception>
 #include <vector>
 
 #include "../../include/flce_ops.h"
@@ -168,11 +170,8 @@ PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, F&& f) {
       Py_DECREF(error);
     }
     return nullptr;
-  } catch (const std::exception& e) {   // out of memory and the like
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown error");
+  } catch (...) {   // out of memory and the like, as PyTorch's own types
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

@@ -53,3 +53,19 @@ def test_a_cuda_error_is_raised_and_the_call_not_made_again(tmp_path):
     r = subprocess.run([gcc, "-shared", "-fPIC", "-o", str(lib), str(src)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     _run(PROGRAM, str(lib))
+
+
+OUT_OF_MEMORY = r"""
+import torch
+import linear_cross_entropy_flce_gb300 as flce
+x = torch.ones(40000, 1024, device="cuda:0")     # 164 MB, of 280 MB that the process may take
+torch.cuda.set_per_process_memory_fraction(280e6 / torch.cuda.get_device_properties(0).total_memory)
+try:
+    flce.layer_norm(x)
+except torch.OutOfMemoryError:
+    print("ok")
+"""
+
+
+def test_out_of_memory_is_pytorchs_own_error():
+    _run(OUT_OF_MEMORY)
