@@ -8,6 +8,7 @@ The plain form of a call (nothing preallocated, the current stream) is made by t
 extension _flce_ops, which takes a third of the time on the host; it returns None, with
 nothing enqueued, for what it does not take, and the general form below then serves the
 call or says what is wrong with it. A CUDA error, which may come after a launch, is raised.
+Without the extension (it is built for one PyTorch) the general form serves every call.
 
 Each call takes an optional `stream` (a torch.cuda.Stream or a raw cudaStream_t; the
 current stream by default). What a call allocates for itself belongs to that stream.
@@ -18,15 +19,37 @@ import contextlib
 import ctypes
 import dataclasses
 import functools
+import re
+import warnings
 from typing import Optional, Sequence
 
 import torch
 
 from ._binding import FLCE_OK, FLCEError, lib
 
-from . import _flce_ops as _fast  # built with libflce.so, which _binding has checked for
 
-_fast.set_error_type(FLCEError)
+class _NoExtension:
+    """Takes no call: all of them go through the general form."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_extension():
+    """_flce_ops, if there is one for this PyTorch."""
+    try:
+        from . import _flce_ops as fast
+        have = re.match(r"[\d.]*\d", torch.__version__).group()
+        if fast.torch_version != have:
+            raise ImportError(f"built for PyTorch {fast.torch_version}, not {have}")
+    except ImportError as e:
+        warnings.warn(f"without _flce_ops, calls take longer on the host: {e}", RuntimeWarning)
+        return _NoExtension()
+    fast.set_error_type(FLCEError)
+    return fast
+
+
+_fast = _load_extension()
 
 MAX_TOP_K = 32
 

@@ -15,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -71,6 +72,17 @@ def _link_ext(obj: str) -> None:
     os.replace(tmp, EXT)
 
 
+def _finish_ext(obj) -> None:
+    """Link _flce_ops.so from its object (a future). Where it cannot be built, without PyTorch's
+    headers for one, the package makes every call through libflce.so alone: said, not raised."""
+    try:
+        _link_ext(obj.result())
+    except Exception as e:
+        if os.path.exists(EXT):   # of other sources than libflce.so's
+            os.remove(EXT)
+        warnings.warn(f"built without _flce_ops.so, calls take longer on the host: {e}", RuntimeWarning)
+
+
 def _compile(src: str, extra) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -98,7 +110,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_ext(ext_obj.result())
+    _finish_ext(ext_obj)
     return LIB
 
 

@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cstdint>
 #include <exception>
@@ -430,4 +431,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_flce_ops", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__flce_ops() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__flce_ops() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    m = nullptr;
+  }
+  return m;
+}
