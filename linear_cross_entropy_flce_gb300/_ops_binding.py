@@ -535,6 +535,14 @@ def _clip(grads: list, max_norm: float, outs, norm, workspace, stream):
         r = _fast.clip_grads(grads, outs, max_norm)
         if r is not None:
             return r
+    if outs is not None and outs is not grads and len(outs) != len(grads):
+        raise ValueError("out must hold one tensor for each gradient")
+    if any(g is None for g in grads):
+        there = [i for i, g in enumerate(grads) if g is not None]
+        some = [grads[i] for i in there]
+        if outs is not None:
+            outs = some if outs is grads else [outs[i] for i in there]
+        return _clip(some, max_norm, outs, norm, workspace, stream)
     n = len(grads)
     dev = torch.device("cuda", torch.cuda.current_device())
     codes = []
@@ -548,8 +556,6 @@ def _clip(grads: list, max_norm: float, outs, norm, workspace, stream):
             raise ValueError("a gradient must fill its memory without gaps or overlaps")
         codes.append(code)
     if outs is not None and outs is not grads:
-        if len(outs) != n:
-            raise ValueError("out must hold one tensor for each gradient")
         for g, o in zip(grads, outs):
             if o.dtype != g.dtype or o.shape != g.shape or o.device != dev or \
                     (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
@@ -573,15 +579,17 @@ def _clip(grads: list, max_norm: float, outs, norm, workspace, stream):
 
 
 def grad_norm(grads: Sequence, *, norm=None, workspace=None, stream=None):
-    """The 2-norm over all elements of the gradients (fp32 and bf16 CUDA tensors), as a
-    float32 [1] tensor, via flce_clip_grads."""
+    """The 2-norm over all elements of the gradients (fp32 and bf16 CUDA tensors; a None, of a
+    parameter without a gradient, counts nothing), as a float32 [1] tensor, via
+    flce_clip_grads."""
     return _clip(list(grads), 1.0, None, norm, workspace, stream)
 
 
 def clip_grads(grads: Sequence, max_norm: float, *, out: Optional[Sequence] = None, norm=None,
                workspace=None, stream=None):
     """Multiplies the gradients by min(1, max_norm / (norm + 1e-6)), norm their global
-    2-norm: in place, or into the tensors of `out`. Returns the norm before clipping as a
-    float32 [1] tensor. Nothing waits for the GPU."""
+    2-norm: in place, or into the tensors of `out`. A None among them, of a parameter without a
+    gradient, is passed over. Returns the norm before clipping as a float32 [1] tensor.
+    Nothing waits for the GPU."""
     grads = list(grads)
     return _clip(grads, float(max_norm), grads if out is None else list(out), norm, workspace, stream)
