@@ -64,9 +64,9 @@ void flce_default_logprob_options(flce_logprob_options* opt);
  * top_k ids are left the remaining slots hold id -1 and -inf. A row whose logits
  * are all -inf has lse = logprob = -inf and entropy 0. A row with a NaN or +inf has
  * NaN for logprob, entropy, lse and its top log probabilities. A token outside
- * [0, V) that is not ignore_index gives logprob NaN and FLCE_ERR_LABEL_RANGE; a
- * wait that ran out of time gives NaN for its row (in the linear form below: undefined
- * outputs) and FLCE_ERR_TIMEOUT.
+ * [0, V) that is not ignore_index gives logprob NaN and FLCE_ERR_LABEL_RANGE; a wait
+ * that ran out of time gives NaN for its row and for those still to come in the same CTAs
+ * (in the linear form below: undefined outputs) and FLCE_ERR_TIMEOUT.
  * Sums and maxima are fp32; results do not change from run to run.
  */
 int flce_token_logprobs(const void* logits, int32_t dtype, int64_t ld, const int32_t* tokens,

@@ -641,6 +641,9 @@ __global__ void __launch_bounds__(kWarpRowWarps * 32)
 
 // ---- longer rows: clusters, through shared memory -------------------------------------------
 
+// In place of a row's maximum: a CTA's wait ran out of time. (Maxima have no such NaN.)
+constexpr uint32_t kLateMark = 0x7FC0A7E5u;
+
 // What a CTA knows of a row: maximum, sums, the token's logit if it is in its slice (0
 // otherwise), and its ranking.
 struct __align__(16) RowMsg {
@@ -679,7 +682,10 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
   __shared__ float s_m[2], s_zt[2];
   __shared__ int s_count[2];
   __shared__ uint64_t s_cand[kTop ? 2 : 1][kTop ? kCandidates : 1];
-  __shared__ volatile int s_late;               // a wait ran out of time
+  // A wait ran out of time. From then on the CTA starts no copy (the slot's last one may still
+  // be on its way), its rows are NaN, and a warp that waited for a peer in vain touches no
+  // barrier of the exchange again: a phase that has not ended takes no second arrival.
+  __shared__ volatile int s_late;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int crank = static_cast<int>(cluster_ctarank()), csize = static_cast<int>(cluster_size());
   const int first = static_cast<int>(blockIdx.x) / csize, step = static_cast<int>(gridDim.x) / csize;
@@ -924,6 +930,7 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
       if (first < N) copy(first, 0);
       if (first + step < N) copy(first + step, 1);
     }
+    bool sending = true;   // of this lane
     int it = 0;
     for (int row = first; row < N; row += step, ++it) {
       const int k = it & 1;
@@ -932,6 +939,7 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
       bar_sync(kBarDone + k, kAll);
       // take what the slot holds, start the copy into it and give it back, then sort
       const int count = kTop ? s_count[k] : 0;
+      const bool copying = more && !s_late;
       float2 sums = lane < kWarps ? s_sum[k][lane] : make_float2(0.f, 0.f);
       RowPart part{s_m[k], 0.f, 0.f};
       float zt = s_zt[k];
@@ -941,7 +949,7 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
         if (lane == 0) {
           s_count[k] = 0;
           s_zt[k] = 0.f;
-          if (more) copy(row + 2 * step, k);
+          if (copying) copy(row + 2 * step, k);
         }
         __syncwarp();
         if (more) bar_arrive(kBarFree + k, kAll);
@@ -1015,18 +1023,21 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
         // to this row's CTA, once it has read the message of two turns before
         const int leader = it % csize, u = it / csize, slot = u & 1;
         if (u >= 2 && !mbar_wait_bounded<true>(smem_u32(&s_used[leader][slot]),
-                                               static_cast<uint32_t>(((u >> 1) - 1) & 1), timeout_ns, &never))
+                                               static_cast<uint32_t>(((u >> 1) - 1) & 1),
+                                               sending ? timeout_ns : 0, &never)) {
+          sending = false;
           s_late = 1;
+        }
         // asynchronous stores, counted in bytes on the receiver's barrier: no fence
         const uint32_t msg = mapa_shared(smem_u32(&s_msg[slot][crank]), static_cast<uint32_t>(leader));
         const uint32_t bar = mapa_shared(smem_u32(&s_got[slot]), static_cast<uint32_t>(leader));
-        if (s_late) part.m = __uint_as_float(0x7FC00000u);   // a row that came to nothing
-        if (lane == 0)
+        if (s_late) part.m = __uint_as_float(kLateMark);   // a row that came to nothing
+        if (sending && lane == 0)
           asm volatile(
               "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(msg),
               "f"(part.m), "f"(part.s), "f"(part.t), "f"(zt), "r"(bar)
               : "memory");
-        if (kTop && lane < top_k)
+        if (kTop && sending && lane < top_k)
           asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
                            msg + 16u + 8u * lane),
                        "l"(list), "r"(bar)
@@ -1065,44 +1076,69 @@ __global__ void __launch_bounds__((kWarps + 3) * 32, kMinBlocks)
     }
   } else if (csize > 1) {
     // joins the rows whose turn this CTA is
+    bool waiting = true;
     int u = 0;
     for (int64_t row = first + static_cast<int64_t>(crank) * step; row < N;
          row += static_cast<int64_t>(csize) * step, ++u) {
       const int slot = u & 1;
       const int y = tokens != nullptr ? tokens[row] : ignore_index;
-      if (lane == 0)
-        mbar_arrive_expect_tx(smem_u32(&s_got[slot]),
-                              static_cast<uint32_t>(csize) * (16u + (kTop ? 8u * top_k : 0u)));
-      __syncwarp();
-      bool late = !mbar_wait_bounded<true>(smem_u32(&s_got[slot]), static_cast<uint32_t>((u >> 1) & 1),
-                                           timeout_ns, &never);
-      late = __any_sync(0xffffffffu, late) || s_late != 0;
-      // lane r joins CTA r's sums; the rankings one after the other
-      const float4 p = lane < csize ? s_msg[slot][lane].part : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      RowPart part{p.x, p.y, p.z};
-      float zt = p.w;
-#pragma unroll
-      for (int o = kMaxRowCluster / 2; o > 0; o >>= 1) {
-        const RowPart q{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o),
-                        __shfl_xor_sync(0xffffffffu, part.t, o)};
-        row_join(part, q, c);
-        zt += __shfl_xor_sync(0xffffffffu, zt, o);
-      }
-      part = RowPart{__shfl_sync(0xffffffffu, part.m, 0), __shfl_sync(0xffffffffu, part.s, 0),
-                     __shfl_sync(0xffffffffu, part.t, 0)};
-      zt = __shfl_sync(0xffffffffu, zt, 0);
+      RowPart part{-INFINITY, 0.f, 0.f};
+      float zt = 0.f;
       uint64_t list = 0;
-      if constexpr (kTop) {
-        for (int r = 0; r < csize; ++r) {
-          const uint64_t key = lane < top_k ? s_msg[slot][r].list[lane] : 0;
-          list = r == 0 ? key : warp_merge_desc(list, key, lane);
+      if (waiting) {
+        if (lane == 0)
+          mbar_arrive_expect_tx(smem_u32(&s_got[slot]),
+                                static_cast<uint32_t>(csize) * (16u + (kTop ? 8u * top_k : 0u)));
+        __syncwarp();
+        waiting = mbar_wait_bounded<true>(smem_u32(&s_got[slot]), static_cast<uint32_t>((u >> 1) & 1),
+                                          timeout_ns, &never);
+        waiting = __all_sync(0xffffffffu, waiting);
+        if (!waiting) {
+          // No CTA sends more than two messages that are not read: those land before the memory
+          // is given back.
+          s_late = 1;
+          if (lane == 0) {
+            const int64_t next = row + static_cast<int64_t>(csize) * step;
+            if (next < N)
+              mbar_arrive_expect_tx(smem_u32(&s_got[slot ^ 1]),
+                                    static_cast<uint32_t>(csize) * (16u + (kTop ? 8u * top_k : 0u)));
+            for (int d = 0; d < (next < N ? 2 : 1); ++d)
+              mbar_wait_bounded<true>(smem_u32(&s_got[(u + d) & 1]), static_cast<uint32_t>(((u + d) >> 1) & 1),
+                                      1000000000ull, &never);
+          }
+          __syncwarp();
         }
       }
-      __syncwarp();
-      if (lane < csize)
-        mbar_arrive_cluster(mapa_shared(smem_u32(&s_used[crank][slot]), static_cast<uint32_t>(lane)));
-      if (late) s_late = 1;
-      finish(static_cast<int>(row), y, part, zt, list, late);
+      bool late = !waiting;
+      if (waiting) {
+        // lane r joins CTA r's sums; the rankings one after the other
+        if (lane < csize) {
+          const float4 p = s_msg[slot][lane].part;
+          part = RowPart{p.x, p.y, p.z};
+          zt = p.w;
+          late = __float_as_uint(p.x) == kLateMark;
+        }
+#pragma unroll
+        for (int o = kMaxRowCluster / 2; o > 0; o >>= 1) {
+          const RowPart q{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o),
+                          __shfl_xor_sync(0xffffffffu, part.t, o)};
+          row_join(part, q, c);
+          zt += __shfl_xor_sync(0xffffffffu, zt, o);
+        }
+        part = RowPart{__shfl_sync(0xffffffffu, part.m, 0), __shfl_sync(0xffffffffu, part.s, 0),
+                       __shfl_sync(0xffffffffu, part.t, 0)};
+        zt = __shfl_sync(0xffffffffu, zt, 0);
+        if constexpr (kTop) {
+          for (int r = 0; r < csize; ++r) {
+            const uint64_t key = lane < top_k ? s_msg[slot][r].list[lane] : 0;
+            list = r == 0 ? key : warp_merge_desc(list, key, lane);
+          }
+        }
+        __syncwarp();
+        if (lane < csize)
+          mbar_arrive_cluster(mapa_shared(smem_u32(&s_used[crank][slot]), static_cast<uint32_t>(lane)));
+      }
+      finish(static_cast<int>(row), y, part, zt, list, __any_sync(0xffffffffu, late || s_late != 0));
     }
   }
   // copies that nobody waited for land before the memory is given back (only after a timeout)

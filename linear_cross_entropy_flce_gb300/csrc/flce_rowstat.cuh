@@ -126,7 +126,9 @@ __device__ __forceinline__ RowOut row_finish(const RowPart& p, float zt, bool ha
   const float h = fmaf(-kLn2, t / (s + em), o.log_s);
   o.entropy = h < 0.f ? 0.f : h;
   // e_t < 2^-60: x_y - lse has no cancellation, and the quotient could overflow
-  o.logprob = !has_token ? 0.f : (et >= 0x1p-60f ? -log1pf(p.s / et) : id_logprob(o, zt, inv_t));
+  if (!has_token) o.logprob = 0.f;
+  else if (top) o.logprob = -o.log_s;
+  else o.logprob = et >= 0x1p-60f ? -log1pf(p.s / et) : id_logprob(o, zt, inv_t);
   return o;
 }
 

@@ -160,3 +160,47 @@ def test_other_views_of_logits():
             got.append((lp, ent, lse, leaf.grad))
         for a, b in zip(*got):
             assert torch.equal(a, b)
+
+
+def _limited(z, y, top_k):
+    """token_logprobs with a limit of 1 ns: (outputs by name, status code)."""
+    from linear_cross_entropy_flce_gb300 import _ops_binding as B
+    N, V = z.shape
+    out = {k: torch.zeros(N, device=DEV) for k in ("logprob", "entropy", "lse")}
+    if top_k:
+        out["top_logprob"] = torch.zeros(N, top_k, device=DEV)
+        out["top_id"] = torch.zeros(N, top_k, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    at = {k: t.data_ptr() for k, t in out.items()}
+    rc = B._token_logprobs(z.data_ptr(), B._DTYPES[z.dtype], V, y.data_ptr(), N, V,
+                           B._options(-100, top_k, 1.0, 0, 1), at["logprob"], at["entropy"], at["lse"],
+                           at.get("top_logprob"), at.get("top_id"), status.data_ptr(),
+                           torch.cuda.current_stream().cuda_stream)
+    assert rc == flce.FLCE_OK
+    return out, flce.check_status(status)
+
+
+@pytest.mark.parametrize("dtype,N,V,sure", [("bf16", 300, 6000, False), ("f32", 2000, 4500, False),
+                                            ("bf16", 3, 128256, False), ("bf16", 400, 60000, True),
+                                            ("f32", 60, 150000, False), ("f32", 120, 210000, True)])
+def test_a_wait_that_runs_out_leaves_nan_and_a_status(dtype, N, V, sure):
+    """A 1-ns limit ends every wait that the hardware's own look at the barrier does not (it takes
+    a microsecond or so): the call ends, its rows are NaN or right, the status says which, and
+    the next call is as ever. With many copies under way some wait does run out."""
+    z = torch.randn(N, V, device=DEV).to(TYPES[dtype])
+    y = (torch.arange(N, device=DEV) * 7 % V).int()
+    ran_out = 0
+    for top_k in (0, 5, 0, 5):
+        want = flce.token_logprobs(z, y, top_k=top_k)
+        out, code = _limited(z, y, top_k)
+        late = torch.isnan(out["lse"])
+        assert code == (flce.FLCE_ERR_TIMEOUT if bool(late.any()) else flce.FLCE_OK)
+        ran_out += code != flce.FLCE_OK
+        for k, t in out.items():
+            assert torch.equal(t[~late], getattr(want, k)[~late]), k
+            if k != "top_id":
+                assert bool(torch.isnan(t[late]).all()), k
+        again = flce.token_logprobs(z, y, top_k=top_k)
+        for k in out:
+            assert torch.equal(getattr(again, k), getattr(want, k)), k
+    assert ran_out or not sure
