@@ -65,8 +65,8 @@ void flce_default_logprob_options(flce_logprob_options* opt);
  * are all -inf has lse = logprob = -inf and entropy 0. A row with a NaN or +inf has
  * NaN for logprob, entropy, lse and its top log probabilities. A token outside
  * [0, V) that is not ignore_index gives logprob NaN and FLCE_ERR_LABEL_RANGE; a wait
- * that ran out of time gives NaN for its row and for those still to come in the same CTAs
- * (in the linear form below: undefined outputs) and FLCE_ERR_TIMEOUT.
+ * that ran out of time gives FLCE_ERR_TIMEOUT and NaN for its row and for those still to
+ * come in the same CTAs (the linear form's calls below: for what they did not compute).
  * Sums and maxima are fp32; results do not change from run to run.
  */
 int flce_token_logprobs(const void* logits, int32_t dtype, int64_t ld, const int32_t* tokens,
@@ -100,9 +100,10 @@ int flce_token_logprobs_backward(const void* logits, int32_t dtype, int64_t ld,
 /*
  * The same from hidden states: z = H W^T with H bf16 [N, D] and W bf16 [V, D]
  * (16-byte aligned, D % 8 == 0), products accumulated in fp32, and no [N, V] array
- * but for up to 128 rows, whose fp32 logits pass through the workspace. Outputs and rules as in flce_token_logprobs. The
- * workspace (16-byte aligned, flce_linear_logprobs_workspace_size() bytes with
- * backward = 0) holds the partial results of each vocabulary range.
+ * but for up to 128 rows, whose fp32 logits pass through the workspace. Outputs and
+ * rules as in flce_token_logprobs. The workspace (16-byte aligned,
+ * flce_linear_logprobs_workspace_size() bytes with backward = 0) holds the partial
+ * results of each vocabulary range.
  */
 int flce_linear_logprobs_workspace_size(int64_t N, int64_t D, int64_t V,
                                         const flce_logprob_options* opt, int32_t backward,

@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (issued_any) {
         // Drain: all MMAs of this warp complete before TMEM is freed.
         const volatile int no_abort = 0;
-        if (lane == 0) umma_commit_cg<kCta>(drain_bar);
+        if (elect_one()) umma_commit_cg<kCta>(drain_bar);   // the lane that issued them
         __syncwarp();
         mbar_wait_bounded(drain_bar, 0, 1000000000ull, &no_abort);
       }
@@ -707,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this warp's two staging boxes, used alternately
     const uint32_t stg = stage0 + Cfg::kRingBytes + static_cast<uint32_t>(quarter) * 2u * Cfg::kStgBytes;
     uint32_t nbox = 0;
+    int stop_u = 0, stop_n = 0;   // the tile that did not come
     for (int u = pair; ok && u < total_units; u += num_pairs) {
       const bool second = kProducts == 2 && u >= units0;
       const GemmArgs& G = second ? g1 : g0;
@@ -779,6 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         got = __shfl_sync(0xffffffffu, got, 0);
         if (!got) {
           ok = false;
+          stop_u = u;
+          stop_n = n_blk;
           break;
         }
         tc_fence_after();
@@ -902,6 +905,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
       if (lane == 0) record_status(p0.status, kStatusTimeout);
       *abort_flag = 1;
+      // this warp's rows of what is not done become NaN, for callers that do not read the status
+      if constexpr (kEpi == EPI_LOGP || kEpi == EPI_LOGP_TOP) {
+        for (int u = stop_u; u < total_units; u += num_pairs) {
+          int m_blk, n_begin, n_end;
+          const int col_unit = unit_tiles<kEpi>(p0, u, m_blk, n_begin, n_end);
+          const int64_t slot =
+              (static_cast<int64_t>(col_unit) * p0.part_stride + m_blk * kCta + static_cast<int>(rank)) * BM + row;
+          p0.part4[slot] = make_float4(__uint_as_float(0x7FC00000u), 0.f, 0.f, 0.f);
+          if constexpr (kEpi == EPI_LOGP_TOP)
+            for (int j = 0; j < p0.top_k; ++j) p0.lists[slot * p0.top_k + j] = 0;
+        }
+      } else if constexpr (kEpi == EPI_LOGP_GRAD || kEpi == EPI_F32) {
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        for (uint32_t at = lane * 16u; at < Cfg::kStgBytes; at += 512u)   // NaN in fp32 and in bf16
+          st_shared_v4(stg + at, 0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu);
+        fence_proxy_async_smem();
+        __syncwarp();
+        for (int u = stop_u; lane == 0 && u < total_units; u += num_pairs) {
+          const bool second = kProducts == 2 && u >= units0;
+          const GemmArgs& G = second ? g1 : g0;
+          int m_blk, n_begin, n_end;
+          unit_tiles<kEpi>(G.p, second ? u - units0 : u, m_blk, n_begin, n_end);
+          const int oy = G.p.out_row0 + m_blk * Cfg::kTileM + static_cast<int>(rank) * BM + quarter * 32;
+          for (int n_blk = u == stop_u ? stop_n : n_begin; n_blk < n_end; ++n_blk)
+            for (int c = 0; c < Cfg::kTileN / 32; ++c) {
+              const int col = n_blk * Cfg::kTileN + c * 32;
+              if constexpr (epi_writes_g(kEpi)) tma_store_3d(&G.c, stg, col & 63, oy, col >> 6);
+              else if (G.p.out_mode == OUT_ADD_F32) tma_reduce_add_2d(&G.c, stg, col, oy);
+              else tma_store_2d(&G.c, stg, col, oy);
+              bulk_commit_group();
+            }
+        }
+        __syncwarp();
+      }
     }
     // every store of this warp has landed before the CTA can exit
     if constexpr (!epi_sums_rows(kEpi)) {

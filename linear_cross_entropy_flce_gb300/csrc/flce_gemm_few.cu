@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     if (!ok) fail();
     if (issued_any) {   // every MMA is done before TMEM is freed
-      if (lane == 0) umma_commit_cg<1>(drain_bar);
+      if (elect_one()) umma_commit_cg<1>(drain_bar);   // the lane that issued them
       __syncwarp();
       mbar_wait_bounded(drain_bar, 0, 1000000000ull, &no_abort);
     }
@@ -225,6 +225,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) {
         fail();
+        // this warp's rows of what is not done become NaN, for callers that do not read the status
+        for (int r = row + quarter * 32 + lane; r < row1; r += BM)
+          for (int j = 0; j < p.N; ++j) p.z[r + j * p.ldz] = __uint_as_float(0x7FC00000u);
         break;
       }
       tc_fence_after();

@@ -93,3 +93,51 @@ def test_rows_with_one_likely_id(N):
         assert torch.count_nonzero(r.entropy[far]) == 0
         if tok is not None:
             assert torch.equal(r.logprob, r.top_logprob[:, 0])
+
+
+@pytest.mark.parametrize("N,D,V,sure", [(3, 512, 33000, True), (100, 1024, 20000, True), (200, 512, 33000, True),
+                                        (700, 1024, 9000, True), (40, 64, 300, False)])
+def test_a_wait_that_runs_out_leaves_nan(N, D, V, sure):
+    """A 1-ns limit: the calls end, what they did not compute is NaN, with a status word or
+    without, the status says so, and the next calls are as ever."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(N)
+    H = torch.randn(N, D, generator=g, device=DEV).bfloat16()
+    W = (torch.randn(V, D, generator=g, device=DEV) * 0.05).bfloat16()
+    y = (torch.arange(N, device=DEV) * 11 % V).int()
+    up = torch.randn(N, generator=g, device=DEV)
+
+    def same_or_nan(got, want):
+        return bool((torch.isnan(got) | (got == want)).all())
+
+    ran_out = [0, 0]
+    for top_k in (0, 5, 0, 5):
+        want = flce.linear_token_logprobs(H, W, y, top_k=top_k)
+        for status in (torch.zeros(1, dtype=torch.int32, device=DEV), None):
+            r = flce.linear_token_logprobs(H, W, y, top_k=top_k, timeout_ns=1, status=status)
+            late = torch.isnan(r.lse)
+            for k in ("logprob", "entropy", "lse") + (("top_logprob",) if top_k else ()):
+                got, right = getattr(r, k), getattr(want, k)
+                assert torch.equal(got[~late], right[~late]) and bool(torch.isnan(got[late]).all()), k
+            if status is not None:
+                code = flce.check_status(status)
+                assert code in (flce.FLCE_OK, flce.FLCE_ERR_TIMEOUT)
+                assert code == flce.FLCE_ERR_TIMEOUT or not bool(late.any())
+                ran_out[0] += bool(late.any())
+        again = flce.linear_token_logprobs(H, W, y, top_k=top_k)
+        assert torch.equal(again.lse, want.lse) and torch.equal(again.logprob, want.logprob)
+    for dtype in ("float32", "bfloat16"):
+        right = flce.linear_token_logprobs_backward(H, W, y, want, dlogprob=up, dentropy=up, dw_dtype=dtype)
+        for need in ((True, True), (True, False), (False, True)):
+            status = torch.zeros(1, dtype=torch.int32, device=DEV)
+            got = flce.linear_token_logprobs_backward(
+                H, W, y, want, dlogprob=up, dentropy=up, dw_dtype=dtype, need_dh=need[0], need_dw=need[1],
+                timeout_ns=1, status=status)
+            code = flce.check_status(status)
+            nan = any(bool(torch.isnan(t).any()) for t in got if t is not None)
+            assert code == (flce.FLCE_ERR_TIMEOUT if nan else flce.FLCE_OK)
+            assert all(same_or_nan(t, w) for t, w in zip(got, right) if t is not None)
+            ran_out[1] += nan
+        again = flce.linear_token_logprobs_backward(H, W, y, want, dlogprob=up, dentropy=up, dw_dtype=dtype)
+        assert torch.equal(again[0], right[0]) and torch.equal(again[1], right[1])
+    assert min(ran_out) > 0 or not sure
