@@ -141,3 +141,43 @@ def test_a_wait_that_runs_out_leaves_nan(N, D, V, sure):
         again = flce.linear_token_logprobs_backward(H, W, y, want, dlogprob=up, dentropy=up, dw_dtype=dtype)
         assert torch.equal(again[0], right[0]) and torch.equal(again[1], right[1])
     assert min(ran_out) > 0 or not sure
+
+
+def _classes(N, V, D=64):
+    """H and W whose logits are 0 where id and row agree mod D, and -128 elsewhere."""
+    H = torch.zeros(N, D, device=DEV)
+    H[torch.arange(N, device=DEV), torch.arange(N, device=DEV) % D] = 1.0
+    W = torch.full((V, D), -128.0, device=DEV)
+    W[torch.arange(V, device=DEV), torch.arange(V, device=DEV) % D] = 0.0
+    return H.bfloat16(), W.bfloat16()
+
+
+@pytest.mark.parametrize("top_k", [0, 32])
+@pytest.mark.parametrize("N,V", [(3, 1000), (40, 4099), (128, 9001), (129, 4099), (200, 33000), (300, 16640),
+                                 (2500, 7013)])
+def test_every_id_counts_once(N, V, top_k):
+    """Each row has V / 64 ids that count: one left out or taken twice moves its log-sum-exp by
+    64 / V, 500 times the bound or more."""
+    H, W = _classes(N, V)
+    cls = torch.arange(N, device=DEV) % 64
+    y = cls.int()
+    count = ((V - 1 - cls) // 64 + 1).double()
+    r = flce.linear_token_logprobs(H, W, y, top_k=top_k)
+    e = 2.0 ** -22 + U * (16 + 8)   # ones, whose sums are exact, joined by powers of 2
+    logn = count.log()
+    assert float((r.lse.double() - logn).abs().max()) <= e + 4 * U * 8
+    assert float((r.entropy.double() - logn).abs().max()) <= 16 * e
+    assert float((r.logprob.double() + logn).abs().max()) <= 4 * e * 8
+    if top_k:
+        k = torch.arange(32, device=DEV)
+        want = cls[:, None] + 64 * k[None, :]
+        there = want < V
+        assert torch.equal(r.top_id[there], want[there].int())
+    dH, dW = flce.linear_token_logprobs_backward(H, W, y, r, dlse=torch.ones(N, device=DEV))
+    # dlse: G = p. dW's row v sums p of its class's rows of H; G is rounded to bf16
+    rows = torch.bincount(cls, minlength=64).double()
+    p = 1 / ((V - 1 - torch.arange(64, device=DEV)) // 64 + 1).double()
+    ids = torch.arange(V, device=DEV)
+    want = torch.zeros(V, 64, dtype=torch.float64, device=DEV)
+    want[ids, ids % 64] = (rows * p)[ids % 64]
+    assert bool(((dW.double() - want).abs() <= (2.0 ** -8 + 1e-4) * want).all())

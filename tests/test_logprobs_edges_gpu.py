@@ -204,3 +204,54 @@ def test_a_wait_that_runs_out_leaves_nan_and_a_status(dtype, N, V, sure):
         for k in out:
             assert torch.equal(getattr(again, k), getattr(want, k)), k
     assert ran_out or not sure
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,pad", [(257, 0), (1000, 3), (2003, 0), (4096, 0), (6001, 5), (10007, 0), (24004, 0),
+                                   (33000, 0), (60001, 0), (128256, 0), (212900, 4), (240007, 1)])
+def test_every_id_counts_once(dtype, V, pad):
+    """Row r has the ids r, r + K, r + 2 K, ... at one value and -inf elsewhere, about 64 of them:
+    one that is left out or taken twice moves the log-sum-exp by 1 / 64."""
+    K = -(-V // 64)
+    full = torch.full((K, V + pad), 50.0, dtype=TYPES[dtype], device=DEV)
+    z = full[:, :V]
+    z.fill_(-math.inf)
+    ids = torch.arange(V, device=DEV)
+    z[ids % K, ids] = 1.5
+    y = torch.arange(K, dtype=torch.int32, device=DEV)
+    count = torch.bincount(ids % K, minlength=K).double()
+    r = flce.token_logprobs(z, y, top_k=32)
+    # the terms are equal: 2^-22 of each, then no more than 65 additions
+    e = 2.0 ** -22 + 80 * U
+    logn = count.log()
+    assert float((r.lse.double() - 1.5 - logn).abs().max()) <= e + 8 * U * 6
+    assert float((r.entropy.double() - logn).abs().max()) <= 10 * e
+    assert float((r.logprob.double() + logn).abs().max()) <= 4 * e * 5
+    k = torch.arange(32, device=DEV)
+    want = y[:, None] + K * k[None, :]
+    there = want < V
+    assert torch.equal(r.top_id, torch.where(there, want, torch.full_like(want, -1)).int())
+    assert float((r.top_logprob.double() + logn[:, None])[there].abs().max()) <= 4 * e * 5
+    a = torch.ones(K, device=DEV)
+    g = flce.token_logprobs_backward(z, y, r, dlogprob=a).double()
+    p = torch.zeros_like(g)
+    p[ids % K, ids] = 1 / count[ids % K]
+    p = -p
+    p[y.long(), y.long()] += 1
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    assert bool(((g - p).abs() <= (half + 64 * U + 4 * e) * p.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("top_k", [0, 5])
+@pytest.mark.parametrize("N,V,threads", [(3000, 6000, 128), (800, 60000, 256), (1300, 3000, 32)])
+def test_many_distinct_rows(dtype, top_k, N, V, threads):
+    """More rows than CTAs or clusters at once: slots, messages and barriers are used again."""
+    t = torch.from_numpy((_rng(N + V).standard_normal((N, V)) * 2).astype(np.float32)).to(DEV).to(TYPES[dtype])
+    z = t.float().cpu().numpy()
+    y = _rng(N).integers(0, V, N).astype(np.int32)
+    y[::7] = -100
+    r = flce.token_logprobs(t, torch.from_numpy(y).to(DEV), top_k=top_k)
+    ref = ho.token_logprobs(z, y, top_k=top_k)
+    check_logprobs(r, ref, z, 1.0, eps=sum_eps(V, threads))
+    assert np.array_equal(r.top_id.cpu().numpy() if top_k else ref["top_id"], ref["top_id"])
