@@ -8,8 +8,8 @@ gradient over sampled tokens with an entropy bonus:
 
 then the gradients are clipped by their global norm and the parameters moved. The [N, V]
 logits exist in no training step. Sampling takes one position of each sequence at a time: the
-norm of a few rows, their logits, and the most likely tokens with their log probabilities in
-one call, of which one is drawn.
+norm of a few rows, and their most likely tokens with their log probabilities straight from
+the hidden states, of which one is drawn.
 
     python examples/policy_head.py [--steps 60] [--tokens 2048] [--vocab 2000] [--hidden 256]
 
@@ -52,8 +52,8 @@ class PolicyHead(torch.nn.Module):
         """Draws a token per row of x among its top_k most likely ones: (tokens int32, their log
         probabilities under the whole distribution)."""
         h = flce.layer_norm(x, self.norm.weight, self.norm.bias, eps=self.norm.eps).y
-        r = flce.token_logprobs(h @ self.weight.bfloat16().T, None, top_k=top_k,
-                                temperature=self.temperature)
+        r = flce.linear_token_logprobs(h, self.weight.bfloat16(), None, top_k=top_k,
+                                       temperature=self.temperature)
         pick = torch.multinomial(r.top_logprob.exp(), 1, generator=generator)
         return r.top_id.gather(1, pick)[:, 0], r.top_logprob.gather(1, pick)[:, 0]
 
