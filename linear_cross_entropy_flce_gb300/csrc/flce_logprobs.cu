@@ -9,7 +9,7 @@
 // logits. One warp sorts them. A row where too many reach it is ranked by k passes
 // instead, each the largest key below the one before.
 //
-//   logprob_stream_kernel : rows of up to 880 KB. Persistent clusters of 1-8 CTAs, one row
+//   logprob_stream_kernel : rows of up to 832 KB. Persistent clusters of 1-8 CTAs, one row
 //       at a time; each CTA's slice is copied into shared memory by the bulk-copy engine,
 //       double-buffered, so both passes read shared memory and every logit leaves DRAM
 //       once. Most of the CTA's warps do the passes; one sorts the candidates of the row
@@ -17,15 +17,15 @@
 //       threshold while the sums are taken; one joins the parts of
 //       the rows that are this CTA's (each row's meet in another CTA of the cluster), so
 //       that none of it holds the passes up.
-//       8192 x 128256 bf16 (2.1 GB, 309 us at the copy rate): 370 us (5.7 TB/s), with 5 alternatives
-//       494, with 20 585; 4096 x 128256 fp32 295, 355, 381. Bound by the exponentials and maxima
+//       8192 x 128256 bf16 (2.1 GB, 309 us at the copy rate): 372 us (5.6 TB/s), with 5 alternatives
+//       494, with 20 582; 4096 x 128256 fp32 293, 355, 381. Bound by the exponentials and maxima
 //       beside the reads (two packed instructions for each pair of logits and pass), and with
 //       alternatives by the second look at the threads whose maximum reaches the threshold.
-//   logprob_warp_kernel : rows of up to 8 KB, one warp each: 16384 x 2000 bf16 17.4 us (3.8 TB/s).
+//   logprob_warp_kernel : rows of up to 8 KB, one warp each: 16384 x 2000 bf16 16.7 us (3.9 TB/s).
 //   logprob_rows_kernel : longer rows; one CTA each, read twice from global memory.
 //
 // Backward, elementwise: every entry of dZ from its logit and five numbers of its row. Bound by
-// HBM: 8192 x 128256 bf16 662 us (6.3 TB/s), 4096 x 128256 fp32 592 us (7.1 TB/s).
+// HBM: 8192 x 128256 bf16 590 us (7.1 TB/s), 4096 x 128256 fp32 590 us (7.1 TB/s).
 //
 // Rows may start at any element: the elements before the first 16-byte boundary and
 // after the last one are read singly.

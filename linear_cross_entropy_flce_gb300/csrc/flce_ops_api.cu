@@ -4,14 +4,17 @@
 // Launch sequences:
 //   flce_token_logprobs            one kernel
 //   flce_token_logprobs_backward   one kernel
-//   flce_linear_token_logprobs     the log-probability GEMM, then the join of its
+//   flce_linear_token_logprobs     up to 128 tokens: the padded copies of the tokens (up to 64),
+//                                  their product, the kernel of flce_token_logprobs over its
+//                                  logits; else the log-probability GEMM, then the join of its
 //                                  vocabulary ranges
 //   flce_linear_token_logprobs_backward   row coefficients, then per token block and
 //                                  vocabulary chunk the gradient GEMM and the dH / dW
 //                                  products (launch_backward_products)
 //   flce_layer_norm                one kernel
-//   flce_layer_norm_backward       column sums and their join, then dx
-//   flce_clip_grads                per table of tensors the squares, then the scaling
+//   flce_layer_norm_backward       dx with partial column sums, then their join; hidden sizes
+//                                  beyond what a CTA holds: column sums, dx, the join
+//   flce_clip_grads                per table of tensors the squares, then per table the scaling
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -53,9 +56,11 @@ int check_rows(int64_t N, int64_t V) {
 constexpr int kPlanPairs = 76;
 
 // Up to this many tokens the forward pass takes the logits of all of them (the kernel for few
-// tokens) and then their rows; above it the large GEMM, which does not store them. D = 4096, V =
-// 128256, with 5 alternatives: 1 token 167 us / 961 by the GEMM, 64 176 / 205, 128 197 / 206 (without
-// alternatives 192 / 190), 129 207.
+// tokens) and then their rows; above it the large GEMM, which does not store them. In us with 5
+// alternatives, here / by the GEMM, for 1, 64 and 128 tokens: D = 4096, V = 128256 168 / 880,
+// 177 / 209, 196 / 208; D = 2048, V = 128256 90 / 486, 100 / 123, 113 / 117; D = 1024, V = 32000
+// 22 / 98, 24 / 49, 27 / 49; D = 512, V = 8000 11 / 37, 13 / 37, 13 / 33. Without alternatives the
+// GEMM is level from 96 tokens on at the first (192 / 193 at 128) and ahead at the second (109 / 99).
 constexpr int64_t kFewTokens = 128;
 
 struct LogpPlan {
