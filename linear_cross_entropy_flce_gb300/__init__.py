@@ -14,6 +14,8 @@ from ._binding import (FLCE_ERR_ALIGN, FLCE_ERR_CUDA, FLCE_ERR_DEVICE, FLCE_ERR_
                        forward_backward, forward_backward_fp8, forward_noalloc, forward_shard,
                        forward_workspace_size, get_plan, lib, make_options, noalloc_setup,
                        quantize_e4m3, scale_grads, status_string, workspace_size)
+from ._embed_binding import (embedding, embedding_backward,
+                             embedding_backward_workspace_size)
 from ._ops_binding import (MAX_TOP_K, LayerNormResult, LogprobOptions, TokenLogprobs, clip_grads,
                            grad_norm, layer_norm, layer_norm_backward,
                            linear_logprobs_workspace_size, linear_token_logprobs,
@@ -21,9 +23,9 @@ from ._ops_binding import (MAX_TOP_K, LayerNormResult, LogprobOptions, TokenLogp
                            token_logprobs_backward)
 from .loss import (FusedLinearCrossEntropyFunction, FusedLinearCrossEntropyLoss,
                    fused_linear_cross_entropy)
-from .ops import (FusedLayerNorm, LayerNormFunction, LinearTokenLogprobsFunction,
-                  TokenLogprobsFunction, fused_layer_norm, fused_linear_token_logprobs,
-                  fused_token_logprobs)
+from .ops import (EmbeddingFunction, FusedEmbedding, FusedLayerNorm, LayerNormFunction,
+                  LinearTokenLogprobsFunction, TokenLogprobsFunction, fused_embedding,
+                  fused_layer_norm, fused_linear_token_logprobs, fused_token_logprobs)
 
 __all__ = ["FLCE_ERR_ALIGN", "FLCE_ERR_CUDA", "FLCE_ERR_DEVICE", "FLCE_ERR_LABEL_RANGE",
            "FLCE_ERR_NULL", "FLCE_ERR_OPTION", "FLCE_ERR_SHAPE", "FLCE_ERR_TIMEOUT",
@@ -39,4 +41,6 @@ __all__ = ["FLCE_ERR_ALIGN", "FLCE_ERR_CUDA", "FLCE_ERR_DEVICE", "FLCE_ERR_LABEL
            "linear_token_logprobs", "linear_token_logprobs_backward", "token_logprobs",
            "token_logprobs_backward", "FusedLayerNorm", "LayerNormFunction",
            "LinearTokenLogprobsFunction", "TokenLogprobsFunction", "fused_layer_norm",
-           "fused_linear_token_logprobs", "fused_token_logprobs"]
+           "fused_linear_token_logprobs", "fused_token_logprobs",
+           "embedding", "embedding_backward", "embedding_backward_workspace_size", "FusedEmbedding",
+           "EmbeddingFunction", "fused_embedding"]

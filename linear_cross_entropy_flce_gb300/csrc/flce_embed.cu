@@ -1,0 +1,333 @@
+// Embedding lookup and its gradient.
+//
+//   y_n = scale W[t_n],   dW_v = scale sum_{n: t_n = v} dy_n
+//
+// Lookup: threads side by side take vectors of a row, four at a time with their loads first.
+//
+// Gradient: with the tokens sorted by id (flce_embed_sort.cu), the sorted order is cut into
+// equal ranges, whatever ids they hold, so that a frequent id is shared out and a rare one costs
+// no more than its rows. A CTA adds up a range's rows of dy in fp32, kAhead rows' loads at a time, for
+// 128 vectors of columns; at the end of an id it writes that row of dW, and where an id goes on beyond
+// the range's ends the partial sum goes to the workspace, of two rows per range. A last launch
+// joins those, in the order of the ranges. The rows of ids without tokens are zeroed by further
+// CTAs of the first launch, which look the ids up in the sorted order.
+//
+// Bound by the bytes of dW for a large table, by dy for a small one.
+#include <cstdint>
+
+#include "flce_embed.h"
+#include "flce_gemm_params.h"
+#include "flce_launch.cuh"
+#include "flce_norm.cuh"
+
+namespace flce {
+
+namespace {
+
+// ---- lookup --------------------------------------------------------------------------
+
+constexpr int kLookup = 4;         // vectors of a row per thread
+constexpr int kLookupThreads = 128;
+
+// X threads per row; VW elements at a time.
+template <int kWbf16, int kBf16, int VW>
+__global__ void __launch_bounds__(kLookupThreads)
+    embedding_kernel(const void* weight, int64_t ldw, const int32_t* tokens, int N, int V, int nvec,
+                     float scale, int ignore_index, void* y, int64_t ldy, int32_t* status, int X) {
+  using In = Param<kWbf16, VW>;
+  using Out = Param<kBf16, VW>;
+  const int row = blockIdx.x * (kLookupThreads / X) + static_cast<int>(threadIdx.x) / X;
+  if (row >= N) return;
+  const int t = static_cast<int>(threadIdx.x) % X;
+  const int token = tokens[row];
+  const bool live = token >= 0 && token < V && token != ignore_index;
+  const float none = token == ignore_index ? 0.f : __uint_as_float(0x7FC00000u);
+  const int first = static_cast<int>(blockIdx.y) * X * kLookup + t;
+  if (!live && token != ignore_index && status != nullptr && first == 0)
+    atomicCAS(reinterpret_cast<int*>(status), 0, kStatusLabelRange);
+  const uint8_t* const from =
+      static_cast<const uint8_t*>(weight) + (live ? token : 0) * ldw * (kWbf16 ? 2 : 4);
+  uint8_t* const to = static_cast<uint8_t*>(y) + row * ldy * (kBf16 ? 2 : 4);
+  In in[kLookup];
+#pragma unroll
+  for (int k = 0; k < kLookup; ++k)
+    if (live && first + k * X < nvec) in[k].load(from, (first + k * X) * VW, 0.f);
+#pragma unroll
+  for (int k = 0; k < kLookup; ++k)
+    if (first + k * X < nvec) {
+      float v[VW];
+      if (live) in[k].widen(v);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) v[e] = live ? v[e] * scale : none;
+      Out out;
+      out.narrow(v);
+      out.save(to, (first + k * X) * VW);
+    }
+}
+
+// ---- gradient ------------------------------------------------------------------------
+
+constexpr int kGradThreads = 128;
+constexpr int kAhead = 8;
+constexpr int kZeroRows = 32;      // rows of dW that one CTA looks up and zeroes
+
+// The first sorted position whose id is at least v.
+__device__ __forceinline__ int lower_bound(const uint32_t* ids, int N, uint32_t v) {
+  int lo = 0, hi = N;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (ids[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// `sum` scaled to (or onto) dW at element `at`, VW elements.
+template <int kWbf16, int VW>
+__device__ __forceinline__ void put_row(void* dW, int64_t at, const float (&sum)[VW], float scale,
+                                        int accumulate) {
+  using Out = Param<kWbf16, VW>;
+  uint8_t* const p = static_cast<uint8_t*>(dW) + at * (kWbf16 ? 2 : 4);
+  float v[VW];
+  if (accumulate) {
+    Out old;
+    old.load(p, 0, 0.f);
+    old.widen(v);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = fmaf(sum[e], scale, v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = sum[e] * scale;
+  }
+  Out out;
+  out.narrow(v);
+  out.save(p, 0);
+}
+
+// CTAs [0, ranges * pieces): a range of the sorted order and a piece of the columns. The others (not
+// accumulating): kZeroRows rows of dW each.
+template <int kBf16, int kWbf16, int VW>
+__global__ void __launch_bounds__(kGradThreads)
+    embedding_grad_kernel(const void* dy, int64_t lddy, const uint32_t* ids, const uint32_t* perm, int N,
+                          int V, int D, float scale, void* dW, int64_t ldw, int accumulate, float* part,
+                          int ranges, int range, int pieces) {
+  using In = Param<kBf16, VW>;
+  __shared__ uint32_t s_id[kGradThreads], s_row[kGradThreads];
+  __shared__ int s_absent[kZeroRows];
+  start_next_launch();
+  wait_for_launch_before();
+  const int nvec = D / VW;
+  if (static_cast<int>(blockIdx.x) >= ranges * pieces) {
+    const int64_t row0 = (static_cast<int64_t>(blockIdx.x) - ranges * pieces) * kZeroRows;
+    if (threadIdx.x < kZeroRows) {
+      const int64_t v = row0 + threadIdx.x;
+      int absent = 0;
+      if (v < V) {
+        const int at = lower_bound(ids, N, static_cast<uint32_t>(v));
+        absent = at == N || ids[at] != static_cast<uint32_t>(v);
+      }
+      s_absent[threadIdx.x] = absent;
+    }
+    __syncthreads();
+    float zero[VW];
+#pragma unroll
+    for (int e = 0; e < VW; ++e) zero[e] = 0.f;
+    Param<kWbf16, VW> z;
+    z.narrow(zero);
+    for (int r = 0; r < kZeroRows; ++r) {
+      if (!s_absent[r]) continue;
+      uint8_t* const p = static_cast<uint8_t*>(dW) + (row0 + r) * ldw * (kWbf16 ? 2 : 4);
+      for (int i = threadIdx.x; i < nvec; i += kGradThreads) z.save(p, i * VW);
+    }
+    return;
+  }
+  const int r = static_cast<int>(blockIdx.x) / pieces;
+  const int first = r * range;
+  const int end = N - first < range ? N : first + range;
+  const int i = static_cast<int>(blockIdx.x) % pieces * kGradThreads + static_cast<int>(threadIdx.x);
+  const bool in = i < nvec;
+  // the ids on either side of the range (V: none)
+  const uint32_t none = static_cast<uint32_t>(V);
+  const uint32_t before = first > 0 ? ids[first - 1] : none;
+  const uint32_t after = end < N ? ids[end] : none;
+  float sum[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) sum[e] = 0.f;
+  bool head = true;   // no id has ended yet in this range
+  uint32_t id = none;
+  auto end_of_id = [&](bool last) {
+    if (id == none) return;
+    const bool joins = (head && id == before) || (last && id == after);
+    if (in) {
+      if (joins) {
+        const int slot = head && id == before ? 0 : 1;
+        Param<0, VW> out;
+        out.narrow(sum);
+        out.save(reinterpret_cast<uint8_t*>(part + (static_cast<int64_t>(r) * 2 + slot) * D), i * VW);
+      } else {
+        put_row<kWbf16, VW>(dW, id * ldw + static_cast<int64_t>(i) * VW, sum, scale, accumulate);
+      }
+    }
+    head = false;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) sum[e] = 0.f;
+  };
+  for (int at = first; at < end; at += kGradThreads) {
+    const int n = end - at < kGradThreads ? end - at : kGradThreads;
+    if (at > first) __syncthreads();
+    if (static_cast<int>(threadIdx.x) < n) {
+      s_id[threadIdx.x] = ids[at + threadIdx.x];
+      s_row[threadIdx.x] = perm[at + threadIdx.x];
+    }
+    __syncthreads();
+    for (int j = 0; j < n; j += kAhead) {
+      In row[kAhead];
+      if (in) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (j + k < n && s_id[j + k] != none)
+            row[k].load(static_cast<const uint8_t*>(dy) + s_row[j + k] * lddy * (kBf16 ? 2 : 4), i * VW, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (j + k >= n) break;
+        const uint32_t here = s_id[j + k];
+        if (here != id) {
+          end_of_id(false);
+          id = here;
+        }
+        if (in && here != none) {
+          float v[VW];
+          row[k].widen(v);
+          add_n(sum, v);
+        }
+      }
+    }
+  }
+  end_of_id(true);
+}
+
+// The ids that go on over the end of a range: the range in which one begins holds its first part in
+// slot 1, the ranges after it the others in slot 0. CTA (range, piece of 32 vectors of columns),
+// the parts dealt to its warps and added in a fixed order.
+constexpr int kJoinWarps = 8;
+
+template <int kWbf16, int VW>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    embedding_join_kernel(const float* part, const uint32_t* ids, int N, int V, int D, float scale, void* dW,
+                          int64_t ldw, int accumulate, int range, int pieces) {
+  __shared__ float s_sum[kJoinWarps][32][VW];
+  __shared__ int s_last;
+  wait_for_launch_before();
+  const int r = static_cast<int>(blockIdx.x) / pieces;   // all ranges but the last
+  const int first = r * range, end = first + range;
+  const uint32_t id = ids[end - 1];
+  if (id == static_cast<uint32_t>(V) || ids[end] != id) return;
+  if (first > 0 && ids[first - 1] == id) return;   // it began in an earlier range
+  if (threadIdx.x == 0) s_last = (lower_bound(ids, N, id + 1) - 1) / range;
+  __syncthreads();
+  const int last = s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = static_cast<int>(blockIdx.x) % pieces * 32 + lane;
+  const bool in = i < D / VW;
+  float sum[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) sum[e] = 0.f;
+  if (in) {
+#pragma unroll 4
+    for (int q = r + warp; q <= last; q += kJoinWarps) {
+      Param<0, VW> in_part;
+      float v[VW];
+      in_part.load(part + (static_cast<int64_t>(q) * 2 + (q == r ? 1 : 0)) * D, i * VW, 0.f);
+      in_part.widen(v);
+      add_n(sum, v);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e) s_sum[warp][lane][e] = sum[e];
+  __syncthreads();
+  if (warp != 0 || !in) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+    for (int e = 0; e < VW; ++e) sum[e] += s_sum[w][lane][e];
+  put_row<kWbf16, VW>(dW, id * ldw + static_cast<int64_t>(i) * VW, sum, scale, accumulate);
+}
+
+// f(VW) for the widest access: 8 elements, 4 or 1.
+template <typename F>
+cudaError_t with_width(int vw, F&& f) {
+  if (vw >= 8) return f(std::integral_constant<int, 8>{});
+  if (vw >= 4) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 1>{});
+}
+
+template <typename F>
+cudaError_t with_types(int a, int b, F&& f) {
+  using One = std::integral_constant<int, 1>;
+  using Zero = std::integral_constant<int, 0>;
+  if (a) return b ? f(One{}, One{}) : f(One{}, Zero{});
+  return b ? f(Zero{}, One{}) : f(Zero{}, Zero{});
+}
+
+// Elements that both matrices allow at a time: rows of 16-byte accesses, or 8-byte ones (fp32's
+// four at a time count as one of bf16's eight).
+int common_width(int D, int bf16_a, int64_t lda, const void* a, int bf16_b, int64_t ldb, const void* b) {
+  auto fits = [&](int v) {
+    auto one = [&](int bf16, int64_t ld, const void* p) {
+      const int elt = bf16 ? 2 : 4, bytes = v * elt < 16 ? v * elt : 16;
+      return ld * elt % bytes == 0 && reinterpret_cast<uintptr_t>(p) % static_cast<unsigned>(bytes) == 0;
+    };
+    return D % v == 0 && one(bf16_a, lda, a) && one(bf16_b, ldb, b);
+  };
+  return fits(8) ? 8 : fits(4) ? 4 : 1;
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const void* weight, int wbf16, int64_t ldw, const int32_t* tokens, int N,
+                             int V, int D, float scale, int ignore_index, void* y, int bf16, int64_t ldy,
+                             int32_t* status, cudaStream_t stream) {
+  const int vw = common_width(D, wbf16, ldw, weight, bf16, ldy, y);
+  return with_width(vw, [&](auto w) {
+    constexpr int VW = w();
+    const int nvec = D / VW;
+    int X = 8;
+    while (X < kLookupThreads && X < nvec) X *= 2;
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) * X + kLookupThreads - 1) / kLookupThreads),
+                    static_cast<unsigned>((nvec + X * kLookup - 1) / (X * kLookup)));
+    return with_types(wbf16, bf16, [&](auto wb, auto b) {
+      embedding_kernel<wb(), b(), VW><<<grid, kLookupThreads, 0, stream>>>(
+          weight, ldw, tokens, N, V, nvec, scale, ignore_index, y, ldy, status, X);
+      return cudaGetLastError();
+    });
+  });
+}
+
+cudaError_t launch_embedding_grad(const void* dy, int bf16, int64_t lddy, const uint32_t* ids,
+                                  const uint32_t* perm, int N, int V, int D, float scale, void* dW, int wbf16,
+                                  int64_t ldw, int accumulate, float* part, cudaStream_t stream) {
+  const int range = embed_range(N), ranges = (N + range - 1) / range;
+  const int vw = common_width(D, bf16, lddy, dy, wbf16, ldw, dW);
+  const unsigned zeros = accumulate ? 0 : static_cast<unsigned>((static_cast<int64_t>(V) + kZeroRows - 1) / kZeroRows);
+  return with_width(vw, [&](auto w) {
+    constexpr int VW = w();
+    const int nvec = D / VW;
+    return with_types(bf16, wbf16, [&](auto b, auto wb) {
+      const int pieces = (nvec + kGradThreads - 1) / kGradThreads;
+      const unsigned grid = static_cast<unsigned>(ranges * pieces) + zeros;
+      if (grid == 0) return cudaSuccess;
+      const cudaError_t e =
+          launch_after(embedding_grad_kernel<b(), wb(), VW>, dim3(grid), dim3(kGradThreads), 0, stream, dy, lddy,
+                       ids, perm, N, V, D, scale, dW, ldw, accumulate, part, ranges, range, pieces);
+      if (e != cudaSuccess || ranges <= 1) return e;
+      const int columns = (nvec + 31) / 32;
+      return launch_after(embedding_join_kernel<wb(), VW>,
+                          dim3(static_cast<unsigned>((ranges - 1) * columns)), dim3(32 * kJoinWarps), 0, stream,
+                          static_cast<const float*>(part), ids, N, V, D, scale, dW, ldw, accumulate, range,
+                          columns);
+    });
+  });
+}
+
+}  // namespace flce

@@ -1,0 +1,278 @@
+// Tokens sorted by id, stably: radix passes of up to 9 bits.
+//
+// A CTA ranks a tile of items by a digit. Its 32 warps own consecutive parts of the tile and
+// walk them 32 items at a time: lanes with equal digits find one another with match.any, and the
+// first of them advances the warp's counter of that digit, so that an item's rank among its
+// warp's equals is known and order is kept. Then the counters of all warps are summed digit by
+// digit, and every item knows its place.
+//
+// Up to kSortTile tokens are one tile: one launch takes all passes in shared memory. More go
+// through tiles with three launches a pass (count, offsets of every digit and tile, place).
+//
+// 8192 tokens of 128256 ids (two passes): see the caller's figures.
+#include <cstdint>
+
+#include "flce_embed.h"
+#include "flce_launch.cuh"
+
+namespace flce {
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 1 << kSortDigitBits;
+
+struct SortShared {
+  uint16_t count[kWarps][kBins];   // a tile has at most 16384 items
+  uint32_t base[kBins];
+  uint32_t warp_sum[kWarps];
+};
+
+__device__ __forceinline__ uint32_t key_of(const int32_t* tokens, int i, int V, int ignore_index) {
+  const int32_t t = tokens[i];
+  return t == ignore_index || t < 0 || t >= V ? static_cast<uint32_t>(V) : static_cast<uint32_t>(t);
+}
+
+// Item j of this thread is at warp * 32 * kItems + j * 32 + lane.
+template <int kItems>
+__device__ __forceinline__ int item_at(int j) {
+  return (threadIdx.x >> 5) * 32 * kItems + j * 32 + (threadIdx.x & 31);
+}
+
+// place[j]: for each of this thread's items (n of them in the tile, keys in key) its place by the
+// digit at `shift`; equal digits keep their order. `base` is what shared.base holds for each digit
+// where kGiven (the caller's, after a barrier here), else the tile's own offsets.
+template <int kItems, bool kGiven>
+__device__ __forceinline__ void rank_tile(SortShared& sh, const uint32_t (&key)[kItems], int n, int shift,
+                                          int bits, uint32_t (&place)[kItems]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t mask = (1u << bits) - 1u;
+  const int bins = 1 << bits;
+  for (int b = lane; b < bins; b += 32) sh.count[warp][b] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    const bool in = item_at<kItems>(j) < n;
+    const uint32_t d = in ? (key[j] >> shift) & mask : kBins;   // kBins: no item
+    const uint32_t peers = __match_any_sync(0xffffffffu, d);
+    const int first = __ffs(static_cast<int>(peers)) - 1;
+    uint32_t before = 0;
+    if (in && lane == first) {
+      before = sh.count[warp][d];
+      sh.count[warp][d] = static_cast<uint16_t>(before + __popc(peers));
+    }
+    before = __shfl_sync(0xffffffffu, before, first);
+    place[j] = before + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+  }
+  __syncthreads();
+  // thread b: digit b's counters become offsets among the warps; the digits' totals are scanned
+  uint32_t total = 0;
+  if (threadIdx.x < bins) {
+#pragma unroll 8
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t c = sh.count[w][threadIdx.x];
+      sh.count[w][threadIdx.x] = static_cast<uint16_t>(total);
+      total += c;
+    }
+  }
+  if constexpr (!kGiven) {
+    uint32_t sum = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) sh.warp_sum[warp] = sum;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < warp && w < kBins / 32; ++w) before += sh.warp_sum[w];
+    if (threadIdx.x < bins) sh.base[threadIdx.x] = before + sum - total;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kItems; ++j)
+    if (item_at<kItems>(j) < n) {
+      const uint32_t d = (key[j] >> shift) & mask;
+      place[j] += sh.base[d] + sh.count[warp][d];
+    }
+}
+
+template <int kItems>
+__global__ void __launch_bounds__(kThreads, 1)
+    sort_one_tile_kernel(const int32_t* tokens, int N, int V, int ignore_index, int bits, int passes,
+                         uint32_t* ids, uint32_t* perm) {
+  extern __shared__ uint32_t s_dyn[];   // [2][1024 kItems]: ids, places
+  __shared__ SortShared sh;
+  start_next_launch();
+  uint32_t* const s_key = s_dyn;
+  uint32_t* const s_idx = s_dyn + kThreads * kItems;
+  uint32_t key[kItems], idx[kItems], place[kItems];
+#pragma unroll
+  for (int j = 0; j < kItems; ++j) {
+    const int i = item_at<kItems>(j);
+    idx[j] = static_cast<uint32_t>(i);
+    key[j] = i < N ? key_of(tokens, i, V, ignore_index) : 0;
+  }
+  const int per = (bits + passes - 1) / passes;
+  for (int p = 0; p < passes; ++p) {
+    rank_tile<kItems, false>(sh, key, N, p * per, per, place);
+    if (p == passes - 1) break;
+#pragma unroll
+    for (int j = 0; j < kItems; ++j)
+      if (item_at<kItems>(j) < N) {
+        s_key[place[j]] = key[j];
+        s_idx[place[j]] = idx[j];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+      const int i = item_at<kItems>(j);
+      if (i < N) {
+        key[j] = s_key[i];
+        idx[j] = s_idx[i];
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < kItems; ++j)
+    if (item_at<kItems>(j) < N) {
+      ids[place[j]] = key[j];
+      perm[place[j]] = idx[j];
+    }
+}
+
+// ---- several tiles -------------------------------------------------------------------
+
+constexpr int kTileItems = kSortTile / kThreads;
+
+// keys null: the first pass, from the tokens
+__global__ void __launch_bounds__(kThreads)
+    sort_count_kernel(const int32_t* tokens, const uint32_t* keys, int N, int V, int ignore_index,
+                      int shift, int bits, uint32_t* counts) {
+  __shared__ uint32_t s_count[kBins];
+  const int bins = 1 << bits;
+  for (int b = threadIdx.x; b < bins; b += kThreads) s_count[b] = 0;
+  __syncthreads();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSortTile;
+#pragma unroll
+  for (int j = 0; j < kTileItems; ++j) {
+    const int64_t i = first + j * kThreads + threadIdx.x;
+    if (i < N) {
+      const uint32_t k = keys != nullptr ? keys[i] : key_of(tokens, static_cast<int>(i), V, ignore_index);
+      atomicAdd(&s_count[(k >> shift) & (bins - 1u)], 1u);
+    }
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < bins; b += kThreads)
+    counts[static_cast<int64_t>(b) * gridDim.x + blockIdx.x] = s_count[b];
+}
+
+// In place: the sum of the entries before each, one CTA.
+__global__ void __launch_bounds__(kThreads) sort_offsets_kernel(uint32_t* counts, int64_t entries) {
+  __shared__ uint32_t s_sum[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t carry = 0;
+  for (int64_t at = 0; at < entries; at += kThreads * 4) {
+    const int64_t i = at + threadIdx.x * 4;
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = i + k < entries ? counts[i + k] : 0;
+    uint32_t sum = c[0] + c[1] + c[2] + c[3];
+    const uint32_t own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+    uint32_t before = carry, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_sum[w];
+      all += s_sum[w];
+    }
+    before += sum - own;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k < entries) counts[i + k] = before;
+      before += c[k];
+    }
+    carry += all;
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    sort_place_kernel(const int32_t* tokens, const uint32_t* keys, const uint32_t* places, int N, int V,
+                      int ignore_index, int shift, int bits, const uint32_t* offsets, uint32_t* ids,
+                      uint32_t* perm) {
+  __shared__ SortShared sh;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSortTile;
+  const int n = static_cast<int>(N - first < kSortTile ? N - first : kSortTile);
+  uint32_t key[kTileItems], place[kTileItems];
+#pragma unroll
+  for (int j = 0; j < kTileItems; ++j) {
+    const int i = item_at<kTileItems>(j);
+    key[j] = i >= n ? 0
+             : keys != nullptr ? keys[first + i]
+                               : key_of(tokens, static_cast<int>(first + i), V, ignore_index);
+  }
+  const int bins = 1 << bits;
+  for (int b = threadIdx.x; b < bins; b += kThreads)
+    sh.base[b] = offsets[static_cast<int64_t>(b) * gridDim.x + blockIdx.x];
+  rank_tile<kTileItems, true>(sh, key, n, shift, bits, place);
+#pragma unroll
+  for (int j = 0; j < kTileItems; ++j) {
+    const int i = item_at<kTileItems>(j);
+    if (i < n) {
+      ids[place[j]] = key[j];
+      perm[place[j]] = places != nullptr ? places[first + i] : static_cast<uint32_t>(first + i);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_sort_tokens(const int32_t* tokens, int N, int V, int ignore_index, uint32_t* ids,
+                               uint32_t* perm, uint32_t* ids2, uint32_t* perm2, uint32_t* counts,
+                               cudaStream_t stream) {
+  int bits = 1;   // of the keys 0 to V
+  while ((static_cast<int64_t>(V) >> bits) != 0) ++bits;
+  const int passes = (bits + kSortDigitBits - 1) / kSortDigitBits;
+  if (N <= kSortTile) {
+    auto go = [&](auto kern, int items) {
+      const int smem = kThreads * items * 8;
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      kern<<<1, kThreads, smem, stream>>>(tokens, N, V, ignore_index, bits, passes, ids, perm);
+      return cudaGetLastError();
+    };
+    if (N <= kThreads) return go(sort_one_tile_kernel<1>, 1);
+    if (N <= kThreads * 4) return go(sort_one_tile_kernel<4>, 4);
+    if (N <= kThreads * 8) return go(sort_one_tile_kernel<8>, 8);
+    return go(sort_one_tile_kernel<16>, 16);
+  }
+  const int tiles = (N + kSortTile - 1) / kSortTile;
+  const int per = (bits + passes - 1) / passes;
+  const uint32_t *keys = nullptr, *places = nullptr;
+  for (int p = 0; p < passes; ++p) {
+    // the last pass ends in ids and perm
+    const bool second = (passes - 1 - p) % 2 != 0;
+    uint32_t* const to_ids = second ? ids2 : ids;
+    uint32_t* const to_perm = second ? perm2 : perm;
+    sort_count_kernel<<<tiles, kThreads, 0, stream>>>(tokens, keys, N, V, ignore_index, p * per, per, counts);
+    sort_offsets_kernel<<<1, kThreads, 0, stream>>>(counts, static_cast<int64_t>(tiles) << per);
+    sort_place_kernel<<<tiles, kThreads, 0, stream>>>(tokens, keys, places, N, V, ignore_index, p * per, per,
+                                                      counts, to_ids, to_perm);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    keys = to_ids;
+    places = to_perm;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace flce

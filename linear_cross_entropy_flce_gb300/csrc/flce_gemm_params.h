@@ -77,6 +77,7 @@ __host__ __device__ constexpr bool epi_writes_g(int epi) { return epi == EPI_GRA
 // to what is there (TMA reduce-add), or store rounded to bf16.
 enum OutMode { OUT_STORE_F32 = 0, OUT_ADD_F32 = 1, OUT_STORE_BF16 = 2 };
 
+constexpr int kStatusLabelRange = 8;  // FLCE_ERR_LABEL_RANGE
 constexpr int kStatusTimeout = 9;  // FLCE_ERR_TIMEOUT
 
 // Instruction descriptor for kind::f16 with bf16 A/B and an fp32 accumulator.

@@ -136,6 +136,15 @@ struct Param {
     for (int k = 0; k < VW / kStep; ++k)
       *reinterpret_cast<typename P::Raw*>(p + (i + k * kStep) * (kWbf16 ? 2 : 4)) = raw[k];
   }
+  __device__ void narrow(const float (&v)[VW]) {
+#pragma unroll
+    for (int k = 0; k < VW / kStep; ++k) {
+      float q[kStep];
+#pragma unroll
+      for (int e = 0; e < kStep; ++e) q[e] = v[k * kStep + e];
+      raw[k] = P::narrow(q);
+    }
+  }
   __device__ void widen(float (&v)[VW]) const {
 #pragma unroll
     for (int k = 0; k < VW / kStep; ++k) {

@@ -1,4 +1,4 @@
-// The ordinary calls of include/flce_ops.h from Python, without ctypes: reads the tensors,
+// The ordinary calls of include/flce_ops.h and flce_embed.h from Python, without ctypes: reads the tensors,
 // allocates the outputs (and the workspace) on the current stream and enqueues the call.
 //
 // A kernel of a decoding step takes a few microseconds; marshalling its arguments through
@@ -14,6 +14,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
@@ -22,6 +23,7 @@
 #include <exception>
 #include <vector>
 
+#include "../../include/flce_embed.h"
 #include "../../include/flce_ops.h"
 
 namespace {
@@ -411,6 +413,70 @@ FUNCTION(clip_grads) {
   });
 }
 
+// A torch.dtype, or `none` for None.
+at::ScalarType type_of(PyObject* o, at::ScalarType none) {
+  if (o == Py_None) return none;
+  check(THPDtype_Check(o));
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+int code_of(at::ScalarType t) {
+  if (t == at::kFloat) return FLCE_DTYPE_F32;
+  if (t == at::kBFloat16) return FLCE_DTYPE_BF16;
+  throw Refused{};
+}
+
+// int32 tokens of any shape, dense.
+const Tensor& ids_of(PyObject* o, int device) {
+  const Tensor& t = required(o, device);
+  check(t.scalar_type() == at::kInt && t.is_contiguous());
+  return t;
+}
+
+// (weight, tokens, scale, ignore_index, dtype)
+FUNCTION(embedding) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    const Here h;
+    const Tensor &w = required(a[0], h.device), &ids = ids_of(a[1], h.device);
+    const int wcode = dtype_of(w);
+    const int64_t ldw = rows_of(w), D = w.size(1);
+    const at::ScalarType type = type_of(a[4], w.scalar_type());
+    const int code = code_of(type);
+    std::vector<int64_t> shape(ids.sizes().begin(), ids.sizes().end());
+    shape.push_back(D);
+    const float scale = static_cast<float>(number(a[2]));
+    const int32_t ignore = static_cast<int32_t>(integer(a[3]));
+    const Tensor y = h.empty(shape, type);
+    check(flce_embedding(w.const_data_ptr(), wcode, ldw, ids.const_data_ptr<int32_t>(), ids.numel(), w.size(0),
+                         D, scale, ignore, y.data_ptr(), code, D, nullptr, h.stream), "flce_embedding");
+    return THPVariable_Wrap(y);
+  });
+}
+
+// (dy, tokens, rows, scale, ignore_index, dtype)
+FUNCTION(embedding_backward) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const Here h;
+    const Tensor &dy = required(a[0], h.device), &ids = ids_of(a[1], h.device);
+    const int dtype = dtype_of(dy);
+    check(dy.dim() == ids.dim() + 1 && dy.sizes().slice(0, dy.dim() - 1) == ids.sizes());
+    const NormRows r(dy);
+    const int64_t rows = integer(a[2]);
+    const at::ScalarType type = type_of(a[5], dy.scalar_type());
+    const int code = code_of(type);
+    const float scale = static_cast<float>(number(a[3]));
+    const int32_t ignore = static_cast<int32_t>(integer(a[4]));
+    size_t bytes = 0;
+    check(flce_embedding_backward_workspace_size(r.N, rows, r.D, &bytes), "flce_embedding_backward_workspace_size");
+    const Tensor dW = h.empty({rows, r.D}, type);
+    const Tensor ws = h.empty({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, at::kByte);
+    check(flce_embedding_backward(dy.const_data_ptr(), dtype, r.ld, ids.const_data_ptr<int32_t>(), r.N, rows, r.D,
+                                  scale, ignore, dW.data_ptr(), code, r.D, 0, ws.data_ptr(), bytes, h.stream),
+          "flce_embedding_backward");
+    return THPVariable_Wrap(dW);
+  });
+}
+
 // (FLCEError): the type of the errors raised here.
 FUNCTION(set_error_type) {
   return guarded(n, 1, [&]() -> PyObject* {
@@ -425,6 +491,7 @@ PyMethodDef methods[] = {METHOD(token_logprobs),        METHOD(token_logprobs_ba
                          METHOD(linear_token_logprobs), METHOD(linear_token_logprobs_backward),
                          METHOD(layer_norm),            METHOD(layer_norm_backward),
                          METHOD(clip_grads),            METHOD(set_error_type),
+                         METHOD(embedding),             METHOD(embedding_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_flce_ops", nullptr, -1, methods,
                       nullptr,               nullptr,     nullptr, nullptr};

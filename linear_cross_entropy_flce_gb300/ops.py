@@ -14,6 +14,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
+from . import _embed_binding as E
 from . import _ops_binding as B
 
 
@@ -154,6 +155,27 @@ class LayerNormFunction(torch.autograd.Function):
         return dx, dw, db, None
 
 
+class EmbeddingFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, weight, scale: float, ignore_index: int, dtype):
+        y = tokens if tokens.dtype == torch.int32 else tokens.to(torch.int32)
+        y = y if y.is_contiguous() else y.contiguous()
+        ctx.save_for_backward(y)
+        ctx.table, ctx.options = (weight.shape[0], weight.dtype), (scale, ignore_index)
+        return E.embedding(weight, y, scale=scale, ignore_index=ignore_index, dtype=dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        if not ctx.needs_input_grad[1]:
+            return None, None, None, None, None
+        tokens, = ctx.saved_tensors
+        scale, ignore_index = ctx.options
+        dW = E.embedding_backward(dy, tokens, ctx.table[0], scale=scale, ignore_index=ignore_index,
+                                  dtype=ctx.table[1])
+        return None, dW, None, None, None
+
+
 def fused_token_logprobs(logits, tokens, *, temperature: float = 1.0, ignore_index: int = -100):
     """(logprob, entropy, lse), each of tokens' shape and fp32, of tokens [...] over
     logits [..., V] (fp32 or bf16); differentiable in the logits."""
@@ -190,3 +212,25 @@ class FusedLayerNorm(torch.nn.Module):
 
     def forward(self, x):
         return fused_layer_norm(x, self.weight, self.bias, self.eps)
+
+
+def fused_embedding(tokens, weight, *, scale: float = 1.0, ignore_index: int = -100, dtype=None):
+    """scale * weight[tokens] of integer tokens [...], as `dtype` (fp32 or bf16; the weight's by
+    default); rows of ignore_index are 0. Differentiable in weight [V, D] (fp32 or bf16), whose
+    gradient sums each id's tokens in fp32 in a fixed order."""
+    return EmbeddingFunction.apply(tokens, weight, float(scale), int(ignore_index), dtype)
+
+
+class FusedEmbedding(torch.nn.Module):
+    """nn.Module form: FusedEmbedding(vocab, hidden)(tokens). A table shared with the head is
+    its `weight`."""
+
+    def __init__(self, num_embeddings: int, embedding_dim: int, scale: float = 1.0, ignore_index: int = -100,
+                 device=None, dtype=None, out_dtype=None):
+        super().__init__()
+        self.scale, self.ignore_index, self.out_dtype = float(scale), int(ignore_index), out_dtype
+        self.weight = torch.nn.Parameter(torch.randn(num_embeddings, embedding_dim, device=device, dtype=dtype))
+
+    def forward(self, tokens):
+        return fused_embedding(tokens, self.weight, scale=self.scale, ignore_index=self.ignore_index,
+                               dtype=self.out_dtype)
