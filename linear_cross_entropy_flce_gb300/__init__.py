@@ -14,6 +14,8 @@ from ._binding import (FLCE_ERR_ALIGN, FLCE_ERR_CUDA, FLCE_ERR_DEVICE, FLCE_ERR_
                        forward_backward, forward_backward_fp8, forward_noalloc, forward_shard,
                        forward_workspace_size, get_plan, lib, make_options, noalloc_setup,
                        quantize_e4m3, scale_grads, status_string, workspace_size)
+from ._blocks_binding import (PackedRows, layer_norm_packed, layer_norm_packed_backward, pack_e4m3,
+                              packed_row_bytes, unpack_e4m3)
 from ._embed_binding import (embedding, embedding_backward,
                              embedding_backward_workspace_size)
 from ._ops_binding import (MAX_TOP_K, LayerNormResult, LogprobOptions, TokenLogprobs, clip_grads,
@@ -24,7 +26,7 @@ from ._ops_binding import (MAX_TOP_K, LayerNormResult, LogprobOptions, TokenLogp
 from .loss import (FusedLinearCrossEntropyFunction, FusedLinearCrossEntropyLoss,
                    fused_linear_cross_entropy)
 from .ops import (EmbeddingFunction, FusedEmbedding, FusedLayerNorm, LayerNormFunction,
-                  LinearTokenLogprobsFunction, TokenLogprobsFunction, fused_embedding,
+                  LinearTokenLogprobsFunction, PackedLayerNormFunction, TokenLogprobsFunction, fused_embedding,
                   fused_layer_norm, fused_linear_token_logprobs, fused_token_logprobs)
 
 __all__ = ["FLCE_ERR_ALIGN", "FLCE_ERR_CUDA", "FLCE_ERR_DEVICE", "FLCE_ERR_LABEL_RANGE",
@@ -43,4 +45,6 @@ __all__ = ["FLCE_ERR_ALIGN", "FLCE_ERR_CUDA", "FLCE_ERR_DEVICE", "FLCE_ERR_LABEL
            "LinearTokenLogprobsFunction", "TokenLogprobsFunction", "fused_layer_norm",
            "fused_linear_token_logprobs", "fused_token_logprobs",
            "embedding", "embedding_backward", "embedding_backward_workspace_size", "FusedEmbedding",
-           "EmbeddingFunction", "fused_embedding"]
+           "EmbeddingFunction", "fused_embedding", "PackedRows", "layer_norm_packed",
+           "layer_norm_packed_backward", "pack_e4m3", "packed_row_bytes", "unpack_e4m3",
+           "PackedLayerNormFunction"]

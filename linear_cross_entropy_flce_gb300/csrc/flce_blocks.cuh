@@ -1,0 +1,78 @@
+// Arithmetic of the block-scaled formats.
+//
+// Scales that are powers of two come from the bits of the block's largest magnitude: with amax =
+// 1.m 2^E and the format's largest value 1.75 2^8 (E4M3) or 1.5 2^2 (E2M1), the smallest e with
+// amax <= largest 2^e is E - 8 (or E - 2), and one more where 1.m is above 1.75 (or 1.5). Dividing
+// by 2^e is then exact, and the hardware's conversion rounds once, to nearest even. Magnitudes
+// are compared as the integers their bits are, by which infinities and NaN come out largest.
+#pragma once
+
+#include <cstdint>
+
+#include "flce_blocks.h"
+
+namespace flce {
+namespace {
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// The byte e + 127 of a block with largest magnitude amax (its bits): kExp and kMant from the
+// format's largest value. 255 for an infinity or NaN, 0 where amax is that small.
+template <int kExp, uint32_t kMant>
+__device__ __forceinline__ uint32_t power_scale_byte(uint32_t amax) {
+  if (amax >= kInfBits) return 255u;
+  const int b = static_cast<int>(amax >> 23) - kExp + ((amax & 0x7FFFFFu) > kMant ? 1 : 0);
+  return static_cast<uint32_t>(b > 0 ? b : 0);
+}
+__device__ __forceinline__ uint32_t e4m3_scale_byte(uint32_t amax) {
+  return power_scale_byte<8, 0x600000u>(amax);
+}
+
+// 2^(byte - 127), NaN for 255; and its reciprocal (of a byte up to 253).
+__device__ __forceinline__ float power_of_byte(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x400000u : b == 255u ? 0x7FC00000u : b << 23);
+}
+__device__ __forceinline__ float inverse_power_of_byte(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+
+// Two values to E4M3, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two E4M3 codes (the low 16 bits) to fp32.
+__device__ __forceinline__ void widen_e4m3x2(uint32_t codes, float& lo, float& hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+}
+
+// Four codes of values times inv.
+__device__ __forceinline__ uint32_t e4m3x4(const float* v, float inv) {
+  return e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The bits of the largest magnitude of VW values.
+template <int VW>
+__device__ __forceinline__ uint32_t largest_bits(const float (&v)[VW]) {
+  uint32_t m = magnitude(v[0]);
+#pragma unroll
+  for (int e = 1; e < VW; ++e) m = max(m, magnitude(v[e]));
+  return m;
+}
+
+// Over groups of kLanes neighbouring lanes (a power of two).
+template <int kLanes>
+__device__ __forceinline__ uint32_t largest_of_lanes(uint32_t m) {
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+}  // namespace
+}  // namespace flce

@@ -21,6 +21,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "flce_blocks.cuh"
 #include "flce_internal.h"
 #include "flce_launch.cuh"
 #include "flce_norm.cuh"
@@ -81,27 +82,37 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
+// Element i of row `row` of x, or (packed) of the 8-bit record there.
+__device__ __forceinline__ float value_of(const void* x, int bf16, int64_t ldx, int64_t row, int i, int D,
+                                          int packed) {
+  if (!packed) return load_as_f32(x, row * ldx + i, bf16);
+  const uint8_t* const record = static_cast<const uint8_t*>(x) + row * ldx;
+  float v, none;
+  widen_e4m3x2(record[i], v, none);
+  return v * power_of_byte(record[packed_codes(D) + (i >> 5)]);
+}
+
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_dx_kernel(const void* dy, int64_t lddy, const void* x, int bf16, int64_t ldx,
                          const void* weight, int wbf16, const float* mean_in,
-                         const float* rstd_in, int N, int D, void* dx, int64_t lddx) {
+                         const float* rstd_in, int N, int D, void* dx, int64_t lddx, int packed) {
   __shared__ float2 s_part[kNormThreads / 32];
   for (int row = blockIdx.x; row < N; row += gridDim.x) {
-    const int64_t xr = row * ldx, yr = row * lddy, gr = row * lddx;
+    const int64_t yr = row * lddy, gr = row * lddx;
     const float mean = mean_in[row], rstd = rstd_in[row];
     float2 sum = make_float2(0.f, 0.f);
     for (int i = threadIdx.x; i < D; i += kNormThreads) {
       const float w = weight != nullptr ? load_as_f32(weight, i, wbf16) : 1.f;
       const float g = load_as_f32(dy, yr + i, bf16) * w;
       sum.x += g;
-      sum.y = fmaf(g, (load_as_f32(x, xr + i, bf16) - mean) * rstd, sum.y);
+      sum.y = fmaf(g, (value_of(x, bf16, ldx, row, i, D, packed) - mean) * rstd, sum.y);
     }
     sum = block_sum2(sum, s_part);
     const float mg = sum.x / D, mgh = sum.y / D;
     for (int i = threadIdx.x; i < D; i += kNormThreads) {
       const float w = weight != nullptr ? load_as_f32(weight, i, wbf16) : 1.f;
       const float g = load_as_f32(dy, yr + i, bf16) * w;
-      const float h = (load_as_f32(x, xr + i, bf16) - mean) * rstd;
+      const float h = (value_of(x, bf16, ldx, row, i, D, packed) - mean) * rstd;
       store_from_f32(dx, gr + i, rstd * (g - mg - h * mgh), bf16);
     }
   }
@@ -111,14 +122,14 @@ __global__ void __launch_bounds__(kNormThreads)
 __global__ void __launch_bounds__(kColumnThreads)
     layer_norm_columns_kernel(const void* dy, int64_t lddy, const void* x, int bf16, int64_t ldx,
                               const float* mean, const float* rstd, int N, int D, int ranges,
-                              float* part) {
+                              float* part, int packed) {
   const int i = blockIdx.x * kColumnThreads + threadIdx.x;
   if (i >= D) return;
   const int range = blockIdx.y;
   float dw = 0.f, db = 0.f;
   for (int row = range; row < N; row += ranges) {
     const float d = load_as_f32(dy, row * lddy + i, bf16);
-    dw = fmaf(d, (load_as_f32(x, row * ldx + i, bf16) - mean[row]) * rstd[row], dw);
+    dw = fmaf(d, (value_of(x, bf16, ldx, row, i, D, packed) - mean[row]) * rstd[row], dw);
     db += d;
   }
   part[(static_cast<int64_t>(range) * 2) * D + i] = dw;
@@ -237,9 +248,37 @@ __global__ void __launch_bounds__(1024, kNv * (Pack<kBf16, VW>::kBytes + 3) / 4 
   }
 }
 
+// VW neighbouring codes of an 8-bit record, of one block, and their scale.
+template <int VW>
+struct RowCodes {
+  uint32_t w[(VW + 3) / 4], byte;
+  __device__ void load(const uint8_t* record, int i, int D) {
+    if constexpr (VW >= 4) {
+#pragma unroll
+      for (int k = 0; k < VW / 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(record + i)[k];
+    } else if constexpr (VW == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(record + i);
+    } else {
+      w[0] = record[i];
+    }
+    byte = record[packed_codes(D) + (i >> 5)];
+  }
+  // (x~ - mean) r
+  __device__ void centred(float (&v)[VW], float mean, float r) const {
+    const float scale = power_of_byte(byte);
+#pragma unroll
+    for (int e = 0; e < VW; e += 2) {
+      float lo, hi;
+      widen_e4m3x2(w[e / 4] >> (e % 4 * 8), lo, hi);
+      v[e] = fmaf(lo, scale, -mean) * r;
+      if (e + 1 < VW) v[(e + 1) % VW] = fmaf(hi, scale, -mean) * r;
+    }
+  }
+};
+
 // dx and, in part (not null), this CTA's sums over its rows: part[blockIdx.x][0][i] of dy h
-// and [1][i] of dy.
-template <int kBf16, int VW, int kNv>
+// and [1][i] of dy. kPacked: x is 8-bit records, ldx their bytes.
+template <int kBf16, int VW, int kNv, int kPacked>
 __global__ void __launch_bounds__(512, kNv * VW <= 8 && VW > 1 ? 2 : 1)
     layer_norm_grad_kernel(const void* dy, int64_t lddy, const void* x, int64_t ldx,
                            const void* weight, int wbf16, const float* __restrict__ mean_in,
@@ -262,7 +301,9 @@ __global__ void __launch_bounds__(512, kNv * VW <= 8 && VW > 1 ? 2 : 1)
     for (int e = 0; e < VW; ++e) dw[k][e] = db[k][e] = 0.f;
     if (t + k * R < nvec) load_param<VW>(weight, (t + k * R) * VW, wbf16, 1.f, w[k]);
   }
-  Raw rx[kNv], rg[kNv];
+  Raw rg[kNv];
+  [[maybe_unused]] Raw rx[kNv];
+  [[maybe_unused]] RowCodes<VW> cx[kNv];
   float mean = 0.f, rstd = 0.f;
   auto fetch = [&](int row) {
     if (row < N) {
@@ -270,7 +311,8 @@ __global__ void __launch_bounds__(512, kNv * VW <= 8 && VW > 1 ? 2 : 1)
       for (int k = 0; k < kNv; ++k) {
         const int i = t + k * R;
         if (i < nvec) {
-          rx[k] = P::load(x, static_cast<int64_t>(row) * ldx + static_cast<int64_t>(i) * VW);
+          if constexpr (kPacked) cx[k].load(static_cast<const uint8_t*>(x) + row * ldx, i * VW, D);
+          else rx[k] = P::load(x, static_cast<int64_t>(row) * ldx + static_cast<int64_t>(i) * VW);
           rg[k] = P::load(dy, static_cast<int64_t>(row) * lddy + static_cast<int64_t>(i) * VW);
         }
       }
@@ -290,11 +332,12 @@ __global__ void __launch_bounds__(512, kNv * VW <= 8 && VW > 1 ? 2 : 1)
 #pragma unroll
     for (int k = 0; k < kNv; ++k)
       if (live && t + k * R < nvec) {
-        P::widen(rx[k], h[k]);
+        if constexpr (kPacked) cx[k].centred(h[k], mean, r);
+        else P::widen(rx[k], h[k]);
         P::widen(rg[k], g[k]);
 #pragma unroll
         for (int e = 0; e < VW; ++e) {
-          h[k][e] = (h[k][e] - mean) * r;
+          if constexpr (!kPacked) h[k][e] = (h[k][e] - mean) * r;
           dw[k][e] = fmaf(g[k][e], h[k][e], dw[k][e]);
           db[k][e] += g[k][e];
           g[k][e] *= w[k][e];
@@ -388,7 +431,7 @@ cudaError_t norm_rows(const void* x, int64_t ldx, const void* weight, const void
 constexpr int kGradBlock = 512;
 constexpr int grad_elems(int vw) { return vw == 1 ? 8 : 16; }
 
-template <int kBf16, int VW>
+template <int kBf16, int VW, int kPacked>
 cudaError_t norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
                       int wbf16, const float* mean, const float* rstd, int N, int D, void* dx,
                       int64_t lddx, float* part, int* ranges, int sms, cudaStream_t stream) {
@@ -406,11 +449,11 @@ cudaError_t norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
     return cudaGetLastError();
   };
   const int per = (nvec + R - 1) / R;
-  if (per <= 1) return go(layer_norm_grad_kernel<kBf16, VW, 1>);
-  if (per <= 2) return go(layer_norm_grad_kernel<kBf16, VW, 2>);
+  if (per <= 1) return go(layer_norm_grad_kernel<kBf16, VW, 1, kPacked>);
+  if (per <= 2) return go(layer_norm_grad_kernel<kBf16, VW, 2, kPacked>);
   if constexpr (kMost >= 4)
-    if (per <= 4) return go(layer_norm_grad_kernel<kBf16, VW, 4>);
-  return go(layer_norm_grad_kernel<kBf16, VW, kMost>);
+    if (per <= 4) return go(layer_norm_grad_kernel<kBf16, VW, 4, kPacked>);
+  return go(layer_norm_grad_kernel<kBf16, VW, kMost, kPacked>);
 }
 
 cudaError_t join_columns(const float* part, int ranges, int D, void* dweight, void* dbias,
@@ -455,25 +498,33 @@ cudaError_t launch_layer_norm(const void* x, int bf16, int64_t ldx, const void* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int bf16,
-                                       int64_t ldx, const void* weight, int wbf16,
-                                       const float* mean, const float* rstd, int N, int D,
-                                       void* dx, int64_t lddx, void* dweight, void* dbias,
-                                       float* part, int sms, cudaStream_t stream) {
+namespace {
+
+// x: its rows, or (kPacked) 8-bit records, ldx their bytes.
+template <int kPacked>
+cudaError_t norm_backward(const void* dy, int64_t lddy, const void* x, int bf16, int64_t ldx,
+                          const void* weight, int wbf16, const float* mean, const float* rstd, int N, int D,
+                          void* dx, int64_t lddx, void* dweight, void* dbias, float* part, int sms,
+                          cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   const bool columns = dweight != nullptr || dbias != nullptr;
   int ranges = 0;
   if (N > 0 && norm_stream_fits(D, bf16 ? 2 : 4)) {
-    e = launch_norm_stream_backward(dy, lddy, x, bf16, ldx, weight, wbf16, mean, rstd, N, D, dx,
-                                    lddx, dweight, dbias, columns ? part : nullptr, &ranges, sms,
-                                    stream);
+    float* const to = columns ? part : nullptr;
+    if constexpr (kPacked)
+      e = launch_norm_stream_backward_packed(dy, lddy, static_cast<const uint8_t*>(x), bf16, weight, wbf16,
+                                             mean, rstd, N, D, dx, lddx, dweight, dbias, to, &ranges, sms,
+                                             stream);
+    else
+      e = launch_norm_stream_backward(dy, lddy, x, bf16, ldx, weight, wbf16, mean, rstd, N, D, dx, lddx,
+                                      dweight, dbias, to, &ranges, sms, stream);
     if (e == cudaSuccess && columns && ranges > 1)
       return join_columns(part, ranges, D, dweight, dbias, wbf16, stream);
     if (e != cudaErrorNotSupported) return e;
     e = cudaSuccess;
   }
-  const int vw = access_width(bf16, D, {lddy, ldx, dx != nullptr ? lddx : 0}, {dy, x, dx}, {weight},
-                              wbf16);
+  const int vw = access_width(bf16, D, {lddy, kPacked ? 0 : ldx, dx != nullptr ? lddx : 0},
+                              {dy, kPacked ? nullptr : x, dx}, {weight}, wbf16);
   if (N > 0 && D <= grad_elems(vw) * kGradBlock) {
     auto go = [&](auto f) {
       return f(dy, lddy, x, ldx, weight, wbf16, mean, rstd, N, D, dx, lddx,
@@ -481,16 +532,16 @@ cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void*
     };
     if (bf16) {
       switch (vw) {
-        case 8: e = go(norm_grad<1, 8>); break;
-        case 4: e = go(norm_grad<1, 4>); break;
-        case 2: e = go(norm_grad<1, 2>); break;
-        default: e = go(norm_grad<1, 1>); break;
+        case 8: e = go(norm_grad<1, 8, kPacked>); break;
+        case 4: e = go(norm_grad<1, 4, kPacked>); break;
+        case 2: e = go(norm_grad<1, 2, kPacked>); break;
+        default: e = go(norm_grad<1, 1, kPacked>); break;
       }
     } else {
       switch (vw) {
-        case 4: e = go(norm_grad<0, 4>); break;
-        case 2: e = go(norm_grad<0, 2>); break;
-        default: e = go(norm_grad<0, 1>); break;
+        case 4: e = go(norm_grad<0, 4, kPacked>); break;
+        case 2: e = go(norm_grad<0, 2, kPacked>); break;
+        default: e = go(norm_grad<0, 1, kPacked>); break;
       }
     }
   } else if (N > 0) {
@@ -500,19 +551,39 @@ cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void*
       const dim3 grid(static_cast<unsigned>((D + kColumnThreads - 1) / kColumnThreads),
                       static_cast<unsigned>(ranges));
       layer_norm_columns_kernel<<<grid, kColumnThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, mean,
-                                                                     rstd, N, D, ranges, part);
+                                                                     rstd, N, D, ranges, part, kPacked);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
     if (dx != nullptr) {
       const int grid = N < sms * 8 ? N : sms * 8;
       layer_norm_dx_kernel<<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, weight,
-                                                              wbf16, mean, rstd, N, D, dx, lddx);
+                                                              wbf16, mean, rstd, N, D, dx, lddx, kPacked);
       e = cudaGetLastError();
     }
   }
   if (e != cudaSuccess || !columns) return e;
   return join_columns(part, ranges, D, dweight, dbias, wbf16, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int bf16,
+                                       int64_t ldx, const void* weight, int wbf16,
+                                       const float* mean, const float* rstd, int N, int D,
+                                       void* dx, int64_t lddx, void* dweight, void* dbias,
+                                       float* part, int sms, cudaStream_t stream) {
+  return norm_backward<0>(dy, lddy, x, bf16, ldx, weight, wbf16, mean, rstd, N, D, dx, lddx, dweight, dbias,
+                          part, sms, stream);
+}
+
+cudaError_t launch_layer_norm_backward_packed(const void* dy, int64_t lddy, const uint8_t* packed, int bf16,
+                                              const void* weight, int wbf16, const float* mean,
+                                              const float* rstd, int N, int D, void* dx, int64_t lddx,
+                                              void* dweight, void* dbias, float* part, int sms,
+                                              cudaStream_t stream) {
+  return norm_backward<1>(dy, lddy, packed, bf16, packed_record(D), weight, wbf16, mean, rstd, N, D, dx, lddx,
+                          dweight, dbias, part, sms, stream);
 }
 
 }  // namespace flce

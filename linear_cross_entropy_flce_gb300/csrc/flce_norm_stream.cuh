@@ -53,6 +53,15 @@ __device__ __forceinline__ float2 stream_sum2(float2 v, int group, int R, float2
   }
   return s;
 }
+
+// One thread: starts a copy of whole, aligned 16-byte chunks.
+__device__ __forceinline__ void copy_bytes(uint32_t to, const uint8_t* from, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+      "l"(from), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // How the rows of a CTA lie in their 16-byte chunks of VW elements.
 template <int kElt, bool kRagged>
 struct RowPlace {
@@ -67,11 +76,7 @@ struct RowPlace {
   __device__ uint32_t whole_bytes(int D) const { return static_cast<uint32_t>((D - head() - tail) * kElt); }
   // one thread: starts the copy of the row's whole chunks
   __device__ void copy(uint32_t slot, const uint8_t* row, int D, uint32_t bar) const {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            slot + (kRagged && s > 0 ? 16u : 0u)),
-        "l"(row + head() * kElt), "r"(whole_bytes(D)), "r"(bar)
-        : "memory");
+    copy_bytes(slot + (kRagged && s > 0 ? 16u : 0u), row + head() * kElt, whole_bytes(D), bar);
   }
   // The q-th element (of 16) that is in no whole chunk, or -1: read by a thread of its own,
   // which writes it to the ring a turn later.

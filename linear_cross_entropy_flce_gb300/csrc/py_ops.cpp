@@ -1,4 +1,4 @@
-// The ordinary calls of include/flce_ops.h and flce_embed.h from Python, without ctypes: reads the tensors,
+// The ordinary calls of include/flce_ops.h, flce_embed.h and flce_blocks.h from Python, without ctypes: reads the tensors,
 // allocates the outputs (and the workspace) on the current stream and enqueues the call.
 //
 // A kernel of a decoding step takes a few microseconds; marshalling its arguments through
@@ -23,6 +23,7 @@
 #include <exception>
 #include <vector>
 
+#include "../../include/flce_blocks.h"
 #include "../../include/flce_embed.h"
 #include "../../include/flce_ops.h"
 
@@ -477,6 +478,108 @@ FUNCTION(embedding_backward) {
   });
 }
 
+int64_t record_of(int64_t D) {
+  int64_t bytes = 0;
+  check(flce_packed_row_bytes(D, &bytes), "flce_packed_row_bytes");
+  return bytes;
+}
+
+// (x): the records
+FUNCTION(pack_e4m3) {
+  return guarded(n, 1, [&]() -> PyObject* {
+    const Here h;
+    const Tensor& x = required(a[0], h.device);
+    const int dtype = dtype_of(x);
+    const NormRows r(x);
+    const Tensor data = h.empty({r.N, record_of(r.D)}, at::kByte);
+    check(flce_pack_e4m3(x.const_data_ptr(), dtype, r.ld, r.N, r.D, static_cast<uint8_t*>(data.data_ptr()),
+                         h.stream), "flce_pack_e4m3");
+    return THPVariable_Wrap(data);
+  });
+}
+
+// Records of a shape (a tuple): rows and D.
+struct Records {
+  std::vector<int64_t> shape;
+  int64_t N = 1, D;
+  const uint8_t* data;
+  Records(PyObject* o, PyObject* size, int device) {
+    check(PyTuple_Check(size) && PyTuple_GET_SIZE(size) >= 1);
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(size); ++i) shape.push_back(integer(PyTuple_GET_ITEM(size, i)));
+    D = shape.back();
+    for (size_t i = 0; i + 1 < shape.size(); ++i) N *= shape[i];
+    const Tensor& t = required(o, device);
+    check(t.scalar_type() == at::kByte && t.dim() == 2 && t.size(0) == N && t.size(1) == record_of(D) &&
+          t.is_contiguous());
+    data = static_cast<const uint8_t*>(t.const_data_ptr());
+  }
+};
+
+// (records, shape, dtype)
+FUNCTION(unpack_e4m3) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    const Here h;
+    const Records r(a[0], a[1], h.device);
+    const at::ScalarType type = type_of(a[2], at::kFloat);
+    const int code = code_of(type);
+    const Tensor x = h.empty(r.shape, type);
+    check(flce_unpack_e4m3(r.data, r.N, r.D, x.data_ptr(), code, r.D, h.stream), "flce_unpack_e4m3");
+    return THPVariable_Wrap(x);
+  });
+}
+
+// (x, weight, bias, eps)
+FUNCTION(layer_norm_packed) {
+  return guarded(n, 4, [&]() -> PyObject* {
+    const Here h;
+    const Tensor& x = required(a[0], h.device);
+    const int dtype = dtype_of(x);
+    const NormRows r(x);
+    int wcode = -1;
+    const void* w = param_of(a[1], r.D, h.device, &wcode);
+    const void* b = param_of(a[2], r.D, h.device, &wcode);
+    const float eps = static_cast<float>(number(a[3]));
+    const Tensor data = h.empty({r.N, record_of(r.D)}, at::kByte);
+    const Tensor y = h.empty(x.sizes(), x.scalar_type());
+    const Tensor mean = h.empty({r.N}, at::kFloat), rstd = h.empty({r.N}, at::kFloat);
+    check(flce_layer_norm_packed(x.const_data_ptr(), dtype, r.ld, w, b, wcode < 0 ? FLCE_DTYPE_F32 : wcode, r.N,
+                                 r.D, eps, y.data_ptr(), r.D, mean.data_ptr<float>(), rstd.data_ptr<float>(),
+                                 static_cast<uint8_t*>(data.data_ptr()), h.stream), "flce_layer_norm_packed");
+    return tuple({y, mean, rstd, data});
+  });
+}
+
+// (dy, records, shape, weight, mean, rstd, need_dx, need_dweight, need_dbias)
+FUNCTION(layer_norm_packed_backward) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const Here h;
+    const Tensor& dy = required(a[0], h.device);
+    const int dtype = dtype_of(dy);
+    const Records x(a[1], a[2], h.device);
+    check(dy.sizes() == at::IntArrayRef(x.shape));
+    const NormRows g(dy);
+    int wcode = -1;
+    const void* w = param_of(a[3], g.D, h.device, &wcode);
+    const float *mean = vector_of(a[4], g.N, h.device), *rstd = vector_of(a[5], g.N, h.device);
+    const at::ScalarType wtype = wcode == FLCE_DTYPE_BF16 ? at::kBFloat16 : at::kFloat;
+    Tensor dx, dw, db, ws;
+    if (integer(a[6])) dx = h.empty(dy.sizes(), dy.scalar_type());
+    if (integer(a[7])) dw = h.empty({g.D}, wtype);
+    if (integer(a[8])) db = h.empty({g.D}, wtype);
+    size_t bytes = 0;
+    if (dw.defined() || db.defined()) {
+      check(flce_layer_norm_workspace_size(g.N, g.D, &bytes), "flce_layer_norm_workspace_size");
+      ws = h.empty({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, at::kByte);
+    }
+    auto at_of = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    check(flce_layer_norm_packed_backward(dy.const_data_ptr(), dtype, g.ld, x.data, w,
+                                          wcode < 0 ? FLCE_DTYPE_F32 : wcode, mean, rstd, g.N, g.D, at_of(dx),
+                                          g.D, at_of(dw), at_of(db), at_of(ws), bytes, h.stream),
+          "flce_layer_norm_packed_backward");
+    return tuple({dx, dw, db});
+  });
+}
+
 // (FLCEError): the type of the errors raised here.
 FUNCTION(set_error_type) {
   return guarded(n, 1, [&]() -> PyObject* {
@@ -492,6 +595,8 @@ PyMethodDef methods[] = {METHOD(token_logprobs),        METHOD(token_logprobs_ba
                          METHOD(layer_norm),            METHOD(layer_norm_backward),
                          METHOD(clip_grads),            METHOD(set_error_type),
                          METHOD(embedding),             METHOD(embedding_backward),
+                         METHOD(pack_e4m3),             METHOD(unpack_e4m3),
+                         METHOD(layer_norm_packed),     METHOD(layer_norm_packed_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_flce_ops", nullptr, -1, methods,
                       nullptr,               nullptr,     nullptr, nullptr};

@@ -14,6 +14,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
+from . import _blocks_binding as Q
 from . import _embed_binding as E
 from . import _ops_binding as B
 
@@ -155,6 +156,27 @@ class LayerNormFunction(torch.autograd.Function):
         return dx, dw, db, None
 
 
+class PackedLayerNormFunction(torch.autograd.Function):
+    """LayerNormFunction that keeps its input in 8 bits between the passes."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps: float):
+        r, packed = Q.layer_norm_packed(x, weight, bias, eps=eps)
+        ctx.save_for_backward(packed.data, weight, r.mean, r.rstd)
+        ctx.packed = packed.shape, packed.dtype
+        return r.y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        data, weight, mean, rstd = ctx.saved_tensors
+        dx, dw, db = Q.layer_norm_packed_backward(
+            dy, Q.PackedRows(data, *ctx.packed), weight, B.LayerNormResult(None, mean, rstd),
+            need_dx=ctx.needs_input_grad[0], need_dweight=ctx.needs_input_grad[1],
+            need_dbias=ctx.needs_input_grad[2])
+        return dx, dw, db, None
+
+
 class EmbeddingFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale: float, ignore_index: int, dtype):
@@ -190,28 +212,30 @@ def fused_linear_token_logprobs(hidden_states, weight, tokens, *, temperature: f
                                              int(ignore_index))
 
 
-def fused_layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
+def fused_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, packed: bool = False):
     """Layer norm over the last dimension of x (fp32 or bf16); differentiable in x,
-    weight and bias (of one dtype, fp32 or bf16)."""
+    weight and bias (of one dtype, fp32 or bf16). `packed`: x is kept in 8 bits for the
+    backward pass (1.03 bytes a value), which uses those values in x's place."""
     if bias is not None and weight is not None and weight.dtype != bias.dtype:
         raise TypeError("weight and bias must have one dtype")
     if bias is not None and weight is None and bias.dtype != torch.float32 and bias.requires_grad:
         raise TypeError("a bias without a weight must be float32 to have a gradient")
-    return LayerNormFunction.apply(x, weight, bias, float(eps))
+    return (PackedLayerNormFunction if packed else LayerNormFunction).apply(x, weight, bias, float(eps))
 
 
 class FusedLayerNorm(torch.nn.Module):
     """nn.Module form: FusedLayerNorm(hidden)(x)."""
 
     def __init__(self, hidden_size: int, eps: float = 1e-5, bias: bool = True, device=None,
-                 dtype=None):
+                 dtype=None, packed: bool = False):
         super().__init__()
         self.eps = float(eps)
+        self.packed = bool(packed)
         self.weight = torch.nn.Parameter(torch.ones(hidden_size, device=device, dtype=dtype))
         self.bias = torch.nn.Parameter(torch.zeros(hidden_size, device=device, dtype=dtype)) if bias else None
 
     def forward(self, x):
-        return fused_layer_norm(x, self.weight, self.bias, self.eps)
+        return fused_layer_norm(x, self.weight, self.bias, self.eps, self.packed)
 
 
 def fused_embedding(tokens, weight, *, scale: float = 1.0, ignore_index: int = -100, dtype=None):
