@@ -63,6 +63,61 @@ int flce_layer_norm_packed_backward(const void* dy, int32_t dtype, int64_t lddy,
                                     void* dx, int64_t lddx, void* dweight, void* dbias,
                                     void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * 4-bit floating point: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with a
+ * scale for each block of neighbouring values of a row (the last block may be shorter).
+ *
+ *   FLCE_FP4_MX   blocks of 32, scale 2^e, e the smallest integer >= -127 for which the
+ *                 block's largest magnitude is at most 6 2^e; code rn(x / 2^e)
+ *   FLCE_FP4_NV   blocks of 16, an E4M3 scale s and an fp32 scale g of the row: g the
+ *                 smallest power of two >= 2^-126 for which the row's largest finite
+ *                 magnitude is at most 6 448 g (1 for a row of zeros), s = rn(largest
+ *                 magnitude of the block / 6 / g), code rn(x / (s g)), 0 where s is 0
+ *
+ * All rounded to nearest even; a code is at most 6. A block that holds an infinity or a
+ * NaN has the scale NaN (byte 255, 127) and the codes 0: it stands for NaN throughout.
+ * Products and values take any fp32 row scales and any scale bytes.
+ *
+ * Three arrays hold [N, D] (flce_fp4_sizes gives the bytes; 16-byte aligned but for
+ * row_scales, 4):
+ *   codes       a row in code_row_bytes: two codes to a byte, the first in the low bits,
+ *               zeros up to the next multiple of 64 values
+ *   scales      bytes (e + 127, or E4M3 codes) in groups of 512: for 128 rows and 4
+ *               neighbouring blocks, row r's four bytes at (r % 32) 16 + (r / 32) 4. Blocks
+ *               are padded with zeros to whole 256 values, rows to whole 128s; the groups
+ *               of 128 rows follow one another
+ *   row_scales  fp32 [N] (FLCE_FP4_NV; NULL otherwise)
+ */
+enum { FLCE_FP4_MX = 0, FLCE_FP4_NV = 1 };
+int flce_fp4_sizes(int64_t N, int64_t D, int32_t format, int64_t* code_row_bytes,
+                   size_t* scale_bytes);
+
+/* x [N, D] of dtype, row stride ldx >= D, aligned to its element size. */
+int flce_quantize_fp4(const void* x, int32_t dtype, int64_t ldx, int64_t N, int64_t D,
+                      int32_t format, uint8_t* codes, uint8_t* scales, float* row_scales,
+                      void* stream);
+
+/* The values, code scale row_scale in fp32, rounded once to dtype. */
+int flce_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float* row_scales,
+                        int64_t N, int64_t D, int32_t format, void* x, int32_t dtype,
+                        int64_t ldx, void* stream);
+
+/*
+ * y = H W^T of two such matrices of one format, H [N, D] (tokens) and W [V, D] (a head or
+ * another linear layer's weight), on the block-scaled tensor cores: the blocks' products
+ * are accumulated in fp32, multiplied by the two rows' scales and rounded once to dtype.
+ *   y        [N, V] of dtype (FLCE_DTYPE_F32 / _BF16), row stride ldy >= V, aligned to its
+ *            element size
+ *   timeout_ns  limit of every device-side wait; 0 = 2 s
+ *   status   int32 [1] or NULL; written only when the device finds an error: a wait that
+ *            ran out of time gives FLCE_ERR_TIMEOUT and NaN for what was not done
+ * Results do not change from run to run, and a token's do not depend on the others'.
+ */
+int flce_linear_fp4(const uint8_t* h_codes, const uint8_t* h_scales, const float* h_row_scales,
+                    const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scales,
+                    int64_t N, int64_t D, int64_t V, int32_t format, void* y, int32_t dtype,
+                    int64_t ldy, int64_t timeout_ns, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

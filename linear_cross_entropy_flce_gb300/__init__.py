@@ -14,8 +14,9 @@ from ._binding import (FLCE_ERR_ALIGN, FLCE_ERR_CUDA, FLCE_ERR_DEVICE, FLCE_ERR_
                        forward_backward, forward_backward_fp8, forward_noalloc, forward_shard,
                        forward_workspace_size, get_plan, lib, make_options, noalloc_setup,
                        quantize_e4m3, scale_grads, status_string, workspace_size)
-from ._blocks_binding import (PackedRows, layer_norm_packed, layer_norm_packed_backward, pack_e4m3,
-                              packed_row_bytes, unpack_e4m3)
+from ._blocks_binding import (FP4_FORMATS, Fp4Matrix, PackedRows, dequantize_fp4, layer_norm_packed,
+                              layer_norm_packed_backward, linear_fp4, pack_e4m3, packed_row_bytes,
+                              quantize_fp4, unpack_e4m3)
 from ._embed_binding import (embedding, embedding_backward,
                              embedding_backward_workspace_size)
 from ._ops_binding import (MAX_TOP_K, LayerNormResult, LogprobOptions, TokenLogprobs, clip_grads,
@@ -47,4 +48,4 @@ __all__ = ["FLCE_ERR_ALIGN", "FLCE_ERR_CUDA", "FLCE_ERR_DEVICE", "FLCE_ERR_LABEL
            "embedding", "embedding_backward", "embedding_backward_workspace_size", "FusedEmbedding",
            "EmbeddingFunction", "fused_embedding", "PackedRows", "layer_norm_packed",
            "layer_norm_packed_backward", "pack_e4m3", "packed_row_bytes", "unpack_e4m3",
-           "PackedLayerNormFunction"]
+           "PackedLayerNormFunction", "FP4_FORMATS", "Fp4Matrix", "dequantize_fp4", "linear_fp4", "quantize_fp4"]

@@ -4,6 +4,7 @@
 //   flce_pack_e4m3, flce_unpack_e4m3   one kernel
 //   flce_layer_norm_packed             the pack of x, then flce_layer_norm
 //   flce_layer_norm_packed_backward    as flce_layer_norm_backward
+//   flce_quantize_fp4, flce_dequantize_fp4, flce_linear_fp4   one kernel
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -11,6 +12,7 @@
 #include "../../include/flce_blocks.h"
 #include "../../include/flce_ops.h"
 #include "flce_blocks.h"
+#include "flce_fp4_gemm.h"
 #include "flce_host.h"
 
 namespace flce {
@@ -24,6 +26,32 @@ int check_matrix(int64_t N, int64_t D, int32_t dtype, int64_t ld) {
   if (N < 0 || N > (int64_t(1) << 30) || D < 1 || D > (int64_t(1) << 24)) return FLCE_ERR_SHAPE;
   if (!known_dtype(dtype)) return FLCE_ERR_OPTION;
   return ld < D ? FLCE_ERR_SHAPE : FLCE_OK;
+}
+
+int check_fp4(int64_t N, int64_t D, int32_t format) {
+  if (N < 0 || N > (int64_t(1) << 30) || D < 1 || D > (int64_t(1) << 24)) return FLCE_ERR_SHAPE;
+  return format == FLCE_FP4_MX || format == FLCE_FP4_NV ? FLCE_OK : FLCE_ERR_OPTION;
+}
+
+// A matrix's three arrays.
+int check_fp4_arrays(const uint8_t* codes, const uint8_t* scales, const float* row_scales, int32_t format) {
+  if (codes == nullptr || scales == nullptr || (format == FLCE_FP4_NV && row_scales == nullptr))
+    return FLCE_ERR_NULL;
+  return aligned(codes, 16) && aligned(scales, 16) && aligned(row_scales, 4) ? FLCE_OK : FLCE_ERR_ALIGN;
+}
+
+// Codes [rows][row_bytes] in boxes of 128 bytes x box_rows with 128-byte swizzle; what is outside reads as
+// zero.
+bool encode_codes(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {row_bytes, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
@@ -131,6 +159,91 @@ int flce_layer_norm_packed_backward(const void* dy, int32_t dtype, int64_t lddy,
                                                 static_cast<int>(D), dx, lddx, dweight, dbias,
                                                 static_cast<float*>(workspace), sms,
                                                 static_cast<cudaStream_t>(stream)));
+}
+
+int flce_fp4_sizes(int64_t N, int64_t D, int32_t format, int64_t* code_row_bytes, size_t* scale_bytes) {
+  if (code_row_bytes == nullptr || scale_bytes == nullptr) return FLCE_ERR_NULL;
+  const int rc = check_fp4(N, D, format);
+  if (rc != FLCE_OK) return rc;
+  *code_row_bytes = fp4_code_bytes(D);
+  *scale_bytes = static_cast<size_t>(fp4_scale_bytes(N, D, format == FLCE_FP4_NV));
+  return FLCE_OK;
+}
+
+int flce_quantize_fp4(const void* x, int32_t dtype, int64_t ldx, int64_t N, int64_t D, int32_t format,
+                      uint8_t* codes, uint8_t* scales, float* row_scales, void* stream) {
+  int rc = check_matrix(N, D, dtype, ldx);
+  if (rc == FLCE_OK) rc = check_fp4(N, D, format);
+  if (rc != FLCE_OK || N == 0) return rc;
+  if (x == nullptr) return FLCE_ERR_NULL;
+  rc = check_fp4_arrays(codes, scales, row_scales, format);
+  if (rc != FLCE_OK) return rc;
+  if (!aligned(x, elem_size(dtype))) return FLCE_ERR_ALIGN;
+  if (x == codes || x == scales || codes == scales) return FLCE_ERR_OPTION;
+  int sms = 0;
+  rc = device_info(&sms);
+  if (rc != FLCE_OK) return rc;
+  return done(launch_quantize_fp4(x, dtype == FLCE_DTYPE_BF16, ldx, static_cast<int>(N), static_cast<int>(D),
+                                  format == FLCE_FP4_NV, codes, scales, row_scales, sms,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+int flce_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float* row_scales, int64_t N,
+                        int64_t D, int32_t format, void* x, int32_t dtype, int64_t ldx, void* stream) {
+  int rc = check_matrix(N, D, dtype, ldx);
+  if (rc == FLCE_OK) rc = check_fp4(N, D, format);
+  if (rc != FLCE_OK || N == 0) return rc;
+  if (x == nullptr) return FLCE_ERR_NULL;
+  rc = check_fp4_arrays(codes, scales, row_scales, format);
+  if (rc != FLCE_OK) return rc;
+  if (!aligned(x, elem_size(dtype))) return FLCE_ERR_ALIGN;
+  if (x == codes || x == scales) return FLCE_ERR_OPTION;
+  int sms = 0;
+  rc = device_info(&sms);
+  if (rc != FLCE_OK) return rc;
+  return done(launch_dequantize_fp4(codes, scales, row_scales, static_cast<int>(N), static_cast<int>(D),
+                                    format == FLCE_FP4_NV, x, dtype == FLCE_DTYPE_BF16, ldx,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+int flce_linear_fp4(const uint8_t* h_codes, const uint8_t* h_scales, const float* h_row_scales,
+                    const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scales, int64_t N,
+                    int64_t D, int64_t V, int32_t format, void* y, int32_t dtype, int64_t ldy,
+                    int64_t timeout_ns, int32_t* status, void* stream) {
+  int rc = check_fp4(N, D, format);
+  if (rc != FLCE_OK) return rc;
+  if (V < 1 || V > (int64_t(1) << 30) || ldy < V) return FLCE_ERR_SHAPE;
+  if (!known_dtype(dtype) || timeout_ns < 0) return FLCE_ERR_OPTION;
+  if (N == 0) return FLCE_OK;
+  rc = check_fp4_arrays(h_codes, h_scales, h_row_scales, format);
+  if (rc == FLCE_OK) rc = check_fp4_arrays(w_codes, w_scales, w_row_scales, format);
+  if (rc != FLCE_OK) return rc;
+  if (y == nullptr) return FLCE_ERR_NULL;
+  if (!aligned(y, elem_size(dtype)) || !aligned(status, 4)) return FLCE_ERR_ALIGN;
+  int sms = 0;
+  rc = device_info(&sms);
+  if (rc != FLCE_OK) return rc;
+  const int kn = fp4_tile(N);
+  const uint64_t row = static_cast<uint64_t>(fp4_code_bytes(D));
+  CUtensorMap mW, mW32, mH;
+  if (!encode_codes(&mW, w_codes, row, static_cast<uint64_t>(V), 128) ||
+      !encode_codes(&mW32, w_codes, row, static_cast<uint64_t>(V), 32) ||
+      !encode_codes(&mH, h_codes, row, static_cast<uint64_t>(N), static_cast<uint32_t>(kn)))
+    return FLCE_ERR_CUDA;
+  Fp4GemmParams p{};
+  p.N = static_cast<int>(N);
+  p.V = static_cast<int>(V);
+  p.stages = static_cast<int>(fp4_stages(D));
+  p.h_scales = h_scales;
+  p.w_scales = w_scales;
+  p.h_rows = h_row_scales;
+  p.w_rows = w_row_scales;
+  p.y = y;
+  p.ldy = ldy;
+  p.timeout_ns = timeout_ns > 0 ? timeout_ns : kDefaultTimeoutNs;
+  p.status = status;
+  return done(launch_fp4_gemm(kn, format == FLCE_FP4_NV, dtype == FLCE_DTYPE_BF16, mW, mW32, mH, p, sms,
+                              static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -580,6 +580,85 @@ FUNCTION(layer_norm_packed_backward) {
   });
 }
 
+// (x, format): codes, scales, row scales
+FUNCTION(quantize_fp4) {
+  return guarded(n, 2, [&]() -> PyObject* {
+    const Here h;
+    const Tensor& x = required(a[0], h.device);
+    const int dtype = dtype_of(x);
+    const NormRows r(x);
+    const int32_t format = static_cast<int32_t>(integer(a[1]));
+    int64_t row = 0;
+    size_t size = 0;
+    check(flce_fp4_sizes(r.N, r.D, format, &row, &size), "flce_fp4_sizes");
+    const Tensor codes = h.empty({r.N, row}, at::kByte), scales = h.empty({static_cast<int64_t>(size)}, at::kByte);
+    Tensor rows;
+    if (format == FLCE_FP4_NV) rows = h.empty({r.N}, at::kFloat);
+    check(flce_quantize_fp4(x.const_data_ptr(), dtype, r.ld, r.N, r.D, format,
+                            static_cast<uint8_t*>(codes.data_ptr()), static_cast<uint8_t*>(scales.data_ptr()),
+                            rows.defined() ? rows.data_ptr<float>() : nullptr, h.stream), "flce_quantize_fp4");
+    return tuple({codes, scales, rows});
+  });
+}
+
+// A 4-bit matrix: codes, scales, row scales and shape.
+struct Fp4 {
+  std::vector<int64_t> shape;
+  int64_t N = 1, D;
+  const uint8_t *codes, *scales;
+  const float* rows;
+  Fp4(PyObject* const* a, int32_t format, int device) {
+    check(PyTuple_Check(a[3]) && PyTuple_GET_SIZE(a[3]) >= 1);
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[3]); ++i) shape.push_back(integer(PyTuple_GET_ITEM(a[3], i)));
+    D = shape.back();
+    for (size_t i = 0; i + 1 < shape.size(); ++i) N *= shape[i];
+    int64_t row = 0;
+    size_t size = 0;
+    check(flce_fp4_sizes(N, D, format, &row, &size), "flce_fp4_sizes");
+    auto bytes = [&](PyObject* o, at::IntArrayRef want) {
+      const Tensor& t = required(o, device);
+      check(t.scalar_type() == at::kByte && t.sizes() == want && t.is_contiguous());
+      return static_cast<const uint8_t*>(t.const_data_ptr());
+    };
+    codes = bytes(a[0], {N, row});
+    scales = bytes(a[1], {static_cast<int64_t>(size)});
+    rows = format == FLCE_FP4_NV ? vector_of(a[2], N, device) : nullptr;
+  }
+};
+
+// (codes, scales, row scales, shape, format, dtype)
+FUNCTION(dequantize_fp4) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const Here h;
+    const int32_t format = static_cast<int32_t>(integer(a[4]));
+    const Fp4 m(a, format, h.device);
+    const at::ScalarType type = type_of(a[5], at::kFloat);
+    const int code = code_of(type);
+    const Tensor x = h.empty(m.shape, type);
+    check(flce_dequantize_fp4(m.codes, m.scales, m.rows, m.N, m.D, format, x.data_ptr(), code, m.D, h.stream),
+          "flce_dequantize_fp4");
+    return THPVariable_Wrap(x);
+  });
+}
+
+// (h: codes, scales, row scales, shape, w: the same, format, dtype)
+FUNCTION(linear_fp4) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    const Here h;
+    const int32_t format = static_cast<int32_t>(integer(a[8]));
+    const Fp4 H(a, format, h.device), W(a + 4, format, h.device);
+    check(W.shape.size() == 2 && W.D == H.D);
+    const at::ScalarType type = type_of(a[9], at::kBFloat16);
+    const int code = code_of(type);
+    std::vector<int64_t> shape(H.shape);
+    shape.back() = W.N;
+    const Tensor y = h.empty(shape, type);
+    check(flce_linear_fp4(H.codes, H.scales, H.rows, W.codes, W.scales, W.rows, H.N, H.D, W.N, format, y.data_ptr(),
+                          code, W.N, 0, nullptr, h.stream), "flce_linear_fp4");
+    return THPVariable_Wrap(y);
+  });
+}
+
 // (FLCEError): the type of the errors raised here.
 FUNCTION(set_error_type) {
   return guarded(n, 1, [&]() -> PyObject* {
@@ -597,6 +676,8 @@ PyMethodDef methods[] = {METHOD(token_logprobs),        METHOD(token_logprobs_ba
                          METHOD(embedding),             METHOD(embedding_backward),
                          METHOD(pack_e4m3),             METHOD(unpack_e4m3),
                          METHOD(layer_norm_packed),     METHOD(layer_norm_packed_backward),
+                         METHOD(quantize_fp4),          METHOD(dequantize_fp4),
+                         METHOD(linear_fp4),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_flce_ops", nullptr, -1, methods,
                       nullptr,               nullptr,     nullptr, nullptr};
