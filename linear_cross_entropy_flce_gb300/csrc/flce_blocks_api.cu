@@ -54,6 +54,19 @@ bool encode_codes(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Groups of 512 scale bytes, in boxes of those of 128 rows' 256 values; none past the last reads as zero.
+bool encode_scales(CUtensorMap* m, const void* base, uint64_t bytes, int nv) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {128, bytes / 512};
+  cuuint64_t strides[1] = {512};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(fp4_stage_scales(nv) / 512)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int done(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
 
 }  // namespace
@@ -225,25 +238,26 @@ int flce_linear_fp4(const uint8_t* h_codes, const uint8_t* h_scales, const float
   if (rc != FLCE_OK) return rc;
   const int kn = fp4_tile(N);
   const uint64_t row = static_cast<uint64_t>(fp4_code_bytes(D));
-  CUtensorMap mW, mW32, mH;
-  if (!encode_codes(&mW, w_codes, row, static_cast<uint64_t>(V), 128) ||
-      !encode_codes(&mW32, w_codes, row, static_cast<uint64_t>(V), 32) ||
-      !encode_codes(&mH, h_codes, row, static_cast<uint64_t>(N), static_cast<uint32_t>(kn)))
+  const int nv = format == FLCE_FP4_NV;
+  Fp4Maps maps;
+  if (!encode_codes(&maps.w, w_codes, row, static_cast<uint64_t>(V), 128) ||
+      !encode_codes(&maps.w32, w_codes, row, static_cast<uint64_t>(V), 32) ||
+      !encode_codes(&maps.h, h_codes, row, static_cast<uint64_t>(N), static_cast<uint32_t>(kn / fp4_ctas(kn))) ||
+      !encode_scales(&maps.w_scales, w_scales, static_cast<uint64_t>(fp4_scale_bytes(V, D, nv)), nv) ||
+      !encode_scales(&maps.h_scales, h_scales, static_cast<uint64_t>(fp4_scale_bytes(N, D, nv)), nv))
     return FLCE_ERR_CUDA;
   Fp4GemmParams p{};
   p.N = static_cast<int>(N);
   p.V = static_cast<int>(V);
   p.stages = static_cast<int>(fp4_stages(D));
-  p.h_scales = h_scales;
-  p.w_scales = w_scales;
   p.h_rows = h_row_scales;
   p.w_rows = w_row_scales;
   p.y = y;
   p.ldy = ldy;
+  p.wide = aligned(y, 16) && ldy * static_cast<int64_t>(elem_size(dtype)) % 16 == 0;
   p.timeout_ns = timeout_ns > 0 ? timeout_ns : kDefaultTimeoutNs;
   p.status = status;
-  return done(launch_fp4_gemm(kn, format == FLCE_FP4_NV, dtype == FLCE_DTYPE_BF16, mW, mW32, mH, p, sms,
-                              static_cast<cudaStream_t>(stream)));
+  return done(launch_fp4_gemm(kn, nv, dtype == FLCE_DTYPE_BF16, maps, p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

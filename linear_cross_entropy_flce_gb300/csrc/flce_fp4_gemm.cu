@@ -25,17 +25,21 @@ constexpr int kWarps = 12;   // TMA, MMA, two without work, eight of the epilogu
 constexpr int kThreads = kWarps * 32;
 constexpr int kEpilogue = 8;
 
-template <int kN, int kNv>
+template <int kN, int kNv, int kCta>
 struct Cfg {
+  static constexpr int kRows = 128 * kCta;                  // of W in a tile
   static constexpr int kTokenTiles = (kN + 127) / 128;
+  // of a CTA: its 128 rows of W, its share of the tokens, the scales of its rows and of all tokens
   static constexpr uint32_t kABytes = 128 * 128;
-  static constexpr uint32_t kBBytes = kN * 128;
+  static constexpr uint32_t kBBytes = kN / kCta * 128;
   static constexpr uint32_t kSf = kNv ? 2048 : 1024;        // scale bytes of 128 rows' 256 values
   static constexpr int kBlocks = kSf / 512;
-  static constexpr uint32_t kStageBytes = kABytes + (kBBytes < 1024 ? 1024 : kBBytes) + kSf * (1 + kTokenTiles);
-  static constexpr int kFit = static_cast<int>((224 * 1024) / kStageBytes);
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSf * (1 + kTokenTiles);
+  // of an epilogue warp: 32 tokens' rows on their way out, its tokens' row scales
+  static constexpr uint32_t kOutBytes = kN >= 64 ? 32 * 64 + kN / 2 * 4 : 0;
+  static constexpr int kFit = static_cast<int>((225 * 1024 - kEpilogue * kOutBytes) / kStageBytes);
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
-  static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + 512;
+  static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogue * kOutBytes + 512;
   static constexpr int kAcc = kN == 256 ? 1 : 2;            // accumulators
   // TMEM: the accumulators, then kSfBuffers times the scales of a stage
   static constexpr int kSfCols = kBlocks * 4 * (1 + kTokenTiles);
@@ -47,48 +51,40 @@ struct Cfg {
   static_assert(kStageBytes % 1024 == 0, "swizzled boxes begin at multiples of 1024 bytes");
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// 512 bytes of scales (32 rows of 16) to 4 TMEM columns, the same in each quarter of the lanes.
+// 512 bytes of scales (32 rows of 16) to 4 TMEM columns, the same in each quarter of the lanes; in a
+// pair, each CTA's to its own.
+template <int kCta>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
   // no swizzle; groups of 8 rows are 128 bytes apart
   const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
                         (1ull << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  if constexpr (kCta == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
-template <int kNv>
+template <int kNv, int kCta>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                         uint32_t sfb, uint32_t accumulate) {
-  if constexpr (kNv)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+#define FLCE_MMA_FP4(form)                                                                                \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma." form                           \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                           \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                              \
+               : "memory")
+  if constexpr (kNv && kCta == 2) FLCE_MMA_FP4("cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X");
+  else if constexpr (kNv) FLCE_MMA_FP4("cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X");
+  else if constexpr (kCta == 2) FLCE_MMA_FP4("cta_group::2.kind::mxf4.block_scale.scale_vec::2X");
+  else FLCE_MMA_FP4("cta_group::1.kind::mxf4.block_scale.scale_vec::2X");
+#undef FLCE_MMA_FP4
 }
 
-// Instruction descriptor of a 128 x kN x 64 step: E2M1 operands, both K-major; scales E4M3 (nvfp4) or
+// Instruction descriptor of a 128 kCta x kN x 64 step: E2M1 operands, both K-major; scales E4M3 (nvfp4) or
 // powers of two; sf: which of the four bytes of a row's scale word the step begins with.
-template <int kN, int kNv>
+template <int kN, int kNv, int kCta>
 __device__ __forceinline__ constexpr uint32_t fp4_idesc(uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kN >> 3) << 17) | ((kNv ? 0u : 1u) << 23) |
-         ((128u >> 4) << 24) | (sf << 29);
+         ((128u * kCta >> 4) << 24) | (sf << 29);
 }
 
 template <int kCols>
@@ -114,62 +110,76 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   }
 }
 
-// The tiles of a CTA: (rows [row, row_end) of W within the 128 from row / 128 * 128 on, tokens from
-// `token` on), one after another.
-template <int kN>
+// The tiles of a CTA (or a pair): rows [row, row_end) of W within the kRows from row / kRows * kRows on,
+// tokens from `token` on, one after another.
+template <int kN, int kRows>
 struct Tiles {
   int row, row_end, token;
-  int last_row;        // share: where this CTA's rows end
+  int last_row;        // share: where its rows end
   int64_t unit, units; // tiles: the next one
-  int token_tiles, V;
+  int step, token_tiles, V;
   bool share;
-  __device__ Tiles(const Fp4GemmParams& p) {
+  __device__ Tiles(const Fp4GemmParams& p, int index, int count) {
     V = p.V;
     share = p.N <= kN;
     token = 0;
     token_tiles = (p.N + kN - 1) / kN;
+    step = count;
     if (share) {
       const int64_t groups = (p.V + 31) / 32;
-      row = static_cast<int>(groups * blockIdx.x / gridDim.x * 32);
-      last_row = min(p.V, static_cast<int>(groups * (blockIdx.x + 1) / gridDim.x * 32));
-      row_end = min(last_row, row / 128 * 128 + 128);
+      row = static_cast<int>(groups * index / count * 32);
+      last_row = min(p.V, static_cast<int>(groups * (index + 1) / count * 32));
+      row_end = min(last_row, row / kRows * kRows + kRows);
     } else {
-      units = static_cast<int64_t>((p.V + 127) / 128) * token_tiles;
-      unit = blockIdx.x;
+      units = static_cast<int64_t>((p.V + kRows - 1) / kRows) * token_tiles;
+      unit = index;
       place();
     }
   }
   __device__ void place() {
-    row = static_cast<int>(unit / token_tiles) * 128;
-    row_end = min(V, row + 128);
+    row = static_cast<int>(unit / token_tiles) * kRows;
+    row_end = min(V, row + kRows);
     token = static_cast<int>(unit % token_tiles) * kN;
   }
   __device__ bool more() const { return share ? row < last_row : unit < units; }
   __device__ void next() {
     if (share) {
       row = row_end;
-      row_end = min(last_row, row + 128);
+      row_end = min(last_row, row + kRows);
     } else {
-      unit += gridDim.x;
+      unit += step;
       if (unit < units) place();
     }
   }
+  // the 32s of rows, counted from CTA `rank`'s 128, that its copies take: [first, end)
+  __device__ void quarters(int rank, int& first, int& end) const {
+    const int base = row / kRows * kRows + rank * 128;
+    first = max(0, (row - base) / 32);
+    end = min(4, (row_end - base + 31) / 32);
+    if (end < first) end = first;
+  }
 };
 
-template <int kN, int kNv, int kBf16>
+// kCta = 2: cluster pairs; each CTA stages its 128 rows of W and half of the tokens, and the even one
+// issues the MMAs of both.
+template <int kN, int kNv, int kBf16, int kCta>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp4_gemm_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mW32,
-                    const __grid_constant__ CUtensorMap mH, const Fp4GemmParams p) {
-  using C = Cfg<kN, kNv>;
+    fp4_gemm_kernel(const __grid_constant__ Fp4Maps maps, const Fp4GemmParams p) {
+  using C = Cfg<kN, kNv, kCta>;
+  using At = Tiles<kN, C::kRows>;
+  constexpr bool kCl = kCta == 2;   // waits acquire at cluster scope
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * C::kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * C::kStageBytes + kEpilogue * C::kOutBytes);
   // full[kStages] | empty[kStages] | tfull[2] | tempty[2] | drain
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kCl ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int index = static_cast<int>(blockIdx.x) / kCta, count = static_cast<int>(gridDim.x) / kCta;
   const uint32_t stage0 = smem_u32(smem);
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
@@ -180,25 +190,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kOffB = C::kABytes, kOffSfA = C::kStageBytes - C::kSf * (1 + C::kTokenTiles),
                      kOffSfB = kOffSfA + C::kSf;
   if (threadIdx.x == 0) {
+    // the even CTA's full[s] counts the copies of both
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), kEpilogue);
+      mbar_init(tempty_bar(a), kEpilogue * kCta);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&mW);
-    tma_prefetch_desc(&mW32);
-    tma_prefetch_desc(&mH);
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.h);
+    tma_prefetch_desc(&maps.w_scales);
+    tma_prefetch_desc(&maps.h_scales);
   }
-  __syncthreads();
+  // the barriers of both CTAs are there before either touches the other's
+  if constexpr (kCl) cluster_sync();
+  else __syncthreads();
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_cg<kCta>(smem_u32(tmem_holder), C::kTmemCols);
+    tmem_relinquish_cg<kCta>();
   }
   tc_fence_before();
   __syncthreads();
@@ -216,35 +230,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     bool ok = true;
     const uint64_t pol_w = make_l2_policy(p.N <= kN ? 1 : 0), pol_h = make_l2_policy(2);
-    for (Tiles<kN> at(p); ok && at.more(); at.next()) {
-      const int tile = at.row / 128;
-      const int q0 = at.row % 128 / 32, q1 = (at.row_end - tile * 128 + 31) / 32;   // its 32s of rows
-      const bool whole = q0 == 0 && q1 == 4;
-      const uint32_t w_bytes = static_cast<uint32_t>(q1 - q0) * 32u * 128u;
-      // the tokens' scale tiles that there are (one at least)
-      const int sf_tiles = C::kTokenTiles == 1 || at.token + 128 >= p.N ? 1 : 2;
-      const uint8_t* const sf_w = p.w_scales + static_cast<int64_t>(tile) * p.stages * C::kSf;
-      const uint8_t* const sf_h = p.h_scales + static_cast<int64_t>(at.token / 128) * p.stages * C::kSf;
+    for (At at(p, index, count); ok && at.more(); at.next()) {
+      const int base = at.row / C::kRows * C::kRows + static_cast<int>(rank) * 128;
+      int q0, q1;
+      at.quarters(static_cast<int>(rank), q0, q1);
+      uint32_t bytes = 0;   // of a stage, both CTAs'
+#pragma unroll
+      for (int c = 0; c < kCta; ++c) {
+        int f, e;
+        at.quarters(c, f, e);
+        bytes += static_cast<uint32_t>(e - f) * 32u * 128u + C::kBBytes + C::kSf * (1 + C::kTokenTiles);
+      }
       for (int ks = 0; ks < p.stages; ++ks) {
-        const bool free_ok = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag);
+        const bool free_ok = mbar_wait_bounded<kCl>(empty_bar(stage), phase ^ 1u, tmo, abort_flag);
         if (!__all_sync(0xffffffffu, free_ok)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          const uint32_t fb = full_bar(stage), at_stage = stage0 + stage * C::kStageBytes;
-          mbar_arrive_expect_tx(fb, w_bytes + C::kBBytes + C::kSf * (1 + sf_tiles));
-          if (whole) {
-            tma_load_2d_hint(at_stage, &mW, ks * 128, tile * 128, fb, pol_w);
+          const uint32_t at_stage = stage0 + stage * C::kStageBytes;
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
+          // copies complete on the even CTA's barrier
+          const uint32_t fb = kCl ? mapa_shared(full_bar(stage), 0) : full_bar(stage);
+          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t pol) {
+            if constexpr (kCl) tma_load_2d_pair(dst, map, x, y, fb, pol);
+            else tma_load_2d_hint(dst, map, x, y, fb, pol);
+          };
+          if (q0 == 0 && q1 == 4) {
+            load(at_stage, &maps.w, ks * 128, base, pol_w);
           } else {
-            for (int q = q0; q < q1; ++q)
-              tma_load_2d_hint(at_stage + q * 32 * 128, &mW32, ks * 128, tile * 128 + q * 32, fb, pol_w);
+            for (int q = q0; q < q1; ++q) load(at_stage + q * 32 * 128, &maps.w32, ks * 128, base + q * 32, pol_w);
           }
-          tma_load_2d_hint(at_stage + kOffB, &mH, ks * 128, at.token, fb, pol_h);
-          bulk_load(at_stage + kOffSfA, sf_w + ks * C::kSf, C::kSf, fb);
-          for (int tt = 0; tt < sf_tiles; ++tt)
-            bulk_load(at_stage + kOffSfB + tt * C::kSf,
-                      sf_h + (static_cast<int64_t>(tt) * p.stages + ks) * C::kSf, C::kSf, fb);
+          load(at_stage + kOffB, &maps.h, ks * 128, at.token + static_cast<int>(rank) * (kN / kCta), pol_h);
+          load(at_stage + kOffSfA, &maps.w_scales, 0, (base / 128 * p.stages + ks) * C::kBlocks, pol_w);
+#pragma unroll
+          for (int tt = 0; tt < C::kTokenTiles; ++tt)
+            load(at_stage + kOffSfB + tt * C::kSf, &maps.h_scales, 0,
+                 ((at.token / 128 + tt) * p.stages + ks) * C::kBlocks, pol_h);
         }
         __syncwarp();
         issued_mask |= 1u << stage;
@@ -256,16 +278,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok) fail();
-    // the copies that were issued land before the CTA's memory is given back
-    for (int s = 0; s < kStages; ++s)
-      if (issued_mask & (1u << s)) mbar_wait_bounded(full_bar(s), (issued_par >> s) & 1u, 1000000000ull, &no_abort);
+    // The copies that were issued land before the CTAs' memory is given back. The even CTA's barriers
+    // count the odd one's too; after an abort the odd CTA may have issued copies that the even one never
+    // armed, so it waits far longer than a copy takes.
+    if (leader) {
+      for (int s = 0; s < kStages; ++s)
+        if (issued_mask & (1u << s))
+          mbar_wait_bounded<kCl>(full_bar(s), (issued_par >> s) & 1u, 1000000000ull, &no_abort);
+    } else if (!ok || *abort_flag) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
+      }
+    }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 && leader) {
     int stage = 0, acc = 0, buffer = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true, issued_any = false;
-    for (Tiles<kN> at(p); ok && at.more(); at.next()) {
-      const bool acc_ok = mbar_wait_bounded(tempty_bar(acc), acc_phase ^ 1u, tmo, abort_flag);
+    for (At at(p, index, count); ok && at.more(); at.next()) {
+      const bool acc_ok = mbar_wait_bounded<kCl>(tempty_bar(acc), acc_phase ^ 1u, tmo, abort_flag);
       if (!__all_sync(0xffffffffu, acc_ok)) {
         ok = false;
         break;
@@ -273,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kN);
       for (int ks = 0; ks < p.stages; ++ks) {
-        const bool full_ok = mbar_wait_bounded(full_bar(stage), phase, tmo, abort_flag);
+        const bool full_ok = mbar_wait_bounded<kCl>(full_bar(stage), phase, tmo, abort_flag);
         if (!__all_sync(0xffffffffu, full_ok)) {
           ok = false;
           break;
@@ -285,20 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sfb = sfa + C::kBlocks * 4;
 #pragma unroll
           for (int b = 0; b < C::kBlocks; ++b) {
-            copy_scales(sfa + b * 4, at_stage + kOffSfA + b * 512);
+            copy_scales<kCta>(sfa + b * 4, at_stage + kOffSfA + b * 512);
 #pragma unroll
             for (int tt = 0; tt < C::kTokenTiles; ++tt)
-              copy_scales(sfb + (b * C::kTokenTiles + tt) * 4, at_stage + kOffSfB + tt * C::kSf + b * 512);
+              copy_scales<kCta>(sfb + (b * C::kTokenTiles + tt) * 4, at_stage + kOffSfB + tt * C::kSf + b * 512);
           }
 #pragma unroll
           for (int k = 0; k < kFp4Stage / 64; ++k) {
             const int b = kNv ? k : k / 2;
             const uint32_t sf = kNv ? 0u : static_cast<uint32_t>(k % 2 * 2);
-            mma_fp4<kNv>(d_tmem, make_sw128_desc(at_stage + k * 32, 16, 1024),
-                         make_sw128_desc(at_stage + kOffB + k * 32, 16, 1024), fp4_idesc<kN, kNv>(sf), sfa + b * 4,
-                         sfb + b * C::kTokenTiles * 4, (ks | k) != 0 ? 1u : 0u);
+            mma_fp4<kNv, kCta>(d_tmem, make_sw128_desc(at_stage + k * 32, 16, 1024),
+                               make_sw128_desc(at_stage + kOffB + k * 32, 16, 1024), fp4_idesc<kN, kNv, kCta>(sf),
+                               sfa + b * 4, sfb + b * C::kTokenTiles * 4, (ks | k) != 0 ? 1u : 0u);
           }
-          umma_commit_cg<1>(empty_bar(stage));
+          umma_commit_pair<kCta>(empty_bar(stage));   // frees the stage in both CTAs
         }
         __syncwarp();
         issued_any = true;
@@ -309,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (elect_one()) umma_commit_cg<1>(tfull_bar(acc));
+      if (elect_one()) umma_commit_pair<kCta>(tfull_bar(acc));
       __syncwarp();
       if (++acc == C::kAcc) {
         acc = 0;
@@ -318,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) fail();
     if (issued_any) {   // every MMA is done before TMEM is freed
-      if (elect_one()) umma_commit_cg<1>(drain_bar);
+      if (elect_one()) umma_commit_cg<kCta>(drain_bar);
       __syncwarp();
       mbar_wait_bounded(drain_bar, 0, 1000000000ull, &no_abort);
     }
@@ -327,22 +358,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kHalf = kN / 2;   // columns of a warp
     const int quarter = warp & 3, half = (warp - (kWarps - kEpilogue)) >> 2;
     const uint32_t from = (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kHalf);
+    uint8_t* const s_out = smem + kStages * C::kStageBytes + (warp - (kWarps - kEpilogue)) * C::kOutBytes;
+    [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(s_out + 32 * 64);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (Tiles<kN> at(p); at.more(); at.next()) {
-      const int r = at.row / 128 * 128 + quarter * 32 + lane;
-      const bool mine = r >= at.row && r < at.row_end;
+    // this lane's row of a tile, and whether the tile has it
+    auto row_of = [&](const At& at, bool& mine) {
+      const int r = at.row / C::kRows * C::kRows + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      mine = r >= at.row && r < at.row_end;
+      return r;
+    };
+    for (At at(p, index, count); at.more(); at.next()) {
+      bool mine;
+      const int r = row_of(at, mine);
       const int first = at.token + half * kHalf;
       const int tokens = min(kHalf, p.N - first);
       int got = 0;
-      if (lane == 0) got = mbar_wait_bounded(tfull_bar(acc), acc_phase, tmo, abort_flag) ? 1 : 0;
+      if (lane == 0) got = mbar_wait_bounded<kCl>(tfull_bar(acc), acc_phase, tmo, abort_flag) ? 1 : 0;
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) {
         fail();
         // this warp's part of what is not done becomes NaN, for callers that do not read the status
         for (; at.more(); at.next()) {
-          const int row = at.row / 128 * 128 + quarter * 32 + lane;
-          if (row < at.row || row >= at.row_end) continue;
+          const int row = row_of(at, mine);
+          if (!mine) continue;
           for (int n = at.token + half * kHalf; n < min(p.N, at.token + half * kHalf + kHalf); ++n) {
             if (kBf16) static_cast<uint16_t*>(p.y)[n * p.ldy + row] = 0x7FC0u;
             else static_cast<float*>(p.y)[n * p.ldy + row] = __uint_as_float(0x7FC00000u);
@@ -356,67 +395,136 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty_bar(acc));
+      if (lane == 0) {
+        if constexpr (kCl) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        else mbar_arrive(tempty_bar(acc));
+      }
       if (++acc == C::kAcc) {
         acc = 0;
         acc_phase ^= 1u;
       }
-      [[maybe_unused]] float w_row = 1.f, h_row[(kHalf + 31) / 32];
-      if constexpr (kNv) {
-        if (mine) w_row = p.w_rows[r];
+      [[maybe_unused]] float w_row = 1.f;
+      if constexpr (kNv) w_row = mine ? p.w_rows[r] : 0.f;
+      if constexpr (kHalf >= 32) {
+        // 32 tokens at a time; where all of a warp's 32 rows of bf16 are there, they meet in shared memory
+        // and leave 16 bytes at a time
+        const bool wide = kBf16 && p.wide && __all_sync(0xffffffffu, mine);
+        if constexpr (kNv) {
+          __syncwarp();
+          for (int c = lane; c < kHalf; c += 32) s_rows[c] = c < tokens ? p.h_rows[first + c] : 0.f;
+          __syncwarp();
+        }
 #pragma unroll
-        for (int k = 0; k < (kHalf + 31) / 32; ++k)
-          h_row[k] = k * 32 + lane < tokens ? p.h_rows[first + k * 32 + lane] : 0.f;
-      }
+        for (int c0 = 0; c0 < kHalf; c0 += 32) {
+          if (c0 >= tokens) break;
+          float o[32];
 #pragma unroll
-      for (int c = 0; c < kHalf; ++c) {
-        float o = __uint_as_float(v[c]);
-        if constexpr (kNv) o = o * w_row * __shfl_sync(0xffffffffu, h_row[c / 32], c % 32);
-        if (c < tokens && mine) {
-          const int64_t to = (first + c) * p.ldy + r;
-          if constexpr (kBf16) static_cast<uint16_t*>(p.y)[to] = static_cast<uint16_t>(pack_bf16x2(o, 0.f) & 0xFFFFu);
-          else static_cast<float*>(p.y)[to] = o;
+          for (int c = 0; c < 32; c += 4) {
+            float4 h = make_float4(1.f, 1.f, 1.f, 1.f);
+            if constexpr (kNv) h = *reinterpret_cast<const float4*>(s_rows + c0 + c);
+            const float hs[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[c + e] = __uint_as_float(v[c0 + c + e]);
+              if constexpr (kNv) o[c + e] = o[c + e] * w_row * hs[e];
+            }
+          }
+          const int n = min(32, tokens - c0);
+          if (wide) {
+            uint16_t* const to = reinterpret_cast<uint16_t*>(s_out) + lane;
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const uint32_t two = pack_bf16x2(o[c], o[c + 1]);
+              to[c * 32] = static_cast<uint16_t>(two & 0xFFFFu);
+              to[(c + 1) * 32] = static_cast<uint16_t>(two >> 16);
+            }
+            __syncwarp();
+            uint8_t* const y = static_cast<uint8_t*>(p.y) + ((first + c0) * p.ldy + (r - lane)) * 2 + (lane & 3) * 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = j * 8 + (lane >> 2);
+              const uint4 out = reinterpret_cast<const uint4*>(s_out)[j * 32 + lane];
+              if (c < n) *reinterpret_cast<uint4*>(y + c * p.ldy * 2) = out;
+            }
+          } else if (mine) {
+            if constexpr (kBf16) {
+              uint16_t* y = static_cast<uint16_t*>(p.y) + (first + c0) * p.ldy + r;
+#pragma unroll
+              for (int c = 0; c < 32; ++c, y += p.ldy)
+                if (c < n) *y = static_cast<uint16_t>(pack_bf16x2(o[c], 0.f) & 0xFFFFu);
+            } else {
+              float* y = static_cast<float*>(p.y) + (first + c0) * p.ldy + r;
+#pragma unroll
+              for (int c = 0; c < 32; ++c, y += p.ldy)
+                if (c < n) *y = o[c];
+            }
+          }
+        }
+      } else {
+        [[maybe_unused]] const float h_row = kNv && lane < tokens ? p.h_rows[first + lane] : 0.f;
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) {
+          float o = __uint_as_float(v[c]);
+          if constexpr (kNv) o = o * w_row * __shfl_sync(0xffffffffu, h_row, c);
+          if (c < tokens && mine) {
+            const int64_t to = (first + c) * p.ldy + r;
+            if constexpr (kBf16) static_cast<uint16_t*>(p.y)[to] = static_cast<uint16_t>(pack_bf16x2(o, 0.f) & 0xFFFFu);
+            else static_cast<float*>(p.y)[to] = o;
+          }
         }
       }
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kCl) cluster_sync();   // the pair's copies and MMAs are done
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, C::kTmemCols);
+  if (warp == 1) tmem_dealloc_cg<kCta>(tmem_base, C::kTmemCols);
 }
 
-template <int kN, int kNv, int kBf16>
-cudaError_t launch(const CUtensorMap& mW, const CUtensorMap& mW32, const CUtensorMap& mH, const Fp4GemmParams& p,
-                   int sms, cudaStream_t stream) {
-  constexpr size_t smem = Cfg<kN, kNv>::kSmemBytes;
-  auto kern = fp4_gemm_kernel<kN, kNv, kBf16>;
+template <int kN, int kNv, int kBf16, int kCta>
+cudaError_t launch(const Fp4Maps& maps, const Fp4GemmParams& p, int sms, cudaStream_t stream) {
+  using C = Cfg<kN, kNv, kCta>;
+  auto kern = fp4_gemm_kernel<kN, kNv, kBf16, kCta>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;
   const int64_t units = p.N <= kN ? (p.V + 31) / 32
-                                  : static_cast<int64_t>((p.V + 127) / 128) * ((p.N + kN - 1) / kN);
-  kern<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, smem, stream>>>(mW, mW32, mH, p);
-  return cudaGetLastError();
+                                  : static_cast<int64_t>((p.V + C::kRows - 1) / C::kRows) * ((p.N + kN - 1) / kN);
+  const int most = sms / kCta;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((units < most ? units : most) * kCta));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCta;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
-template <int kN>
-cudaError_t launch_types(int nv, int bf16, const CUtensorMap& mW, const CUtensorMap& mW32, const CUtensorMap& mH,
-                         const Fp4GemmParams& p, int sms, cudaStream_t stream) {
-  if (nv) return bf16 ? launch<kN, 1, 1>(mW, mW32, mH, p, sms, stream) : launch<kN, 1, 0>(mW, mW32, mH, p, sms, stream);
-  return bf16 ? launch<kN, 0, 1>(mW, mW32, mH, p, sms, stream) : launch<kN, 0, 0>(mW, mW32, mH, p, sms, stream);
+template <int kN, int kCta>
+cudaError_t launch_types(int nv, int bf16, const Fp4Maps& maps, const Fp4GemmParams& p, int sms,
+                         cudaStream_t stream) {
+  if (nv) return bf16 ? launch<kN, 1, 1, kCta>(maps, p, sms, stream) : launch<kN, 1, 0, kCta>(maps, p, sms, stream);
+  return bf16 ? launch<kN, 0, 1, kCta>(maps, p, sms, stream) : launch<kN, 0, 0, kCta>(maps, p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_fp4_gemm(int kn, int nv, int bf16, const CUtensorMap& mW, const CUtensorMap& mW32,
-                            const CUtensorMap& mH, const Fp4GemmParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_fp4_gemm(int kn, int nv, int bf16, const Fp4Maps& maps, const Fp4GemmParams& p, int sms,
+                            cudaStream_t stream) {
   switch (kn) {
-    case 16: return launch_types<16>(nv, bf16, mW, mW32, mH, p, sms, stream);
-    case 32: return launch_types<32>(nv, bf16, mW, mW32, mH, p, sms, stream);
-    case 64: return launch_types<64>(nv, bf16, mW, mW32, mH, p, sms, stream);
-    case 128: return launch_types<128>(nv, bf16, mW, mW32, mH, p, sms, stream);
-    default: return launch_types<256>(nv, bf16, mW, mW32, mH, p, sms, stream);
+    case 16: return launch_types<16, fp4_ctas(16)>(nv, bf16, maps, p, sms, stream);
+    case 32: return launch_types<32, fp4_ctas(32)>(nv, bf16, maps, p, sms, stream);
+    case 64: return launch_types<64, fp4_ctas(64)>(nv, bf16, maps, p, sms, stream);
+    case 128: return launch_types<128, fp4_ctas(128)>(nv, bf16, maps, p, sms, stream);
+    default: return launch_types<256, fp4_ctas(256)>(nv, bf16, maps, p, sms, stream);
   }
 }
 
