@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "flce_blocks.h"
+#include "flce_norm.cuh"
 
 namespace flce {
 namespace {
@@ -98,12 +99,74 @@ __device__ __forceinline__ uint32_t largest_bits(const float (&v)[VW]) {
   return m;
 }
 
+// The same of VW bf16 as loaded, two at a time.
+template <int kWords>
+__device__ __forceinline__ uint32_t largest_bits_bf16(const uint32_t* w) {
+  uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int k = 1; k < kWords; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+  return max(m & 0xFFFF0000u, m << 16);
+}
+
 // Over groups of kLanes neighbouring lanes (a power of two).
 template <int kLanes>
 __device__ __forceinline__ uint32_t largest_of_lanes(uint32_t m) {
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
+}
+
+// Rows that do not allow wide accesses: a warp's 32 VW neighbouring elements go through shared memory,
+// so that its accesses of 2 or 4 bytes lie side by side while each lane has VW neighbours.
+// (A lane's are VW + 1 words apart, an odd number.)
+template <int VW>
+constexpr int kWarpStage = 32 * (VW + 1);   // floats of a warp
+
+// v: elements [first + lane VW, + VW) of the row, 0 from D on.
+template <int kBf16, int VW>
+__device__ __forceinline__ void load_staged(const void* row, int first, int D, float* stage, float (&v)[VW]) {
+  const int lane = threadIdx.x & 31;
+  float in[VW];
+#pragma unroll
+  for (int k = 0; k < VW; ++k) {
+    const int i = k * 32 + lane;
+    in[k] = first + i < D ? load_as_f32(row, first + i, kBf16) : 0.f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < VW; ++k) stage[k * 32 + lane + (k * 32 + lane) / VW] = in[k];
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < VW; ++e) v[e] = stage[lane * (VW + 1) + e];
+}
+
+// The other way round.
+template <int kBf16, int VW>
+__device__ __forceinline__ void store_staged(void* row, int first, int D, float* stage, const float (&v)[VW]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < VW; ++e) stage[lane * (VW + 1) + e] = v[e];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < VW; ++k) {
+    const int i = k * 32 + lane;
+    if (first + i < D) store_from_f32(row, first + i, stage[i + i / VW], kBf16);
+  }
+}
+
+// Threads of a row of nvec vectors, a power of two from `least` to `limit`: enough for `each` vectors
+// apiece, and more while the rows alone do not fill a quarter of the GPU's threads.
+inline int threads_of_row(int64_t rows, int nvec, int each, int least, int limit) {
+  constexpr int64_t kQuarter = 152 * 512;
+  int X = least;
+  while (X < limit && X * each < nvec) X *= 2;
+  while (X < limit && X < nvec && rows * X < kQuarter) X *= 2;
+  return X;
+}
+
+inline bool whole_vectors(const void* x, int bf16, int64_t ldx) {
+  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * (bf16 ? 2 : 4) % 16 == 0;
 }
 
 }  // namespace

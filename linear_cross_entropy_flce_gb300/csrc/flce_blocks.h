@@ -43,7 +43,7 @@ __host__ __device__ constexpr int64_t fp4_scale_at(int64_t r, int64_t q, int64_t
 
 // nv: nvfp4 (row_scales [N] fp32), else mxfp4 (null).
 cudaError_t launch_quantize_fp4(const void* x, int bf16, int64_t ldx, int N, int D, int nv, uint8_t* codes,
-                                uint8_t* scales, float* row_scales, int sms, cudaStream_t stream);
+                                uint8_t* scales, float* row_scales, cudaStream_t stream);
 cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float* row_scales, int N,
                                   int D, int nv, void* x, int bf16, int64_t ldx, cudaStream_t stream);
 

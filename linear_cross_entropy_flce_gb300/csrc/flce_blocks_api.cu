@@ -197,7 +197,7 @@ int flce_quantize_fp4(const void* x, int32_t dtype, int64_t ldx, int64_t N, int6
   rc = device_info(&sms);
   if (rc != FLCE_OK) return rc;
   return done(launch_quantize_fp4(x, dtype == FLCE_DTYPE_BF16, ldx, static_cast<int>(N), static_cast<int>(D),
-                                  format == FLCE_FP4_NV, codes, scales, row_scales, sms,
+                                  format == FLCE_FP4_NV, codes, scales, row_scales,
                                   static_cast<cudaStream_t>(stream)));
 }
 

@@ -6,164 +6,227 @@
 // Codes are E2M1, rounded once, to nearest even (nvfp4's largest may saturate where s was rounded
 // down).
 //
-// A group of R threads holds a row in registers, eight neighbouring values a vector, so that it is
-// read once for the row's and the blocks' largest magnitudes and the codes; rows of more than 32768
-// values are read again instead. 1 / s is rounded, so the quotient x r is corrected by its
+// A group of R threads holds a row in registers, 16 neighbouring values a chunk, so that it is
+// read once for the row's and the blocks' largest magnitudes and the codes; rows of more than 16384
+// values are read again instead. Rows that do not allow 16-byte accesses come through shared memory, a
+// warp's 512 values at a time. 1 / s is rounded, so the quotient x r is corrected by its
 // residual, which makes it x / s rounded once (Markstein's theorem): a value halfway between two codes
 // stays there. (In fp32 no other quotient is rounded onto such a place: its distance from it is at
 // least the quotient's own last place.)
 #include <cstdint>
 
 #include "flce_blocks.cuh"
-#include "flce_norm.cuh"
 
 namespace flce {
 
 namespace {
 
 constexpr int kFp4Threads = 256;
-constexpr int kFp4Vectors = 4;   // of a row in a thread's registers at most
+constexpr int kFp4Limit = 512;   // threads of a row at most
+constexpr int kFp4Held = 2;      // chunks of 16 in a thread's registers at most
+constexpr int kFp4Values = 4;    // vectors of 8 per thread, of the values back
 
-// Vector i (8 values from 8 i on) of a row of D; zeros behind it.
+// 16 values as loaded.
+template <int kBf16>
+struct Chunk {
+  uint4 w[kBf16 ? 2 : 4];
+  __device__ void load_if(const uint8_t* row, int i, bool ok) {
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k)
+      w[k] = ok ? reinterpret_cast<const uint4*>(row + i * 16 * (kBf16 ? 2 : 4))[k] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ void narrow(const float (&v)[16]) {   // of values that are kBf16's
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
+      constexpr int n = kBf16 ? 8 : 4;
+      float q[n];
+#pragma unroll
+      for (int e = 0; e < n; ++e) q[e] = v[k * n + e];
+      w[k] = Pack<kBf16, n>::narrow(q);
+    }
+  }
+  __device__ void widen(float (&v)[16]) const {
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
+      constexpr int n = kBf16 ? 8 : 4;
+      float q[n];
+      Pack<kBf16, n>::widen(w[k], q);
+#pragma unroll
+      for (int e = 0; e < n; ++e) v[k * n + e] = q[e];
+    }
+  }
+  __device__ uint32_t largest() const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if constexpr (kBf16) {
+      return largest_bits_bf16<8>(u);
+    } else {
+      uint32_t m = u[0] & 0x7FFFFFFFu;
+#pragma unroll
+      for (int e = 1; e < 16; ++e) m = max(m, u[e] & 0x7FFFFFFFu);
+      return m;
+    }
+  }
+};
+
+// Chunk i of a row of D values, 0 behind it; all lanes of the warp. kWhole: 16-byte accesses.
 template <int kBf16, int kWhole>
-__device__ __forceinline__ void load_vector(const uint8_t* row, int i, int D, float (&v)[8]) {
-  if (kWhole && i * 8 + 8 <= D) {
-    Param<kBf16, 8> raw;
-    raw.load(row, i * 8, 0.f);
-    raw.widen(v);
+__device__ __forceinline__ Chunk<kBf16> load_chunk(const uint8_t* row, int i, int D, float* stage) {
+  Chunk<kBf16> c;
+  if constexpr (kWhole) {
+    c.load_if(row, i, i * 16 + 16 <= D);
+    if (i * 16 < D && i * 16 + 16 > D) {   // the chunk in which the row ends
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = i * 16 + e < D ? load_as_f32(row, i * 16 + e, kBf16) : 0.f;
+      c.narrow(v);
+    }
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = i * 8 + e < D ? load_as_f32(row, i * 8 + e, kBf16) : 0.f;
+    float v[16];
+    load_staged<kBf16, 16>(row, (i - static_cast<int>(threadIdx.x & 31)) * 16, D, stage, v);
+    c.narrow(v);
   }
+  return c;
 }
 
-// The largest finite magnitude.
-__device__ __forceinline__ uint32_t largest_finite(const float (&v)[8], uint32_t m) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = magnitude(v[e]);
-    m = max(m, b < kInfBits ? b : 0u);
-  }
-  return m;
-}
+// The row's power of two (its byte) and that of its inverse.
+struct RowScale {
+  uint32_t byte;
+  __device__ float value() const { return power_of_byte(byte); }
+  __device__ float inverse() const { return inverse_power_of_byte(byte); }
+};
 
-// One vector's codes and its block's scale byte. All lanes of the warp.
-template <int kNv>
-__device__ __forceinline__ uint32_t quantize_vector(float (&v)[8], float inv_row, uint32_t& byte) {
-  const uint32_t amax = largest_of_lanes<kNv ? 2 : 4>(largest_bits(v));
+// A chunk's codes, eight to a word, and its scale byte (of 16 values, or of 32 with its neighbour's).
+// amax: the bits of the block's largest magnitude.
+template <int kBf16, int kNv>
+__device__ __forceinline__ uint2 quantize_chunk(const Chunk<kBf16>& c, uint32_t amax, RowScale g, uint32_t& byte) {
+  float v[16];
+  c.widen(v);
   const bool finite = amax < kInfBits;
   if constexpr (kNv) {
-    byte = finite ? e4m3x2(__fdiv_rn(__uint_as_float(amax), 6.f) * inv_row, 0.f) & 0xFFu : 0x7Fu;
+    byte = finite ? e4m3x2(__fdiv_rn(__uint_as_float(amax), 6.f) * g.inverse(), 0.f) & 0xFFu : 0x7Fu;
     float s, none;
     widen_e4m3x2(finite ? byte : 0u, s, none);
     const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    // Powers of two do not round: x = v / g is as good as v, with s g for s and r / g for r, but where r / g
+    // would overflow or a residual vanish.
+    const bool tiny = g.byte < 32u;
+    const float t = tiny ? s : s * g.value(), rt = tiny ? r : r * g.inverse(), f = tiny ? g.inverse() : 1.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = finite ? v[e] * inv_row : 0.f;
-      const float q = x * r;
-      v[e] = copysignf(fmaf(fmaf(-q, s, x), r, q), x);   // the correction makes +0 of -0
+    for (int e = 0; e < 16; ++e) {
+      const float x = v[e] * f;
+      const float q = x * rt;
+      v[e] = fmaf(-fmaf(q, t, -x), rt, q);   // (in this order -0 stays -0)
     }
   } else {
     byte = power_scale_byte<2, 0x400000u>(amax);
     const float inv = finite ? inverse_power_of_byte(byte) : 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = finite ? v[e] * inv : 0.f;
+    for (int e = 0; e < 16; ++e) v[e] *= inv;
   }
-  return e2m1x8(v);
+  const float(&lo)[8] = *reinterpret_cast<const float(*)[8]>(v);
+  const float(&hi)[8] = *reinterpret_cast<const float(*)[8]>(v + 8);
+  return finite ? make_uint2(e2m1x8(lo), e2m1x8(hi)) : make_uint2(0, 0);
 }
 
-// The bytes of four neighbouring blocks, in the first of their lanes.
-template <int kNv>
-__device__ __forceinline__ uint32_t four_bytes(uint32_t byte) {
-  constexpr int kLanes = kNv ? 2 : 4;   // of a block
-  uint32_t w = byte << (8 * ((threadIdx.x / kLanes) & 3));
-  w |= __shfl_xor_sync(0xffffffffu, w, kLanes);
-  w |= __shfl_xor_sync(0xffffffffu, w, 2 * kLanes);
-  return w;
-}
-
-// Rows up to the next multiple of 128: those past N have scales alone, 0. kHeld: vectors of a row in
-// a thread's registers; 0: read twice.
+// Rows up to the next multiple of 128: those past N have scales alone, 0. R threads a row; kHeld: chunks of
+// it in a thread's registers; 0: read twice.
 template <int kBf16, int kNv, int kWhole, int kHeld>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kFp4Limit)
     quantize_fp4_kernel(const void* x, int64_t ldx, int N, int D, uint8_t* codes, uint8_t* scales,
                         float* row_scales, int R) {
-  __shared__ uint32_t s_max[32];
+  __shared__ uint32_t s_max[kFp4Limit / 32];
+  __shared__ float s_stage[kWhole ? 1 : kFp4Limit / 32][kWhole ? 1 : kWarpStage<16>];
   constexpr int kElt = kBf16 ? 2 : 4;
-  constexpr int kLanes4 = (kNv ? 2 : 4) * 4;   // threads of four blocks
-  const int t = static_cast<int>(threadIdx.x) % R;
+  constexpr int kLanes = kNv ? 1 : 2;   // of a block
+  const int t = static_cast<int>(threadIdx.x) % R, warp = static_cast<int>(threadIdx.x) >> 5;
+  float* const stage = s_stage[kWhole ? 0 : warp];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / R) + threadIdx.x / R;
   const bool live = row < N;
   const uint8_t* const from = static_cast<const uint8_t*>(x) + row * ldx * kElt;
   const int width = live ? D : 0;
-  const int nvec = static_cast<int>(fp4_stages(D)) * (kFp4Stage / 8);
+  const int chunks = static_cast<int>(fp4_stages(D)) * (kFp4Stage / 16);
   const int code_bytes = static_cast<int>(fp4_code_bytes(D));
-  float held[kHeld > 0 ? kHeld : 1][8];
+  // a block's largest magnitude; the row's over its finite values
+  auto block_max = [&](const Chunk<kBf16>& c) { return largest_of_lanes<kLanes>(c.largest()); };
+  auto row_max = [&](const Chunk<kBf16>& c, uint32_t block, uint32_t m) {
+    if (block < kInfBits) return max(m, block);
+    float v[16];
+    c.widen(v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = magnitude(v[e]) < kInfBits ? max(m, magnitude(v[e])) : m;
+    return m;
+  };
+  Chunk<kBf16> held[kHeld > 0 ? kHeld : 1];
+  uint32_t amax[kHeld > 0 ? kHeld : 1];
   if constexpr (kHeld > 0) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) load_vector<kBf16, kWhole>(from, t + k * R, width, held[k]);
+    for (int k = 0; k < kHeld; ++k) held[k] = load_chunk<kBf16, kWhole>(from, t + k * R, width, stage);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) amax[k] = block_max(held[k]);
   }
-  float inv_row = 1.f;
+  RowScale g{127u};
   if constexpr (kNv) {
     uint32_t m = 0;
     if constexpr (kHeld > 0) {
 #pragma unroll
-      for (int k = 0; k < kHeld; ++k) m = largest_finite(held[k], m);
+      for (int k = 0; k < kHeld; ++k) m = row_max(held[k], amax[k], m);
     } else {
-      for (int i = t; i < nvec; i += R) {
-        float v[8];
-        load_vector<kBf16, kWhole>(from, i, width, v);
-        m = largest_finite(v, m);
+      for (int i = t; i < chunks; i += R) {
+        const Chunk<kBf16> c = load_chunk<kBf16, kWhole>(from, i, width, stage);
+        m = row_max(c, block_max(c), m);
       }
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (R > 32) {
-      const int warp = static_cast<int>(threadIdx.x) >> 5, per = R >> 5;
+      const int per = R >> 5;
       if ((threadIdx.x & 31) == 0) s_max[warp] = m;
       __syncthreads();
       for (int w = 0; w < per; ++w) m = max(m, s_max[warp / per * per + w]);
     }
-    uint32_t byte = power_scale_byte<11, 0x280000u>(m);
-    byte = m == 0 ? 127u : byte < 1u ? 1u : byte;
-    inv_row = inverse_power_of_byte(byte);
-    if (t == 0 && live) row_scales[row] = power_of_byte(byte);
+    const uint32_t byte = power_scale_byte<11, 0x280000u>(m);
+    g.byte = m == 0 ? 127u : byte < 1u ? 1u : byte;
+    if (t == 0 && live) row_scales[row] = g.value();
   }
-  auto put = [&](int i, float (&v)[8]) {
+  auto put = [&](int i, const Chunk<kBf16>& c, uint32_t block) {
     uint32_t byte;
-    const uint32_t c = quantize_vector<kNv>(v, inv_row, byte);
-    // (a block behind the row, whose largest is 0, has the byte 0 too)
-    const uint32_t w = four_bytes<kNv>(byte);
-    if (i >= nvec) return;
-    if (live && i * 4 < code_bytes) *reinterpret_cast<uint32_t*>(codes + row * code_bytes + i * 4) = c;
-    if (t % kLanes4 == 0) *reinterpret_cast<uint32_t*>(scales + fp4_scale_at(row, i / kLanes4, D, kNv)) = w;
+    const uint2 code = quantize_chunk<kBf16, kNv>(c, block, g, byte);
+    // the bytes of four neighbouring blocks, in the first of their lanes (a block behind the row, whose
+    // largest is 0, has the byte 0 too)
+    uint32_t w = byte << (8 * ((threadIdx.x / kLanes) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, kLanes);
+    w |= __shfl_xor_sync(0xffffffffu, w, 2 * kLanes);
+    if (i >= chunks) return;
+    if (live && i * 8 < code_bytes) *reinterpret_cast<uint2*>(codes + row * code_bytes + i * 8) = code;
+    if (t % (4 * kLanes) == 0)
+      *reinterpret_cast<uint32_t*>(scales + fp4_scale_at(row, i / (4 * kLanes), D, kNv)) = w;
   };
   if constexpr (kHeld > 0) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) put(t + k * R, held[k]);
+    for (int k = 0; k < kHeld; ++k) put(t + k * R, held[k], amax[k]);
   } else {
-    for (int i = t; i < (nvec + R - 1) / R * R; i += R) {   // whole warps, for the shuffles
-      float v[8];
-      load_vector<kBf16, kWhole>(from, i, width, v);
-      put(i, v);
+    for (int i = t; i < (chunks + R - 1) / R * R; i += R) {   // whole warps, for the shuffles
+      const Chunk<kBf16> c = load_chunk<kBf16, kWhole>(from, i, width, stage);
+      put(i, c, block_max(c));
     }
   }
 }
 
-template <int kBf16, int kNv>
+template <int kBf16, int kNv, int kWhole>
 __global__ void __launch_bounds__(kFp4Threads)
     dequantize_fp4_kernel(const uint8_t* codes, const uint8_t* scales, const float* row_scales, int N, int D,
-                          void* x, int64_t ldx, int X, int whole) {
+                          void* x, int64_t ldx, int X) {
+  __shared__ float s_stage[kWhole ? 1 : kFp4Threads / 32][kWhole ? 1 : kWarpStage<8>];
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kBlock = fp4_block(kNv);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kFp4Threads / X) + threadIdx.x / X;
-  if (row >= N) return;
+  if (row >= N) return;   // whole warps: X is at least 32
   const int t = static_cast<int>(threadIdx.x) % X;
   uint8_t* const to = static_cast<uint8_t*>(x) + row * ldx * kElt;
   const float row_scale = kNv ? row_scales[row] : 1.f;
-  const int first = static_cast<int>(blockIdx.y) * X * kFp4Vectors + t;
-  uint32_t c[kFp4Vectors], byte[kFp4Vectors];
+  const int first = static_cast<int>(blockIdx.y) * X * kFp4Values + t;
+  uint32_t c[kFp4Values] = {}, byte[kFp4Values] = {};
 #pragma unroll
-  for (int k = 0; k < kFp4Vectors; ++k) {
+  for (int k = 0; k < kFp4Values; ++k) {
     const int i = first + k * X;
     if (i * 8 < D) {
       const int block = i * 8 / kBlock;
@@ -172,9 +235,9 @@ __global__ void __launch_bounds__(kFp4Threads)
     }
   }
 #pragma unroll
-  for (int k = 0; k < kFp4Vectors; ++k) {
+  for (int k = 0; k < kFp4Values; ++k) {
     const int i = first + k * X;
-    if (i * 8 >= D) break;
+    if ((i - (t & 31)) * 8 >= D) break;
     float s, none;
     if (kNv) widen_e4m3x2(byte[k], s, none);
     else s = power_of_byte(byte[k]);
@@ -182,7 +245,9 @@ __global__ void __launch_bounds__(kFp4Threads)
     widen_e2m1x8(c[k], v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] * s * row_scale;
-    if (whole && i * 8 + 8 <= D) {
+    if constexpr (!kWhole) {
+      store_staged<kBf16, 8>(to, (i - (t & 31)) * 8, D, s_stage[threadIdx.x >> 5], v);
+    } else if (i * 8 + 8 <= D) {
       Param<kBf16, 8> out;
       out.narrow(v);
       out.save(to, i * 8);
@@ -192,10 +257,6 @@ __global__ void __launch_bounds__(kFp4Threads)
         if (i * 8 + e < D) store_from_f32(to, i * 8 + e, v[e], kBf16);
     }
   }
-}
-
-bool whole_vectors(const void* x, int bf16, int64_t ldx) {
-  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * (bf16 ? 2 : 4) % 16 == 0;
 }
 
 // f with a, b, c as compile-time constants.
@@ -211,14 +272,10 @@ cudaError_t with_flags(bool a, bool b, bool c, F&& f) {
 }  // namespace
 
 cudaError_t launch_quantize_fp4(const void* x, int bf16, int64_t ldx, int N, int D, int nv, uint8_t* codes,
-                                uint8_t* scales, float* row_scales, int sms, cudaStream_t stream) {
-  const int nvec = static_cast<int>(fp4_stages(D)) * (kFp4Stage / 8);
+                                uint8_t* scales, float* row_scales, cudaStream_t stream) {
+  const int chunks = static_cast<int>(fp4_stages(D)) * (kFp4Stage / 16);
   const int64_t rows = (static_cast<int64_t>(N) + kFp4RowTile - 1) / kFp4RowTile * kFp4RowTile;
-  // Threads of a row: enough for kFp4Vectors vectors each, and more while the rows alone do not
-  // fill the GPU.
-  int R = 32;
-  while (R < 1024 && R * kFp4Vectors < nvec) R *= 2;
-  while (R < 1024 && R < nvec && N * static_cast<int64_t>(R) < static_cast<int64_t>(sms) * 512) R *= 2;
+  const int R = threads_of_row(N, chunks, kFp4Held, 32, kFp4Limit);
   const int block = R < kFp4Threads ? kFp4Threads : R;
   const unsigned grid = static_cast<unsigned>((rows * R + block - 1) / block);
   return with_flags(bf16 != 0, nv != 0, whole_vectors(x, bf16, ldx), [&](auto b, auto n, auto w) {
@@ -226,10 +283,9 @@ cudaError_t launch_quantize_fp4(const void* x, int bf16, int64_t ldx, int N, int
       kern<<<grid, block, 0, stream>>>(x, ldx, N, D, codes, scales, row_scales, R);
       return cudaGetLastError();
     };
-    const int per = (nvec + R - 1) / R;
+    const int per = (chunks + R - 1) / R;
     if (per <= 1) return go(quantize_fp4_kernel<b(), n(), w(), 1>);
-    if (per <= 2) return go(quantize_fp4_kernel<b(), n(), w(), 2>);
-    if (per <= kFp4Vectors) return go(quantize_fp4_kernel<b(), n(), w(), kFp4Vectors>);
+    if (per <= kFp4Held) return go(quantize_fp4_kernel<b(), n(), w(), kFp4Held>);
     return go(quantize_fp4_kernel<b(), n(), w(), 0>);
   });
 }
@@ -237,13 +293,11 @@ cudaError_t launch_quantize_fp4(const void* x, int bf16, int64_t ldx, int N, int
 cudaError_t launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float* row_scales, int N,
                                   int D, int nv, void* x, int bf16, int64_t ldx, cudaStream_t stream) {
   const int nvec = (D + 7) / 8;
-  int X = 4;
-  while (X < kFp4Threads && X < nvec) X *= 2;
+  const int X = threads_of_row(N, nvec, kFp4Values, 32, kFp4Threads);
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(N) * X + kFp4Threads - 1) / kFp4Threads),
-                  static_cast<unsigned>((nvec + X * kFp4Vectors - 1) / (X * kFp4Vectors)));
-  return with_flags(bf16 != 0, nv != 0, false, [&](auto b, auto n, auto) {
-    dequantize_fp4_kernel<b(), n()><<<grid, kFp4Threads, 0, stream>>>(codes, scales, row_scales, N, D, x, ldx, X,
-                                                                      whole_vectors(x, bf16, ldx));
+                  static_cast<unsigned>((nvec + X * kFp4Values - 1) / (X * kFp4Values)));
+  return with_flags(bf16 != 0, nv != 0, whole_vectors(x, bf16, ldx), [&](auto b, auto n, auto w) {
+    dequantize_fp4_kernel<b(), n(), w()><<<grid, kFp4Threads, 0, stream>>>(codes, scales, row_scales, N, D, x, ldx, X);
     return cudaGetLastError();
   });
 }
