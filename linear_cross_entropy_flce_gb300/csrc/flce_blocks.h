@@ -54,6 +54,10 @@ cudaError_t launch_unpack_e4m3(const uint8_t* packed, int N, int D, void* x, int
 
 // Layer norm that leaves x packed, and its backward pass from that (bf16 / wbf16: types of the rows /
 // of weight, bias and their gradients). part as launch_layer_norm_backward's.
+cudaError_t launch_layer_norm_packed(const void* x, int bf16, int64_t ldx, const void* weight,
+                                     const void* bias, int wbf16, int N, int D, float eps, void* y,
+                                     int64_t ldy, float* mean, float* rstd, uint8_t* packed, int sms,
+                                     cudaStream_t stream);
 cudaError_t launch_layer_norm_backward_packed(const void* dy, int64_t lddy, const uint8_t* packed, int bf16,
                                               const void* weight, int wbf16, const float* mean,
                                               const float* rstd, int N, int D, void* dx, int64_t lddx,

@@ -2,7 +2,7 @@
 // sequences.
 //
 //   flce_pack_e4m3, flce_unpack_e4m3   one kernel
-//   flce_layer_norm_packed             the pack of x, then flce_layer_norm
+//   flce_layer_norm_packed             many rows: one kernel; else the pack of x, then flce_layer_norm's
 //   flce_layer_norm_packed_backward    as flce_layer_norm_backward
 //   flce_quantize_fp4, flce_dequantize_fp4, flce_linear_fp4   one kernel
 #include <algorithm>
@@ -115,7 +115,6 @@ int flce_layer_norm_packed(const void* x, int32_t dtype, int64_t ldx, const void
                            const void* bias, int32_t wdtype, int64_t N, int64_t D, float eps,
                            void* y, int64_t ldy, float* mean, float* rstd, uint8_t* packed,
                            void* stream) {
-  // what flce_layer_norm refuses is refused before the pack is enqueued
   int rc = check_matrix(N, D, dtype, ldx);
   if (rc != FLCE_OK) return rc;
   if (!known_dtype(wdtype) || !(eps >= 0.f) || std::isinf(eps)) return FLCE_ERR_OPTION;
@@ -130,12 +129,9 @@ int flce_layer_norm_packed(const void* x, int32_t dtype, int64_t ldx, const void
   int sms = 0;
   rc = device_info(&sms);
   if (rc != FLCE_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_pack_e4m3(x, dtype == FLCE_DTYPE_BF16, ldx, static_cast<int>(N), static_cast<int>(D), packed, st) !=
-      cudaSuccess)
-    return FLCE_ERR_CUDA;
-  return done(launch_layer_norm(x, dtype == FLCE_DTYPE_BF16, ldx, weight, bias, wdtype == FLCE_DTYPE_BF16,
-                                static_cast<int>(N), static_cast<int>(D), eps, y, ldy, mean, rstd, sms, st));
+  return done(launch_layer_norm_packed(x, dtype == FLCE_DTYPE_BF16, ldx, weight, bias, wdtype == FLCE_DTYPE_BF16,
+                                       static_cast<int>(N), static_cast<int>(D), eps, y, ldy, mean, rstd, packed,
+                                       sms, static_cast<cudaStream_t>(stream)));
 }
 
 int flce_layer_norm_packed_backward(const void* dy, int32_t dtype, int64_t lddy,

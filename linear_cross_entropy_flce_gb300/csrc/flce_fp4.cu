@@ -7,12 +7,12 @@
 // down).
 //
 // A group of R threads holds a row in registers, 16 neighbouring values a chunk, so that it is
-// read once for the row's and the blocks' largest magnitudes and the codes; rows of more than 16384
-// values are read again instead. Rows that do not allow 16-byte accesses come through shared memory, a
-// warp's 512 values at a time. 1 / s is rounded, so the quotient x r is corrected by its
-// residual, which makes it x / s rounded once (Markstein's theorem): a value halfway between two codes
-// stays there. (In fp32 no other quotient is rounded onto such a place: its distance from it is at
-// least the quotient's own last place.)
+// read once for the row's and the blocks' largest magnitudes and the codes; rows of more than 32768
+// values (16384 through shared memory) are read again instead. Rows that do not allow 16-byte accesses come through shared memory, a
+// warp's 512 values at a time. 1 / s is taken in two parts, r and its
+// rest, so that x r + x rest is x / s to within 2^-46, rounded once: a value halfway between two codes
+// stays there. (And no other quotient is rounded onto such a place: its distance from it is more than
+// half the quotient's own last place.)
 #include <cstdint>
 
 #include "flce_blocks.cuh"
@@ -23,7 +23,9 @@ namespace {
 
 constexpr int kFp4Threads = 256;
 constexpr int kFp4Limit = 512;   // threads of a row at most
-constexpr int kFp4Held = 2;      // chunks of 16 in a thread's registers at most
+// Chunks of 16 in a thread's registers at most. In us with 2 / 4 / 8: 128256 x 4096 bf16 nvfp4 294 / 262 / 277,
+// mxfp4 221 / 190 / 210, 64128 x 4096 fp32 262 / 214 / 486; through shared memory 3001 x 1111 fp32 6.9 / 8.7.
+constexpr int fp4_held(bool whole) { return whole ? 4 : 2; }
 constexpr int kFp4Values = 4;    // vectors of 8 per thread, of the values back
 
 // 16 values as loaded.
@@ -95,6 +97,9 @@ struct RowScale {
   __device__ float inverse() const { return inverse_power_of_byte(byte); }
 };
 
+// 1 / 6 rounded down, and what is left of it.
+constexpr float kSixth = 0x1.555554p-3f, kSixthRest = 0x1.555556p-27f;
+
 // A chunk's codes, eight to a word, and its scale byte (of 16 values, or of 32 with its neighbour's).
 // amax: the bits of the block's largest magnitude.
 template <int kBf16, int kNv>
@@ -103,20 +108,25 @@ __device__ __forceinline__ uint2 quantize_chunk(const Chunk<kBf16>& c, uint32_t 
   c.widen(v);
   const bool finite = amax < kInfBits;
   if constexpr (kNv) {
-    byte = finite ? e4m3x2(__fdiv_rn(__uint_as_float(amax), 6.f) * g.inverse(), 0.f) & 0xFFu : 0x7Fu;
+    // Powers of two do not round, so v r / g is (v / g) r; but in rows so small that one of these
+    // leaves the normal numbers, v is divided first and amax / 6 taken as it is defined.
+    const bool tiny = g.byte < 32u;
+    const float a = __uint_as_float(amax);
+    const float sixth = (tiny ? __fdiv_rn(a, 6.f) : fmaf(a, kSixth, a * kSixthRest)) * g.inverse();
+    byte = finite ? e4m3x2(sixth, 0.f) & 0xFFu : 0x7Fu;
     float s, none;
     widen_e4m3x2(finite ? byte : 0u, s, none);
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    // Powers of two do not round: x = v / g is as good as v, with s g for s and r / g for r, but where r / g
-    // would overflow or a residual vanish.
-    const bool tiny = g.byte < 32u;
-    const float t = tiny ? s : s * g.value(), rt = tiny ? r : r * g.inverse(), f = tiny ? g.inverse() : 1.f;
+    // 1 / s = r + rest, r rounded down, so that the rest is not negative and -0 stays -0
+    float r = s > 0.f ? __frcp_rd(s) : 0.f, rest = fmaf(-s, r, 1.f) * r;
+    if (tiny) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float x = v[e] * f;
-      const float q = x * rt;
-      v[e] = fmaf(-fmaf(q, t, -x), rt, q);   // (in this order -0 stays -0)
+      for (int e = 0; e < 16; ++e) v[e] *= g.inverse();
+    } else {
+      r *= g.inverse();
+      rest *= g.inverse();
     }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = fmaf(v[e], r, v[e] * rest);
   } else {
     byte = power_scale_byte<2, 0x400000u>(amax);
     const float inv = finite ? inverse_power_of_byte(byte) : 0.f;
@@ -275,17 +285,20 @@ cudaError_t launch_quantize_fp4(const void* x, int bf16, int64_t ldx, int N, int
                                 uint8_t* scales, float* row_scales, cudaStream_t stream) {
   const int chunks = static_cast<int>(fp4_stages(D)) * (kFp4Stage / 16);
   const int64_t rows = (static_cast<int64_t>(N) + kFp4RowTile - 1) / kFp4RowTile * kFp4RowTile;
-  const int R = threads_of_row(N, chunks, kFp4Held, 32, kFp4Limit);
+  const bool whole = whole_vectors(x, bf16, ldx);
+  const int R = threads_of_row(N, chunks, fp4_held(whole), 32, kFp4Limit);
   const int block = R < kFp4Threads ? kFp4Threads : R;
   const unsigned grid = static_cast<unsigned>((rows * R + block - 1) / block);
-  return with_flags(bf16 != 0, nv != 0, whole_vectors(x, bf16, ldx), [&](auto b, auto n, auto w) {
+  return with_flags(bf16 != 0, nv != 0, whole, [&](auto b, auto n, auto w) {
     auto go = [&](auto kern) {
       kern<<<grid, block, 0, stream>>>(x, ldx, N, D, codes, scales, row_scales, R);
       return cudaGetLastError();
     };
     const int per = (chunks + R - 1) / R;
     if (per <= 1) return go(quantize_fp4_kernel<b(), n(), w(), 1>);
-    if (per <= kFp4Held) return go(quantize_fp4_kernel<b(), n(), w(), kFp4Held>);
+    if (per <= 2) return go(quantize_fp4_kernel<b(), n(), w(), 2>);
+    if constexpr (fp4_held(w()) >= 4)
+      if (per <= 4) return go(quantize_fp4_kernel<b(), n(), w(), 4>);
     return go(quantize_fp4_kernel<b(), n(), w(), 0>);
   });
 }

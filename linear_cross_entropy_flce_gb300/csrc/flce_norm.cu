@@ -568,6 +568,20 @@ cudaError_t norm_backward(const void* dy, int64_t lddy, const void* x, int bf16,
 
 }  // namespace
 
+cudaError_t launch_layer_norm_packed(const void* x, int bf16, int64_t ldx, const void* weight,
+                                     const void* bias, int wbf16, int N, int D, float eps, void* y,
+                                     int64_t ldy, float* mean, float* rstd, uint8_t* packed, int sms,
+                                     cudaStream_t stream) {
+  if (norm_stream_fits(D, bf16 ? 2 : 4)) {
+    const cudaError_t e = launch_norm_stream_packed(x, bf16, ldx, weight, bias, wbf16, N, D, eps, y, ldy,
+                                                    mean, rstd, packed, sms, stream);
+    if (e != cudaErrorNotSupported) return e;
+  }
+  const cudaError_t e = launch_pack_e4m3(x, bf16, ldx, N, D, packed, stream);   // (y may be x)
+  if (e != cudaSuccess) return e;
+  return launch_layer_norm(x, bf16, ldx, weight, bias, wbf16, N, D, eps, y, ldy, mean, rstd, sms, stream);
+}
+
 cudaError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int bf16,
                                        int64_t ldx, const void* weight, int wbf16,
                                        const float* mean, const float* rstd, int N, int D,
