@@ -82,16 +82,14 @@ __device__ __forceinline__ int lower_bound(const uint32_t* ids, int N, uint32_t 
   return lo;
 }
 
-// `sum` scaled to (or onto) dW at element `at`, VW elements.
-template <int kWbf16, int VW>
+// `sum` scaled to (kAdd: onto `old`) dW at element `at`, VW elements.
+template <int kWbf16, int VW, int kAdd>
 __device__ __forceinline__ void put_row(void* dW, int64_t at, const float (&sum)[VW], float scale,
-                                        int accumulate) {
+                                        const Param<kWbf16, VW>& old) {
   using Out = Param<kWbf16, VW>;
   uint8_t* const p = static_cast<uint8_t*>(dW) + at * (kWbf16 ? 2 : 4);
   float v[VW];
-  if (accumulate) {
-    Out old;
-    old.load(p, 0, 0.f);
+  if constexpr (kAdd) {
     old.widen(v);
 #pragma unroll
     for (int e = 0; e < VW; ++e) v[e] = fmaf(sum[e], scale, v[e]);
@@ -104,12 +102,30 @@ __device__ __forceinline__ void put_row(void* dW, int64_t at, const float (&sum)
   out.save(p, 0);
 }
 
+// D zeros, 16 bytes at a time wherever the row begins, by the whole CTA.
+template <int kWbf16>
+__device__ __forceinline__ void zero_row(uint8_t* row, int D) {
+  constexpr int kElt = kWbf16 ? 2 : 4;
+  const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / kElt;
+  const int t = threadIdx.x;
+  const int whole = D > head ? (D - head) * kElt / 16 : 0;
+  const int tail = head + whole * (16 / kElt);   // elements from here on, and before head, go alone
+  auto one = [&](int i) {
+    if (kWbf16) reinterpret_cast<uint16_t*>(row)[i] = 0;
+    else reinterpret_cast<uint32_t*>(row)[i] = 0;
+  };
+  if (t < head && t < D) one(t);
+  if (t >= 32 && t < 64 && tail + t - 32 < D) one(tail + t - 32);
+  for (int i = t; i < whole; i += kGradThreads)
+    reinterpret_cast<uint4*>(row + head * kElt)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // CTAs [0, ranges * pieces): a range of the sorted order and a piece of the columns. The others (not
 // accumulating): kZeroRows rows of dW each.
-template <int kBf16, int kWbf16, int VW>
+template <int kBf16, int kWbf16, int VW, int kAdd>
 __global__ void __launch_bounds__(kGradThreads)
     embedding_grad_kernel(const void* dy, int64_t lddy, const uint32_t* ids, const uint32_t* perm, int N,
-                          int V, int D, float scale, void* dW, int64_t ldw, int accumulate, float* part,
+                          int V, int D, float scale, void* dW, int64_t ldw, float* part,
                           int ranges, int range, int pieces) {
   using In = Param<kBf16, VW>;
   __shared__ uint32_t s_id[kGradThreads], s_row[kGradThreads];
@@ -129,16 +145,8 @@ __global__ void __launch_bounds__(kGradThreads)
       s_absent[threadIdx.x] = absent;
     }
     __syncthreads();
-    float zero[VW];
-#pragma unroll
-    for (int e = 0; e < VW; ++e) zero[e] = 0.f;
-    Param<kWbf16, VW> z;
-    z.narrow(zero);
-    for (int r = 0; r < kZeroRows; ++r) {
-      if (!s_absent[r]) continue;
-      uint8_t* const p = static_cast<uint8_t*>(dW) + (row0 + r) * ldw * (kWbf16 ? 2 : 4);
-      for (int i = threadIdx.x; i < nvec; i += kGradThreads) z.save(p, i * VW);
-    }
+    for (int r = 0; r < kZeroRows; ++r)
+      if (s_absent[r]) zero_row<kWbf16>(static_cast<uint8_t*>(dW) + (row0 + r) * ldw * (kWbf16 ? 2 : 4), D);
     return;
   }
   const int r = static_cast<int>(blockIdx.x) / pieces;
@@ -155,7 +163,7 @@ __global__ void __launch_bounds__(kGradThreads)
   for (int e = 0; e < VW; ++e) sum[e] = 0.f;
   bool head = true;   // no id has ended yet in this range
   uint32_t id = none;
-  auto end_of_id = [&](bool last) {
+  auto end_of_id = [&](bool last, const Param<kWbf16, VW>& old) {
     if (id == none) return;
     const bool joins = (head && id == before) || (last && id == after);
     if (in) {
@@ -165,12 +173,19 @@ __global__ void __launch_bounds__(kGradThreads)
         out.narrow(sum);
         out.save(reinterpret_cast<uint8_t*>(part + (static_cast<int64_t>(r) * 2 + slot) * D), i * VW);
       } else {
-        put_row<kWbf16, VW>(dW, id * ldw + static_cast<int64_t>(i) * VW, sum, scale, accumulate);
+        put_row<kWbf16, VW, kAdd>(dW, id * ldw + static_cast<int64_t>(i) * VW, sum, scale, old);
       }
     }
     head = false;
 #pragma unroll
     for (int e = 0; e < VW; ++e) sum[e] = 0.f;
+  };
+  // the old values of the rows that end: read with the rows of dy (adding)
+  Param<kWbf16, VW> old[kAdd ? kAhead : 1], last_old;
+  auto read_old = [&](uint32_t row) {
+    Param<kWbf16, VW> v;
+    v.load(static_cast<const uint8_t*>(dW) + row * ldw * (kWbf16 ? 2 : 4), i * VW, 0.f);
+    return v;
   };
   for (int at = first; at < end; at += kGradThreads) {
     const int n = end - at < kGradThreads ? end - at : kGradThreads;
@@ -187,14 +202,25 @@ __global__ void __launch_bounds__(kGradThreads)
         for (int k = 0; k < kAhead; ++k)
           if (j + k < n && s_id[j + k] != none)
             row[k].load(static_cast<const uint8_t*>(dy) + s_row[j + k] * lddy * (kBf16 ? 2 : 4), i * VW, 0.f);
+        if constexpr (kAdd) {
+          uint32_t before_k = id;
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            if (j + k >= n) break;
+            const uint32_t here = s_id[j + k];
+            if (here != before_k && here != none) old[k] = read_old(here);
+            before_k = here;
+          }
+        }
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (j + k >= n) break;
         const uint32_t here = s_id[j + k];
         if (here != id) {
-          end_of_id(false);
+          end_of_id(false, last_old);
           id = here;
+          if constexpr (kAdd) last_old = old[k];
         }
         if (in && here != none) {
           float v[VW];
@@ -204,19 +230,20 @@ __global__ void __launch_bounds__(kGradThreads)
       }
     }
   }
-  end_of_id(true);
+  end_of_id(true, last_old);
 }
 
 // The ids that go on over the end of a range: the range in which one begins holds its first part in
-// slot 1, the ranges after it the others in slot 0. CTA (range, piece of 32 vectors of columns),
-// the parts dealt to its warps and added in a fixed order.
+// slot 1, the ranges after it the others in slot 0. CTA (range, piece of 128 vectors of columns, four a
+// lane, so that few CTAs come for nothing), the parts dealt to its warps and added in a fixed order.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinVectors = 4;
 
-template <int kWbf16, int VW>
+template <int kWbf16, int VW, int kAdd>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     embedding_join_kernel(const float* part, const uint32_t* ids, int N, int V, int D, float scale, void* dW,
-                          int64_t ldw, int accumulate, int range, int pieces) {
-  __shared__ float s_sum[kJoinWarps][32][VW];
+                          int64_t ldw, int range, int pieces) {
+  __shared__ __align__(16) float s_sum[kJoinWarps][32 * kJoinVectors * VW];
   __shared__ int s_last;
   wait_for_launch_before();
   const int r = static_cast<int>(blockIdx.x) / pieces;   // all ranges but the last
@@ -228,30 +255,51 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   __syncthreads();
   const int last = s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = static_cast<int>(blockIdx.x) % pieces * 32 + lane;
-  const bool in = i < D / VW;
-  float sum[VW];
+  const int base = static_cast<int>(blockIdx.x) % pieces * 32 * kJoinVectors, nvec = D / VW;
+  float sum[kJoinVectors][VW];
 #pragma unroll
-  for (int e = 0; e < VW; ++e) sum[e] = 0.f;
-  if (in) {
-#pragma unroll 4
-    for (int q = r + warp; q <= last; q += kJoinWarps) {
-      Param<0, VW> in_part;
-      float v[VW];
-      in_part.load(part + (static_cast<int64_t>(q) * 2 + (q == r ? 1 : 0)) * D, i * VW, 0.f);
-      in_part.widen(v);
-      add_n(sum, v);
+  for (int k = 0; k < kJoinVectors; ++k)
+#pragma unroll
+    for (int e = 0; e < VW; ++e) sum[k][e] = 0.f;
+#pragma unroll 2
+  for (int q = r + warp; q <= last; q += kJoinWarps) {
+    const float* const from = part + (static_cast<int64_t>(q) * 2 + (q == r ? 1 : 0)) * D;
+#pragma unroll
+    for (int k = 0; k < kJoinVectors; ++k) {
+      const int i = base + k * 32 + lane;
+      if (i < nvec) {
+        Param<0, VW> in;
+        float v[VW];
+        in.load(from, i * VW, 0.f);
+        in.widen(v);
+        add_n(sum[k], v);
+      }
     }
   }
 #pragma unroll
-  for (int e = 0; e < VW; ++e) s_sum[warp][lane][e] = sum[e];
+  for (int k = 0; k < kJoinVectors; ++k) {
+    Param<0, VW> out;
+    out.narrow(sum[k]);
+    out.save(reinterpret_cast<uint8_t*>(s_sum[warp]), (k * 32 + lane) * VW);
+  }
   __syncthreads();
-  if (warp != 0 || !in) return;
+  const int i = base + static_cast<int>(threadIdx.x);   // a vector a thread
+  if (threadIdx.x >= 32 * kJoinVectors || i >= nvec) return;
+  float total[VW];
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w)
+  for (int e = 0; e < VW; ++e) total[e] = 0.f;
 #pragma unroll
-    for (int e = 0; e < VW; ++e) sum[e] += s_sum[w][lane][e];
-  put_row<kWbf16, VW>(dW, id * ldw + static_cast<int64_t>(i) * VW, sum, scale, accumulate);
+  for (int w = 0; w < kJoinWarps; ++w) {
+    Param<0, VW> in;
+    float v[VW];
+    in.load(s_sum[w], static_cast<int>(threadIdx.x) * VW, 0.f);
+    in.widen(v);
+    add_n(total, v);
+  }
+  Param<kWbf16, VW> old;
+  const int64_t at = id * ldw + static_cast<int64_t>(i) * VW;
+  if constexpr (kAdd) old.load(static_cast<const uint8_t*>(dW) + at * (kWbf16 ? 2 : 4), 0, 0.f);
+  put_row<kWbf16, VW, kAdd>(dW, at, total, scale, old);
 }
 
 // f(VW) for the widest access: 8 elements, 4 or 1.
@@ -314,18 +362,20 @@ cudaError_t launch_embedding_grad(const void* dy, int bf16, int64_t lddy, const 
     constexpr int VW = w();
     const int nvec = D / VW;
     return with_types(bf16, wbf16, [&](auto b, auto wb) {
-      const int pieces = (nvec + kGradThreads - 1) / kGradThreads;
-      const unsigned grid = static_cast<unsigned>(ranges * pieces) + zeros;
-      if (grid == 0) return cudaSuccess;
-      const cudaError_t e =
-          launch_after(embedding_grad_kernel<b(), wb(), VW>, dim3(grid), dim3(kGradThreads), 0, stream, dy, lddy,
-                       ids, perm, N, V, D, scale, dW, ldw, accumulate, part, ranges, range, pieces);
-      if (e != cudaSuccess || ranges <= 1) return e;
-      const int columns = (nvec + 31) / 32;
-      return launch_after(embedding_join_kernel<wb(), VW>,
-                          dim3(static_cast<unsigned>((ranges - 1) * columns)), dim3(32 * kJoinWarps), 0, stream,
-                          static_cast<const float*>(part), ids, N, V, D, scale, dW, ldw, accumulate, range,
-                          columns);
+      auto go = [&](auto add) {
+        const int pieces = (nvec + kGradThreads - 1) / kGradThreads;
+        const unsigned grid = static_cast<unsigned>(ranges * pieces) + zeros;
+        if (grid == 0) return cudaSuccess;
+        const cudaError_t e =
+            launch_after(embedding_grad_kernel<b(), wb(), VW, add()>, dim3(grid), dim3(kGradThreads), 0, stream, dy,
+                         lddy, ids, perm, N, V, D, scale, dW, ldw, part, ranges, range, pieces);
+        if (e != cudaSuccess || ranges <= 1) return e;
+        const int columns = (nvec + 32 * kJoinVectors - 1) / (32 * kJoinVectors);
+        return launch_after(embedding_join_kernel<wb(), VW, add()>,
+                            dim3(static_cast<unsigned>((ranges - 1) * columns)), dim3(32 * kJoinWarps), 0, stream,
+                            static_cast<const float*>(part), ids, N, V, D, scale, dW, ldw, range, columns);
+      };
+      return accumulate ? go(std::integral_constant<int, 1>{}) : go(std::integral_constant<int, 0>{});
     });
   });
 }

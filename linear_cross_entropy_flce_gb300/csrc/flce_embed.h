@@ -9,13 +9,16 @@
 
 namespace flce {
 
-// Tokens that one CTA sorts, in shared memory; more are sorted in tiles of as many.
-constexpr int kSortTile = 16384;
+// Tokens that one cluster sorts, in shared memory; more are sorted in tiles.
+constexpr int kSortCluster = 16384;
+constexpr int kSortTile = 4096;
 constexpr int kSortDigitBits = 9;
 
-// Positions of the sorted order that one CTA adds up: 32, and more where that would make more
-// than 2048 ranges, whose partial rows the workspace holds.
+// Positions of the sorted order that one CTA adds up: 8 for few tokens, so that they are spread over the
+// GPU, else 32, and more where that would make more than 2048 ranges, whose partial rows the workspace
+// holds.
 inline int embed_range(int64_t N) {
+  if (N <= 1024) return 8;
   const int64_t t = (N + 2047) / 2048;
   return static_cast<int>(std::max<int64_t>(32, (t + 7) / 8 * 8));
 }
@@ -34,13 +37,13 @@ inline EmbedPlan make_embed_plan(int64_t N, int64_t D) {
     return here;
   };
   p.ranges = (N + embed_range(N) - 1) / embed_range(N);
-  p.tiles = (N + kSortTile - 1) / kSortTile;
+  p.tiles = N <= kSortCluster ? 0 : (N + kSortTile - 1) / kSortTile;
   const size_t n4 = static_cast<size_t>(N) * 4;
   p.off_ids = take(n4);
   p.off_perm = take(n4);
-  p.off_ids2 = take(p.tiles > 1 ? n4 : 0);
-  p.off_perm2 = take(p.tiles > 1 ? n4 : 0);
-  p.off_counts = take(p.tiles > 1 ? (static_cast<size_t>(p.tiles) << kSortDigitBits) * 4 : 0);
+  p.off_ids2 = take(p.tiles > 0 ? n4 : 0);
+  p.off_perm2 = take(p.tiles > 0 ? n4 : 0);
+  p.off_counts = take(p.tiles > 0 ? (static_cast<size_t>(p.tiles) << kSortDigitBits) * 4 : 0);
   p.off_part = take(static_cast<size_t>(p.ranges) * 2 * static_cast<size_t>(D) * 4);
   p.total = at;
   return p;

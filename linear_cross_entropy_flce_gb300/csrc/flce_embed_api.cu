@@ -3,7 +3,7 @@
 //
 //   flce_embedding            one kernel
 //   flce_embedding_backward   the sort of the tokens (one kernel up to 16384 of them, else three a
-//                             pass), the ranges' sums with the zeros of the other rows, the join of the
+//                             radix pass), the ranges' sums with the zeros of the other rows, the join of the
 //                             ids that cross ranges
 #include <cmath>
 #include <cstdint>

@@ -6,14 +6,17 @@
 // warp's equals is known and order is kept. Then the counters of all warps are summed digit by
 // digit, and every item knows its place.
 //
-// Up to kSortTile tokens are one tile: one launch takes all passes in shared memory. More go
-// through tiles with three launches a pass (count, offsets of every digit and tile, place).
+// Up to 16384 tokens one cluster of up to 8 CTAs takes all passes: each has a consecutive part of the items,
+// reads the others' digit counts and puts every item where it goes, in the shared memory of whichever
+// CTA owns that place. More tokens go through tiles with three launches a pass (count, offsets of every
+// digit and tile, place).
 //
-// 8192 tokens of 128256 ids (two passes): see the caller's figures.
+// Bound by latency: barriers and dependent accesses to shared memory.
 #include <cstdint>
 
 #include "flce_embed.h"
 #include "flce_launch.cuh"
+#include "ptx.cuh"
 
 namespace flce {
 
@@ -24,7 +27,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1 << kSortDigitBits;
 
 struct SortShared {
-  uint16_t count[kWarps][kBins];   // a tile has at most 16384 items
+  uint16_t count[kWarps][kBins];   // a tile has at most 4096 items
+  uint32_t total[kBins];           // of the tile
   uint32_t base[kBins];
   uint32_t warp_sum[kWarps];
 };
@@ -40,16 +44,16 @@ __device__ __forceinline__ int item_at(int j) {
   return (threadIdx.x >> 5) * 32 * kItems + j * 32 + (threadIdx.x & 31);
 }
 
-// place[j]: for each of this thread's items (n of them in the tile, keys in key) its place by the
-// digit at `shift`; equal digits keep their order. `base` is what shared.base holds for each digit
-// where kGiven (the caller's, after a barrier here), else the tile's own offsets.
-template <int kItems, bool kGiven>
+// place[j]: for each of this thread's items (n of them in the tile, keys in key) its rank by the digit at
+// `shift` among the equal ones of its warp; sh.count: the equal ones in the warps before; sh.total: all of the
+// tile's. Ends with a barrier.
+template <int kItems>
 __device__ __forceinline__ void rank_tile(SortShared& sh, const uint32_t (&key)[kItems], int n, int shift,
                                           int bits, uint32_t (&place)[kItems]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t mask = (1u << bits) - 1u;
   const int bins = 1 << bits;
-  for (int b = lane; b < bins; b += 32) sh.count[warp][b] = 0;
+  for (int b = lane; b < bins / 2; b += 32) reinterpret_cast<uint32_t*>(sh.count[warp])[b] = 0;
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
@@ -67,86 +71,120 @@ __device__ __forceinline__ void rank_tile(SortShared& sh, const uint32_t (&key)[
     __syncwarp();
   }
   __syncthreads();
-  // thread b: digit b's counters become offsets among the warps; the digits' totals are scanned
-  uint32_t total = 0;
   if (threadIdx.x < bins) {
-#pragma unroll 8
+    uint32_t total = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const uint32_t c = sh.count[w][threadIdx.x];
       sh.count[w][threadIdx.x] = static_cast<uint16_t>(total);
       total += c;
     }
-  }
-  if constexpr (!kGiven) {
-    uint32_t sum = total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) sh.warp_sum[warp] = sum;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp && w < kBins / 32; ++w) before += sh.warp_sum[w];
-    if (threadIdx.x < bins) sh.base[threadIdx.x] = before + sum - total;
+    sh.total[threadIdx.x] = total;
   }
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kItems; ++j)
-    if (item_at<kItems>(j) < n) {
-      const uint32_t d = (key[j] >> shift) & mask;
-      place[j] += sh.base[d] + sh.count[warp][d];
-    }
 }
 
+// Of one value per thread, those of the threads before; two barriers.
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* warp_sum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t sum = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += up;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  uint32_t all = lane < kWarps ? warp_sum[lane] : 0;   // each warp scans the warps' sums
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += up;
+  }
+  const uint32_t before = __shfl_sync(0xffffffffu, all, warp > 0 ? warp - 1 : 0);
+  __syncthreads();
+  return (warp > 0 ? before : 0) + sum - v;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+// One cluster; CTA c has items [c per, (c + 1) per), per = 1024 kItems at most.
 template <int kItems>
 __global__ void __launch_bounds__(kThreads, 1)
-    sort_one_tile_kernel(const int32_t* tokens, int N, int V, int ignore_index, int bits, int passes,
-                         uint32_t* ids, uint32_t* perm) {
-  extern __shared__ uint32_t s_dyn[];   // [2][1024 kItems]: ids, places
+    sort_cluster_kernel(const int32_t* tokens, int N, int V, int ignore_index, int bits, int passes, int per,
+                        uint32_t* ids, uint32_t* perm) {
   __shared__ SortShared sh;
+  extern __shared__ uint2 s_items[];   // [1024 kItems]: key, index
   start_next_launch();
-  uint32_t* const s_key = s_dyn;
-  uint32_t* const s_idx = s_dyn + kThreads * kItems;
-  uint32_t key[kItems], idx[kItems], place[kItems];
+  const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(cluster_ctarank());
+  const int first = rank * per;
+  const int n = N - first < per ? N - first : per;
+  uint32_t key[kItems], index[kItems], place[kItems];
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     const int i = item_at<kItems>(j);
-    idx[j] = static_cast<uint32_t>(i);
-    key[j] = i < N ? key_of(tokens, i, V, ignore_index) : 0;
+    index[j] = static_cast<uint32_t>(first + i);
+    key[j] = i < n ? key_of(tokens, first + i, V, ignore_index) : 0;
   }
-  const int per = (bits + passes - 1) / passes;
+  const int digit = (bits + passes - 1) / passes;
   for (int p = 0; p < passes; ++p) {
-    rank_tile<kItems, false>(sh, key, N, p * per, per, place);
-    if (p == passes - 1) break;
+    const int shift = p * digit;
+    const uint32_t mask = (1u << digit) - 1u;
+    rank_tile<kItems>(sh, key, n, shift, digit, place);
+    cluster_sync();   // every CTA's totals are there, and its items of the pass before are read
+    // where this CTA's items of each digit begin: behind all smaller digits, and the CTAs before
+    uint32_t all = 0, before = 0;
+    if (threadIdx.x <= mask) {
+      const uint32_t at = smem_u32(&sh.total[threadIdx.x]);
+#pragma unroll 8
+      for (int c = 0; c < ctas; ++c) {
+        const uint32_t t = ld_cluster_u32(mapa_shared(at, static_cast<uint32_t>(c)));
+        all += t;
+        before += c < rank ? t : 0;
+      }
+    }
+    const uint32_t smaller = sum_before(all, sh.warp_sum);
+    if (threadIdx.x <= mask) sh.base[threadIdx.x] = smaller + before;
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kItems; ++j)
-      if (item_at<kItems>(j) < N) {
-        s_key[place[j]] = key[j];
-        s_idx[place[j]] = idx[j];
+      if (item_at<kItems>(j) < n) {
+        const uint32_t d = (key[j] >> shift) & mask;
+        place[j] += sh.base[d] + sh.count[threadIdx.x >> 5][d];
+        if (p == passes - 1) {
+          ids[place[j]] = key[j];
+          perm[place[j]] = index[j];
+        } else {
+          const uint32_t owner = place[j] / static_cast<uint32_t>(per);
+          st_cluster_v2(mapa_shared(smem_u32(&s_items[place[j] - owner * per]), owner), key[j], index[j]);
+        }
       }
-    __syncthreads();
+    // (also before the CTA leaves: the others read its totals)
+    cluster_sync();
+    if (p == passes - 1) break;
 #pragma unroll
     for (int j = 0; j < kItems; ++j) {
       const int i = item_at<kItems>(j);
-      if (i < N) {
-        key[j] = s_key[i];
-        idx[j] = s_idx[i];
+      if (i < n) {
+        const uint2 v = s_items[i];
+        key[j] = v.x;
+        index[j] = v.y;
       }
     }
-    __syncthreads();
   }
-#pragma unroll
-  for (int j = 0; j < kItems; ++j)
-    if (item_at<kItems>(j) < N) {
-      ids[place[j]] = key[j];
-      perm[place[j]] = idx[j];
-    }
 }
 
 // ---- several tiles -------------------------------------------------------------------
 
 constexpr int kTileItems = kSortTile / kThreads;
+static_assert(kTileItems <= 4, "the counters hold 16 bits");
 
 // keys null: the first pass, from the tokens
 __global__ void __launch_bounds__(kThreads)
@@ -223,11 +261,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int bins = 1 << bits;
   for (int b = threadIdx.x; b < bins; b += kThreads)
     sh.base[b] = offsets[static_cast<int64_t>(b) * gridDim.x + blockIdx.x];
-  rank_tile<kTileItems, true>(sh, key, n, shift, bits, place);
+  rank_tile<kTileItems>(sh, key, n, shift, bits, place);
 #pragma unroll
   for (int j = 0; j < kTileItems; ++j) {
     const int i = item_at<kTileItems>(j);
     if (i < n) {
+      const uint32_t d = (key[j] >> shift) & (bins - 1u);
+      place[j] += sh.base[d] + sh.count[threadIdx.x >> 5][d];
       ids[place[j]] = key[j];
       perm[place[j]] = places != nullptr ? places[first + i] : static_cast<uint32_t>(first + i);
     }
@@ -242,18 +282,28 @@ cudaError_t launch_sort_tokens(const int32_t* tokens, int N, int V, int ignore_i
   int bits = 1;   // of the keys 0 to V
   while ((static_cast<int64_t>(V) >> bits) != 0) ++bits;
   const int passes = (bits + kSortDigitBits - 1) / kSortDigitBits;
-  if (N <= kSortTile) {
+  if (N <= kSortCluster) {
+    const int ctas = N <= 1024 ? 1 : N <= 2048 ? 2 : N <= 4096 ? 4 : 8;
+    const int per = ((N + ctas - 1) / ctas + 31) / 32 * 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     auto go = [&](auto kern, int items) {
-      const int smem = kThreads * items * 8;
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cfg.dynamicSmemBytes = static_cast<size_t>(kThreads) * items * sizeof(uint2);
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(cfg.dynamicSmemBytes));
       if (e != cudaSuccess) return e;
-      kern<<<1, kThreads, smem, stream>>>(tokens, N, V, ignore_index, bits, passes, ids, perm);
-      return cudaGetLastError();
+      return cudaLaunchKernelEx(&cfg, kern, tokens, N, V, ignore_index, bits, passes, per, ids, perm);
     };
-    if (N <= kThreads) return go(sort_one_tile_kernel<1>, 1);
-    if (N <= kThreads * 4) return go(sort_one_tile_kernel<4>, 4);
-    if (N <= kThreads * 8) return go(sort_one_tile_kernel<8>, 8);
-    return go(sort_one_tile_kernel<16>, 16);
+    return per <= kThreads ? go(sort_cluster_kernel<1>, 1) : go(sort_cluster_kernel<2>, 2);
   }
   const int tiles = (N + kSortTile - 1) / kSortTile;
   const int per = (bits + passes - 1) / passes;
