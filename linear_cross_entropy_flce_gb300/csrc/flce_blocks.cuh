@@ -18,12 +18,12 @@ namespace {
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 // The byte e + 127 of a block with largest magnitude amax (its bits): kExp and kMant from the
-// format's largest value. 255 for an infinity or NaN, 0 where amax is that small.
+// format's largest value, whose mantissa has nothing beyond kMant: what is above it carries into the exponent.
+// 255 for an infinity or NaN, 0 where amax is that small.
 template <int kExp, uint32_t kMant>
 __device__ __forceinline__ uint32_t power_scale_byte(uint32_t amax) {
-  if (amax >= kInfBits) return 255u;
-  const int b = static_cast<int>(amax >> 23) - kExp + ((amax & 0x7FFFFFu) > kMant ? 1 : 0);
-  return static_cast<uint32_t>(b > 0 ? b : 0);
+  const int b = static_cast<int>((amax + (0x7FFFFFu - kMant)) >> 23) - kExp;
+  return amax >= kInfBits ? 255u : static_cast<uint32_t>(max(b, 0));
 }
 __device__ __forceinline__ uint32_t e4m3_scale_byte(uint32_t amax) {
   return power_scale_byte<8, 0x600000u>(amax);
@@ -31,7 +31,9 @@ __device__ __forceinline__ uint32_t e4m3_scale_byte(uint32_t amax) {
 
 // 2^(byte - 127), NaN for 255; and its reciprocal (of a byte up to 253).
 __device__ __forceinline__ float power_of_byte(uint32_t b) {
-  return __uint_as_float(b == 0 ? 0x400000u : b == 255u ? 0x7FC00000u : b << 23);
+  uint32_t two;   // bf16, exact
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>(b)));
+  return __uint_as_float(two << 16);
 }
 __device__ __forceinline__ float inverse_power_of_byte(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
@@ -99,12 +101,14 @@ __device__ __forceinline__ uint32_t largest_bits(const float (&v)[VW]) {
   return m;
 }
 
-// The same of VW bf16 as loaded, two at a time.
+// The same of bf16 as loaded, two at a time (a NaN comes out as one).
 template <int kWords>
 __device__ __forceinline__ uint32_t largest_bits_bf16(const uint32_t* w) {
-  uint32_t m = w[0] & 0x7FFF7FFFu;
+  uint32_t m;
+  asm("abs.bf16x2 %0, %1;" : "=r"(m) : "r"(w[0]));
 #pragma unroll
-  for (int k = 1; k < kWords; ++k) m = __vmaxu2(m, w[k] & 0x7FFF7FFFu);
+  for (int k = 1; k < kWords; ++k)
+    asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %1;\n\tmax.NaN.bf16x2 %0, %0, a;\n\t}" : "+r"(m) : "r"(w[k]));
   return max(m & 0xFFFF0000u, m << 16);
 }
 

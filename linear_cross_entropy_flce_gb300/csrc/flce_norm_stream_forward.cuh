@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
   const float inv_d = 1.f / static_cast<float>(D);
   const RowPlace<kElt, kRagged> place(static_cast<const uint8_t*>(x) + blockIdx.x * ldx * kElt, D);
   const int chunks = place.chunks;
+  [[maybe_unused]] const int codes = static_cast<int>(packed_codes(D));
   // [each group's ring, and two rows on their way out][weight][bias]
   const int group_bytes = (kRing + (kRagged && apart ? 1 : 0)) * 2 * slot_bytes;
   uint8_t* const ring = reinterpret_cast<uint8_t*>(s_dyn) + group * group_bytes;
@@ -141,32 +142,16 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
       raw[0][k] = P::load_if(in, (t + k * R) * VW, inside(k));
       raw[1][k] = P::load_if(in + slot_bytes, (t + k * R) * VW, inside(k));
     }
-    if constexpr (kPacked) {
-      const int64_t bytes = packed_record(D);
-      const int codes = static_cast<int>(packed_codes(D));
+    if constexpr (kPacked && kRagged) {   // from the ring
+      for (int r = 0; r < 1 + two; ++r) {
+        uint8_t* const record = packed + (row + r * half) * packed_record(D);
+        const uint8_t* const from = in + r * slot_bytes + place.s * kElt;
+        for (int i = t * 8; i - (t & 31) * 8 < codes; i += R * 8) {
+          float q[8];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (r == 1 && !two) break;
-        uint8_t* const record = packed + (row + r * half) * bytes;
-        if constexpr (!kRagged) {
-#pragma unroll
-          for (int k = 0; k < kNv; ++k) {
-            float q[VW];
-            P::widen(raw[r][k], q);
-            const uint32_t* const words = reinterpret_cast<const uint32_t*>(&raw[r][k]);
-            const int i = (t + k * R) * VW;
-            pack_values<VW>(record, i, D, q, kBf16 ? largest_bits_bf16<4>(words) : largest_bits(q), i < codes);
-          }
-        } else {
-          const uint8_t* const from = in + r * slot_bytes + place.s * kElt;
-          for (int i = t * 8; i - (t & 31) * 8 < codes; i += R * 8) {
-            float q[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = i + e < D ? load_as_f32(from, i + e, kBf16) : 0.f;
-            pack_values<8>(record, i, D, q, largest_bits(q), i < codes);
-          }
+          for (int e = 0; e < 8; ++e) q[e] = i + e < D ? load_as_f32(from, i + e, kBf16) : 0.f;
+          pack_values<8>(record, i, D, q, largest_bits(q), i < codes);
         }
-        for (int i = codes + codes / kPackBlock + t; i < bytes; i += R) record[i] = 0;
       }
     }
     float v[2][kNv][VW], part[2];
@@ -177,6 +162,13 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
       for (int k = 0; k < kNv; ++k) {
         P::widen(raw[r][k], v[r][k]);
         place.mask(v[r][k], t + k * R, D);
+        if constexpr (kPacked && !kRagged) {
+          const int i = (t + k * R) * VW;
+          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, v[r][k],
+                          kBf16 ? largest_bits_bf16<4>(reinterpret_cast<const uint32_t*>(&raw[r][k]))
+                                : largest_bits(v[r][k]),
+                          i < codes && (r == 0 || two));
+        }
         if (k == 0) {
 #pragma unroll
           for (int e = 0; e < VW; ++e) acc[e] = v[r][0][e];
@@ -243,6 +235,11 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
       for (int r = 0; r < 1 + two; ++r)
         place.copy_out(staged + r * slot_bytes,
                        static_cast<uint8_t*>(y) + (row + r * half) * ldy * kElt, D, t, R);
+    }
+    if constexpr (kPacked) {   // the zeros behind the scales
+      for (int r = 0; r < 1 + two; ++r)
+        for (int i = codes / kPackBlock * 33 + t; i < packed_record(D); i += R)
+          packed[(row + r * half) * packed_record(D) + i] = 0;
     }
     if (t == 0)
       for (int r = 0; r < 1 + two; ++r) {
