@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "flce_blocks.cuh"
+#include "flce_launch.cuh"
 
 namespace flce {
 
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kFp4Limit)
   __shared__ float s_stage[kWhole ? 1 : kFp4Limit / 32][kWhole ? 1 : kWarpStage<16>];
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kLanes = kNv ? 1 : 2;   // of a block
+  start_next_launch();   // (flce_fp4_gemm.cu's)
   const int t = static_cast<int>(threadIdx.x) % R, warp = static_cast<int>(threadIdx.x) >> 5;
   float* const stage = s_stage[kWhole ? 0 : warp];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / R) + threadIdx.x / R;

@@ -15,6 +15,7 @@
 #include "flce_blocks.h"
 #include "flce_fp4_gemm.h"
 #include "flce_gemm_params.h"
+#include "flce_launch.cuh"
 #include "ptx.cuh"
 
 namespace flce {
@@ -24,6 +25,7 @@ namespace {
 constexpr int kWarps = 12;   // TMA, MMA, two without work, eight of the epilogue
 constexpr int kThreads = kWarps * 32;
 constexpr int kEpilogue = 8;
+constexpr int kOutTokens = 16;
 
 template <int kN, int kNv, int kCta>
 struct Cfg {
@@ -35,8 +37,8 @@ struct Cfg {
   static constexpr uint32_t kSf = kNv ? 2048 : 1024;        // scale bytes of 128 rows' 256 values
   static constexpr int kBlocks = kSf / 512;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSf * (1 + kTokenTiles);
-  // of an epilogue warp: 32 tokens' rows on their way out, its tokens' row scales
-  static constexpr uint32_t kOutBytes = kN >= 64 ? 32 * 64 + kN / 2 * 4 : 0;
+  // of an epilogue warp: kOutTokens rows on their way out, its tokens' row scales
+  static constexpr uint32_t kOutBytes = kN >= 64 ? kOutTokens * 64 + (kNv ? kN / 2 * 4 : 0) : 0;
   static constexpr int kFit = static_cast<int>((225 * 1024 - kEpilogue * kOutBytes) / kStageBytes);
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
   static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogue * kOutBytes + 512;
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
+  wait_for_launch_before();   // nothing of the operands is read, nothing of y written before
   const uint64_t tmo = p.timeout_ns;
   const volatile int no_abort = 0;
   auto fail = [&]() {
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - (kWarps - kEpilogue)) >> 2;
     const uint32_t from = (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kHalf);
     uint8_t* const s_out = smem + kStages * C::kStageBytes + (warp - (kWarps - kEpilogue)) * C::kOutBytes;
-    [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(s_out + 32 * 64);
+    [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(s_out + kOutTokens * 64);
     int acc = 0;
     uint32_t acc_phase = 0;
     // this lane's row of a tile, and whether the tile has it
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       [[maybe_unused]] float w_row = 1.f;
       if constexpr (kNv) w_row = mine ? p.w_rows[r] : 0.f;
       if constexpr (kHalf >= 32) {
-        // 32 tokens at a time; where all of a warp's 32 rows of bf16 are there, they meet in shared memory
+        // some tokens at a time; where all of a warp's 32 rows of bf16 are there, they meet in shared memory
         // and leave 16 bytes at a time
         const bool wide = kBf16 && p.wide && __all_sync(0xffffffffu, mine);
         if constexpr (kNv) {
@@ -415,11 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
 #pragma unroll
-        for (int c0 = 0; c0 < kHalf; c0 += 32) {
+        for (int c0 = 0; c0 < kHalf; c0 += kOutTokens) {
           if (c0 >= tokens) break;
-          float o[32];
+          float o[kOutTokens];
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
+          for (int c = 0; c < kOutTokens; c += 4) {
             float4 h = make_float4(1.f, 1.f, 1.f, 1.f);
             if constexpr (kNv) h = *reinterpret_cast<const float4*>(s_rows + c0 + c);
             const float hs[4] = {h.x, h.y, h.z, h.w};
@@ -429,12 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (kNv) o[c + e] = o[c + e] * w_row * hs[e];
             }
           }
-          const int n = min(32, tokens - c0);
+          const int n = min(kOutTokens, tokens - c0);
           if (wide) {
             uint16_t* const to = reinterpret_cast<uint16_t*>(s_out) + lane;
             __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
+            for (int c = 0; c < kOutTokens; c += 2) {
               const uint32_t two = pack_bf16x2(o[c], o[c + 1]);
               to[c * 32] = static_cast<uint16_t>(two & 0xFFFFu);
               to[(c + 1) * 32] = static_cast<uint16_t>(two >> 16);
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             uint8_t* const y = static_cast<uint8_t*>(p.y) + ((first + c0) * p.ldy + (r - lane)) * 2 + (lane & 3) * 16;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kOutTokens / 8; ++j) {
               const int c = j * 8 + (lane >> 2);
               const uint4 out = reinterpret_cast<const uint4*>(s_out)[j * 32 + lane];
               if (c < n) *reinterpret_cast<uint4*>(y + c * p.ldy * 2) = out;
@@ -451,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kBf16) {
               uint16_t* y = static_cast<uint16_t*>(p.y) + (first + c0) * p.ldy + r;
 #pragma unroll
-              for (int c = 0; c < 32; ++c, y += p.ldy)
+              for (int c = 0; c < kOutTokens; ++c, y += p.ldy)
                 if (c < n) *y = static_cast<uint16_t>(pack_bf16x2(o[c], 0.f) & 0xFFFFu);
             } else {
               float* y = static_cast<float*>(p.y) + (first + c0) * p.ldy + r;
 #pragma unroll
-              for (int c = 0; c < 32; ++c, y += p.ldy)
+              for (int c = 0; c < kOutTokens; ++c, y += p.ldy)
                 if (c < n) *y = o[c];
             }
           }
@@ -498,13 +501,16 @@ cudaError_t launch(const Fp4Maps& maps, const Fp4GemmParams& p, int sms, cudaStr
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCta;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // the tokens' quantisation, most often the launch before, lets this one set itself up meanwhile
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
