@@ -339,8 +339,8 @@ def linear_fp4(h: Fp4Matrix, w: Fp4Matrix, *, dtype: torch.dtype = torch.bfloat1
             out = torch.empty(shape, dtype=dtype, device=dev)
     else:
         _same_device(out, dev, "out")
-        if tuple(out.shape) != shape:
-            raise ValueError(f"out must be of shape {shape}")
+        if tuple(out.shape) != shape or out.dim() != 2 and not out.is_contiguous():
+            raise ValueError(f"out must be of shape {shape}, and contiguous if not a matrix")
     flat = out if out.dim() == 2 else out.view(-1, V)
     _, _, ldy = _logits(flat, "out")
     _check(_linear_fp4(h.codes.data_ptr(), h.scales.data_ptr(), _ptr(h.row_scales), w.codes.data_ptr(),

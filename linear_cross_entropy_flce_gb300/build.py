@@ -33,7 +33,7 @@ SOURCES = ["flce_api.cu", "flce_reduce.cu", "flce_gemm_lse.cu", "flce_gemm_grad.
            "flce_ops_api.cu", "flce_logprobs.cu", "flce_logprob_merge.cu", "flce_norm.cu",
            "flce_norm_stream.cu", "flce_norm_stream_grad.cu",
            "flce_clip.cu", "flce_embed.cu", "flce_embed_sort.cu", "flce_embed_api.cu", "flce_pack.cu",
-           "flce_norm_stream_packed.cu", "flce_norm_stream_grad_packed.cu", "flce_blocks_api.cu",
+           "flce_norm_packed.cu", "flce_norm_stream_packed.cu", "flce_norm_stream_grad_packed.cu", "flce_blocks_api.cu",
            "flce_fp4.cu", "flce_fp4_gemm.cu"]
 
 

@@ -159,6 +159,68 @@ __device__ __forceinline__ void store_staged(void* row, int first, int D, float*
   }
 }
 
+// 16 values as loaded.
+template <int kBf16>
+struct Chunk {
+  uint4 w[kBf16 ? 2 : 4];
+  __device__ void load_if(const uint8_t* row, int i, bool ok) {
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k)
+      w[k] = ok ? reinterpret_cast<const uint4*>(row + i * 16 * (kBf16 ? 2 : 4))[k] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ void narrow(const float (&v)[16]) {   // of values that are kBf16's
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
+      constexpr int n = kBf16 ? 8 : 4;
+      float q[n];
+#pragma unroll
+      for (int e = 0; e < n; ++e) q[e] = v[k * n + e];
+      w[k] = Pack<kBf16, n>::narrow(q);
+    }
+  }
+  __device__ void widen(float (&v)[16]) const {
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
+      constexpr int n = kBf16 ? 8 : 4;
+      float q[n];
+      Pack<kBf16, n>::widen(w[k], q);
+#pragma unroll
+      for (int e = 0; e < n; ++e) v[k * n + e] = q[e];
+    }
+  }
+  __device__ uint32_t largest() const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if constexpr (kBf16) {
+      return largest_bits_bf16<8>(u);
+    } else {
+      uint32_t m = u[0] & 0x7FFFFFFFu;
+#pragma unroll
+      for (int e = 1; e < 16; ++e) m = max(m, u[e] & 0x7FFFFFFFu);
+      return m;
+    }
+  }
+};
+
+// Chunk i of a row of D values, 0 behind it; all lanes of the warp. kWhole: 16-byte accesses.
+template <int kBf16, int kWhole>
+__device__ __forceinline__ Chunk<kBf16> load_chunk(const uint8_t* row, int i, int D, float* stage) {
+  Chunk<kBf16> c;
+  if constexpr (kWhole) {
+    c.load_if(row, i, i * 16 + 16 <= D);
+    if (i * 16 < D && i * 16 + 16 > D) {   // the chunk in which the row ends
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = i * 16 + e < D ? load_as_f32(row, i * 16 + e, kBf16) : 0.f;
+      c.narrow(v);
+    }
+  } else {
+    float v[16];
+    load_staged<kBf16, 16>(row, (i - static_cast<int>(threadIdx.x & 31)) * 16, D, stage, v);
+    c.narrow(v);
+  }
+  return c;
+}
+
 // Threads of a row of nvec vectors, a power of two from `least` to `limit`: enough for `each` vectors
 // apiece, and more while the rows alone do not fill a quarter of the GPU's threads.
 inline int threads_of_row(int64_t rows, int nvec, int each, int least, int limit) {

@@ -2,7 +2,8 @@
 // sequences.
 //
 //   flce_pack_e4m3, flce_unpack_e4m3   one kernel
-//   flce_layer_norm_packed             many rows: one kernel; else the pack of x, then flce_layer_norm's
+//   flce_layer_norm_packed             one kernel; rows that no CTA holds: the pack of x, then
+//                                      flce_layer_norm's
 //   flce_layer_norm_packed_backward    as flce_layer_norm_backward
 //   flce_quantize_fp4, flce_dequantize_fp4, flce_linear_fp4   one kernel
 #include <algorithm>

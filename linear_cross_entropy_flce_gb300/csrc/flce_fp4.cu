@@ -29,68 +29,6 @@ constexpr int kFp4Limit = 512;   // threads of a row at most
 constexpr int fp4_held(bool whole) { return whole ? 4 : 2; }
 constexpr int kFp4Values = 4;    // vectors of 8 per thread, of the values back
 
-// 16 values as loaded.
-template <int kBf16>
-struct Chunk {
-  uint4 w[kBf16 ? 2 : 4];
-  __device__ void load_if(const uint8_t* row, int i, bool ok) {
-#pragma unroll
-    for (int k = 0; k < (kBf16 ? 2 : 4); ++k)
-      w[k] = ok ? reinterpret_cast<const uint4*>(row + i * 16 * (kBf16 ? 2 : 4))[k] : make_uint4(0, 0, 0, 0);
-  }
-  __device__ void narrow(const float (&v)[16]) {   // of values that are kBf16's
-#pragma unroll
-    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
-      constexpr int n = kBf16 ? 8 : 4;
-      float q[n];
-#pragma unroll
-      for (int e = 0; e < n; ++e) q[e] = v[k * n + e];
-      w[k] = Pack<kBf16, n>::narrow(q);
-    }
-  }
-  __device__ void widen(float (&v)[16]) const {
-#pragma unroll
-    for (int k = 0; k < (kBf16 ? 2 : 4); ++k) {
-      constexpr int n = kBf16 ? 8 : 4;
-      float q[n];
-      Pack<kBf16, n>::widen(w[k], q);
-#pragma unroll
-      for (int e = 0; e < n; ++e) v[k * n + e] = q[e];
-    }
-  }
-  __device__ uint32_t largest() const {
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
-    if constexpr (kBf16) {
-      return largest_bits_bf16<8>(u);
-    } else {
-      uint32_t m = u[0] & 0x7FFFFFFFu;
-#pragma unroll
-      for (int e = 1; e < 16; ++e) m = max(m, u[e] & 0x7FFFFFFFu);
-      return m;
-    }
-  }
-};
-
-// Chunk i of a row of D values, 0 behind it; all lanes of the warp. kWhole: 16-byte accesses.
-template <int kBf16, int kWhole>
-__device__ __forceinline__ Chunk<kBf16> load_chunk(const uint8_t* row, int i, int D, float* stage) {
-  Chunk<kBf16> c;
-  if constexpr (kWhole) {
-    c.load_if(row, i, i * 16 + 16 <= D);
-    if (i * 16 < D && i * 16 + 16 > D) {   // the chunk in which the row ends
-      float v[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = i * 16 + e < D ? load_as_f32(row, i * 16 + e, kBf16) : 0.f;
-      c.narrow(v);
-    }
-  } else {
-    float v[16];
-    load_staged<kBf16, 16>(row, (i - static_cast<int>(threadIdx.x & 31)) * 16, D, stage, v);
-    c.narrow(v);
-  }
-  return c;
-}
-
 // The row's power of two (its byte) and that of its inverse.
 struct RowScale {
   uint32_t byte;

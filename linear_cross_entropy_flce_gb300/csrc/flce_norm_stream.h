@@ -24,7 +24,11 @@ cudaError_t launch_norm_stream_backward(const void* dy, int64_t lddy, const void
                                         void* dx, int64_t lddx, void* dweight, void* dbias,
                                         float* part, int* ranges, int sms, cudaStream_t stream);
 
-// The forward pass that leaves x in 8 bits as well, and the backward pass from that (flce_blocks.h).
+// The forward pass that leaves x in 8 bits as well (of whole rows in registers, and of many), and the
+// backward pass from that (flce_blocks.h).
+cudaError_t launch_norm_pack(const void* x, int bf16, int64_t ldx, const void* weight, const void* bias,
+                             int wbf16, int N, int D, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                             uint8_t* packed, cudaStream_t stream);
 cudaError_t launch_norm_stream_packed(const void* x, int bf16, int64_t ldx, const void* weight,
                                       const void* bias, int wbf16, int N, int D, float eps, void* y,
                                       int64_t ldy, float* mean, float* rstd, uint8_t* packed, int sms,

@@ -13,8 +13,8 @@
 // 4001 bf16 76 (148). A full CTA has 512 threads, as many as 128
 // registers each allow.
 //
-// kPacked: x is left in 8 bits as well (flce_pack.cu's records), from the registers the row is in, where its
-// 16-byte chunks are the codes' eights; ragged rows from the ring, before it is filled again.
+// kPacked: x is left in 8 bits as well (flce_pack.cu's records): whole rows of fp32 from the registers the row
+// is in; ragged rows from the ring, before it is filled again. (Whole rows of bf16: flce_norm_packed.cu.)
 #pragma once
 
 #include <cstdint>
@@ -164,9 +164,7 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
         place.mask(v[r][k], t + k * R, D);
         if constexpr (kPacked && !kRagged) {
           const int i = (t + k * R) * VW;
-          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, v[r][k],
-                          kBf16 ? largest_bits_bf16<4>(reinterpret_cast<const uint32_t*>(&raw[r][k]))
-                                : largest_bits(v[r][k]),
+          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, v[r][k], largest_bits(v[r][k]),
                           i < codes && (r == 0 || two));
         }
         if (k == 0) {
@@ -274,15 +272,19 @@ cudaError_t launch_stream_forward(const void* x, int bf16, int64_t ldx, const vo
   if (s.groups == 0 || N < static_cast<int64_t>(kForwardBlock / s.R) * grid)
     return cudaErrorNotSupported;
   return with_stream_types(bf16, wbf16, !lay.whole, [&](auto b, auto wb, auto ragged) {
-    return with_stream_vectors((chunks + s.R - 1) / s.R, [&](auto nv) {
-      auto kern = norm_stream_kernel<b(), wb(), ragged(), nv(), kPacked>;
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(s.smem));
-      if (e != cudaSuccess) return e;
-      kern<<<grid, s.groups * s.R, s.smem, stream>>>(x, ldx, weight, bias, N, D, eps, y, ldy, mean,
-                                                    rstd, packed, s.R, slot, lay.apart);
-      return cudaGetLastError();
-    });
+    if constexpr (kPacked && b() && !ragged()) {
+      return cudaErrorNotSupported;
+    } else {
+      return with_stream_vectors((chunks + s.R - 1) / s.R, [&](auto nv) {
+        auto kern = norm_stream_kernel<b(), wb(), ragged(), nv(), kPacked>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(s.smem));
+        if (e != cudaSuccess) return e;
+        kern<<<grid, s.groups * s.R, s.smem, stream>>>(x, ldx, weight, bias, N, D, eps, y, ldy, mean,
+                                                      rstd, packed, s.R, slot, lay.apart);
+        return cudaGetLastError();
+      });
+    }
   });
 }
 

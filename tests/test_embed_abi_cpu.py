@@ -68,7 +68,8 @@ def test_workspace_size():
     assert lib.flce_embedding_backward_workspace_size(1, 1, 1, None) == NULL
     assert _ws(-1)[0] == SHAPE and _ws(1, V=0)[0] == SHAPE and _ws(1, D=0)[0] == SHAPE
     assert _ws(0) == (OK, 0)
-    # the sorted order, and two fp32 rows for each of at most 2048 ranges
+    # the sorted order, and two fp32 rows for each of at most 2048 ranges; past one cluster's tokens the
+    # order twice, and 512 counters for each tile of 4096
     assert _ws(8192, 128256, 4096)[1] <= 8192 * 8 + 256 * 2 * 4096 * 4 + 1024
-    assert _ws(1 << 24, 128256, 4096)[1] <= (1 << 24) * 16 + 2049 * 2 * 4096 * 4 + 1024 * 512 * 4 + 4096
+    assert _ws(1 << 24, 128256, 4096)[1] <= (1 << 24) * 16 + 2049 * 2 * 4096 * 4 + 4096 * 512 * 4 + 4096
     assert flce.embedding_backward_workspace_size(100, 50, 33) == _ws(100, 50, 33)[1]

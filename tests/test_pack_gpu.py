@@ -79,14 +79,16 @@ def _run(x, dy, w, b, dtype, wdtype, *, pad=0, shift=0, gpad=None, gshift=None):
     wt, w = _put(w, wdtype) if w is not None else (None, None)
     bt, b = _put(b, wdtype) if b is not None else (None, None)
     r, packed = flce.layer_norm_packed(xt, wt, bt)
-    plain = flce.layer_norm(xt, wt, bt)
-    assert torch.equal(r.y, plain.y) and torch.equal(r.mean, plain.mean) and torch.equal(r.rstd, plain.rstd)
+    y, mean, rstd = ho.layer_norm(x, w, b, 1e-5)
+    e, h, dh = _errors(x, mean, rstd)
+    aw, ab = (1.0 if w is None else np.abs(w)), (0.0 if b is None else np.abs(b))
+    _within(r.mean, mean, e * np.abs(x).mean(axis=1) + U * np.abs(mean), "mean")
+    _within(r.rstd, rstd, rstd * (2 * e + 8 * U + (e * np.abs(x).mean(axis=1) * rstd) ** 2), "rstd")
+    _within(r.y, y, aw * dh + 2 * U * (np.abs(h) * aw + ab) + half_step(r.y.dtype) * np.abs(y) * 1.01, "y")
     assert torch.equal(packed.data, flce.pack_e4m3(xt).data)
     kept = flce.unpack_e4m3(packed, dtype=torch.float32).double().cpu().numpy()
     dyt, dy = _put(dy, dtype, pad if gpad is None else gpad, shift if gshift is None else gshift)
     got = flce.layer_norm_packed_backward(dyt, packed, wt, r)
-    _, mean, rstd = ho.layer_norm(x, None, None, 1e-5)
-    e, _, _ = _errors(x, mean, rstd)
     D = x.shape[1]
     h = (kept - mean[:, None]) * rstd[:, None]
     dm = e * np.abs(x).mean(axis=1)
