@@ -82,54 +82,56 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
-// Element i of row `row` of x, or (packed) of the 8-bit record there.
-__device__ __forceinline__ float value_of(const void* x, int bf16, int64_t ldx, int64_t row, int i, int D,
-                                          int packed) {
-  if (!packed) return load_as_f32(x, row * ldx + i, bf16);
-  const uint8_t* const record = static_cast<const uint8_t*>(x) + row * ldx;
+// Element i of the row of x that begins at `at`, or (kPacked) of the 8-bit record there.
+template <int kPacked>
+__device__ __forceinline__ float value_of(const void* x, int bf16, int64_t at, int i, int D) {
+  if constexpr (!kPacked) return load_as_f32(x, at + i, bf16);
+  const uint8_t* const record = static_cast<const uint8_t*>(x) + at;
   float v, none;
   widen_e4m3x2(record[i], v, none);
   return v * power_of_byte(record[packed_codes(D) + (i >> 5)]);
 }
 
+template <int kPacked>
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_dx_kernel(const void* dy, int64_t lddy, const void* x, int bf16, int64_t ldx,
                          const void* weight, int wbf16, const float* mean_in,
-                         const float* rstd_in, int N, int D, void* dx, int64_t lddx, int packed) {
+                         const float* rstd_in, int N, int D, void* dx, int64_t lddx) {
   __shared__ float2 s_part[kNormThreads / 32];
   for (int row = blockIdx.x; row < N; row += gridDim.x) {
-    const int64_t yr = row * lddy, gr = row * lddx;
+    const int64_t xr = row * ldx, yr = row * lddy, gr = row * lddx;
     const float mean = mean_in[row], rstd = rstd_in[row];
     float2 sum = make_float2(0.f, 0.f);
     for (int i = threadIdx.x; i < D; i += kNormThreads) {
       const float w = weight != nullptr ? load_as_f32(weight, i, wbf16) : 1.f;
       const float g = load_as_f32(dy, yr + i, bf16) * w;
       sum.x += g;
-      sum.y = fmaf(g, (value_of(x, bf16, ldx, row, i, D, packed) - mean) * rstd, sum.y);
+      sum.y = fmaf(g, (value_of<kPacked>(x, bf16, xr, i, D) - mean) * rstd, sum.y);
     }
     sum = block_sum2(sum, s_part);
     const float mg = sum.x / D, mgh = sum.y / D;
     for (int i = threadIdx.x; i < D; i += kNormThreads) {
       const float w = weight != nullptr ? load_as_f32(weight, i, wbf16) : 1.f;
       const float g = load_as_f32(dy, yr + i, bf16) * w;
-      const float h = (value_of(x, bf16, ldx, row, i, D, packed) - mean) * rstd;
+      const float h = (value_of<kPacked>(x, bf16, xr, i, D) - mean) * rstd;
       store_from_f32(dx, gr + i, rstd * (g - mg - h * mgh), bf16);
     }
   }
 }
 
 // Partial sums over a range of rows: part[range][0][i] = sum dy h, [1][i] = sum dy.
+template <int kPacked>
 __global__ void __launch_bounds__(kColumnThreads)
     layer_norm_columns_kernel(const void* dy, int64_t lddy, const void* x, int bf16, int64_t ldx,
                               const float* mean, const float* rstd, int N, int D, int ranges,
-                              float* part, int packed) {
+                              float* part) {
   const int i = blockIdx.x * kColumnThreads + threadIdx.x;
   if (i >= D) return;
   const int range = blockIdx.y;
   float dw = 0.f, db = 0.f;
   for (int row = range; row < N; row += ranges) {
     const float d = load_as_f32(dy, row * lddy + i, bf16);
-    dw = fmaf(d, (value_of(x, bf16, ldx, row, i, D, packed) - mean[row]) * rstd[row], dw);
+    dw = fmaf(d, (value_of<kPacked>(x, bf16, row * ldx, i, D) - mean[row]) * rstd[row], dw);
     db += d;
   }
   part[(static_cast<int64_t>(range) * 2) * D + i] = dw;
@@ -550,15 +552,15 @@ cudaError_t norm_backward(const void* dy, int64_t lddy, const void* x, int bf16,
       ranges = N < kNormRanges ? N : kNormRanges;
       const dim3 grid(static_cast<unsigned>((D + kColumnThreads - 1) / kColumnThreads),
                       static_cast<unsigned>(ranges));
-      layer_norm_columns_kernel<<<grid, kColumnThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, mean,
-                                                                     rstd, N, D, ranges, part, kPacked);
+      layer_norm_columns_kernel<kPacked><<<grid, kColumnThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, mean,
+                                                                     rstd, N, D, ranges, part);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
     if (dx != nullptr) {
       const int grid = N < sms * 8 ? N : sms * 8;
-      layer_norm_dx_kernel<<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, weight,
-                                                              wbf16, mean, rstd, N, D, dx, lddx, kPacked);
+      layer_norm_dx_kernel<kPacked><<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, bf16, ldx, weight,
+                                                              wbf16, mean, rstd, N, D, dx, lddx);
       e = cudaGetLastError();
     }
   }

@@ -103,10 +103,14 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
   // [each group's ring, x and dy of each row, and a row on its way out][weight]
   const int codes = static_cast<int>(packed_codes(D));
   const int x_bytes = kPacked ? kRecordFront + static_cast<int>(packed_record(D)) + 16 : slot_bytes;
-  const int turn_bytes = x_bytes + slot_bytes;
-  const int group_bytes = kRing * turn_bytes + (kRagged && apart ? slot_bytes : 0);
+  // where turn `slot` has x, or (half = 1) dy; past the last, the row on its way out
+  auto place_of = [&](int slot, int half) {
+    return kPacked ? slot * (x_bytes + slot_bytes) + half * x_bytes : (slot * 2 + half) * slot_bytes;
+  };
+  const int extra = kRagged && apart ? 1 : 0;
+  const int group_bytes = kPacked ? place_of(kRing, 0) + extra * slot_bytes : (kRing * 2 + extra) * slot_bytes;
   uint8_t* const ring = reinterpret_cast<uint8_t*>(s_dyn) + group * group_bytes;
-  uint8_t* const staged = ring + kRing * turn_bytes;
+  uint8_t* const staged = ring + place_of(kRing, 0);
   uint8_t* const s_w = reinterpret_cast<uint8_t*>(s_dyn) + groups * group_bytes;
 
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
     if (row >= N) return;
     const uint8_t* const from_x = static_cast<const uint8_t*>(x) + row * ldx * (kPacked ? 1 : kElt);
     const uint8_t* const from_g = static_cast<const uint8_t*>(dy) + row * lddy * kElt;
-    uint8_t* const to = ring + slot * turn_bytes;
+    uint8_t* const to = ring + place_of(slot, 0);
     if (t == 0) {
       const uint32_t bar = smem_u32(&s_full[group][slot]);
       if constexpr (kPacked) {
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
   };
   auto land = [&](int slot, uint32_t single) {
     if (kRagged && t < 32 && (!kPacked || t >= 16))
-      place.write_single(ring + slot * turn_bytes + (t < 16 ? 0 : x_bytes), t & 15, D, single);
+      place.write_single(ring + place_of(slot, t >> 4), t & 15, D, single);
   };
   if (t == 0) {
     for (int k = 0; k < kRing; ++k) mbar_init(smem_u32(&s_full[group][k]), 1);
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
       if (t == 0 && limit != 0) drain_ring(s_full[group], kRing, slot, phase, row, step, N);
       limit = 0;
     }
-    const uint8_t* in_x = ring + slot * turn_bytes;
+    const uint8_t* in_x = ring + place_of(slot, 0);
     const uint8_t* in_g = in_x + x_bytes;
     // elements past the row have dy = 0 and so count nowhere
     auto inside = [&](int k) { return k < kNv - 1 || t + k * R < chunks; };
@@ -190,23 +194,21 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
     for (int e = 0; e < VW; ++e) s0[e] = s1[e] = 0.f;
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
+      if constexpr (kPacked) cx[k].widen(h[k]);
+      else P::widen(rx[k], h[k]);
       P::widen(rg[k], g[k]);
-      place.mask(g[k], t + k * R, D);
       if constexpr (kPacked && !kRagged) {
         const float scale = power_of_byte(cx[k].byte0);
-        cx[k].widen(h[k]);
 #pragma unroll
         for (int e = 0; e < VW; ++e) h[k][e] = fmaf(h[k][e], scale, -mean) * rstd;   // x~ is exact
       } else {
         if constexpr (kPacked) {
           const float scale0 = power_of_byte(cx[k].byte0), scale1 = power_of_byte(cx[k].byte1);
-          cx[k].widen(h[k]);
 #pragma unroll
           for (int e = 0; e < VW; ++e) h[k][e] *= e < cx[k].split ? scale0 : scale1;
-        } else {
-          P::widen(rx[k], h[k]);
         }
         place.mask(h[k], t + k * R, D);
+        place.mask(g[k], t + k * R, D);
 #pragma unroll
         for (int e = 0; e < VW; ++e) h[k][e] = (h[k][e] - mean) * rstd;
       }
