@@ -221,16 +221,6 @@ __device__ __forceinline__ Chunk<kBf16> load_chunk(const uint8_t* row, int i, in
   return c;
 }
 
-// Threads of a row of nvec vectors, a power of two from `least` to `limit`: enough for `each` vectors
-// apiece, and more while the rows alone do not fill a quarter of the GPU's threads.
-inline int threads_of_row(int64_t rows, int nvec, int each, int least, int limit) {
-  constexpr int64_t kQuarter = 152 * 512;
-  int X = least;
-  while (X < limit && X * each < nvec) X *= 2;
-  while (X < limit && X < nvec && rows * X < kQuarter) X *= 2;
-  return X;
-}
-
 inline bool whole_vectors(const void* x, int bf16, int64_t ldx) {
   return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * (bf16 ? 2 : 4) % 16 == 0;
 }

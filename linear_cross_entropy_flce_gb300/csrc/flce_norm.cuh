@@ -181,6 +181,16 @@ __device__ __forceinline__ float sum_n(const float (&a)[VW]) {
   return s;
 }
 
+// Threads of a row of nvec vectors, a power of two from `least` to `limit`: enough for `each` vectors
+// apiece, and more while the rows alone do not fill a quarter of the GPU's threads.
+inline int threads_of_row(int64_t rows, int nvec, int each, int least, int limit) {
+  constexpr int64_t kQuarter = 152 * 512;
+  int X = least;
+  while (X < limit && X * each < nvec) X *= 2;
+  while (X < limit && X < nvec && rows * X < kQuarter) X *= 2;
+  return X;
+}
+
 // The widest access (elements) that D, the row strides and the addresses allow.
 inline int access_width(int bf16, int D, std::initializer_list<int64_t> strides,
                  std::initializer_list<const void*> rows, std::initializer_list<const void*> params,
