@@ -85,25 +85,40 @@ __device__ __forceinline__ int lower_bound(const uint32_t* ids, int N, uint32_t 
   return lo;
 }
 
-// `sum` scaled to (kAdd: onto `old`) dW at element `at`, VW elements.
-template <int kWbf16, int VW, int kAdd>
-__device__ __forceinline__ void put_row(void* dW, int64_t at, const float (&sum)[VW], float scale,
-                                        const Param<kWbf16, VW>& old) {
-  using Out = Param<kWbf16, VW>;
-  uint8_t* const p = static_cast<uint8_t*>(dW) + at * (kWbf16 ? 2 : 4);
-  float v[VW];
-  if constexpr (kAdd) {
-    old.widen(v);
+// `sum` scaled, and (kAdd) added to old values.
+template <int n, int kAdd>
+__device__ __forceinline__ void finish_sum(float (&sum)[n], float scale, const float (&old)[n]) {
 #pragma unroll
-    for (int e = 0; e < VW; ++e) v[e] = fmaf(sum[e], scale, v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) v[e] = sum[e] * scale;
-  }
-  Out out;
-  out.narrow(v);
-  out.save(p, 0);
+  for (int e = 0; e < n; ++e) sum[e] = kAdd ? fmaf(sum[e], scale, old[e]) : sum[e] * scale;
 }
+
+// What a thread has of a row: a vector of VW elements; where that is one element, four of them, kGradThreads
+// apart, so that a CTA's piece of a row is not too short.
+constexpr int row_parts(int vw) { return vw == 1 ? 4 : 1; }
+template <int kBf16, int VW>
+struct RowPart {
+  static constexpr int kParts = row_parts(VW), kValues = kParts * VW;
+  Param<kBf16, VW> p[kParts];
+  // (what is behind the row stays unset, and is not saved)
+  __device__ void load(const void* row, int i, int nvec) {
+#pragma unroll
+    for (int c = 0; c < kParts; ++c)
+      if (i + c * kGradThreads < nvec) p[c].load(row, (i + c * kGradThreads) * VW, 0.f);
+  }
+  __device__ void save(void* row, int i, int nvec) const {
+#pragma unroll
+    for (int c = 0; c < kParts; ++c)
+      if (i + c * kGradThreads < nvec) p[c].save(static_cast<uint8_t*>(row), (i + c * kGradThreads) * VW);
+  }
+  __device__ void widen(float (&v)[kValues]) const {
+#pragma unroll
+    for (int c = 0; c < kParts; ++c) p[c].widen(reinterpret_cast<float(&)[VW]>(v[c * VW]));
+  }
+  __device__ void narrow(const float (&v)[kValues]) {
+#pragma unroll
+    for (int c = 0; c < kParts; ++c) p[c].narrow(reinterpret_cast<const float(&)[VW]>(v[c * VW]));
+  }
+};
 
 // D zeros, 16 bytes at a time wherever the row begins, by the whole CTA.
 template <int kWbf16>
@@ -130,7 +145,9 @@ __global__ void __launch_bounds__(kGradThreads)
     embedding_grad_kernel(const void* dy, int64_t lddy, const uint32_t* ids, const uint32_t* perm, int N,
                           int V, int D, float scale, void* dW, int64_t ldw, float* part,
                           int ranges, int range, int pieces) {
-  using In = Param<kBf16, VW>;
+  using In = RowPart<kBf16, VW>;
+  using Out = RowPart<kWbf16, VW>;
+  constexpr int kValues = In::kValues;
   __shared__ uint32_t s_id[kGradThreads], s_row[kGradThreads];
   __shared__ int s_absent[kZeroRows];
   start_next_launch();
@@ -155,41 +172,38 @@ __global__ void __launch_bounds__(kGradThreads)
   const int r = static_cast<int>(blockIdx.x) / pieces;
   const int first = r * range;
   const int end = N - first < range ? N : first + range;
-  const int i = static_cast<int>(blockIdx.x) % pieces * kGradThreads + static_cast<int>(threadIdx.x);
-  const bool in = i < nvec;
+  const int i = static_cast<int>(blockIdx.x) % pieces * kGradThreads * In::kParts + static_cast<int>(threadIdx.x);
   // the ids on either side of the range (V: none)
   const uint32_t none = static_cast<uint32_t>(V);
   const uint32_t before = first > 0 ? ids[first - 1] : none;
   const uint32_t after = end < N ? ids[end] : none;
-  float sum[VW];
+  float sum[kValues];
 #pragma unroll
-  for (int e = 0; e < VW; ++e) sum[e] = 0.f;
+  for (int e = 0; e < kValues; ++e) sum[e] = 0.f;
   bool head = true;   // no id has ended yet in this range
   uint32_t id = none;
-  auto end_of_id = [&](bool last, const Param<kWbf16, VW>& old) {
+  auto row_of_id = [&](uint32_t row) { return static_cast<uint8_t*>(dW) + row * ldw * (kWbf16 ? 2 : 4); };
+  auto end_of_id = [&](bool last, const Out& old) {
     if (id == none) return;
-    const bool joins = (head && id == before) || (last && id == after);
-    if (in) {
-      if (joins) {
-        const int slot = head && id == before ? 0 : 1;
-        Param<0, VW> out;
-        out.narrow(sum);
-        out.save(reinterpret_cast<uint8_t*>(part + (static_cast<int64_t>(r) * 2 + slot) * D), i * VW);
-      } else {
-        put_row<kWbf16, VW, kAdd>(dW, id * ldw + static_cast<int64_t>(i) * VW, sum, scale, old);
-      }
+    if ((head && id == before) || (last && id == after)) {
+      const int slot = head && id == before ? 0 : 1;
+      RowPart<0, VW> out;
+      out.narrow(sum);
+      out.save(part + (static_cast<int64_t>(r) * 2 + slot) * D, i, nvec);
+    } else {
+      float v[kValues];
+      if constexpr (kAdd) old.widen(v);
+      finish_sum<kValues, kAdd>(sum, scale, v);
+      Out out;
+      out.narrow(sum);
+      out.save(row_of_id(id), i, nvec);
     }
     head = false;
 #pragma unroll
-    for (int e = 0; e < VW; ++e) sum[e] = 0.f;
+    for (int e = 0; e < kValues; ++e) sum[e] = 0.f;
   };
   // the old values of the rows that end: read with the rows of dy (adding)
-  Param<kWbf16, VW> old[kAdd ? kAhead : 1], last_old;
-  auto read_old = [&](uint32_t row) {
-    Param<kWbf16, VW> v;
-    v.load(static_cast<const uint8_t*>(dW) + row * ldw * (kWbf16 ? 2 : 4), i * VW, 0.f);
-    return v;
-  };
+  Out old[kAdd ? kAhead : 1], last_old;
   for (int at = first; at < end; at += kGradThreads) {
     const int n = end - at < kGradThreads ? end - at : kGradThreads;
     if (at > first) __syncthreads();
@@ -200,20 +214,18 @@ __global__ void __launch_bounds__(kGradThreads)
     __syncthreads();
     for (int j = 0; j < n; j += kAhead) {
       In row[kAhead];
-      if (in) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (j + k < n && s_id[j + k] != none)
-            row[k].load(static_cast<const uint8_t*>(dy) + s_row[j + k] * lddy * (kBf16 ? 2 : 4), i * VW, 0.f);
-        if constexpr (kAdd) {
-          uint32_t before_k = id;
+      for (int k = 0; k < kAhead; ++k)
+        if (j + k < n && s_id[j + k] != none)
+          row[k].load(static_cast<const uint8_t*>(dy) + s_row[j + k] * lddy * (kBf16 ? 2 : 4), i, nvec);
+      if constexpr (kAdd) {
+        uint32_t before_k = id;
 #pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            if (j + k >= n) break;
-            const uint32_t here = s_id[j + k];
-            if (here != before_k && here != none) old[k] = read_old(here);
-            before_k = here;
-          }
+        for (int k = 0; k < kAhead; ++k) {
+          if (j + k >= n) break;
+          const uint32_t here = s_id[j + k];
+          if (here != before_k && here != none) old[k].load(row_of_id(here), i, nvec);
+          before_k = here;
         }
       }
 #pragma unroll
@@ -225,8 +237,8 @@ __global__ void __launch_bounds__(kGradThreads)
           id = here;
           if constexpr (kAdd) last_old = old[k];
         }
-        if (in && here != none) {
-          float v[VW];
+        if (here != none) {
+          float v[kValues];
           row[k].widen(v);
           add_n(sum, v);
         }
@@ -299,10 +311,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     in.widen(v);
     add_n(total, v);
   }
-  Param<kWbf16, VW> old;
-  const int64_t at = id * ldw + static_cast<int64_t>(i) * VW;
-  if constexpr (kAdd) old.load(static_cast<const uint8_t*>(dW) + at * (kWbf16 ? 2 : 4), 0, 0.f);
-  put_row<kWbf16, VW, kAdd>(dW, at, total, scale, old);
+  uint8_t* const row = static_cast<uint8_t*>(dW) + id * ldw * (kWbf16 ? 2 : 4);
+  Param<kWbf16, VW> at;
+  float old[VW];
+  if constexpr (kAdd) {
+    at.load(row, i * VW, 0.f);
+    at.widen(old);
+  }
+  finish_sum<VW, kAdd>(total, scale, old);
+  at.narrow(total);
+  at.save(row, i * VW);
 }
 
 // f(VW) for the widest access: 8 elements, 4 or 1.
@@ -365,7 +383,7 @@ cudaError_t launch_embedding_grad(const void* dy, int bf16, int64_t lddy, const 
     const int nvec = D / VW;
     return with_types(bf16, wbf16, [&](auto b, auto wb) {
       auto go = [&](auto add) {
-        const int pieces = (nvec + kGradThreads - 1) / kGradThreads;
+        const int piece = kGradThreads * row_parts(VW), pieces = (nvec + piece - 1) / piece;
         const unsigned grid = static_cast<unsigned>(ranges * pieces) + zeros;
         if (grid == 0) return cudaSuccess;
         const cudaError_t e =
