@@ -120,22 +120,22 @@ struct RowPart {
   }
 };
 
-// D zeros, 16 bytes at a time wherever the row begins, by the whole CTA.
+// D zeros, 16 bytes at a time wherever the row begins, by a warp.
 template <int kWbf16>
 __device__ __forceinline__ void zero_row(uint8_t* row, int D) {
   constexpr int kElt = kWbf16 ? 2 : 4;
+  const int lane = threadIdx.x & 31;
   const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / kElt;
-  const int t = threadIdx.x;
   const int whole = D > head ? (D - head) * kElt / 16 : 0;
   const int tail = head + whole * (16 / kElt);   // elements from here on, and before head, go alone
   auto one = [&](int i) {
     if (kWbf16) reinterpret_cast<uint16_t*>(row)[i] = 0;
     else reinterpret_cast<uint32_t*>(row)[i] = 0;
   };
-  if (t < head && t < D) one(t);
-  if (t >= 32 && t < 64 && tail + t - 32 < D) one(tail + t - 32);
-  for (int i = t; i < whole; i += kGradThreads)
-    reinterpret_cast<uint4*>(row + head * kElt)[i] = make_uint4(0, 0, 0, 0);
+  if (lane < head && lane < D) one(lane);
+  if (tail + lane < D) one(tail + lane);
+#pragma unroll 4
+  for (int i = lane; i < whole; i += 32) reinterpret_cast<uint4*>(row + head * kElt)[i] = make_uint4(0, 0, 0, 0);
 }
 
 // CTAs [0, ranges * pieces): a range of the sorted order and a piece of the columns. The others (not
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kGradThreads)
       s_absent[threadIdx.x] = absent;
     }
     __syncthreads();
-    for (int r = 0; r < kZeroRows; ++r)
+    for (int r = static_cast<int>(threadIdx.x >> 5); r < kZeroRows; r += kGradThreads / 32)
       if (s_absent[r]) zero_row<kWbf16>(static_cast<uint8_t*>(dW) + (row0 + r) * ldw * (kWbf16 ? 2 : 4), D);
     return;
   }
