@@ -4,8 +4,10 @@ The loss of a language-model head, mean over non-ignored tokens of
 logsumexp(h_i W^T) - h_i . w_{y_i}, and its gradients dH and dW, computed by
 hand-written tcgen05/TMA CUDA kernels without writing the [N, V] logits to
 device memory. Around the head: log probabilities of given tokens with entropy and
-top alternatives, layer norm, and gradient clipping. The C ABI is include/flce.h and
-include/flce_ops.h; this package is its Python binding.
+top alternatives, layer norm, and gradient clipping; at the table's other end the
+embedding and its gradient; in fewer bits, activations kept for the backward pass in 8
+and the head's product in 4. The C ABI is include/flce.h, flce_ops.h, flce_embed.h and
+flce_blocks.h; this package is its Python binding.
 """
 from ._binding import (FLCE_ERR_ALIGN, FLCE_ERR_CUDA, FLCE_ERR_DEVICE, FLCE_ERR_LABEL_RANGE,
                        FLCE_ERR_NULL, FLCE_ERR_OPTION, FLCE_ERR_SHAPE, FLCE_ERR_TIMEOUT,

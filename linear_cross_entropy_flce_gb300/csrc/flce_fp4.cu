@@ -13,6 +13,10 @@
 // rest, so that x r + x rest is x / s to within 2^-46, rounded once: a value halfway between two codes
 // stays there. (And no other quotient is rounded onto such a place: its distance from it is more than
 // half the quotient's own last place.)
+//
+// Bound by instructions for nvfp4, by bytes for mxfp4 and for the values back: 128256 x 4096 bf16 258, 187 and 210 us
+// (the bytes 201, 198); 8192 x 4096 20.3 and 15.6; 64128 x 4096 fp32 214; 3001 x 1111 fp32 mxfp4 6.9 and 4.3; one
+// row of 4096 2.2 and 1.8. The quotient corrected by its residual instead (three operations a value) 317.
 #include <cstdint>
 
 #include "flce_blocks.cuh"

@@ -5,7 +5,10 @@
 // shuffles; rows that do not allow 16-byte accesses go through shared memory, a warp's 256 values
 // at a time. Each thread has kAtOnce vectors in flight.
 //
-// Bound by the bytes: D + D / 32 written or read for 2 D or 4 D.
+// Bound by the bytes, D + D / 32 written or read for 2 D or 4 D, and the instructions beside them: 16384 x 8192
+// bf16 66 us packed and 60 unpacked (0.91 and 1.02 of the copy rate), 8192 x 4096 18.5 and 14.2, 4000 x 4096 fp32
+// 13.2 and 18.0, 3001 x 1111 fp32 6.0 and 4.3, 1 x 4096 1.9 and 1.8. As many threads a row as have kAtOnce vectors
+// each: with a thread for each vector 8192 x 4096 took 26.8 and 17.4.
 #include <cstdint>
 
 #include "flce_blocks.cuh"
