@@ -10,7 +10,7 @@
 // read once for the row's and the blocks' largest magnitudes and the codes; rows of more than 32768
 // values (16384 through shared memory) are read again instead. Rows that do not allow 16-byte accesses come through shared memory, a
 // warp's 512 values at a time. 1 / s is taken in two parts, r and its
-// rest, so that x r + x rest is x / s to within 2^-46, rounded once: a value halfway between two codes
+// rest, so that x r + x rest is x / s to within 2^-43, rounded once: a value halfway between two codes
 // stays there. (And no other quotient is rounded onto such a place: its distance from it is more than
 // half the quotient's own last place.)
 //
@@ -59,8 +59,12 @@ __device__ __forceinline__ uint2 quantize_chunk(const Chunk<kBf16>& c, uint32_t 
     byte = finite ? e4m3x2(sixth, 0.f) & 0xFFu : 0x7Fu;
     float s, none;
     widen_e4m3x2(finite ? byte : 0u, s, none);
-    // 1 / s = r + rest, r rounded down, so that the rest is not negative and -0 stays -0
-    float r = s > 0.f ? __frcp_rd(s) : 0.f, rest = fmaf(-s, r, 1.f) * r;
+    // 1 / s = r + rest: the approximate reciprocal, which is off by 2^-23 of it at most, two units lower, so that
+    // the rest is not negative and -0 stays -0
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = s > 0.f ? __uint_as_float(__float_as_uint(r) - 2u) : 0.f;
+    float rest = fmaf(-s, r, 1.f) * r;
     if (tiny) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] *= g.inverse();
