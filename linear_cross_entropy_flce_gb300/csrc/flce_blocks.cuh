@@ -126,16 +126,19 @@ __device__ __forceinline__ uint32_t largest_of_lanes(uint32_t m) {
 template <int VW>
 constexpr int kWarpStage = 32 * (VW + 1);   // floats of a warp
 
-// v: elements [first + lane VW, + VW) of the row, 0 from D on.
+// in: elements first + lane, first + 32 + lane, ... of the row, 0 from D on.
 template <int kBf16, int VW>
-__device__ __forceinline__ void load_staged(const void* row, int first, int D, float* stage, float (&v)[VW]) {
-  const int lane = threadIdx.x & 31;
-  float in[VW];
+__device__ __forceinline__ void load_apart(const void* row, int first, int D, float (&in)[VW]) {
 #pragma unroll
   for (int k = 0; k < VW; ++k) {
-    const int i = k * 32 + lane;
-    in[k] = first + i < D ? load_as_f32(row, first + i, kBf16) : 0.f;
+    const int i = first + k * 32 + static_cast<int>(threadIdx.x & 31);
+    in[k] = i < D ? load_as_f32(row, i, kBf16) : 0.f;
   }
+}
+// v: the elements [lane VW, + VW) of those.
+template <int VW>
+__device__ __forceinline__ void to_neighbours(const float (&in)[VW], float* stage, float (&v)[VW]) {
+  const int lane = threadIdx.x & 31;
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < VW; ++k) stage[k * 32 + lane + (k * 32 + lane) / VW] = in[k];
@@ -144,7 +147,7 @@ __device__ __forceinline__ void load_staged(const void* row, int first, int D, f
   for (int e = 0; e < VW; ++e) v[e] = stage[lane * (VW + 1) + e];
 }
 
-// The other way round.
+// Both, the other way round.
 template <int kBf16, int VW>
 __device__ __forceinline__ void store_staged(void* row, int first, int D, float* stage, const float (&v)[VW]) {
   const int lane = threadIdx.x & 31;
@@ -201,24 +204,35 @@ struct Chunk {
   }
 };
 
-// Chunk i of a row of D values, 0 behind it; all lanes of the warp. kWhole: 16-byte accesses.
-template <int kBf16, int kWhole>
-__device__ __forceinline__ Chunk<kBf16> load_chunk(const uint8_t* row, int i, int D, float* stage) {
-  Chunk<kBf16> c;
+// Chunks t, t + R, ... of a row of D values, 0 behind it; all lanes of the warp. kWhole: 16-byte accesses.
+template <int kBf16, int kWhole, int n>
+__device__ __forceinline__ void load_chunks(const uint8_t* row, int t, int R, int D, float* stage,
+                                            Chunk<kBf16> (&c)[n]) {
   if constexpr (kWhole) {
-    c.load_if(row, i, i * 16 + 16 <= D);
-    if (i * 16 < D && i * 16 + 16 > D) {   // the chunk in which the row ends
-      float v[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = i * 16 + e < D ? load_as_f32(row, i * 16 + e, kBf16) : 0.f;
-      c.narrow(v);
+    for (int k = 0; k < n; ++k) c[k].load_if(row, t + k * R, (t + k * R) * 16 + 16 <= D);
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const int i = (t + k * R) * 16;
+      if (i < D && i + 16 > D) {   // the chunk in which the row ends
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = i + e < D ? load_as_f32(row, i + e, kBf16) : 0.f;
+        c[k].narrow(v);
+      }
     }
   } else {
-    float v[16];
-    load_staged<kBf16, 16>(row, (i - static_cast<int>(threadIdx.x & 31)) * 16, D, stage, v);
-    c.narrow(v);
+    float in[n][16];   // all loads first
+#pragma unroll
+    for (int k = 0; k < n; ++k)
+      load_apart<kBf16, 16>(row, (t + k * R - static_cast<int>(threadIdx.x & 31)) * 16, D, in[k]);
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      float v[16];
+      to_neighbours(in[k], stage, v);
+      c[k].narrow(v);
+    }
   }
-  return c;
 }
 
 inline bool whole_vectors(const void* x, int bf16, int64_t ldx) {

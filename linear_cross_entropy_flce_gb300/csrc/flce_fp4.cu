@@ -117,8 +117,7 @@ __global__ void __launch_bounds__(kFp4Limit)
   Chunk<kBf16> held[kHeld > 0 ? kHeld : 1];
   uint32_t amax[kHeld > 0 ? kHeld : 1];
   if constexpr (kHeld > 0) {
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) held[k] = load_chunk<kBf16, kWhole>(from, t + k * R, width, stage);
+    load_chunks<kBf16, kWhole>(from, t, R, width, stage, held);
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) amax[k] = block_max(held[k]);
   }
@@ -130,8 +129,9 @@ __global__ void __launch_bounds__(kFp4Limit)
       for (int k = 0; k < kHeld; ++k) m = row_max(held[k], amax[k], m);
     } else {
       for (int i = t; i < chunks; i += R) {
-        const Chunk<kBf16> c = load_chunk<kBf16, kWhole>(from, i, width, stage);
-        m = row_max(c, block_max(c), m);
+        Chunk<kBf16> c[1];
+        load_chunks<kBf16, kWhole>(from, i, 0, width, stage, c);
+        m = row_max(c[0], block_max(c[0]), m);
       }
     }
     m = __reduce_max_sync(0xffffffffu, m);
@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kFp4Limit)
     for (int k = 0; k < kHeld; ++k) put(t + k * R, held[k], amax[k]);
   } else {
     for (int i = t; i < (chunks + R - 1) / R * R; i += R) {   // whole warps, for the shuffles
-      const Chunk<kBf16> c = load_chunk<kBf16, kWhole>(from, i, width, stage);
-      put(i, c, block_max(c));
+      Chunk<kBf16> c[1];
+      load_chunks<kBf16, kWhole>(from, i, 0, width, stage, c);
+      put(i, c[0], block_max(c[0]));
     }
   }
 }

@@ -52,8 +52,7 @@ __global__ void __launch_bounds__(kNormPackLimit, 2)
   const uint8_t* const from = static_cast<const uint8_t*>(x) + row * ldx * kElt;
   const float inv_d = 1.f / static_cast<float>(D);
   Chunk<kBf16> c[kHeld];
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) c[k] = load_chunk<kBf16, kWhole>(from, t + k * R, width, stage);
+  load_chunks<kBf16, kWhole>(from, t, R, width, stage, c);
   float part = 0.f;
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {

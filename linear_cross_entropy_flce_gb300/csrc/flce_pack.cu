@@ -58,7 +58,9 @@ __global__ void __launch_bounds__(kPackThreads)
         for (int e = 0; e < 8; ++e) v[e] = i * 8 + e < width ? load_as_f32(from, i * 8 + e, kBf16) : 0.f;
       }
     } else {
-      load_staged<kBf16, 8>(from, (i - (t & 31)) * 8, width, s_stage[threadIdx.x >> 5], v);
+      float apart[8];   // (all vectors' loads first, in 32 registers, took 73 us instead of 58 for 16000 x 4001 bf16)
+      load_apart<kBf16, 8>(from, (i - (t & 31)) * 8, width, apart);
+      to_neighbours(apart, s_stage[threadIdx.x >> 5], v);
     }
     const uint32_t byte = e4m3_scale_byte(largest_of_lanes<4>(largest_bits(v)));
     if (row < N && i < nvec) {
