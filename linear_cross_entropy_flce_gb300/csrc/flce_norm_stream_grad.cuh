@@ -184,11 +184,9 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
     auto inside = [&](int k) { return k < kNv - 1 || t + k * R < chunks; };
     Raw rg[kNv];
     [[maybe_unused]] Raw rx[kNv];
-    [[maybe_unused]] ChunkCodes<VW, kRagged> cx[kNv];
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
-      if constexpr (kPacked) cx[k].load(in_x + kRecordFront, codes, (t + k * R) * VW - place.s, inside(k));
-      else rx[k] = P::load_if(in_x, (t + k * R) * VW, inside(k));
+      if constexpr (!kPacked) rx[k] = P::load_if(in_x, (t + k * R) * VW, inside(k));
       rg[k] = P::load_if(in_g, (t + k * R) * VW, inside(k));
     }
     float g[kNv][VW], h[kNv][VW], s0[VW], s1[VW];
@@ -196,19 +194,20 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
     for (int e = 0; e < VW; ++e) s0[e] = s1[e] = 0.f;
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
-      if constexpr (kPacked) cx[k].widen(h[k]);
-      else P::widen(rx[k], h[k]);
-      P::widen(rg[k], g[k]);
-      if constexpr (kPacked && !kRagged) {
-        const float scale = power_of_byte(cx[k].byte0);
+      if constexpr (kPacked) {   // x~ is exact, so its difference from the mean is rounded once
+        ChunkCodes<VW, kRagged> c;
+        c.load(in_x + kRecordFront, codes, (t + k * R) * VW - place.s, inside(k));
+        c.widen(h[k]);
+        P::widen(rg[k], g[k]);
+        const float scale0 = power_of_byte(c.byte0), scale1 = kRagged ? power_of_byte(c.byte1) : 0.f;
 #pragma unroll
-        for (int e = 0; e < VW; ++e) h[k][e] = fmaf(h[k][e], scale, -mean) * rstd;   // x~ is exact
+        for (int e = 0; e < VW; ++e)
+          h[k][e] = fmaf(h[k][e], !kRagged || e < c.split ? scale0 : scale1, -mean) * rstd;
+        place.mask(h[k], t + k * R, D);
+        place.mask(g[k], t + k * R, D);
       } else {
-        if constexpr (kPacked) {
-          const float scale0 = power_of_byte(cx[k].byte0), scale1 = power_of_byte(cx[k].byte1);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) h[k][e] *= e < cx[k].split ? scale0 : scale1;
-        }
+        P::widen(rx[k], h[k]);
+        P::widen(rg[k], g[k]);
         place.mask(h[k], t + k * R, D);
         place.mask(g[k], t + k * R, D);
 #pragma unroll
