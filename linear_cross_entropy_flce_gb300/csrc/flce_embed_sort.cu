@@ -6,13 +6,13 @@
 // warp's equals is known and order is kept. Then the counters of all warps are summed digit by
 // digit, and every item knows its place.
 //
-// Up to 16384 tokens one cluster of up to 8 CTAs takes all passes: each has a consecutive part of the items,
-// reads the others' digit counts and puts every item where it goes, in the shared memory of whichever
-// CTA owns that place. More tokens go through tiles with three launches a pass (count, offsets of every
-// digit and tile, place).
+// Up to 16384 tokens one cluster of 8 CTAs takes all passes: each has a consecutive part of the items, reads
+// the others' digit counts and puts every item where it goes, in the shared memory of whichever CTA owns
+// that place. More tokens go through tiles with three launches a pass (count, offsets of every digit and
+// tile, place). Up to kSortCount tokens, finally, are counted against one another without any passes.
 //
 // Bound by latency: barriers and dependent accesses to shared memory. 8192 tokens of 128256 ids, two passes, 11 us
-// (23 by one CTA with eight items a thread), 3001 of 32000 9 (10), 65536 of 32000 35 in six launches.
+// (23 by one CTA with eight items a thread), 65536 of 32000 35 in six launches.
 #include <cstdint>
 
 #include "flce_embed.h"
@@ -54,10 +54,13 @@ __device__ __forceinline__ void rank_tile(SortShared& sh, const uint32_t (&key)[
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t mask = (1u << bits) - 1u;
   const int bins = 1 << bits;
-  for (int b = lane; b < bins / 2; b += 32) reinterpret_cast<uint32_t*>(sh.count[warp])[b] = 0;
+  const int warps = min(kWarps, (n + 32 * kItems - 1) / (32 * kItems));   // that have items
+  if (warp < warps)
+    for (int b = lane; b < bins / 2; b += 32) reinterpret_cast<uint32_t*>(sh.count[warp])[b] = 0;
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
+    if (warp >= warps) break;
     const bool in = item_at<kItems>(j) < n;
     const uint32_t d = in ? (key[j] >> shift) & mask : kBins;   // kBins: no item
     const uint32_t peers = __match_any_sync(0xffffffffu, d);
@@ -74,8 +77,8 @@ __device__ __forceinline__ void rank_tile(SortShared& sh, const uint32_t (&key)[
   __syncthreads();
   if (threadIdx.x < bins) {
     uint32_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) {
       const uint32_t c = sh.count[w][threadIdx.x];
       sh.count[w][threadIdx.x] = static_cast<uint16_t>(total);
       total += c;
@@ -116,6 +119,8 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t a, uint32_t x, uint32_t y
   asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
+constexpr int kCluster = 8;
+
 // One cluster; CTA c has items [c per, (c + 1) per), per = 1024 kItems at most.
 template <int kItems>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -124,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ SortShared sh;
   extern __shared__ uint2 s_items[];   // [1024 kItems]: key, index
   start_next_launch();
-  const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(cluster_ctarank());
+  constexpr int ctas = kCluster;
+  const int rank = static_cast<int>(cluster_ctarank());
   const int first = rank * per;
   const int n = N - first < per ? N - first : per;
   uint32_t key[kItems], index[kItems], place[kItems];
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t all = 0, before = 0;
     if (threadIdx.x <= mask) {
       const uint32_t at = smem_u32(&sh.total[threadIdx.x]);
-#pragma unroll 8
+#pragma unroll
       for (int c = 0; c < ctas; ++c) {
         const uint32_t t = ld_cluster_u32(mapa_shared(at, static_cast<uint32_t>(c)));
         all += t;
@@ -179,6 +185,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         index[j] = v.y;
       }
     }
+  }
+}
+
+// ---- few tokens ----------------------------------------------------------------------
+
+// A token's place is the number of tokens that come before it: a CTA counts for 32 of them, a lane each, its
+// warps taking shares of all the keys, four at a time. N^2 comparisons, but no pass waits for another.
+constexpr int kCountThreads = 256;
+constexpr int kCountWarps = kCountThreads / 32;
+__global__ void __launch_bounds__(kCountThreads)
+    sort_count_all_kernel(const int32_t* tokens, int N, int V, int ignore_index, uint32_t* ids, uint32_t* perm) {
+  extern __shared__ uint4 s_keys[];   // four keys each, past N the largest
+  __shared__ uint32_t s_place[kCountWarps][32];
+  start_next_launch();
+  const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x) >> 5;
+  const int vectors = (N + 3) / 4;
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(s_keys);
+#pragma unroll 8
+  for (int i = threadIdx.x; i < vectors * 4; i += kCountThreads)
+    keys[i] = i < N ? key_of(tokens, i, V, ignore_index) : 0xFFFFFFFFu;
+  __syncthreads();
+  const int first = static_cast<int>(blockIdx.x) * 32, i = first + lane;
+  const uint32_t key = i < N ? keys[i] : 0xFFFFFFFEu;
+  uint32_t place = 0;
+  const int share = (vectors + kCountWarps - 1) / kCountWarps;
+  const int end = min(vectors, (warp + 1) * share);
+  // of equal ids those before this CTA's tokens come first, those after it later
+  auto count = [&](int from, int to, uint32_t below) {
+#pragma unroll 4
+    for (int j = from; j < to; ++j) {
+      const uint4 k = s_keys[j];
+      place += (k.x < below) + (k.y < below) + (k.z < below) + (k.w < below);
+    }
+  };
+  const int begin = warp * share, own = first / 4;
+  count(begin, min(end, own), key + 1u);
+  count(max(begin, own), end, key);
+  s_place[warp][lane] = place;
+  __syncthreads();
+  if (warp != 0) return;
+  const uint32_t equal = __match_any_sync(0xffffffffu, key);   // and of this CTA's own the earlier ones
+  place = __popc(equal & ((1u << lane) - 1u));
+#pragma unroll
+  for (int w = 0; w < kCountWarps; ++w) place += s_place[w][lane];
+  if (i < N) {
+    ids[place] = key;
+    perm[place] = static_cast<uint32_t>(i);
   }
 }
 
@@ -283,8 +336,13 @@ cudaError_t launch_sort_tokens(const int32_t* tokens, int N, int V, int ignore_i
   int bits = 1;   // of the keys 0 to V
   while ((static_cast<int64_t>(V) >> bits) != 0) ++bits;
   const int passes = (bits + kSortDigitBits - 1) / kSortDigitBits;
+  if (N <= kSortCount) {
+    const int smem = (N + 3) / 4 * 16;   // 16 KB at most
+    sort_count_all_kernel<<<(N + 31) / 32, kCountThreads, smem, stream>>>(tokens, N, V, ignore_index, ids, perm);
+    return cudaGetLastError();
+  }
   if (N <= kSortCluster) {
-    const int ctas = N <= 1024 ? 1 : N <= 2048 ? 2 : N <= 4096 ? 4 : 8;
+    constexpr int ctas = kCluster;
     const int per = ((N + ctas - 1) / ctas + 31) / 32 * 32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
