@@ -17,6 +17,8 @@
 // Up to 128 tokens bound by the reads of W: D = 4096, V = 128256 nvfp4 51 us for 1 token, 55 for 64, 57 for 128
 // (5.7 to 5.9 TB/s); 75 for 256. Long prompts: 8192 tokens 1.44 ms in short runs and 1.56 under the power cap
 // (5.5 to 6.0 PFLOP/s), mxfp4 1.33 and 1.43; a stage takes 262 ns without its loads and 350 with them.
+// Short rows are bound by the outputs: 4000 x 512 x 120000 to fp32 364 us (5.4 TB/s; with the rows' scales read
+// only once the tile is done 435), 8000 x 512 x 120000 to bf16 830 us (913 with a single staging place a warp).
 #include <cstdint>
 
 #include "flce_blocks.h"
@@ -44,8 +46,8 @@ struct Cfg {
   static constexpr uint32_t kSf = kNv ? 2048 : 1024;        // scale bytes of 128 rows' 256 values
   static constexpr int kBlocks = kSf / 512;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSf * (1 + kTokenTiles);
-  // of an epilogue warp: kOutTokens rows on their way out, its tokens' row scales
-  static constexpr uint32_t kOutBytes = kN >= 64 ? kOutTokens * 64 + (kNv ? kN / 2 * 4 : 0) : 0;
+  // of an epilogue warp: twice kOutTokens rows on their way out, its tokens' row scales
+  static constexpr uint32_t kOutBytes = kN >= 64 ? 2 * kOutTokens * 64 + (kNv ? kN / 2 * 4 : 0) : 0;
   static constexpr int kFit = static_cast<int>((225 * 1024 - kEpilogue * kOutBytes) / kStageBytes);
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
   static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogue * kOutBytes + 512;
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - (kWarps - kEpilogue)) >> 2;
     const uint32_t from = (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kHalf);
     uint8_t* const s_out = smem + kStages * C::kStageBytes + (warp - (kWarps - kEpilogue)) * C::kOutBytes;
-    [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(s_out + kOutTokens * 64);
+    [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(s_out + 2 * kOutTokens * 64);
     int acc = 0;
     uint32_t acc_phase = 0;
     // this lane's row of a tile, and whether the tile has it
@@ -383,6 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = row_of(at, mine);
       const int first = at.token + half * kHalf;
       const int tokens = min(kHalf, p.N - first);
+      // the rows' scales, on their way while the tile is
+      [[maybe_unused]] float w_row = 1.f, h_row[(kHalf + 31) / 32];
+      if constexpr (kNv) {
+        w_row = mine ? p.w_rows[r] : 0.f;
+#pragma unroll
+        for (int k = 0; k < (kHalf + 31) / 32; ++k)
+          h_row[k] = k * 32 + lane < tokens ? p.h_rows[first + k * 32 + lane] : 0.f;
+      }
       int got = 0;
       if (lane == 0) got = mbar_wait_bounded<kCl>(tfull_bar(acc), acc_phase, tmo, abort_flag) ? 1 : 0;
       got = __shfl_sync(0xffffffffu, got, 0);
@@ -413,15 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc = 0;
         acc_phase ^= 1u;
       }
-      [[maybe_unused]] float w_row = 1.f;
-      if constexpr (kNv) w_row = mine ? p.w_rows[r] : 0.f;
       if constexpr (kHalf >= 32) {
         // some tokens at a time; where all of a warp's 32 rows of bf16 are there, they meet in shared memory
         // and leave 16 bytes at a time
         const bool wide = kBf16 && p.wide && __all_sync(0xffffffffu, mine);
         if constexpr (kNv) {
           __syncwarp();
-          for (int c = lane; c < kHalf; c += 32) s_rows[c] = c < tokens ? p.h_rows[first + c] : 0.f;
+#pragma unroll
+          for (int k = 0; k < kHalf / 32; ++k) s_rows[k * 32 + lane] = h_row[k];
           __syncwarp();
         }
 #pragma unroll
@@ -441,8 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int n = min(kOutTokens, tokens - c0);
           if (wide) {
-            uint16_t* const to = reinterpret_cast<uint16_t*>(s_out) + lane;
-            __syncwarp();
+            // one place after the other: what was read from this one two steps ago is behind a barrier
+            uint8_t* const place = s_out + c0 / kOutTokens % 2 * (kOutTokens * 64);
+            uint16_t* const to = reinterpret_cast<uint16_t*>(place) + lane;
 #pragma unroll
             for (int c = 0; c < kOutTokens; c += 2) {
               const uint32_t two = pack_bf16x2(o[c], o[c + 1]);
@@ -454,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kOutTokens / 8; ++j) {
               const int c = j * 8 + (lane >> 2);
-              const uint4 out = reinterpret_cast<const uint4*>(s_out)[j * 32 + lane];
+              const uint4 out = reinterpret_cast<const uint4*>(place)[j * 32 + lane];
               if (c < n) *reinterpret_cast<uint4*>(y + c * p.ldy * 2) = out;
             }
           } else if (mine) {
@@ -472,11 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        [[maybe_unused]] const float h_row = kNv && lane < tokens ? p.h_rows[first + lane] : 0.f;
 #pragma unroll
         for (int c = 0; c < kHalf; ++c) {
           float o = __uint_as_float(v[c]);
-          if constexpr (kNv) o = o * w_row * __shfl_sync(0xffffffffu, h_row, c);
+          if constexpr (kNv) o = o * w_row * __shfl_sync(0xffffffffu, h_row[0], c);
           if (c < tokens && mine) {
             const int64_t to = (first + c) * p.ldy + r;
             if constexpr (kBf16) static_cast<uint16_t*>(p.y)[to] = static_cast<uint16_t>(pack_bf16x2(o, 0.f) & 0xFFFFu);
