@@ -31,9 +31,9 @@ namespace flce {
 
 namespace {
 
-constexpr int kWarps = 12;   // TMA, MMA, two without work, eight of the epilogue
-constexpr int kThreads = kWarps * 32;
-constexpr int kEpilogue = 8;
+constexpr int kEpilogue = 8;              // warps of the epilogue, then the copying one and the MMAs'
+constexpr int kCopyWarp = kEpilogue, kMmaWarp = kEpilogue + 1;
+constexpr int kThreads = (kEpilogue + 2) * 32;
 constexpr int kOutTokens = 16;
 
 template <int kN, int kNv, int kCta>
@@ -96,6 +96,26 @@ template <int kN, int kNv, int kCta>
 __device__ __forceinline__ constexpr uint32_t fp4_idesc(uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kN >> 3) << 17) | ((kNv ? 0u : 1u) << 23) |
          ((128u * kCta >> 4) << 24) | (sf << 29);
+}
+
+// 16 lanes x 32 columns: of columns 8 k and on, lane l holds columns 2 (l % 4) and the next, of rows l / 4
+// (r[4 k], r[4 k + 1]) and l / 4 + 8 (the two after them)
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// four 8 x 8 matrices of 16 bits, held as above, to shared memory by columns: lane l gives the place of
+// column l % 8 of matrix l / 8
+__device__ __forceinline__ void st_matrices_by_column(uint32_t a, uint32_t m0, uint32_t m1, uint32_t m2,
+                                                      uint32_t m3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(m0),
+               "r"(m1), "r"(m2), "r"(m3)
+               : "memory");
 }
 
 template <int kCols>
@@ -221,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the barriers of both CTAs are there before either touches the other's
   if constexpr (kCl) cluster_sync();
   else __syncthreads();
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc_cg<kCta>(smem_u32(tmem_holder), C::kTmemCols);
     tmem_relinquish_cg<kCta>();
   }
@@ -237,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
   };
 
-  if (warp == 0) {
+  if (warp == kCopyWarp) {
     int stage = 0;
     uint32_t phase = 0, issued_mask = 0, issued_par = 0;
     bool ok = true;
@@ -303,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1 && leader) {
+  } else if (warp == kMmaWarp && leader) {
     int stage = 0, acc = 0, buffer = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true, issued_any = false;
@@ -366,11 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(drain_bar, 0, 1000000000ull, &no_abort);
     }
     __syncwarp();
-  } else if (warp >= kWarps - kEpilogue) {
+  } else if (warp < kEpilogue) {
     constexpr int kHalf = kN / 2;   // columns of a warp
-    const int quarter = warp & 3, half = (warp - (kWarps - kEpilogue)) >> 2;
+    const int quarter = warp & 3, half = warp >> 2;
     const uint32_t from = (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kHalf);
-    uint8_t* const s_out = smem + kStages * C::kStageBytes + (warp - (kWarps - kEpilogue)) * C::kOutBytes;
+    uint8_t* const s_out = smem + kStages * C::kStageBytes + warp * C::kOutBytes;
     [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(s_out + 2 * kOutTokens * 64);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -385,10 +405,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = row_of(at, mine);
       const int first = at.token + half * kHalf;
       const int tokens = min(kHalf, p.N - first);
-      // the rows' scales, on their way while the tile is
-      [[maybe_unused]] float w_row = 1.f, h_row[(kHalf + 31) / 32];
+      // where all of a warp's 32 rows of bf16 are there, they meet in shared memory and leave 16 bytes at a time
+      const bool wide = kBf16 && kHalf >= 32 && p.wide && __all_sync(0xffffffffu, mine);
+      // the rows' scales, on their way while the tile is: of this lane's row, or of the four that it holds then
+      [[maybe_unused]] float w_row[4], h_row[(kHalf + 31) / 32];
       if constexpr (kNv) {
-        w_row = mine ? p.w_rows[r] : 0.f;
+        if (wide) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) w_row[m] = p.w_rows[r - lane + (lane >> 2) + 8 * m];
+        } else {
+          w_row[0] = mine ? p.w_rows[r] : 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < (kHalf + 31) / 32; ++k)
           h_row[k] = k * 32 + lane < tokens ? p.h_rows[first + k * 32 + lane] : 0.f;
@@ -410,29 +437,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      uint32_t v[kHalf];
-      tmem_ld<kHalf>(tmem_base + from + static_cast<uint32_t>(acc * kN), v);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kCl) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
-        else mbar_arrive(tempty_bar(acc));
-      }
-      if (++acc == C::kAcc) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
-      if constexpr (kHalf >= 32) {
-        // some tokens at a time; where all of a warp's 32 rows of bf16 are there, they meet in shared memory
-        // and leave 16 bytes at a time
-        const bool wide = kBf16 && p.wide && __all_sync(0xffffffffu, mine);
-        if constexpr (kNv) {
-          __syncwarp();
+      if constexpr (kNv && kHalf >= 32) {
+        __syncwarp();   // the tile before has read them
 #pragma unroll
-          for (int k = 0; k < kHalf / 32; ++k) s_rows[k * 32 + lane] = h_row[k];
-          __syncwarp();
+        for (int k = 0; k < kHalf / 32; ++k) s_rows[k * 32 + lane] = h_row[k];
+      }
+      const uint32_t at_tmem = tmem_base + from + static_cast<uint32_t>(acc * kN);
+      auto read = [&]() {   // the accumulator has been read
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kCl) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+          else mbar_arrive(tempty_bar(acc));
         }
+        if (++acc == C::kAcc) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      };
+      if constexpr (kBf16 && kHalf >= 32) {
+        if (wide) {
+          uint32_t v[2][kHalf / 2];   // rows 0 to 15 of the warp's 32, and the rest
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 32)
+              tmem_ld_16x256b_x4(at_tmem + (static_cast<uint32_t>(u * 16) << 16) + c,
+                                 *reinterpret_cast<uint32_t(*)[16]>(&v[u][c / 2]));
+          }
+          read();
+          // a token's 64 bytes: its four 16-byte pieces in an order that keeps eight tokens on all banks
+          const uint32_t put = static_cast<uint32_t>((lane & 7) * 64 + ((lane >> 3) ^ ((lane >> 1) & 3)) * 16);
+          const int got_from = (lane >> 2) * 64 + ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
+          uint8_t* y = static_cast<uint8_t*>(p.y) + (first * p.ldy + (r - lane)) * 2 +
+                       (lane >> 2) * p.ldy * 2 + (lane & 3) * 16;
+#pragma unroll
+          for (int c0 = 0; c0 < kHalf; c0 += kOutTokens) {
+            if (c0 >= tokens) break;
+            // one place after the other: what was read from this one two steps ago is behind a barrier
+            uint8_t* const place = s_out + c0 / kOutTokens % 2 * (kOutTokens * 64);
+#pragma unroll
+            for (int c = 0; c < kOutTokens; c += 8) {
+              float2 h = make_float2(1.f, 1.f);
+              if constexpr (kNv) h = *reinterpret_cast<const float2*>(s_rows + c0 + c + (lane & 3) * 2);
+              uint32_t out[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int k = (c0 + c) / 2 + (m & 1) * 2;
+                float a = __uint_as_float(v[m >> 1][k]), b = __uint_as_float(v[m >> 1][k + 1]);
+                if constexpr (kNv) {
+                  a = a * w_row[m] * h.x;
+                  b = b * w_row[m] * h.y;
+                }
+                out[m] = pack_bf16x2(a, b);
+              }
+              st_matrices_by_column(smem_u32(place) + c * 64 + put, out[0], out[1], out[2], out[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kOutTokens / 8; ++j) {
+              const uint4 out = *reinterpret_cast<const uint4*>(place + j * 512 + got_from);
+              if (c0 + j * 8 + (lane >> 2) < tokens) *reinterpret_cast<uint4*>(y) = out;
+              y += 8 * p.ldy * 2;
+            }
+          }
+          continue;
+        }
+      }
+      uint32_t v[kHalf];
+      tmem_ld<kHalf>(at_tmem, v);
+      read();
+      if constexpr (kHalf >= 32) {
+        // some tokens at a time
 #pragma unroll
         for (int c0 = 0; c0 < kHalf; c0 += kOutTokens) {
           if (c0 >= tokens) break;
@@ -445,47 +522,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               o[c + e] = __uint_as_float(v[c0 + c + e]);
-              if constexpr (kNv) o[c + e] = o[c + e] * w_row * hs[e];
+              if constexpr (kNv) o[c + e] = o[c + e] * w_row[0] * hs[e];
             }
           }
           const int n = min(kOutTokens, tokens - c0);
-          if (wide) {
-            // one place after the other: what was read from this one two steps ago is behind a barrier
-            uint8_t* const place = s_out + c0 / kOutTokens % 2 * (kOutTokens * 64);
-            uint16_t* const to = reinterpret_cast<uint16_t*>(place) + lane;
+          if (!mine) continue;
+          if constexpr (kBf16) {
+            uint16_t* y = static_cast<uint16_t*>(p.y) + (first + c0) * p.ldy + r;
 #pragma unroll
-            for (int c = 0; c < kOutTokens; c += 2) {
-              const uint32_t two = pack_bf16x2(o[c], o[c + 1]);
-              to[c * 32] = static_cast<uint16_t>(two & 0xFFFFu);
-              to[(c + 1) * 32] = static_cast<uint16_t>(two >> 16);
-            }
-            __syncwarp();
-            uint8_t* const y = static_cast<uint8_t*>(p.y) + ((first + c0) * p.ldy + (r - lane)) * 2 + (lane & 3) * 16;
+            for (int c = 0; c < kOutTokens; ++c, y += p.ldy)
+              if (c < n) *y = static_cast<uint16_t>(pack_bf16x2(o[c], 0.f) & 0xFFFFu);
+          } else {
+            float* y = static_cast<float*>(p.y) + (first + c0) * p.ldy + r;
 #pragma unroll
-            for (int j = 0; j < kOutTokens / 8; ++j) {
-              const int c = j * 8 + (lane >> 2);
-              const uint4 out = reinterpret_cast<const uint4*>(place)[j * 32 + lane];
-              if (c < n) *reinterpret_cast<uint4*>(y + c * p.ldy * 2) = out;
-            }
-          } else if (mine) {
-            if constexpr (kBf16) {
-              uint16_t* y = static_cast<uint16_t*>(p.y) + (first + c0) * p.ldy + r;
-#pragma unroll
-              for (int c = 0; c < kOutTokens; ++c, y += p.ldy)
-                if (c < n) *y = static_cast<uint16_t>(pack_bf16x2(o[c], 0.f) & 0xFFFFu);
-            } else {
-              float* y = static_cast<float*>(p.y) + (first + c0) * p.ldy + r;
-#pragma unroll
-              for (int c = 0; c < kOutTokens; ++c, y += p.ldy)
-                if (c < n) *y = o[c];
-            }
+            for (int c = 0; c < kOutTokens; ++c, y += p.ldy)
+              if (c < n) *y = o[c];
           }
         }
       } else {
 #pragma unroll
         for (int c = 0; c < kHalf; ++c) {
           float o = __uint_as_float(v[c]);
-          if constexpr (kNv) o = o * w_row * __shfl_sync(0xffffffffu, h_row[0], c);
+          if constexpr (kNv) o = o * w_row[0] * __shfl_sync(0xffffffffu, h_row[0], c);
           if (c < tokens && mine) {
             const int64_t to = (first + c) * p.ldy + r;
             if constexpr (kBf16) static_cast<uint16_t*>(p.y)[to] = static_cast<uint16_t>(pack_bf16x2(o, 0.f) & 0xFFFFu);
@@ -499,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kCl) cluster_sync();   // the pair's copies and MMAs are done
   else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_cg<kCta>(tmem_base, C::kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc_cg<kCta>(tmem_base, C::kTmemCols);
 }
 
 template <int kN, int kNv, int kBf16, int kCta>
