@@ -68,6 +68,19 @@ bool encode_scales(CUtensorMap* m, const void* base, uint64_t bytes, int nv) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// y in boxes of 32 values of kFp4OutTokens rows; nothing outside y is written.
+bool encode_y(CUtensorMap* m, void* y, int64_t V, int64_t N, int64_t ldy) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(V), static_cast<cuuint64_t>(N)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldy) * 2};
+  cuuint32_t box[2] = {32, kFp4OutTokens};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 int done(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
 
 }  // namespace
@@ -236,7 +249,7 @@ int flce_linear_fp4(const uint8_t* h_codes, const uint8_t* h_scales, const float
   const int kn = fp4_tile(N);
   const uint64_t row = static_cast<uint64_t>(fp4_code_bytes(D));
   const int nv = format == FLCE_FP4_NV;
-  Fp4Maps maps;
+  Fp4Maps maps{};
   if (!encode_codes(&maps.w, w_codes, row, static_cast<uint64_t>(V), 128) ||
       !encode_codes(&maps.w32, w_codes, row, static_cast<uint64_t>(V), 32) ||
       !encode_codes(&maps.h, h_codes, row, static_cast<uint64_t>(N), static_cast<uint32_t>(kn / fp4_ctas(kn))) ||
@@ -251,7 +264,8 @@ int flce_linear_fp4(const uint8_t* h_codes, const uint8_t* h_scales, const float
   p.w_rows = w_row_scales;
   p.y = y;
   p.ldy = ldy;
-  p.wide = aligned(y, 16) && ldy * static_cast<int64_t>(elem_size(dtype)) % 16 == 0;
+  p.wide = fp4_boxes(kn, dtype == FLCE_DTYPE_BF16) && aligned(y, 16) && ldy % 8 == 0 &&
+           encode_y(&maps.y, y, V, N, ldy);
   p.timeout_ns = timeout_ns > 0 ? timeout_ns : kDefaultTimeoutNs;
   p.status = status;
   return done(launch_fp4_gemm(kn, nv, dtype == FLCE_DTYPE_BF16, maps, p, sms, static_cast<cudaStream_t>(stream)));

@@ -11,14 +11,19 @@
 // tcgen05.cp takes them to TMEM. Up to 256 tokens each CTA streams its own share of W's rows, in whole
 // 32s; more tokens go tile by tile, all of a row tile's tokens before the next. From 65 tokens on a cluster pair
 // shares a tile of 256 rows, each CTA staging half of the tokens (8192 x 4096 x 128256 nvfp4 by single CTAs
-// 1.88 ms, by pairs 1.83, with rows of y 16 bytes at a time 1.43-1.57). The scales are copied to TMEM with
-// each stage, in the order in which the tensor core takes the MMAs after them.
+// 1.88 ms, by pairs 1.83, with rows of y 16 bytes at a time 1.60, in boxes 1.50). The scales are copied to TMEM
+// with each stage, in the order in which the tensor core takes the MMAs after them.
 //
-// Up to 128 tokens bound by the reads of W: D = 4096, V = 128256 nvfp4 51 us for 1 token, 55 for 64, 57 for 128
-// (5.7 to 5.9 TB/s); 75 for 256. Long prompts: 8192 tokens 1.44 ms in short runs and 1.56 under the power cap
-// (5.5 to 6.0 PFLOP/s), mxfp4 1.33 and 1.43; a stage takes 262 ns without its loads and 350 with them.
+// y in bf16: a warp reads its 32 rows of the accumulator as matrix fragments, so that two tokens' values of a
+// row are neighbours in a register, turns 8 x 8 of them at a time on their way to shared memory, and 32 rows of
+// 16 tokens leave in a box while the next 16 are made. Rows of y that are not aligned, and fp32, go by columns.
+//
+// Up to 128 tokens bound by the reads of W: D = 4096, V = 128256 nvfp4 51 us for 1 token, 55 for 64, 56 for 128
+// (5.7 to 5.9 TB/s); 74 for 256. Long prompts: 8192 tokens 1.38 ms in short runs and 1.50 under the power cap
+// (5.7 to 6.2 PFLOP/s), mxfp4 1.30 and 1.35; a stage takes 262 ns without its loads and 350 with them.
 // Short rows are bound by the outputs: 4000 x 512 x 120000 to fp32 364 us (5.4 TB/s; with the rows' scales read
-// only once the tile is done 435), 8000 x 512 x 120000 to bf16 830 us (913 with a single staging place a warp).
+// only once the tile is done 435), 8000 x 512 x 120000 to bf16 604 us, mxfp4 507 (row by row through shared
+// memory 830 and 601).
 #include <cstdint>
 
 #include "flce_blocks.h"
@@ -34,7 +39,7 @@ namespace {
 constexpr int kEpilogue = 8;              // warps of the epilogue, then the copying one and the MMAs'
 constexpr int kCopyWarp = kEpilogue, kMmaWarp = kEpilogue + 1;
 constexpr int kThreads = (kEpilogue + 2) * 32;
-constexpr int kOutTokens = 16;
+constexpr int kOutTokens = kFp4OutTokens;
 
 template <int kN, int kNv, int kCta>
 struct Cfg {
@@ -390,8 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kHalf = kN / 2;   // columns of a warp
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t from = (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kHalf);
-    uint8_t* const s_out = smem + kStages * C::kStageBytes + warp * C::kOutBytes;
-    [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(s_out + 2 * kOutTokens * 64);
+    const uint32_t s_out = stage0 + kStages * C::kStageBytes + warp * (2 * kOutTokens * 64);
+    [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(
+        smem + kStages * C::kStageBytes + kEpilogue * (2 * kOutTokens * 64) + warp * (kHalf * 4));
     int acc = 0;
     uint32_t acc_phase = 0;
     // this lane's row of a tile, and whether the tile has it
@@ -405,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = row_of(at, mine);
       const int first = at.token + half * kHalf;
       const int tokens = min(kHalf, p.N - first);
-      // where all of a warp's 32 rows of bf16 are there, they meet in shared memory and leave 16 bytes at a time
-      const bool wide = kBf16 && kHalf >= 32 && p.wide && __all_sync(0xffffffffu, mine);
+      // where all of a warp's 32 rows of bf16 are there, they meet in shared memory and leave in boxes
+      const bool wide = fp4_boxes(kN, kBf16) && p.wide && __all_sync(0xffffffffu, mine);
       // the rows' scales, on their way while the tile is: of this lane's row, or of the four that it holds then
       [[maybe_unused]] float w_row[4], h_row[(kHalf + 31) / 32];
       if constexpr (kNv) {
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc_phase ^= 1u;
         }
       };
-      if constexpr (kBf16 && kHalf >= 32) {
+      if constexpr (fp4_boxes(kN, kBf16)) {
         if (wide) {
           uint32_t v[2][kHalf / 2];   // rows 0 to 15 of the warp's 32, and the rest
 #pragma unroll
@@ -467,16 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  *reinterpret_cast<uint32_t(*)[16]>(&v[u][c / 2]));
           }
           read();
-          // a token's 64 bytes: its four 16-byte pieces in an order that keeps eight tokens on all banks
+          // a token's 64 bytes, its four 16-byte pieces as the copy swizzles them: eight tokens are on all banks
           const uint32_t put = static_cast<uint32_t>((lane & 7) * 64 + ((lane >> 3) ^ ((lane >> 1) & 3)) * 16);
-          const int got_from = (lane >> 2) * 64 + ((lane & 3) ^ ((lane >> 3) & 3)) * 16;
-          uint8_t* y = static_cast<uint8_t*>(p.y) + (first * p.ldy + (r - lane)) * 2 +
-                       (lane >> 2) * p.ldy * 2 + (lane & 3) * 16;
 #pragma unroll
           for (int c0 = 0; c0 < kHalf; c0 += kOutTokens) {
             if (c0 >= tokens) break;
-            // one place after the other: what was read from this one two steps ago is behind a barrier
-            uint8_t* const place = s_out + c0 / kOutTokens % 2 * (kOutTokens * 64);
+            // one place after the other: the copy from this one, two steps ago, has read it
+            const uint32_t place = s_out + c0 / kOutTokens % 2 * (kOutTokens * 64);
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < kOutTokens; c += 8) {
               float2 h = make_float2(1.f, 1.f);
@@ -492,14 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 out[m] = pack_bf16x2(a, b);
               }
-              st_matrices_by_column(smem_u32(place) + c * 64 + put, out[0], out[1], out[2], out[3]);
+              st_matrices_by_column(place + c * 64 + put, out[0], out[1], out[2], out[3]);
             }
+            fence_proxy_async_smem();
             __syncwarp();
-#pragma unroll
-            for (int j = 0; j < kOutTokens / 8; ++j) {
-              const uint4 out = *reinterpret_cast<const uint4*>(place + j * 512 + got_from);
-              if (c0 + j * 8 + (lane >> 2) < tokens) *reinterpret_cast<uint4*>(y) = out;
-              y += 8 * p.ldy * 2;
+            if (lane == 0) {   // tokens behind the last are not written
+              tma_store_2d(&maps.y, place, r, first + c0);
+              bulk_commit_group();
             }
           }
           continue;
@@ -551,6 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+    }
+    if constexpr (fp4_boxes(kN, kBf16)) {
+      if (lane == 0) bulk_wait_group_all();
     }
   }
   tc_fence_before();

@@ -14,7 +14,7 @@ struct Fp4GemmParams {
   const float *h_rows, *w_rows;   // row scales, or null
   void* y;                  // [N][ldy], fp32 or bf16
   int64_t ldy;
-  int wide;                 // rows of y allow 16-byte accesses
+  int wide;                 // y takes boxes by maps.y
   int64_t timeout_ns;
   int32_t* status;
 };
@@ -24,9 +24,12 @@ inline int fp4_tile(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 
 constexpr int fp4_ctas(int kn) { return kn >= 128 ? 2 : 1; }
 
 // W's codes in boxes of 128 bytes x 128 and x 32 rows, H's in boxes of 128 bytes x kn / ctas rows, both
-// with 128-byte swizzle; the scales' groups of 512 bytes in boxes of those of 256 values.
+// with 128-byte swizzle; the scales' groups of 512 bytes in boxes of those of 256 values; y in bf16, where
+// fp4_boxes and the alignment say so, in boxes of 32 x kFp4OutTokens with 64-byte swizzle.
+constexpr int kFp4OutTokens = 16;
+constexpr bool fp4_boxes(int kn, int bf16) { return bf16 && kn >= 64; }
 struct Fp4Maps {
-  CUtensorMap w, w32, h, w_scales, h_scales;
+  CUtensorMap w, w32, h, w_scales, h_scales, y;
 };
 
 // y = H W^T, kn = fp4_tile(p.N).
