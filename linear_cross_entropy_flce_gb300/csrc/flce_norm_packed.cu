@@ -21,6 +21,31 @@ constexpr int kNormPackThreads = 256;
 constexpr int kNormPackLimit = 512;   // threads of a row at most
 constexpr int kNormPackHeld = 2;      // chunks in a thread's registers at most
 
+// Two values at a time, each rounded as by itself.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // 16 values of weight or bias (or `none` without one) from element i on; what is behind D is not read.
 template <int kWbf16>
 __device__ __forceinline__ void load_param16(const void* p, int wide, int i, int D, float none, float (&v)[16]) {
@@ -53,18 +78,23 @@ __global__ void __launch_bounds__(kNormPackLimit, 2)
   const float inv_d = 1.f / static_cast<float>(D);
   Chunk<kBf16> c[kHeld];
   load_chunks<kBf16, kWhole>(from, t, R, width, stage, c);
-  float part = 0.f;
+  uint64_t two = pair(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     float v[16];
     c[k].widen(v);
-    part += sum_n(v);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) two = add2(two, pair(v[e], v[e + 1]));
   }
+  float part, other;
+  split(two, part, other);
+  part += other;
   const float mean = stream_sum2(make_float2(part, 0.f), group, R, s_sum).x * inv_d;
   // the codes, while the others arrive
   uint8_t* const record = packed + row * packed_record(D);
   const int codes = static_cast<int>(packed_codes(D));
-  part = 0.f;
+  const uint64_t less = pair(-mean, -mean);
+  two = pair(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     const int i = (t + k * R) * 16;
@@ -75,7 +105,15 @@ __global__ void __launch_bounds__(kNormPackLimit, 2)
       uint4 q;
       if (byte != 255u) {
         const float inv = inverse_power_of_byte(byte);
-        q = make_uint4(e4m3x4(v, inv), e4m3x4(v + 4, inv), e4m3x4(v + 8, inv), e4m3x4(v + 12, inv));
+        const uint64_t by = pair(inv, inv);
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          float lo, hi;
+          split(mul2(pair(v[e], v[e + 1]), by), lo, hi);
+          w[e / 2] = e4m3x2(lo, hi);
+        }
+        q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
       } else {   // NaN, but for what is behind the row
         uint32_t w[4];
 #pragma unroll
@@ -90,12 +128,19 @@ __global__ void __launch_bounds__(kNormPackLimit, 2)
     }
     if (i + 16 <= D) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) part = fmaf(v[e] - mean, v[e] - mean, part);
+      for (int e = 0; e < 16; e += 2) {
+        const uint64_t d = add2(pair(v[e], v[e + 1]), less);
+        two = fma2(d, d, two);
+      }
     } else {
+      split(two, part, other);
 #pragma unroll
       for (int e = 0; e < 16; ++e) part = i + e < D ? fmaf(v[e] - mean, v[e] - mean, part) : part;
+      two = pair(part, other);
     }
   }
+  split(two, part, other);
+  part += other;
   if (live)
     for (int i = codes / kPackBlock * 33 + t; i < packed_record(D); i += R) record[i] = 0;
   // rsqrtf is off by 2 units of its last place at most, below the sums' own rounding
@@ -110,7 +155,9 @@ __global__ void __launch_bounds__(kNormPackLimit, 2)
     load_param16<kWbf16>(weight, wide_params, i, D, 1.f, w);
     load_param16<kWbf16>(bias, wide_params, i, D, 0.f, b);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+    for (int e = 0; e < 16; e += 2)
+      split(fma2(mul2(add2(pair(v[e], v[e + 1]), less), pair(rstd, rstd)), pair(w[e], w[e + 1]), pair(b[e], b[e + 1])),
+            v[e], v[e + 1]);
     if constexpr (!kWhole) {
       store_staged<kBf16, 16>(to, i - (t & 31) * 16, width, stage, v);
     } else if (live) {
