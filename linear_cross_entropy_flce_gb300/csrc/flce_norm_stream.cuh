@@ -62,6 +62,16 @@ __device__ __forceinline__ void copy_bytes(uint32_t to, const uint8_t* from, uin
       : "memory");
 }
 
+// The 16 bytes that begin 4 q + bits / 8 bytes (fewer than 16) into o and go on in n.
+__device__ __forceinline__ uint4 of_two_chunks(uint4 o, uint4 n, int q, int bits) {
+  const uint32_t w[8] = {o.x, o.y, o.z, o.w, n.x, n.y, n.z, n.w};
+  uint32_t u[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) u[k] = q == 0 ? w[k] : q == 1 ? w[k + 1] : q == 2 ? w[k + 2] : w[(k + 3) & 7];
+  return make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
+                    __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+}
+
 // How the rows of a CTA lie in their 16-byte chunks of VW elements.
 template <int kElt, bool kRagged>
 struct RowPlace {
@@ -129,14 +139,7 @@ struct RowPlace {
         const uint4* const from = reinterpret_cast<const uint4*>(staged) + (i + s) / VW;
         uint4 o = from[0];
         if (shift != 0) {
-          const uint4 n = from[1];
-          const uint32_t w[8] = {o.x, o.y, o.z, o.w, n.x, n.y, n.z, n.w};
-          uint32_t u[5];
-#pragma unroll
-          for (int k = 0; k < 5; ++k)
-            u[k] = q == 0 ? w[k] : q == 1 ? w[k + 1] : q == 2 ? w[k + 2] : w[(k + 3) & 7];
-          o = make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
-                         __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+          o = of_two_chunks(o, from[1], q, bits);
         }
         *reinterpret_cast<uint4*>(row + i * kElt) = o;
       } else {

@@ -14,7 +14,8 @@
 // registers each allow.
 //
 // kPacked: x is left in 8 bits as well (flce_pack.cu's records): whole rows of fp32 from the registers the row
-// is in; ragged rows from the ring, before it is filled again. (Whole rows of bf16: flce_norm_packed.cu.)
+// is in; ragged rows, whose blocks do not begin with a chunk, from the ring, before it is filled again. (Whole
+// rows of bf16: flce_norm_packed.cu.)
 #pragma once
 
 #include <cstdint>
@@ -30,13 +31,13 @@ namespace {
 constexpr int kForwardBlock = 512;
 constexpr int kRing = 2;   // turns of a group in the ring, of two rows each
 
-// VW neighbouring values to a record's codes and, by the first lane of a block's, its scale byte. All lanes of
-// the warp, whose values are neighbours; `there`: element i is before the codes' end.
+// VW neighbouring values to a record's codes and, by the first lane of a block's, its scale byte; largest: of the
+// block. `there`: element i is before the codes' end.
 template <int VW>
 __device__ __forceinline__ void pack_values(uint8_t* record, int i, int D, const float (&v)[VW], uint32_t largest,
                                             bool there) {
-  const uint32_t byte = e4m3_scale_byte(largest_of_lanes<kPackBlock / VW>(largest));
   if (!there) return;
+  const uint32_t byte = e4m3_scale_byte(largest);
   uint32_t codes[VW / 4];
   if (byte != 255u) {
     const float inv = inverse_power_of_byte(byte);
@@ -136,23 +137,39 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
     // zeros from the mean.
     const bool two = row + half < N;
     auto inside = [&](int k) { return k < kNv - 1 || t + k * R < chunks; };
+    if constexpr (kPacked && kRagged) {   // each vector of the row put together from two chunks
+      const int shift = place.s * kElt, q = shift >> 2, bits = (shift & 3) * 8;
+      for (int c = t; (c - (t & 31)) * VW < codes; c += R) {
+        const int i = c * VW;
+        float of[2][VW];
+        uint32_t largest[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint8_t* const from = in + r * slot_bytes;
+          P::widen(of_two_chunks(P::load_if(from, c * VW, c < chunks),
+                                 P::load_if(from, (c + 1) * VW, c + 1 < chunks), q, bits), of[r]);
+          if (i + VW > D) {
+#pragma unroll
+            for (int e = 0; e < VW; ++e) of[r][e] = i + e < D ? of[r][e] : 0.f;
+          }
+          largest[r] = largest_bits(of[r]);
+        }
+#pragma unroll
+        for (int o = 1; o < kPackBlock / VW; o <<= 1) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) largest[r] = max(largest[r], __shfl_xor_sync(0xffffffffu, largest[r], o));
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, of[r], largest[r],
+                          i < codes && (r == 0 || two));
+      }
+    }
     Raw raw[2][kNv];
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
       raw[0][k] = P::load_if(in, (t + k * R) * VW, inside(k));
       raw[1][k] = P::load_if(in + slot_bytes, (t + k * R) * VW, inside(k));
-    }
-    if constexpr (kPacked && kRagged) {   // from the ring
-      for (int r = 0; r < 1 + two; ++r) {
-        uint8_t* const record = packed + (row + r * half) * packed_record(D);
-        const uint8_t* const from = in + r * slot_bytes + place.s * kElt;
-        for (int i = t * 8; i - (t & 31) * 8 < codes; i += R * 8) {
-          float q[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) q[e] = i + e < D ? load_as_f32(from, i + e, kBf16) : 0.f;
-          pack_values<8>(record, i, D, q, largest_bits(q), i < codes);
-        }
-      }
     }
     float v[2][kNv][VW], part[2];
 #pragma unroll
@@ -164,7 +181,8 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
         place.mask(v[r][k], t + k * R, D);
         if constexpr (kPacked && !kRagged) {
           const int i = (t + k * R) * VW;
-          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, v[r][k], largest_bits(v[r][k]),
+          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, v[r][k],
+                          largest_of_lanes<kPackBlock / VW>(largest_bits(v[r][k])),
                           i < codes && (r == 0 || two));
         }
         if (k == 0) {
