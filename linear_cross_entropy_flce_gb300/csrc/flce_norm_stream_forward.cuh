@@ -179,12 +179,6 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
       for (int k = 0; k < kNv; ++k) {
         P::widen(raw[r][k], v[r][k]);
         place.mask(v[r][k], t + k * R, D);
-        if constexpr (kPacked && !kRagged) {
-          const int i = (t + k * R) * VW;
-          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, v[r][k],
-                          largest_of_lanes<kPackBlock / VW>(largest_bits(v[r][k])),
-                          i < codes && (r == 0 || two));
-        }
         if (k == 0) {
 #pragma unroll
           for (int e = 0; e < VW; ++e) acc[e] = v[r][0][e];
@@ -193,6 +187,32 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
         }
       }
       part[r] = sum_n(acc);
+    }
+    if constexpr (kPacked && !kRagged) {   // all blocks' shuffles side by side
+      uint32_t largest[2][kNv];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int k = 0; k < kNv; ++k) largest[r][k] = largest_bits(v[r][k]);
+      }
+#pragma unroll
+      for (int o = 1; o < kPackBlock / VW; o <<= 1) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int k = 0; k < kNv; ++k)
+            largest[r][k] = max(largest[r][k], __shfl_xor_sync(0xffffffffu, largest[r][k], o));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int k = 0; k < kNv; ++k) {
+          const int i = (t + k * R) * VW;
+          pack_values<VW>(packed + (row + r * half) * packed_record(D), i, D, v[r][k], largest[r][k],
+                          i < codes && (r == 0 || two));
+        }
+      }
     }
     const float2 sum = stream_sum2(make_float2(part[0] + nan, part[1] + nan), group, R, s_sum);
     const float mean[2] = {sum.x * inv_d, sum.y * inv_d};
