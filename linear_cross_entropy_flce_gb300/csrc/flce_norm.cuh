@@ -173,6 +173,64 @@ __device__ __forceinline__ void mul_n(float (&d)[VW], const float (&a)[VW]) {
 #pragma unroll
   for (int e = 0; e < VW; ++e) d[e] *= a[e];
 }
+// Two values at a time, each rounded as by itself.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The above and more of them, kPairs: two values an instruction.
+template <int kPairs>
+struct Each {
+  template <int VW>
+  __device__ static void fma(float (&d)[VW], const float (&a)[VW], const float (&b)[VW], const float (&c)[VW]) {
+    if constexpr (kPairs && VW % 2 == 0) {
+#pragma unroll
+      for (int e = 0; e < VW; e += 2)
+        split(fma2(pair(a[e], a[e + 1]), pair(b[e], b[e + 1]), pair(c[e], c[e + 1])), d[e], d[e + 1]);
+    } else {
+      fma_n(d, a, b, c);
+    }
+  }
+  template <int VW>
+  __device__ static void add(float (&d)[VW], const float (&a)[VW]) {
+    if constexpr (kPairs && VW % 2 == 0) {
+#pragma unroll
+      for (int e = 0; e < VW; e += 2) split(add2(pair(d[e], d[e + 1]), pair(a[e], a[e + 1])), d[e], d[e + 1]);
+    } else {
+      add_n(d, a);
+    }
+  }
+  template <int VW>
+  __device__ static void mul(float (&d)[VW], const float (&a)[VW]) {
+    if constexpr (kPairs && VW % 2 == 0) {
+#pragma unroll
+      for (int e = 0; e < VW; e += 2) split(mul2(pair(d[e], d[e + 1]), pair(a[e], a[e + 1])), d[e], d[e + 1]);
+    } else {
+      mul_n(d, a);
+    }
+  }
+};
+
 template <int VW>
 __device__ __forceinline__ float sum_n(const float (&a)[VW]) {
   float s = a[0];

@@ -42,7 +42,13 @@ __device__ __forceinline__ void pack_values(uint8_t* record, int i, int D, const
   if (byte != 255u) {
     const float inv = inverse_power_of_byte(byte);
 #pragma unroll
-    for (int k = 0; k < VW / 4; ++k) codes[k] = e4m3x4(v + 4 * k, inv);
+    for (int k = 0; k < VW / 4; ++k) {
+      float q[4];
+      const uint64_t by = pair(inv, inv);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) split(mul2(pair(v[4 * k + e], v[4 * k + e + 1]), by), q[e], q[e + 1]);
+      codes[k] = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
+    }
   } else {   // NaN, but for what is behind the row
 #pragma unroll
     for (int k = 0; k < VW / 4; ++k) {
@@ -64,6 +70,7 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
                        uint8_t* packed, int R, int slot_bytes, int apart) {
   constexpr int kElt = kBf16 ? 2 : 4, kWelt = kWbf16 ? 2 : 4, VW = 16 / kElt;
   constexpr int kFetchers = kRagged ? 32 : 1;
+  using E = Each<kPacked>;
   using P = Pack<kBf16, VW>;
   using Raw = typename P::Raw;
   using W = Param<kWbf16, VW>;
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
 #pragma unroll
           for (int e = 0; e < VW; ++e) acc[e] = v[r][0][e];
         } else {
-          add_n(acc, v[r][k]);
+          E::add(acc, v[r][k]);
         }
       }
       part[r] = sum_n(acc);
@@ -229,10 +236,17 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
 #pragma unroll
       for (int k = 0; k < kNv; ++k) {
         const float m = inside(k) ? mean[r] : 0.f;
+        if constexpr (kPacked) {
+          const uint64_t less = pair(-m, -m);
 #pragma unroll
-        for (int e = 0; e < VW; ++e) v[r][k][e] -= m;
+          for (int e = 0; e < VW; e += 2)
+            split(add2(pair(v[r][k][e], v[r][k][e + 1]), less), v[r][k][e], v[r][k][e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) v[r][k][e] -= m;
+        }
         place.mask(v[r][k], t + k * R, D);
-        fma_n(acc, v[r][k], v[r][k], acc);
+        E::fma(acc, v[r][k], v[r][k], acc);
       }
       part[r] = sum_n(acc);
     }

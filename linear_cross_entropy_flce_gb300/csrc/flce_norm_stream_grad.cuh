@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
                             int slot_bytes, int apart) {
   constexpr int kElt = kBf16 ? 2 : 4, VW = 16 / kElt;
   constexpr int kFetchers = kRagged ? 32 : 1;
+  using E = Each<kPacked>;
   using P = Pack<kBf16, VW>;
   using Raw = typename P::Raw;
   using W = Param<kWbf16, VW>;
@@ -200,9 +201,13 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
         c.widen(h[k]);
         P::widen(rg[k], g[k]);
         const float scale0 = power_of_byte(c.byte0), scale1 = kRagged ? power_of_byte(c.byte1) : 0.f;
+        const uint64_t less = pair(-mean, -mean), by = pair(rstd, rstd);
 #pragma unroll
-        for (int e = 0; e < VW; ++e)
-          h[k][e] = fmaf(h[k][e], !kRagged || e < c.split ? scale0 : scale1, -mean) * rstd;
+        for (int e = 0; e < VW; e += 2) {
+          const uint64_t scale = pair(!kRagged || e < c.split ? scale0 : scale1,
+                                      !kRagged || e + 1 < c.split ? scale0 : scale1);
+          split(mul2(fma2(pair(h[k][e], h[k][e + 1]), scale, less), by), h[k][e], h[k][e + 1]);
+        }
         place.mask(h[k], t + k * R, D);
         place.mask(g[k], t + k * R, D);
       } else {
@@ -213,17 +218,17 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
 #pragma unroll
         for (int e = 0; e < VW; ++e) h[k][e] = (h[k][e] - mean) * rstd;
       }
-      fma_n(dw[k], g[k], h[k], dw[k]);
-      add_n(db[k], g[k]);
+      E::fma(dw[k], g[k], h[k], dw[k]);
+      E::add(db[k], g[k]);
       if (weight != nullptr) {
         W p;
         float w[VW];
         p.load_if(s_w, (t + k * R) * VW, inside(k));
         p.widen(w);
-        mul_n(g[k], w);
+        E::mul(g[k], w);
       }
-      add_n(s0, g[k]);
-      fma_n(s1, g[k], h[k], s1);
+      E::add(s0, g[k]);
+      E::fma(s1, g[k], h[k], s1);
     }
     const float2 sum =
         stream_sum2(make_float2(sum_n(s0), sum_n(s1)), group, R, s_sum[turn & 1]);
@@ -236,9 +241,17 @@ __global__ void __launch_bounds__(backward_block(kBf16), 1)
       const float mg = -rstd * sum.x * inv_d, mgh = -rstd * sum.y * inv_d;
 #pragma unroll
       for (int k = 0; k < kNv; ++k) {
+        if constexpr (kPacked) {
+          const uint64_t by = pair(rstd, rstd), mgs = pair(mg, mg), mghs = pair(mgh, mgh);
 #pragma unroll
-        for (int e = 0; e < VW; ++e)
-          g[k][e] = fmaf(g[k][e], rstd, fmaf(h[k][e], mgh, mg));
+          for (int e = 0; e < VW; e += 2)
+            split(fma2(pair(g[k][e], g[k][e + 1]), by, fma2(pair(h[k][e], h[k][e + 1]), mghs, mgs)), g[k][e],
+                  g[k][e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VW; ++e)
+            g[k][e] = fmaf(g[k][e], rstd, fmaf(h[k][e], mgh, mg));
+        }
         if (inside(k)) {
           if (kRagged && apart) P::store(staged, (t + k * R) * VW, g[k]);
           else place.template store<kBf16>(dx, row * lddx, g[k], t + k * R, D);
