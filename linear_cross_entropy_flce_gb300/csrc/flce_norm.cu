@@ -574,12 +574,14 @@ cudaError_t launch_layer_norm_packed(const void* x, int bf16, int64_t ldx, const
                                      const void* bias, int wbf16, int N, int D, float eps, void* y,
                                      int64_t ldy, float* mean, float* rstd, uint8_t* packed, int sms,
                                      cudaStream_t stream) {
-  // Rows in registers serve few rows, and many where they are bf16 in whole 16 bytes; the ring does better
-  // with 16 neighbouring fp32, 64 bytes, of each thread, and with many ragged rows. In us, in registers / through
-  // the ring: bf16 16384 x 1024 17.8 / 21.6, 8192 x 4096 37.0 / 38.4, 2000 x 1024 4.4 / 6.8, 16384 x 1001
-  // 38.1 / 36.7; fp32 16384 x 1024 44.4 / 30.0, 2000 x 4096 24.0 / 19.1, 3001 x 1111 16.9 / 13.7.
+  // The ring takes what does not allow 16-byte accesses and fp32, and bf16 from 16 million values on, but for short
+  // rows; rows in registers the rest. In us, in registers / through the ring: bf16 16384 x 1024 17.1 / 19.3,
+  // 8192 x 2048 18.0 / 19.9, 4000 x 4096 18.9 / 19.9, 8192 x 4096 35.9 / 33.0, 16384 x 2560 57.1 / 44.7, 16384 x
+  // 8192 136.5 / 115.5; fp32 16384 x 1024 44.4 / 30.0, 2000 x 4096 24.0 / 19.1, 3001 x 1111 16.9 / 12.8.
+  const bool small = D <= 1024 || static_cast<int64_t>(N) * D <= (int64_t(1) << 24);
+  const bool whole = whole_vectors(x, bf16, ldx) && whole_vectors(y, bf16, ldy);
   cudaError_t e = cudaErrorNotSupported;
-  if (!(bf16 && whole_vectors(x, bf16, ldx) && whole_vectors(y, bf16, ldy)) && norm_stream_fits(D, bf16 ? 2 : 4))
+  if (!(bf16 && whole && small) && norm_stream_fits(D, bf16 ? 2 : 4))
     e = launch_norm_stream_packed(x, bf16, ldx, weight, bias, wbf16, N, D, eps, y, ldy, mean, rstd, packed, sms,
                                   stream);
   if (e == cudaErrorNotSupported)

@@ -6,8 +6,9 @@
 // the output. Rows that do not allow 16-byte accesses come and go through shared memory, a warp's 512
 // values at a time. Which calls come here is decided, with figures, in flce_norm.cu.
 //
-// Bound by instructions (about 17 a value) and their latency: 8192 x 4096 bf16 37 us (50 with registers
-// for 16 warps an SM instead of 32), of which the bytes are 25.
+// Bound by instructions and their latency: 16384 x 1024 bf16 17.1 us, 4000 x 4096 18.9, of which the bytes are 12.6
+// and 12.3 (8192 x 4096 36 us; 50 with registers for 16 warps an SM instead of 32, 40.8 with two rows of a chunk
+// a thread).
 #include <cstdint>
 
 #include "flce_blocks.cuh"

@@ -13,9 +13,10 @@
 // 4001 bf16 76 (148). A full CTA has 512 threads, as many as 128
 // registers each allow.
 //
-// kPacked: x is left in 8 bits as well (flce_pack.cu's records): whole rows of fp32 from the registers the row
-// is in; ragged rows, whose blocks do not begin with a chunk, from the ring, before it is filled again. (Whole
-// rows of bf16: flce_norm_packed.cu.)
+// kPacked: x is left in 8 bits as well (flce_pack.cu's records): whole rows from the registers the row is in;
+// ragged rows, whose blocks do not begin with a chunk, from the ring, before it is filled again.
+// 16384 x 8192 bf16 115.5 us (5.8 TB/s), 8192 x 4096 33, 4000 x 4096 fp32 29.8, 3001 x 1111 fp32 12.8, 16000 x 4001
+// bf16 107. Two values an instruction: it is bound by instructions.
 #pragma once
 
 #include <cstdint>
@@ -200,7 +201,10 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int k = 0; k < kNv; ++k) largest[r][k] = largest_bits(v[r][k]);
+        for (int k = 0; k < kNv; ++k) {
+          if constexpr (kBf16) largest[r][k] = largest_bits_bf16<VW / 2>(reinterpret_cast<const uint32_t*>(&raw[r][k]));
+          else largest[r][k] = largest_bits(v[r][k]);
+        }
       }
 #pragma unroll
       for (int o = 1; o < kPackBlock / VW; o <<= 1) {
@@ -269,12 +273,28 @@ __global__ void __launch_bounds__(kForwardBlock, 1)
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        if constexpr (kPacked) {
+          if (weight == nullptr) {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          float& o = v[r][k][e];
-          o *= rstd[r];
-          if (weight != nullptr) o = bias != nullptr ? fmaf(o, w[e], b[e]) : o * w[e];
-          else if (bias != nullptr) o += b[e];
+            for (int e = 0; e < VW; ++e) w[e] = 1.f;
+          }
+          if (bias == nullptr) {
+#pragma unroll
+            for (int e = 0; e < VW; ++e) b[e] = 0.f;
+          }
+          const uint64_t by = pair(rstd[r], rstd[r]);
+#pragma unroll
+          for (int e = 0; e < VW; e += 2)
+            split(fma2(mul2(pair(v[r][k][e], v[r][k][e + 1]), by), pair(w[e], w[e + 1]), pair(b[e], b[e + 1])),
+                  v[r][k][e], v[r][k][e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            float& o = v[r][k][e];
+            o *= rstd[r];
+            if (weight != nullptr) o = bias != nullptr ? fmaf(o, w[e], b[e]) : o * w[e];
+            else if (bias != nullptr) o += b[e];
+          }
         }
         if (kRagged && apart) P::store(staged + r * slot_bytes, c * VW, v[r][k]);
         else if (r == 0 || two) place.template store<kBf16>(y, (row + r * half) * ldy, v[r][k], c, D);
@@ -324,19 +344,15 @@ cudaError_t launch_stream_forward(const void* x, int bf16, int64_t ldx, const vo
   if (s.groups == 0 || N < static_cast<int64_t>(kForwardBlock / s.R) * grid)
     return cudaErrorNotSupported;
   return with_stream_types(bf16, wbf16, !lay.whole, [&](auto b, auto wb, auto ragged) {
-    if constexpr (kPacked && b() && !ragged()) {
-      return cudaErrorNotSupported;
-    } else {
-      return with_stream_vectors((chunks + s.R - 1) / s.R, [&](auto nv) {
-        auto kern = norm_stream_kernel<b(), wb(), ragged(), nv(), kPacked>;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(s.smem));
-        if (e != cudaSuccess) return e;
-        kern<<<grid, s.groups * s.R, s.smem, stream>>>(x, ldx, weight, bias, N, D, eps, y, ldy, mean,
-                                                      rstd, packed, s.R, slot, lay.apart);
-        return cudaGetLastError();
-      });
-    }
+    return with_stream_vectors((chunks + s.R - 1) / s.R, [&](auto nv) {
+      auto kern = norm_stream_kernel<b(), wb(), ragged(), nv(), kPacked>;
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(s.smem));
+      if (e != cudaSuccess) return e;
+      kern<<<grid, s.groups * s.R, s.smem, stream>>>(x, ldx, weight, bias, N, D, eps, y, ldy, mean,
+                                                    rstd, packed, s.R, slot, lay.apart);
+      return cudaGetLastError();
+    });
   });
 }
 

@@ -34,6 +34,22 @@ def test_products_into_columns_of_a_wider_matrix():
     assert bool((some[1] == 3).all()) and bool((some[3] == 3).all())
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("N,V", [(33, 40), (64, 96), (65, 40), (129, 264), (257, 1000), (300, 520)])
+def test_products_whose_last_rows_are_not_whole(fmt, N, V):
+    h, w = _pair(N, 144, V, fmt, N + V)
+    dense = flce.linear_fp4(h, w, dtype=torch.bfloat16)
+    _check(dense, h, w)
+    wide = torch.full((N + 2, V + 40), 3.0, dtype=torch.bfloat16, device=DEV)
+    for first in (0, 8, 1, 39):   # rows of whole 16 bytes, and not
+        for to in (wide[1:-1, first:first + V], wide.view(-1)[:(N + 2) * (V + 39)].view(N + 2, V + 39)[1:-1, :V]):
+            wide.fill_(3.0)
+            flce.linear_fp4(h, w, out=to)
+            assert torch.equal(to, dense)
+            to.fill_(3.0)
+            assert bool((wide == 3).all())
+
+
 def test_two_calls_at_once():
     g = torch.Generator(device=DEV).manual_seed(3)
     x = torch.randn(700, 2048, generator=g, device=DEV).bfloat16()

@@ -146,6 +146,17 @@ def test_layer_norm_in_parts_in_place_and_in_other_strides(dtype, N, D, pad, shi
     assert got_y.y is xt and torch.equal(xt, want_y.y) and got_p.data is buf and torch.equal(buf, want_p.data)
 
 
+@pytest.mark.parametrize("N,D,wdtype", [(16395, 1032, "f32"), (2051, 8200, "bf16")])
+def test_layer_norm_of_many_bf16_rows(N, D, wdtype):
+    x, dy, w, b = _draw(N, D, N + D)
+    _run(x, dy, w, b, "bf16", wdtype)
+    xt = _put(_values(N, D, 11), "bf16")[0]
+    r, packed = flce.layer_norm_packed(xt)
+    assert torch.equal(packed.data, flce.pack_e4m3(xt).data)
+    bad = ~xt.isfinite().all(dim=1)
+    assert bool(bad.any()) and bool(r.y[bad].isnan().any(dim=1).all()) and bool(r.mean[~bad].isfinite().all())
+
+
 def test_no_rows():
     x = torch.zeros(0, 40, device=DEV)
     r, p = flce.layer_norm_packed(x)
