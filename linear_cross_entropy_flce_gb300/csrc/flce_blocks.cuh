@@ -55,7 +55,11 @@ __device__ __forceinline__ void widen_e4m3x2(uint32_t codes, float& lo, float& h
 
 // Four codes of values times inv.
 __device__ __forceinline__ uint32_t e4m3x4(const float* v, float inv) {
-  return e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
+  const uint64_t by = pair(inv, inv);
+  float q[4];
+  split(mul2(pair(v[0], v[1]), by), q[0], q[1]);
+  split(mul2(pair(v[2], v[3]), by), q[2], q[3]);
+  return e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
 }
 
 // Eight values to E2M1, the first in the lowest bits.

@@ -15,7 +15,7 @@
 // Bound by the bytes of dW for a large table, by dy for a small one: 8192 tokens x 4096 bf16 take 13.6 us
 // looked up, 171 for the gradient of 128256 rows (0.97 of the copy rate) and 42 added to a table that is there
 // (3600 rows; the sort 11, the ranges 25, the join 9, which overlap a little); 3001 x 1111 fp32 of 32000 rows
-// 5.5 and 40; one token 1.9 us. Ranges of 32: 8 make four times the partial rows, and 8 are what few tokens get.
+// 5.5 and 40; one token 1.9 us and, added to a table, 3.1. Ranges of 32: 8 make four times the partial rows, and 8 are what few tokens get.
 #include <cstdint>
 
 #include "flce_embed.h"

@@ -14,9 +14,10 @@
 // stays there. (And no other quotient is rounded onto such a place: its distance from it is more than
 // half the quotient's own last place.)
 //
-// Bound by instructions for nvfp4, by bytes for mxfp4 and for the values back: 128256 x 4096 bf16 258, 187 and 210 us
-// (the bytes 201, 198); 8192 x 4096 20.3 and 15.6; 64128 x 4096 fp32 214; 3001 x 1111 fp32 mxfp4 6.9 and 4.3; one
-// row of 4096 2.2 and 1.8. The quotient corrected by its residual instead (three operations a value) 317.
+// Bound by instructions for nvfp4 (so two values an instruction), by bytes for mxfp4 and for the values back: 128256 x
+// 4096 bf16 235, 184 and 208 us (the bytes 201, 198); 8192 x 4096 18.5 and 15.0; 64128 x 4096 fp32 199; 3001 x 1111
+// fp32 mxfp4 6.1 and 4.2; one row of 4096 2.2 and 1.8. The quotient corrected by its residual instead (three
+// operations a value) 317.
 #include <cstdint>
 
 #include "flce_blocks.cuh"
@@ -72,13 +73,18 @@ __device__ __forceinline__ uint2 quantize_chunk(const Chunk<kBf16>& c, uint32_t 
       r *= g.inverse();
       rest *= g.inverse();
     }
+    const uint64_t rs = pair(r, r), rests = pair(rest, rest);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = fmaf(v[e], r, v[e] * rest);
+    for (int e = 0; e < 16; e += 2) {
+      const uint64_t two = pair(v[e], v[e + 1]);
+      split(fma2(two, rs, mul2(two, rests)), v[e], v[e + 1]);
+    }
   } else {
     byte = power_scale_byte<2, 0x400000u>(amax);
     const float inv = finite ? inverse_power_of_byte(byte) : 0.f;
+    const uint64_t by = pair(inv, inv);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] *= inv;
+    for (int e = 0; e < 16; e += 2) split(mul2(pair(v[e], v[e + 1]), by), v[e], v[e + 1]);
   }
   const float(&lo)[8] = *reinterpret_cast<const float(*)[8]>(v);
   const float(&hi)[8] = *reinterpret_cast<const float(*)[8]>(v + 8);
@@ -202,8 +208,12 @@ __global__ void __launch_bounds__(kFp4Threads)
     else s = power_of_byte(byte[k]);
     float v[8];
     widen_e2m1x8(c[k], v);
+    const uint64_t by = pair(s, s), rows = pair(row_scale, row_scale);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * s * row_scale;
+    for (int e = 0; e < 8; e += 2) {
+      const uint64_t two = mul2(pair(v[e], v[e + 1]), by);
+      split(kNv ? mul2(two, rows) : two, v[e], v[e + 1]);
+    }
     if constexpr (!kWhole) {
       store_staged<kBf16, 8>(to, (i - (t & 31)) * 8, D, s_stage[threadIdx.x >> 5], v);
     } else if (i * 8 + 8 <= D) {

@@ -81,15 +81,7 @@ __global__ void __launch_bounds__(kNormPackLimit, 2)
       uint4 q;
       if (byte != 255u) {
         const float inv = inverse_power_of_byte(byte);
-        const uint64_t by = pair(inv, inv);
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float lo, hi;
-          split(mul2(pair(v[e], v[e + 1]), by), lo, hi);
-          w[e / 2] = e4m3x2(lo, hi);
-        }
-        q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        q = make_uint4(e4m3x4(v, inv), e4m3x4(v + 4, inv), e4m3x4(v + 8, inv), e4m3x4(v + 12, inv));
       } else {   // NaN, but for what is behind the row
         uint32_t w[4];
 #pragma unroll

@@ -43,13 +43,7 @@ __device__ __forceinline__ void pack_values(uint8_t* record, int i, int D, const
   if (byte != 255u) {
     const float inv = inverse_power_of_byte(byte);
 #pragma unroll
-    for (int k = 0; k < VW / 4; ++k) {
-      float q[4];
-      const uint64_t by = pair(inv, inv);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) split(mul2(pair(v[4 * k + e], v[4 * k + e + 1]), by), q[e], q[e + 1]);
-      codes[k] = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
-    }
+    for (int k = 0; k < VW / 4; ++k) codes[k] = e4m3x4(v + 4 * k, inv);
   } else {   // NaN, but for what is behind the row
 #pragma unroll
     for (int k = 0; k < VW / 4; ++k) {

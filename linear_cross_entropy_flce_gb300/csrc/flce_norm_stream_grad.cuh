@@ -16,9 +16,9 @@
 //
 // kPacked: x comes as 8-bit records (flce_pack.cu) instead, 1.03 bytes a value, each copied whole.
 // dy's place in its 16-byte chunks then is the thread's, and its codes are put together from the
-// words they lie in; a chunk has one scale, or two where rows are ragged. 8192 x 4096 bf16 42 us (102 MB read
-// instead of 134, 1.5 more instructions a value), 4000 x 4096 fp32 32.6 (from x 37.4), 3001 x 1111 fp32 16.7,
-// 16000 x 4001 bf16 141 (from x 102: codes and scales of unaligned chunks).
+// words they lie in; a chunk has one scale, or two where rows are ragged. 8192 x 4096 bf16 39.5 us (102 MB read
+// instead of 134; 41.6 with one value an instruction), 16384 x 8192 145, 4000 x 4096 fp32 32.4 (from x 37.4),
+// 3001 x 1111 fp32 16.0, 16000 x 4001 bf16 140 (from x 102: codes and scales of unaligned chunks).
 #pragma once
 
 #include <cstdint>

@@ -6,8 +6,8 @@
 // at a time. Each thread has kAtOnce vectors in flight.
 //
 // Bound by the bytes, D + D / 32 written or read for 2 D or 4 D, and the instructions beside them: 16384 x 8192
-// bf16 66 us packed and 60 unpacked (0.91 and 1.02 of the copy rate), 8192 x 4096 18.5 and 14.2, 4000 x 4096 fp32
-// 13.2 and 18.0, 3001 x 1111 fp32 6.0 and 4.3, 1 x 4096 1.9 and 1.8. As many threads a row as have kAtOnce vectors
+// bf16 65 us packed and 59 unpacked (0.94 and 1.02 of the copy rate), 8192 x 4096 18.0 and 14.2, 4000 x 4096 fp32
+// 13.1 and 18.0, 3001 x 1111 fp32 5.9 and 4.2, 1 x 4096 1.9 and 1.8. As many threads a row as have kAtOnce vectors
 // each: with a thread for each vector 8192 x 4096 took 26.8 and 17.4.
 #include <cstdint>
 
@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(kPackThreads)
     widen_e4m3x2(codes[k].x >> 16, v[2], v[3]);
     widen_e4m3x2(codes[k].y, v[4], v[5]);
     widen_e4m3x2(codes[k].y >> 16, v[6], v[7]);
+    const uint64_t by = pair(s, s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= s;
+    for (int e = 0; e < 8; e += 2) split(mul2(pair(v[e], v[e + 1]), by), v[e], v[e + 1]);
     if constexpr (!kWhole) {
       store_staged<kBf16, 8>(to, (i - (t & 31)) * 8, D, s_stage[threadIdx.x >> 5], v);
     } else if (i * 8 + 8 <= D) {
