@@ -95,11 +95,11 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 #undef FLCE_MMA_FP4
 }
 
-// Instruction descriptor of a 128 kCta x kN x 64 step: E2M1 operands, both K-major; scales E4M3 (nvfp4) or
+// Instruction descriptor of a 128 kCta x n x 64 step: E2M1 operands, both K-major; scales E4M3 (nvfp4) or
 // powers of two; sf: which of the four bytes of a row's scale word the step begins with.
-template <int kN, int kNv, int kCta>
-__device__ __forceinline__ constexpr uint32_t fp4_idesc(uint32_t sf) {
-  return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kN >> 3) << 17) | ((kNv ? 0u : 1u) << 23) |
+template <int kNv, int kCta>
+__device__ __forceinline__ constexpr uint32_t fp4_idesc(int n, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((kNv ? 0u : 1u) << 23) |
          ((128u * kCta >> 4) << 24) | (sf << 29);
 }
 
@@ -153,10 +153,12 @@ struct Tiles {
   int row, row_end, token;
   int last_row;        // share: where its rows end
   int64_t unit, units; // tiles: the next one
-  int step, token_tiles, V;
+  int step, index, token_tiles, V, N;
   bool share;
-  __device__ Tiles(const Fp4GemmParams& p, int index, int count) {
+  __device__ Tiles(const Fp4GemmParams& p, int first, int count) {
     V = p.V;
+    N = p.N;
+    index = first;
     share = p.N <= kN;
     token = 0;
     token_tiles = (p.N + kN - 1) / kN;
@@ -184,9 +186,16 @@ struct Tiles {
       row_end = min(last_row, row + kRows);
     } else {
       unit += step;
+      if (N % kN != 0) {   // dealt out one CTA on, so that the shorter last tiles of the tokens go round
+        unit -= index;
+        index = index + 1 == step ? 0 : index + 1;
+        unit += index;
+      }
       if (unit < units) place();
     }
   }
+  // the tokens of its MMAs: the last tile's are as few as its tokens, in 32s, 16 from either CTA of a pair
+  __device__ int width() const { return kRows == 128 ? kN : min(kN, (N - token + 31) / 32 * 32); }
   // the 32s of rows, counted from CTA `rank`'s 128, that its copies take: [first, end)
   __device__ void quarters(int rank, int& first, int& end) const {
     const int base = row / kRows * kRows + rank * 128;
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             for (int q = q0; q < q1; ++q) load(at_stage + q * 32 * 128, &maps.w32, ks * 128, base + q * 32, pol_w);
           }
-          load(at_stage + kOffB, &maps.h, ks * 128, at.token + static_cast<int>(rank) * (kN / kCta), pol_h);
+          load(at_stage + kOffB, &maps.h, ks * 128, at.token + static_cast<int>(rank) * (at.width() / kCta), pol_h);
           load(at_stage + kOffSfA, &maps.w_scales, 0, (base / 128 * p.stages + ks) * C::kBlocks, pol_w);
 #pragma unroll
           for (int tt = 0; tt < C::kTokenTiles; ++tt)
@@ -340,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kN);
+      const int width = at.width();
       for (int ks = 0; ks < p.stages; ++ks) {
         const bool full_ok = mbar_wait_bounded<kCl>(full_bar(stage), phase, tmo, abort_flag);
         if (!__all_sync(0xffffffffu, full_ok)) {
@@ -363,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b = kNv ? k : k / 2;
             const uint32_t sf = kNv ? 0u : static_cast<uint32_t>(k % 2 * 2);
             mma_fp4<kNv, kCta>(d_tmem, make_sw128_desc(at_stage + k * 32, 16, 1024),
-                               make_sw128_desc(at_stage + kOffB + k * 32, 16, 1024), fp4_idesc<kN, kNv, kCta>(sf),
+                               make_sw128_desc(at_stage + kOffB + k * 32, 16, 1024), fp4_idesc<kNv, kCta>(width, sf),
                                sfa + b * 4, sfb + b * C::kTokenTiles * 4, (ks | k) != 0 ? 1u : 0u);
           }
           umma_commit_pair<kCta>(empty_bar(stage));   // frees the stage in both CTAs
@@ -443,11 +453,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      if constexpr (kNv && kHalf >= 32) {
-        __syncwarp();   // the tile before has read them
-#pragma unroll
-        for (int k = 0; k < kHalf / 32; ++k) s_rows[k * 32 + lane] = h_row[k];
-      }
       const uint32_t at_tmem = tmem_base + from + static_cast<uint32_t>(acc * kN);
       auto read = [&]() {   // the accumulator has been read
         tmem_wait_ld();
@@ -462,6 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc_phase ^= 1u;
         }
       };
+      if (tokens <= 0) {   // the other half's warps have them all
+        read();
+        continue;
+      }
+      if constexpr (kNv && kHalf >= 32) {
+        __syncwarp();   // the tile before has read them
+#pragma unroll
+        for (int k = 0; k < kHalf / 32; ++k) s_rows[k * 32 + lane] = h_row[k];
+      }
       if constexpr (fp4_boxes(kN, kBf16)) {
         if (wide) {
           uint32_t v[2][kHalf / 2];   // rows 0 to 15 of the warp's 32, and the rest
