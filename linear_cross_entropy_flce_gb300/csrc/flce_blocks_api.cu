@@ -246,13 +246,15 @@ int flce_linear_fp4(const uint8_t* h_codes, const uint8_t* h_scales, const float
   int sms = 0;
   rc = device_info(&sms);
   if (rc != FLCE_OK) return rc;
-  const int kn = fp4_tile(N);
-  const uint64_t row = static_cast<uint64_t>(fp4_code_bytes(D));
-  const int nv = format == FLCE_FP4_NV;
   Fp4Maps maps{};
+  const int bf16 = dtype == FLCE_DTYPE_BF16;
+  const int nv = format == FLCE_FP4_NV;
+  const bool boxes = fp4_boxes(fp4_tile(N), bf16) && aligned(y, 16) && ldy % 8 == 0 && encode_y(&maps.y, y, V, N, ldy);
+  const int kn = boxes ? fp4_wide_tile(N, V, sms, nv) : fp4_tile(N);
+  const uint64_t row = static_cast<uint64_t>(fp4_code_bytes(D));
   if (!encode_codes(&maps.w, w_codes, row, static_cast<uint64_t>(V), 128) ||
       !encode_codes(&maps.w32, w_codes, row, static_cast<uint64_t>(V), 32) ||
-      !encode_codes(&maps.h, h_codes, row, static_cast<uint64_t>(N), static_cast<uint32_t>(kn / fp4_ctas(kn))) ||
+      !encode_codes(&maps.h, h_codes, row, static_cast<uint64_t>(N), kn > 256 ? 64u : static_cast<uint32_t>(kn / fp4_ctas(kn))) ||
       !encode_scales(&maps.w_scales, w_scales, static_cast<uint64_t>(fp4_scale_bytes(V, D, nv)), nv) ||
       !encode_scales(&maps.h_scales, h_scales, static_cast<uint64_t>(fp4_scale_bytes(N, D, nv)), nv))
     return FLCE_ERR_CUDA;
@@ -264,11 +266,10 @@ int flce_linear_fp4(const uint8_t* h_codes, const uint8_t* h_scales, const float
   p.w_rows = w_row_scales;
   p.y = y;
   p.ldy = ldy;
-  p.wide = fp4_boxes(kn, dtype == FLCE_DTYPE_BF16) && aligned(y, 16) && ldy % 8 == 0 &&
-           encode_y(&maps.y, y, V, N, ldy);
+  p.wide = boxes;
   p.timeout_ns = timeout_ns > 0 ? timeout_ns : kDefaultTimeoutNs;
   p.status = status;
-  return done(launch_fp4_gemm(kn, nv, dtype == FLCE_DTYPE_BF16, maps, p, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_fp4_gemm(kn, nv, bf16, maps, p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

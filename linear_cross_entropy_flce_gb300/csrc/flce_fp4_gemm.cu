@@ -56,7 +56,7 @@ struct Cfg {
   static constexpr int kFit = static_cast<int>((225 * 1024 - kEpilogue * kOutBytes) / kStageBytes);
   static constexpr int kStages = kFit > 10 ? 10 : kFit;
   static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpilogue * kOutBytes + 512;
-  static constexpr int kAcc = kN == 256 ? 1 : 2;            // accumulators
+  static constexpr int kAcc = kN >= 256 ? 1 : 2;            // accumulators
   // TMEM: the accumulators, then kSfBuffers times the scales of a stage
   static constexpr int kSfCols = kBlocks * 4 * (1 + kTokenTiles);
   static constexpr int kSfBuffers = 2;
@@ -194,8 +194,11 @@ struct Tiles {
       if (unit < units) place();
     }
   }
-  // the tokens of its MMAs: the last tile's are as few as its tokens, in 32s, 16 from either CTA of a pair
-  __device__ int width() const { return kRows == 128 ? kN : min(kN, (N - token + 31) / 32 * 32); }
+  // the tokens of an MMA, of the tile's from `first` on: the last tile's are as few as its tokens, in 32s, 16 from
+  // either CTA of a pair
+  __device__ int width(int first, int most) const {
+    return kRows == 128 ? most : max(0, min(most, (N - token - first + 31) / 32 * 32));
+  }
   // the 32s of rows, counted from CTA `rank`'s 128, that its copies take: [first, end)
   __device__ void quarters(int rank, int& first, int& end) const {
     const int base = row / kRows * kRows + rank * 128;
@@ -307,7 +310,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             for (int q = q0; q < q1; ++q) load(at_stage + q * 32 * 128, &maps.w32, ks * 128, base + q * 32, pol_w);
           }
-          load(at_stage + kOffB, &maps.h, ks * 128, at.token + static_cast<int>(rank) * (at.width() / kCta), pol_h);
+          if constexpr (kN > 256) {   // both MMAs' halves
+            const int one = at.token + static_cast<int>(rank) * (at.width(0, 256) / 2);
+            load(at_stage + kOffB, &maps.h, ks * 128, one, pol_h);
+            load(at_stage + kOffB + 64 * 128, &maps.h, ks * 128, one + 64, pol_h);
+            load(at_stage + kOffB + 128 * 128, &maps.h, ks * 128,
+                 at.token + 256 + static_cast<int>(rank) * (at.width(256, 128) / 2), pol_h);
+          } else {
+            load(at_stage + kOffB, &maps.h, ks * 128, at.token + static_cast<int>(rank) * (at.width(0, kN) / kCta),
+                 pol_h);
+          }
           load(at_stage + kOffSfA, &maps.w_scales, 0, (base / 128 * p.stages + ks) * C::kBlocks, pol_w);
 #pragma unroll
           for (int tt = 0; tt < C::kTokenTiles; ++tt)
@@ -349,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kN);
-      const int width = at.width();
+      constexpr int kFirst = kN > 256 ? 256 : kN;
+      const int width = at.width(0, kFirst);
+      [[maybe_unused]] const int beyond = at.width(kFirst, kN - kFirst);
       for (int ks = 0; ks < p.stages; ++ks) {
         const bool full_ok = mbar_wait_bounded<kCl>(full_bar(stage), phase, tmo, abort_flag);
         if (!__all_sync(0xffffffffu, full_ok)) {
@@ -375,6 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_fp4<kNv, kCta>(d_tmem, make_sw128_desc(at_stage + k * 32, 16, 1024),
                                make_sw128_desc(at_stage + kOffB + k * 32, 16, 1024), fp4_idesc<kNv, kCta>(width, sf),
                                sfa + b * 4, sfb + b * C::kTokenTiles * 4, (ks | k) != 0 ? 1u : 0u);
+            if constexpr (kN > 256) {
+              if (beyond > 0)
+                mma_fp4<kNv, kCta>(d_tmem + 256, make_sw128_desc(at_stage + k * 32, 16, 1024),
+                                   make_sw128_desc(at_stage + kOffB + 128 * 128 + k * 32, 16, 1024),
+                                   fp4_idesc<kNv, kCta>(beyond, sf), sfa + b * 4,
+                                   sfb + (b * C::kTokenTiles + 2) * 4, (ks | k) != 0 ? 1u : 0u);
+            }
           }
           umma_commit_pair<kCta>(empty_bar(stage));   // frees the stage in both CTAs
         }
@@ -478,13 +499,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if constexpr (fp4_boxes(kN, kBf16)) {
         if (wide) {
-          uint32_t v[2][kHalf / 2];   // rows 0 to 15 of the warp's 32, and the rest
+          // 32 rows of 8 tokens, two tokens of a row in a register, rows l / 4 + 8 m of lane l
+          constexpr int kHeld = kHalf <= 128 ? kHalf : 32;   // tokens held as they are
+          uint32_t v[2][kHeld / 2];   // rows 0 to 15 of the warp's 32, and the rest
+          [[maybe_unused]] uint32_t done[kHalf / 8][4];
+          auto load = [&](int first_column) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 2; ++u) {
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 32)
-              tmem_ld_16x256b_x4(at_tmem + (static_cast<uint32_t>(u * 16) << 16) + c,
-                                 *reinterpret_cast<uint32_t(*)[16]>(&v[u][c / 2]));
+              for (int c = 0; c < kHeld; c += 32)
+                tmem_ld_16x256b_x4(at_tmem + (static_cast<uint32_t>(u * 16) << 16) + first_column + c,
+                                   *reinterpret_cast<uint32_t(*)[16]>(&v[u][c / 2]));
+            }
+          };
+          // tokens c to c + 7 of those from `held` on that are in v
+          auto narrow = [&](int held, int c, uint32_t (&out)[4]) {
+            float2 h = make_float2(1.f, 1.f);
+            if constexpr (kNv) h = *reinterpret_cast<const float2*>(s_rows + held + c + (lane & 3) * 2);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const int k = c / 2 + (m & 1) * 2;
+              float a = __uint_as_float(v[m >> 1][k]), b = __uint_as_float(v[m >> 1][k + 1]);
+              if constexpr (kNv) {
+                a = a * w_row[m] * h.x;
+                b = b * w_row[m] * h.y;
+              }
+              out[m] = pack_bf16x2(a, b);
+            }
+          };
+          if constexpr (kHeld == kHalf) {
+            load(0);
+          } else {   // more than the registers take: narrowed as they are read
+            __syncwarp();
+#pragma unroll
+            for (int held = 0; held < kHalf; held += kHeld) {
+              load(held);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < kHeld; c += 8) narrow(held, c, done[(held + c) / 8]);
+            }
           }
           read();
           // a token's 64 bytes, its four 16-byte pieces as the copy swizzles them: eight tokens are on all banks
@@ -498,18 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < kOutTokens; c += 8) {
-              float2 h = make_float2(1.f, 1.f);
-              if constexpr (kNv) h = *reinterpret_cast<const float2*>(s_rows + c0 + c + (lane & 3) * 2);
               uint32_t out[4];
+              if constexpr (kHeld == kHalf) {
+                narrow(0, c0 + c, out);
+              } else {
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const int k = (c0 + c) / 2 + (m & 1) * 2;
-                float a = __uint_as_float(v[m >> 1][k]), b = __uint_as_float(v[m >> 1][k + 1]);
-                if constexpr (kNv) {
-                  a = a * w_row[m] * h.x;
-                  b = b * w_row[m] * h.y;
-                }
-                out[m] = pack_bf16x2(a, b);
+                for (int m = 0; m < 4; ++m) out[m] = done[(c0 + c) / 8][m];
               }
               st_matrices_by_column(place + c * 64 + put, out[0], out[1], out[2], out[3]);
             }
@@ -522,6 +569,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
+      }
+      if constexpr (kHalf > 128) {   // the warp in which W's rows end: 32 tokens at a time
+        __syncwarp();
+        for (int c0 = 0; c0 < tokens; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld<32>(at_tmem + c0, v);
+          tmem_wait_ld();
+          uint16_t* y = static_cast<uint16_t*>(p.y) + (first + c0) * p.ldy + r;
+#pragma unroll
+          for (int c = 0; c < 32; ++c, y += p.ldy) {
+            float o = __uint_as_float(v[c]);
+            if constexpr (kNv) o = o * w_row[0] * s_rows[c0 + c];
+            if (mine && c0 + c < tokens) *y = static_cast<uint16_t>(pack_bf16x2(o, 0.f) & 0xFFFFu);
+          }
+        }
+        read();
+        continue;
       }
       uint32_t v[kHalf];
       tmem_ld<kHalf>(at_tmem, v);
@@ -609,11 +673,18 @@ cudaError_t launch(const Fp4Maps& maps, const Fp4GemmParams& p, int sms, cudaStr
   return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
+// (384 tokens only for y in bf16 and boxes)
 template <int kN, int kCta>
 cudaError_t launch_types(int nv, int bf16, const Fp4Maps& maps, const Fp4GemmParams& p, int sms,
                          cudaStream_t stream) {
-  if (nv) return bf16 ? launch<kN, 1, 1, kCta>(maps, p, sms, stream) : launch<kN, 1, 0, kCta>(maps, p, sms, stream);
-  return bf16 ? launch<kN, 0, 1, kCta>(maps, p, sms, stream) : launch<kN, 0, 0, kCta>(maps, p, sms, stream);
+  if constexpr (kN > 256) {
+    if (!bf16) return cudaErrorInvalidValue;
+    return nv ? launch<kN, 1, 1, kCta>(maps, p, sms, stream) : launch<kN, 0, 1, kCta>(maps, p, sms, stream);
+  } else if (nv) {
+    return bf16 ? launch<kN, 1, 1, kCta>(maps, p, sms, stream) : launch<kN, 1, 0, kCta>(maps, p, sms, stream);
+  } else {
+    return bf16 ? launch<kN, 0, 1, kCta>(maps, p, sms, stream) : launch<kN, 0, 0, kCta>(maps, p, sms, stream);
+  }
 }
 
 }  // namespace
@@ -625,6 +696,7 @@ cudaError_t launch_fp4_gemm(int kn, int nv, int bf16, const Fp4Maps& maps, const
     case 32: return launch_types<32, fp4_ctas(32)>(nv, bf16, maps, p, sms, stream);
     case 64: return launch_types<64, fp4_ctas(64)>(nv, bf16, maps, p, sms, stream);
     case 128: return launch_types<128, fp4_ctas(128)>(nv, bf16, maps, p, sms, stream);
+    case 384: return launch_types<384, fp4_ctas(384)>(nv, bf16, maps, p, sms, stream);
     default: return launch_types<256, fp4_ctas(256)>(nv, bf16, maps, p, sms, stream);
   }
 }

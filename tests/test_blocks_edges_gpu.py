@@ -50,6 +50,17 @@ def test_products_whose_last_rows_are_not_whole(fmt, N, V):
             assert bool((wide == 3).all())
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("N,D,V", [(700, 144, 19456), (1150, 64, 19432), (634, 300, 19456), (534, 1111, 19424)])
+def test_products_of_many_tokens_and_rows(fmt, N, D, V):
+    h, w = _pair(N, D, V, fmt, N + D)
+    y = flce.linear_fp4(h, w, dtype=torch.bfloat16)
+    _check(y, h, w)
+    wide = torch.full((N + 1, V + 8), 3.0, dtype=torch.bfloat16, device=DEV)
+    flce.linear_fp4(h, w, out=wide[:N, :V])
+    assert torch.equal(wide[:N, :V], y) and bool((wide[N] == 3).all()) and bool((wide[:, V:] == 3).all())
+
+
 def test_two_calls_at_once():
     g = torch.Generator(device=DEV).manual_seed(3)
     x = torch.randn(700, 2048, generator=g, device=DEV).bfloat16()
