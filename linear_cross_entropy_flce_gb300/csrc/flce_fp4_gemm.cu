@@ -6,30 +6,34 @@
 // the tensor cores with the operands, from TMEM; the rows' are multiplied in at the end.
 //
 // The rows of W take the M side of a tile (128 per tcgen05.mma) and the tokens the N side, padded to
-// kN = 16 to 256, so that a tile's work follows the tokens there are. A ring stage holds 256 values of
-// each row, 128 bytes as TMA swizzles them, and the scale bytes of both, which lie in memory as
-// tcgen05.cp takes them to TMEM. Up to 256 tokens each CTA streams its own share of W's rows, in whole
+// kN = 16 to 384, so that a tile's work follows the tokens there are (above 64, the last tile's to 32s). A ring
+// stage holds 256 values of each row, 128 bytes as TMA swizzles them, and the scale bytes of both, which lie in
+// memory as tcgen05.cp takes them to TMEM. Up to 256 tokens each CTA streams its own share of W's rows, in whole
 // 32s; more tokens go tile by tile, all of a row tile's tokens before the next. From 65 tokens on a cluster pair
 // shares a tile of 256 rows, each CTA staging half of the tokens (8192 x 4096 x 128256 nvfp4 by single CTAs
-// 1.88 ms, by pairs 1.83, with rows of y 16 bytes at a time 1.60, in boxes 1.50). The scales are copied to TMEM
-// with each stage, in the order in which the tensor core takes the MMAs after them.
+// 1.88 ms, by pairs 1.83, with rows of y 16 bytes at a time 1.60, in boxes 1.51). Tiles of 384 tokens are two MMAs
+// on one copy of W's rows; which calls take them is decided in flce_fp4_gemm.h. The scales are copied to TMEM with
+// each stage, in the order in which the tensor core takes the MMAs after them.
 //
 // y in bf16: a warp reads its 32 rows of the accumulator as matrix fragments, so that two tokens' values of a
 // row are neighbours in a register, turns 8 x 8 of them at a time on their way to shared memory, and 32 rows of
 // 16 tokens leave in a box while the next 16 are made. Rows of y that are not aligned, and fp32, go by columns.
+// The next tile's MMAs wait for the accumulator to be read: as it is, up to 256 tokens; 384 are more than the
+// registers hold, so they are scaled and narrowed first.
 //
 // Up to 128 tokens bound by the reads of W: D = 4096, V = 128256 nvfp4 51 us for 1 token, 55 for 64, 56 for 128
-// (5.7 to 5.9 TB/s); 74 for 256. Long prompts: 8192 tokens 1.38 ms in short runs and 1.50 under the power cap
-// (5.7 to 6.2 PFLOP/s), mxfp4 1.30 and 1.35; a stage takes 262 ns without its loads and 350 with them.
-// Short rows are bound by the outputs: 4000 x 512 x 120000 to fp32 364 us (5.4 TB/s; with the rows' scales read
-// only once the tile is done 435), 8000 x 512 x 120000 to bf16 604 us, mxfp4 507 (row by row through shared
-// memory 830 and 601).
+// (5.7 to 5.9 TB/s); 74 for 256. Long prompts: 8192 tokens 1.35 ms in short runs and 1.47 under the power cap
+// (5.9 to 6.4 PFLOP/s), mxfp4 1.20 and 1.27 (6.8 to 7.2); a stage of 256 tokens takes 262 ns without its loads and
+// 350 with them. Short rows are bound by the outputs: 4000 x 512 x 120000 to fp32 364 us (5.4 TB/s; with the rows'
+// scales read only once the tile is done 435), 8000 x 512 x 120000 to bf16 604 us, mxfp4 507 (row by row through
+// shared memory 830 and 601; in tiles of 256).
 #include <cstdint>
 
 #include "flce_blocks.h"
 #include "flce_fp4_gemm.h"
 #include "flce_gemm_params.h"
 #include "flce_launch.cuh"
+#include "flce_norm.cuh"
 #include "ptx.cuh"
 
 namespace flce {
@@ -521,8 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int k = c / 2 + (m & 1) * 2;
               float a = __uint_as_float(v[m >> 1][k]), b = __uint_as_float(v[m >> 1][k + 1]);
               if constexpr (kNv) {
-                a = a * w_row[m] * h.x;
-                b = b * w_row[m] * h.y;
+                split(mul2(mul2(pair(a, b), pair(w_row[m], w_row[m])), pair(h.x, h.y)), a, b);
               }
               out[m] = pack_bf16x2(a, b);
             }
