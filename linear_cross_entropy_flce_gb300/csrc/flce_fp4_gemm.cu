@@ -157,12 +157,11 @@ struct Tiles {
   int row, row_end, token;
   int last_row;        // share: where its rows end
   int64_t unit, units; // tiles: the next one
-  int step, index, token_tiles, V, N;
+  int step, token_tiles, V, N;
   bool share;
-  __device__ Tiles(const Fp4GemmParams& p, int first, int count) {
+  __device__ Tiles(const Fp4GemmParams& p, int index, int count) {
     V = p.V;
     N = p.N;
-    index = first;
     share = p.N <= kN;
     token = 0;
     token_tiles = (p.N + kN - 1) / kN;
@@ -190,11 +189,6 @@ struct Tiles {
       row_end = min(last_row, row + kRows);
     } else {
       unit += step;
-      if (N % kN != 0) {   // dealt out one CTA on, so that the shorter last tiles of the tokens go round
-        unit -= index;
-        index = index + 1 == step ? 0 : index + 1;
-        unit += index;
-      }
       if (unit < units) place();
     }
   }
