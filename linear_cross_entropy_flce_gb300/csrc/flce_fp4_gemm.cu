@@ -25,8 +25,8 @@
 // (5.7 to 5.9 TB/s); 74 for 256. Long prompts: 8192 tokens 1.35 ms in short runs and 1.47 under the power cap
 // (5.9 to 6.4 PFLOP/s), mxfp4 1.20 and 1.27 (6.8 to 7.2); a stage of 256 tokens takes 262 ns without its loads and
 // 350 with them. Short rows are bound by the outputs: 4000 x 512 x 120000 to fp32 364 us (5.4 TB/s; with the rows'
-// scales read only once the tile is done 435), 8000 x 512 x 120000 to bf16 604 us, mxfp4 507 (row by row through
-// shared memory 830 and 601; in tiles of 256).
+// scales read only once the tile is done 435), 8000 x 512 x 120000 to bf16 515 us, mxfp4 444 (in tiles of
+// 256 604 and 507, row by row through shared memory 830 and 601).
 #include <cstdint>
 
 #include "flce_blocks.h"
