@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kFp4Limit)
   const uint8_t* const from = static_cast<const uint8_t*>(x) + row * ldx * kElt;
   const int width = live ? D : 0;
   const int chunks = static_cast<int>(fp4_stages(D)) * (kFp4Stage / 16);
+  // where rows are read twice: whole warps go on together, as they load and shuffle together (chunks come in 16s)
+  [[maybe_unused]] const int padded = (chunks + R - 1) / R * R;
   const int code_bytes = static_cast<int>(fp4_code_bytes(D));
   // a block's largest magnitude; the row's over its finite values
   auto block_max = [&](const Chunk<kBf16>& c) { return largest_of_lanes<kLanes>(c.largest()); };
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kFp4Limit)
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) m = row_max(held[k], amax[k], m);
     } else {
-      for (int i = t; i < chunks; i += R) {
+      for (int i = t; i < padded; i += R) {
         Chunk<kBf16> c[1];
         load_chunks<kBf16, kWhole>(from, i, 0, width, stage, c);
         m = row_max(c[0], block_max(c[0]), m);
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kFp4Limit)
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) put(t + k * R, held[k], amax[k]);
   } else {
-    for (int i = t; i < (chunks + R - 1) / R * R; i += R) {   // whole warps, for the shuffles
+    for (int i = t; i < padded; i += R) {
       Chunk<kBf16> c[1];
       load_chunks<kBf16, kWhole>(from, i, 0, width, stage, c);
       put(i, c[0], block_max(c[0]));
