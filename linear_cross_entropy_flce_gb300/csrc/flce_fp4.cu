@@ -52,11 +52,12 @@ __device__ __forceinline__ uint2 quantize_chunk(const Chunk<kBf16>& c, uint32_t 
   c.widen(v);
   const bool finite = amax < kInfBits;
   if constexpr (kNv) {
-    // Powers of two do not round, so v r / g is (v / g) r; but in rows so small that one of these
-    // leaves the normal numbers, v is divided first and amax / 6 taken as it is defined.
-    const bool tiny = g.byte < 32u;
+    // Powers of two do not round, so v r / g is (v / g) r. In rows so small or so large (below 2^-95, from 2^97 on)
+    // that a factor or a / 6 leaves the normal numbers, v and a are divided by g first: what that takes out of the
+    // normal numbers is far below every tie.
+    const bool apart = g.byte - 32u > 191u;
     const float a = __uint_as_float(amax);
-    const float sixth = (tiny ? __fdiv_rn(a, 6.f) : fmaf(a, kSixth, a * kSixthRest)) * g.inverse();
+    const float sixth = apart ? __fdiv_rn(a * g.inverse(), 6.f) : fmaf(a, kSixth, a * kSixthRest) * g.inverse();
     byte = finite ? e4m3x2(sixth, 0.f) & 0xFFu : 0x7Fu;
     float s, none;
     widen_e4m3x2(finite ? byte : 0u, s, none);
@@ -66,7 +67,7 @@ __device__ __forceinline__ uint2 quantize_chunk(const Chunk<kBf16>& c, uint32_t 
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     r = s > 0.f ? __uint_as_float(__float_as_uint(r) - 2u) : 0.f;
     float rest = fmaf(-s, r, 1.f) * r;
-    if (tiny) {
+    if (apart) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] *= g.inverse();
     } else {
