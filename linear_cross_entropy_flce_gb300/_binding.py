@@ -200,6 +200,21 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
 
 
+def int32_ids(ids, ignore_index: int):
+    """Token ids of any integer type as int32. What int32 does not hold is no id of any table, and
+    stays out of every range: it becomes an end of int32's, or -1 where that is ignore_index."""
+    import torch
+    if ids.dtype == torch.int32:
+        return ids
+    if ids.dtype == torch.int64:
+        least, most = -2 ** 31, 2 ** 31 - 1
+        if ignore_index in (least, most):
+            ids = ids.where((ids >= least) & (ids <= most), -1)
+        else:
+            ids = ids.clamp(least, most)
+    return ids.to(torch.int32)
+
+
 def _check_inputs(H, W, labels):
     import torch
     if not (H.is_cuda and W.is_cuda and labels.is_cuda):

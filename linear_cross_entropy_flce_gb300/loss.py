@@ -29,9 +29,7 @@ class FusedLinearCrossEntropyFunction(torch.autograd.Function):
         H = hidden_states.reshape(-1, D)
         if not H.is_contiguous():
             raise ValueError("hidden_states must be contiguous")
-        y = labels.reshape(-1)
-        if y.dtype != torch.int32:
-            y = y.to(torch.int32)
+        y = B.int32_ids(labels.reshape(-1), ignore_index)
         need_dh = ctx.needs_input_grad[0]
         need_dw = ctx.needs_input_grad[1]
         if reduction == "none" and (need_dh or need_dw):

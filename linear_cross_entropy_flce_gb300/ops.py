@@ -17,13 +17,13 @@ from torch.autograd.function import once_differentiable
 from . import _blocks_binding as Q
 from . import _embed_binding as E
 from . import _ops_binding as B
+from ._binding import int32_ids
 
 
-def _flat_tokens(tokens):
+def _flat_tokens(tokens, ignore_index):
     if tokens is None:
         return None
-    t = tokens.reshape(-1)
-    t = t if t.dtype == torch.int32 else t.to(torch.int32)
+    t = int32_ids(tokens.reshape(-1), ignore_index)
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -81,7 +81,7 @@ class TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, temperature: float, ignore_index: int):
         z, places = _rows(logits)
-        y = _flat_tokens(tokens)
+        y = _flat_tokens(tokens, ignore_index)
         rows = logits.shape[:-1]
         if places is not None and y is not None:
             if y.numel() != rows.numel():
@@ -115,7 +115,7 @@ class LinearTokenLogprobsFunction(torch.autograd.Function):
     def forward(ctx, hidden_states, weight, tokens, temperature: float, ignore_index: int):
         H = hidden_states.reshape(-1, hidden_states.shape[-1])
         H = H if H.is_contiguous() else H.contiguous()
-        y = _flat_tokens(tokens)
+        y = _flat_tokens(tokens, ignore_index)
         r = B.linear_token_logprobs(H, weight, y, temperature=temperature,
                                     ignore_index=ignore_index)
         ctx.set_materialize_grads(False)
@@ -180,7 +180,9 @@ class PackedLayerNormFunction(torch.autograd.Function):
 class EmbeddingFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale: float, ignore_index: int, dtype):
-        y = tokens if tokens.dtype == torch.int32 else tokens.to(torch.int32)
+        if tokens.dtype.is_floating_point or tokens.dtype.is_complex:
+            raise TypeError("tokens must be integers")
+        y = int32_ids(tokens, ignore_index)
         y = y if y.is_contiguous() else y.contiguous()
         ctx.save_for_backward(y)
         ctx.table, ctx.options = (weight.shape[0], weight.dtype), (scale, ignore_index)
