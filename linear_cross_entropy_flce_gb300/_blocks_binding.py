@@ -202,6 +202,11 @@ def _fp4_bytes(N: int, D: int, code: int) -> Tuple[int, int]:
     return int(row.value), int(scales.value)
 
 
+def _fp4_groups(D: int, format: str) -> int:
+    """Groups of four neighbouring blocks of a row, padded to whole 256 values."""
+    return -(-D // 256) * (64 // _FP4_BLOCK[format])
+
+
 @dataclasses.dataclass
 class Fp4Matrix:
     """Values [*shape] in 4-bit floating point, as the tensor cores read them: `codes` uint8 [rows,
@@ -218,9 +223,9 @@ class Fp4Matrix:
         """The blocks' scale bytes row by row, uint8 [rows, blocks], a copy."""
         N, D = self.codes.shape[0], self.shape[-1]
         blocks = -(-D // _FP4_BLOCK[self.format])
-        tiles = -(-N // 128)
-        t = self.scales.view(tiles, -1, 32, 4, 4).permute(0, 3, 2, 1, 4)   # tile, r / 32, r % 32, group, block
-        return t.reshape(tiles * 128, -1)[:N, :blocks].contiguous()
+        tiles, groups = -(-N // 128), _fp4_groups(D, self.format)
+        t = self.scales.view(tiles, groups, 32, 4, 4).permute(0, 3, 2, 1, 4)   # tile, r / 32, r % 32, group, block
+        return t.reshape(tiles * 128, 4 * groups)[:N, :blocks].contiguous()
 
     @classmethod
     def from_rows(cls, codes, block_scales, row_scales=None, *, width: Optional[int] = None,
@@ -236,15 +241,15 @@ class Fp4Matrix:
         if codes.shape[1] != (D + 1) // 2 or tuple(block_scales.shape) != (N, blocks) \
                 or block_scales.element_size() != 1:
             raise ValueError("codes and block_scales must hold ceil(width / 2) bytes and one byte per block of a row")
-        row, size = _fp4_bytes(N, D, code)
+        row, _ = _fp4_bytes(N, D, code)
         wide = codes.new_zeros((N, row))
         wide[:, :codes.shape[1]] = codes
         if D % 2:
             wide[:, codes.shape[1] - 1] &= 15
-        tiles = -(-N // 128)
-        full = codes.new_zeros((tiles * 128, size // max(tiles * 128, 1)))
+        tiles, groups = -(-N // 128), _fp4_groups(D, format)
+        full = codes.new_zeros((tiles * 128, 4 * groups))
         full[:N, :blocks] = block_scales.view(torch.uint8)
-        scales = full.view(tiles, 4, 32, -1, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+        scales = full.view(tiles, 4, 32, groups, 4).permute(0, 3, 2, 1, 4).reshape(-1)
         if format == "nvfp4":
             one = torch.ones(N, dtype=torch.float32, device=codes.device)
             row_scales = one if row_scales is None else (one * row_scales.to(torch.float32)).contiguous()

@@ -1,0 +1,27 @@
+"""4-bit matrices whose codes and scales lie row by row, as checkpoints hold them: no rows, one value, odd
+widths, and what is not taken."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import linear_cross_entropy_flce_gb300 as flce
+
+DEV = "cuda:0"
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("N", [0, 1, 127, 128, 129])
+@pytest.mark.parametrize("D", [1, 16, 40, 63, 256, 257, 1000])
+def test_there_and_back(fmt, N, D):
+    m = flce.quantize_fp4(torch.randn(N, D, device=DEV), format=fmt)
+    blocks = -(-D // (16 if fmt == "nvfp4" else 32))
+    scales = m.block_scales()
+    assert scales.shape == (N, blocks) and scales.dtype == torch.uint8
+    n = flce.Fp4Matrix.from_rows(m.codes[:, :(D + 1) // 2], scales, m.row_scales, width=D, format=fmt)
+    assert n.shape == (N, D) and torch.equal(n.codes, m.codes) and torch.equal(n.scales, m.scales)
+    assert m.row_scales is None and n.row_scales is None or torch.equal(n.row_scales, m.row_scales)
+    assert torch.equal(flce.dequantize_fp4(n), flce.dequantize_fp4(m))
+    w = flce.quantize_fp4(torch.randn(5, D, device=DEV), format=fmt)
+    assert torch.equal(flce.linear_fp4(n, w), flce.linear_fp4(m, w))
