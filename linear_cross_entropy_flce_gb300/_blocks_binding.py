@@ -232,7 +232,7 @@ class Fp4Matrix:
                   format: str = "nvfp4") -> "Fp4Matrix":
         """A matrix [N, width] of codes and scales that lie row by row, as checkpoints hold them:
         codes uint8 [N, ceil(width / 2)] (the first of two in the low bits), block_scales uint8
-        or float8 [N, blocks], and for nvfp4 row_scales, fp32 of one value or [N] (1 if None)."""
+        or float8 [N, blocks], and for nvfp4 row_scales, one value or [N] (1 if None)."""
         code = _fp4_code(format)
         if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_cuda:
             raise TypeError("codes must be a [N, bytes] uint8 CUDA tensor")
@@ -251,8 +251,10 @@ class Fp4Matrix:
         full[:N, :blocks] = block_scales.view(torch.uint8)
         scales = full.view(tiles, 4, 32, groups, 4).permute(0, 3, 2, 1, 4).reshape(-1)
         if format == "nvfp4":
-            one = torch.ones(N, dtype=torch.float32, device=codes.device)
-            row_scales = one if row_scales is None else (one * row_scales.to(torch.float32)).contiguous()
+            given = torch.as_tensor(1.0 if row_scales is None else row_scales, dtype=torch.float32, device=codes.device)
+            if given.numel() != 1 and tuple(given.shape) != (N,):
+                raise ValueError("row_scales must be one value or [N]")
+            row_scales = given.reshape(-1).expand(N).clone(memory_format=torch.contiguous_format)
         elif row_scales is not None:
             raise ValueError("mxfp4 has no row scales")
         return cls(wide, scales, row_scales, (N, D), format)

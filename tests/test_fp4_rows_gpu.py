@@ -25,3 +25,21 @@ def test_there_and_back(fmt, N, D):
     assert torch.equal(flce.dequantize_fp4(n), flce.dequantize_fp4(m))
     w = flce.quantize_fp4(torch.randn(5, D, device=DEV), format=fmt)
     assert torch.equal(flce.linear_fp4(n, w), flce.linear_fp4(m, w))
+
+
+def test_row_scales():
+    m = flce.quantize_fp4(torch.randn(3, 64, device=DEV))
+
+    def rows(scales):
+        return flce.Fp4Matrix.from_rows(m.codes, m.block_scales(), scales).row_scales
+
+    one = torch.ones(3, device=DEV)
+    assert torch.equal(rows(None), one) and torch.equal(rows(0.25), one / 4) and torch.equal(rows(one[:1] * 3), one * 3)
+    assert torch.equal(rows(one.sum()), one * 3) and torch.equal(rows(m.row_scales), m.row_scales)
+    assert torch.equal(rows(torch.arange(3)), torch.arange(3.0, device=DEV))
+    for wrong in (one[:, None], one[:2], torch.ones(4, device=DEV), one[None]):
+        with pytest.raises(ValueError):
+            rows(wrong)
+    w = rows(one)
+    w.zero_()   # its own memory
+    assert bool((one == 1).all())
