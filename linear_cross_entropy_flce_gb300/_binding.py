@@ -130,6 +130,14 @@ def status_string(code: int) -> str:
     return lib.flce_status_string(int(code)).decode()
 
 
+def ignore_id(ignore_index) -> int:
+    """ignore_index as the library has it, 32 bits."""
+    i = int(ignore_index)
+    if not -2 ** 31 <= i < 2 ** 31:
+        raise ValueError("ignore_index must be a 32-bit integer")
+    return i
+
+
 def make_options(*, ignore_index: int = -100, reduction: str = "mean", grad_scale: float = 1.0,
                  normalizer: float = 0.0, dw_dtype: str = "float32", v_splits: int = 0,
                  n_block: int = 0, v_chunk: int = 0, timeout_ns: int = 0,
@@ -139,7 +147,7 @@ def make_options(*, ignore_index: int = -100, reduction: str = "mean", grad_scal
     after its k-th kernel."""
     o = Options()
     lib.flce_default_options(ctypes.byref(o))
-    o.ignore_index = int(ignore_index)
+    o.ignore_index = ignore_id(ignore_index)
     o.reduction = REDUCTIONS[reduction]
     o.grad_scale = float(grad_scale)
     o.normalizer = float(normalizer)

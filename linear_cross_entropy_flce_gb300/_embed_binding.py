@@ -11,6 +11,7 @@ from typing import Optional
 
 import torch
 
+from ._binding import ignore_id
 from ._ops_binding import (_c_int, _check, _declare, _device_of, _dtype_of, _f32, _fast, _i32, _i64,
                            _logits, _norm_rows, _ptr, _psize, _same_device, _size, _status, _stream,
                            _vp, _workspace)
@@ -57,7 +58,7 @@ def embedding(weight, tokens, *, scale: float = 1.0, ignore_index: int = -100,
             raise ValueError("out must be a contiguous [*tokens.shape, D] tensor of the dtype asked for")
     code = _dtype_of(out, "the result")
     _check(_embedding(weight.data_ptr(), wcode, ldw, ids.data_ptr(), ids.numel(), V, D, float(scale),
-                      int(ignore_index), out.data_ptr(), code, D, _status(status, dev), raw), "flce_embedding")
+                      ignore_id(ignore_index), out.data_ptr(), code, D, _status(status, dev), raw), "flce_embedding")
     return out
 
 
@@ -104,7 +105,7 @@ def embedding_backward(dy, tokens, rows: int, *, scale: float = 1.0, ignore_inde
         _, _, ldw = _logits(out, "out")
         ws = _workspace(workspace, _embedding_ws_bytes(N, rows, D), dev)
     _check(_embedding_backward(g.data_ptr(), code, ldg, _ptr(ids), N, rows, D, float(scale),
-                               int(ignore_index), out.data_ptr(), wcode, ldw, int(accumulate),
+                               ignore_id(ignore_index), out.data_ptr(), wcode, ldw, int(accumulate),
                                ws.data_ptr(), ws.numel() * ws.element_size(), raw),
            "flce_embedding_backward")
     return out

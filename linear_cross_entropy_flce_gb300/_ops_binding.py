@@ -25,7 +25,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from ._binding import FLCE_OK, FLCEError, lib
+from ._binding import FLCE_OK, FLCEError, ignore_id, lib
 
 
 class _NoExtension:
@@ -200,7 +200,7 @@ def _status(status, dev) -> Optional[int]:
 
 
 def _options(ignore_index, top_k, temperature, dw_dtype=0, timeout_ns=0) -> LogprobOptions:
-    return LogprobOptions(int(ignore_index), int(top_k), float(temperature), dw_dtype,
+    return LogprobOptions(ignore_id(ignore_index), int(top_k), float(temperature), dw_dtype,
                           int(timeout_ns))
 
 

@@ -61,6 +61,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+int32_t integer32(PyObject* o) {
+  const int64_t v = integer(o);
+  if (v != static_cast<int32_t>(v)) throw Refused{};
+  return static_cast<int32_t>(v);
+}
+
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) {
@@ -129,7 +135,7 @@ flce_logprob_options options(PyObject* ignore_index, int64_t top_k, PyObject* te
                              int dw_dtype = FLCE_DTYPE_F32) {
   flce_logprob_options o;
   flce_default_logprob_options(&o);
-  o.ignore_index = static_cast<int32_t>(integer(ignore_index));
+  o.ignore_index = integer32(ignore_index);
   o.top_k = static_cast<int32_t>(top_k);
   o.temperature = static_cast<float>(number(temperature));
   o.dw_dtype = dw_dtype;
@@ -446,7 +452,7 @@ FUNCTION(embedding) {
     std::vector<int64_t> shape(ids.sizes().begin(), ids.sizes().end());
     shape.push_back(D);
     const float scale = static_cast<float>(number(a[2]));
-    const int32_t ignore = static_cast<int32_t>(integer(a[3]));
+    const int32_t ignore = integer32(a[3]);
     const Tensor y = h.empty(shape, type);
     check(flce_embedding(w.const_data_ptr(), wcode, ldw, ids.const_data_ptr<int32_t>(), ids.numel(), w.size(0),
                          D, scale, ignore, y.data_ptr(), code, D, nullptr, h.stream), "flce_embedding");
@@ -466,7 +472,7 @@ FUNCTION(embedding_backward) {
     const at::ScalarType type = type_of(a[5], dy.scalar_type());
     const int code = code_of(type);
     const float scale = static_cast<float>(number(a[3]));
-    const int32_t ignore = static_cast<int32_t>(integer(a[4]));
+    const int32_t ignore = integer32(a[4]);
     size_t bytes = 0;
     check(flce_embedding_backward_workspace_size(r.N, rows, r.D, &bytes), "flce_embedding_backward_workspace_size");
     const Tensor dW = h.empty({rows, r.D}, type);
@@ -587,7 +593,7 @@ FUNCTION(quantize_fp4) {
     const Tensor& x = required(a[0], h.device);
     const int dtype = dtype_of(x);
     const NormRows r(x);
-    const int32_t format = static_cast<int32_t>(integer(a[1]));
+    const int32_t format = integer32(a[1]);
     int64_t row = 0;
     size_t size = 0;
     check(flce_fp4_sizes(r.N, r.D, format, &row, &size), "flce_fp4_sizes");
@@ -630,7 +636,7 @@ struct Fp4 {
 FUNCTION(dequantize_fp4) {
   return guarded(n, 6, [&]() -> PyObject* {
     const Here h;
-    const int32_t format = static_cast<int32_t>(integer(a[4]));
+    const int32_t format = integer32(a[4]);
     const Fp4 m(a, format, h.device);
     const at::ScalarType type = type_of(a[5], at::kFloat);
     const int code = code_of(type);
@@ -645,7 +651,7 @@ FUNCTION(dequantize_fp4) {
 FUNCTION(linear_fp4) {
   return guarded(n, 10, [&]() -> PyObject* {
     const Here h;
-    const int32_t format = static_cast<int32_t>(integer(a[8]));
+    const int32_t format = integer32(a[8]);
     const Fp4 H(a, format, h.device), W(a + 4, format, h.device);
     check(W.shape.size() == 2 && W.D == H.D);
     const at::ScalarType type = type_of(a[9], at::kBFloat16);

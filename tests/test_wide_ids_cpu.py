@@ -3,6 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import linear_cross_entropy_flce_gb300 as flce
 from linear_cross_entropy_flce_gb300._binding import int32_ids
 
 LEAST, MOST = -2 ** 31, 2 ** 31 - 1
@@ -23,3 +24,11 @@ def test_other_types():
     assert int32_ids(t, -100) is t
     for dtype in (torch.uint8, torch.int8, torch.int16):
         assert int32_ids(torch.tensor([1, 2], dtype=dtype), -100).tolist() == [1, 2]
+
+
+def test_ignore_index_past_32_bits_is_refused():
+    for i in (LEAST, MOST, -100):
+        assert flce.make_options(ignore_index=i).ignore_index == i
+    for i in (2 ** 32 - 100, 2 ** 31, LEAST - 1):
+        with pytest.raises(ValueError):
+            flce.make_options(ignore_index=i)

@@ -55,3 +55,19 @@ def test_narrow_and_wrong_types():
         assert torch.equal(y.cpu(), W.index_select(0, t.flatten()).view(2, 1, 8))
     with pytest.raises(TypeError):
         flce.fused_embedding(torch.tensor([3.0], device=DEV), W.to(DEV))
+
+
+@pytest.mark.parametrize("ignore", [2 ** 32 + 3, 2 ** 31, LEAST - 1])
+def test_ignore_index_past_32_bits_is_refused(ignore):
+    """2^32 + 3 is not the id 3."""
+    W, z = torch.randn(10, 64, device=DEV), torch.randn(2, 10, device=DEV)
+    t = torch.tensor([3, 4], dtype=torch.int32, device=DEV)
+    H = torch.randn(2, 64, device=DEV).bfloat16()
+    for call in (
+            lambda: flce.embedding(W, t, ignore_index=ignore), lambda: flce.fused_embedding(t, W, ignore_index=ignore),
+            lambda: flce.embedding_backward(torch.ones(2, 64, device=DEV), t, 10, ignore_index=ignore),
+            lambda: flce.token_logprobs(z, t, ignore_index=ignore),
+            lambda: flce.linear_token_logprobs(H, W.bfloat16(), t, ignore_index=ignore),
+            lambda: flce.forward(H, W.bfloat16(), t, ignore_index=ignore)):
+        with pytest.raises(ValueError):
+            call()
