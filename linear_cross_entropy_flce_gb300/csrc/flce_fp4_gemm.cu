@@ -677,7 +677,7 @@ template <int kN, int kCta>
 cudaError_t launch_types(int nv, int bf16, const Fp4Maps& maps, const Fp4GemmParams& p, int sms,
                          cudaStream_t stream) {
   if constexpr (kN > 256) {
-    if (!bf16) return cudaErrorInvalidValue;
+    if (!bf16 || !p.wide) return cudaErrorInvalidValue;
     return nv ? launch<kN, 1, 1, kCta>(maps, p, sms, stream) : launch<kN, 0, 1, kCta>(maps, p, sms, stream);
   } else if (nv) {
     return bf16 ? launch<kN, 1, 1, kCta>(maps, p, sms, stream) : launch<kN, 1, 0, kCta>(maps, p, sms, stream);
@@ -695,8 +695,9 @@ cudaError_t launch_fp4_gemm(int kn, int nv, int bf16, const Fp4Maps& maps, const
     case 32: return launch_types<32, fp4_ctas(32)>(nv, bf16, maps, p, sms, stream);
     case 64: return launch_types<64, fp4_ctas(64)>(nv, bf16, maps, p, sms, stream);
     case 128: return launch_types<128, fp4_ctas(128)>(nv, bf16, maps, p, sms, stream);
+    case 256: return launch_types<256, fp4_ctas(256)>(nv, bf16, maps, p, sms, stream);
     case 384: return launch_types<384, fp4_ctas(384)>(nv, bf16, maps, p, sms, stream);
-    default: return launch_types<256, fp4_ctas(256)>(nv, bf16, maps, p, sms, stream);
+    default: return cudaErrorInvalidValue;
   }
 }
 

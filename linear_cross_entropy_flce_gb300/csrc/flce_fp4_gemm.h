@@ -43,7 +43,8 @@ struct Fp4Maps {
   CUtensorMap w, w32, h, w_scales, h_scales, y;
 };
 
-// y = H W^T, kn = fp4_tile(p.N).
+// y = H W^T in tiles of kn tokens: fp4_tile(p.N), or 384 where fp4_wide_tile says so, which takes y in bf16,
+// p.wide and H's boxes of 64 rows. Any other kn is cudaErrorInvalidValue.
 cudaError_t launch_fp4_gemm(int kn, int nv, int bf16, const Fp4Maps& maps, const Fp4GemmParams& p, int sms,
                             cudaStream_t stream);
 
