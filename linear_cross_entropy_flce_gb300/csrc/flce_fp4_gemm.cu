@@ -427,7 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_out = stage0 + kStages * C::kStageBytes + warp * (2 * kOutTokens * 64);
     [[maybe_unused]] float* const s_rows = reinterpret_cast<float*>(
         smem + kStages * C::kStageBytes + kEpilogue * (2 * kOutTokens * 64) + warp * (kHalf * 4));
-    [[maybe_unused]] uint32_t turn = 0;   // the place of the next box; goes on from tile to tile
     int acc = 0;
     uint32_t acc_phase = 0;
     // this lane's row of a tile, and whether the tile has it
@@ -543,10 +542,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c0 = 0; c0 < kHalf; c0 += kOutTokens) {
             if (c0 >= tokens) break;
-            // one place after the other: the copy from this one, two boxes ago (of whatever tile), has read it
-            const uint32_t place = s_out + turn * (kOutTokens * 64);
-            turn ^= 1u;
-            if (lane == 0) bulk_wait_group_read<1>();
+            const uint32_t place = s_out + c0 / kOutTokens % 2 * (kOutTokens * 64);
+            // one place after the other: the copy from this one, two steps ago, has read it. A tile begins at the first
+            // place, from which the one before took its last box where it had an odd number of them, so all have to be
+            // read (as they long are; a place that goes on from tile to tile took 580 us instead of 547 for 8000 x 512 x
+            // 120000 nvfp4, in whose registers it had no room)
+            if (lane == 0) {
+              if (c0 == 0) bulk_wait_group_read<0>();
+              else bulk_wait_group_read<1>();
+            }
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < kOutTokens; c += 8) {
