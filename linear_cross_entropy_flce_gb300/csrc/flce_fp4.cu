@@ -53,11 +53,11 @@ __device__ __forceinline__ uint2 quantize_chunk(const Chunk<kBf16>& c, uint32_t 
   const bool finite = amax < kInfBits;
   if constexpr (kNv) {
     // Powers of two do not round, so v r / g is (v / g) r. In rows so small or so large (below 2^-95, from 2^97 on)
-    // that a factor or a / 6 leaves the normal numbers, v and a are divided by g first: what that takes out of the
-    // normal numbers is far below every tie.
+    // that a factor leaves the normal numbers, v is divided by g first, and the largest magnitude in every row: what
+    // that takes out of the normal numbers is far below every tie.
     const bool apart = g.byte - 32u > 191u;
-    const float a = __uint_as_float(amax);
-    const float sixth = apart ? __fdiv_rn(a * g.inverse(), 6.f) : fmaf(a, kSixth, a * kSixthRest) * g.inverse();
+    const float a = __uint_as_float(amax) * g.inverse();
+    const float sixth = fmaf(a, kSixth, a * kSixthRest);
     byte = finite ? e4m3x2(sixth, 0.f) & 0xFFu : 0x7Fu;
     float s, none;
     widen_e4m3x2(finite ? byte : 0u, s, none);
