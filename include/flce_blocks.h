@@ -24,13 +24,14 @@ extern "C" {
 /*
  * 8 bits: each 32 values of a row (the last block may be shorter) have a scale 2^e, e the
  * smallest integer >= -127 for which the block's largest magnitude is at most 448 2^e, and
- * are held as E4M3 codes of x / 2^e rounded to nearest even (no value saturates).
+ * are held as E4M3 codes of x / 2^e rounded to nearest even (no value saturates, where the
+ * rounding down of e that the microscaling standard describes lets the largest ones).
  *
  * A row of D values is a record of flce_packed_row_bytes(D) bytes, a multiple of 16:
  *   D codes, zeros up to the next multiple of 32, then one byte e + 127 per block, zeros
  *   to the record's end. Records follow one another.
  * A block that holds an infinity or a NaN has the byte 255 and stands for NaN throughout;
- * one of zeros alone has the byte 0. Values of more than 248 2^120 round to infinity.
+ * one of zeros alone has the byte 0. Values of 248 2^120 and more stand for infinity.
  */
 int flce_packed_row_bytes(int64_t D, int64_t* bytes);
 
@@ -74,9 +75,14 @@ int flce_layer_norm_packed_backward(const void* dy, int32_t dtype, int64_t lddy,
  *                 magnitude is at most 6 448 g (1 for a row of zeros), s = rn(largest
  *                 magnitude of the block / 6 / g), code rn(x / (s g)), 0 where s is 0
  *
- * All rounded to nearest even; a code is at most 6. A block that holds an infinity or a
- * NaN has the scale NaN (byte 255, 127) and the codes 0: it stands for NaN throughout.
- * Products and values take any fp32 row scales and any scale bytes.
+ * All rounded to nearest even, once; a code is at most 6. A block that holds an infinity or
+ * a NaN has the scale NaN (byte 255, 127) and the codes 0: it stands for NaN throughout.
+ * What a block of the largest fp32 numbers stands for may be past them: infinity.
+ *
+ * Where the usual rules differ: the microscaling standard rounds e down, so that a block's
+ * largest values may saturate, here up; nvfp4 elsewhere has one fp32 number g for the tensor.
+ * Such matrices are decoded and multiplied all the same: any bytes e + 127, any E4M3 scales
+ * without a sign (bytes 0 to 127), any fp32 row scales.
  *
  * Three arrays hold [N, D] (flce_fp4_sizes gives the bytes; 16-byte aligned but for
  * row_scales, 4):
@@ -105,7 +111,8 @@ int flce_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float
 /*
  * y = H W^T of two such matrices of one format, H [N, D] (tokens) and W [V, D] (a head or
  * another linear layer's weight), on the block-scaled tensor cores: the blocks' products
- * are accumulated in fp32, multiplied by the two rows' scales and rounded once to dtype.
+ * are accumulated in fp32, multiplied in fp32 by W's row scale and then by H's, and rounded
+ * once to dtype.
  *   y        [N, V] of dtype (FLCE_DTYPE_F32 / _BF16), row stride ldy >= V, aligned to its
  *            element size
  *   timeout_ns  limit of every device-side wait; 0 = 2 s

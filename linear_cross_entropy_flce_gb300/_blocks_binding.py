@@ -232,7 +232,7 @@ class Fp4Matrix:
                   format: str = "nvfp4") -> "Fp4Matrix":
         """A matrix [N, width] of codes and scales that lie row by row, as checkpoints hold them:
         codes uint8 [N, ceil(width / 2)] (the first of two in the low bits), block_scales uint8
-        or float8 [N, blocks], and for nvfp4 row_scales, one value or [N] (1 if None)."""
+        or float8 [N, blocks] (nvfp4: not negative), and for nvfp4 row_scales, one value or [N] (1 if None)."""
         code = _fp4_code(format)
         if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_cuda:
             raise TypeError("codes must be a [N, bytes] uint8 CUDA tensor")

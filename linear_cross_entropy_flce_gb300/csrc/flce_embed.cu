@@ -30,8 +30,10 @@ namespace {
 // ---- lookup --------------------------------------------------------------------------
 
 constexpr int kLookupThreads = 128;
-// Vectors of a row per thread. One element at a time in us with 4 / 8 / 12 / 16: 3001 x 1111 fp32 to bf16
-// 7.9 / 7.3 / 6.1 / 6.6, 8192 x 4001 bf16 47 / 36 / 34 / 31.
+// Vectors of a row per thread. One element at a time, 12 is best on the whole: over rows of 601 to 8191 elements, 64
+// to 16384 tokens and three pairs of types (75 sizes) 8 takes 7 % longer and 16 3 %, which is ahead for long rows
+// alone. In us with 8 / 12 / 16, bf16: 8192 x 601 9.8 / 8.0 / 8.8, 16384 x 2731 50 / 45 / 51, 8192 x 4001 36 / 34 / 31,
+// 3001 x 8191 27 / 26 / 24; the bytes of 8192 x 4001 are 20: 2 bytes an access.
 constexpr int lookup_vectors(int vw) { return vw == 1 ? 12 : 4; }
 
 // X threads per row; VW elements at a time.

@@ -12,12 +12,13 @@
 // warp's 512 values at a time. 1 / s is taken in two parts, r and its
 // rest, so that x r + x rest is x / s to within 2^-43, rounded once: a value halfway between two codes
 // stays there. (And no other quotient is rounded onto such a place: its distance from it is more than
-// half the quotient's own last place.)
+// half the quotient's own last place.) amax / 6 is rounded in the same way, so that the scale's rounding is the one
+// that counts.
 //
 // Bound by instructions for nvfp4 (so two values an instruction), by bytes for mxfp4 and for the values back: 128256 x
-// 4096 bf16 235, 184 and 208 us (the bytes 201, 198); 8192 x 4096 18.5 and 15.0; 64128 x 4096 fp32 199; 3001 x 1111
-// fp32 mxfp4 6.1 and 4.2; one row of 4096 2.2 and 1.8. The quotient corrected by its residual instead (three
-// operations a value) 317.
+// 4096 bf16 233, 186 and 208 us (the bytes 201, 198); 8192 x 4096 18.8 and 14.7; 64128 x 4096 fp32 194; 3001 x 1111
+// fp32 7.7, 5.5 and 4.2 (the bytes 2.3; rows that are not whole 16 bytes are read 2 or 4 bytes at a time); one row of
+// 4096 1.9 and 1.6. The quotient corrected by its residual instead (three operations a value) 317.
 #include <cstdint>
 
 #include "flce_blocks.cuh"

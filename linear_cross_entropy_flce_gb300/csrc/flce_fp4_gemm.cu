@@ -22,11 +22,13 @@
 // registers hold, so they are scaled and narrowed first.
 //
 // Up to 128 tokens bound by the reads of W: D = 4096, V = 128256 nvfp4 51 us for 1 token, 55 for 64, 56 for 128
-// (5.7 to 5.9 TB/s); 74 for 256. Long prompts: 8192 tokens 1.35 ms in short runs and 1.47 under the power cap
-// (5.9 to 6.4 PFLOP/s), mxfp4 1.20 and 1.27 (6.8 to 7.2); a stage of 256 tokens takes 262 ns without its loads and
+// (5.7 to 5.9 TB/s); 74 for 256. Long prompts: 8192 tokens 1.33 to 1.37 ms in short runs and 1.47 to 1.53 under the
+// power cap (5.6 to 6.4 PFLOP/s), mxfp4 1.21 and 1.29 (6.7 to 7.1); a library's nvfp4 product, without row scales, 1.20
+// and 1.31. Steps are of K = 64, 10.3 PFLOP/s at full clock (this chip also has dense ones of K = 96, at the nominal
+// 13.5, which are not used); a stage of 256 tokens takes 262 ns without its loads, of which the steps are 247, and
 // 350 with them. Short rows are bound by the outputs: 4000 x 512 x 120000 to fp32 364 us (5.4 TB/s; with the rows'
-// scales read only once the tile is done 435), 8000 x 512 x 120000 to bf16 515 us, mxfp4 444 (in tiles of
-// 256 604 and 507, row by row through shared memory 830 and 601).
+// scales read only once the tile is done 435), 8000 x 512 x 120000 to bf16 547 us, mxfp4 448 (the library's nvfp4
+// 361; in tiles of 256 604 and 507, row by row through shared memory 830 and 601).
 #include <cstdint>
 
 #include "flce_blocks.h"

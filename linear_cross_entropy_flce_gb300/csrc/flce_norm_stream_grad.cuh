@@ -9,8 +9,9 @@
 // One row of a turn, as the accumulators leave no registers for a second. 8192 x 4096 bf16 takes
 // 40.8 us (4.9 TB/s) with the partials (their join 4, their writing 2), 16384 x 8192 148 us (5.5
 // TB/s), 4000 x 4096 fp32 38.4 us (5.1 TB/s), 2000 x 8000 39.6 us; the rows' loads in registers
-// instead of the ring 55, 175, 46, 50. Bound by its instructions (23 per element, 12 warps per
-// SM): reading the slot again for dx, to hold less and run 16 warps, took 53 us.
+// instead of the ring 55, 175, 46, 50. Bound by latency: 23 instructions per element from 12 warps an
+// SM, whose 168 registers a thread leave no room for more, keep half of the issue slots busy. Reading
+// the slot again for dx, to hold less and run 16 warps, took 53 us.
 // Ragged rows (loads in registers in brackets): 3001 x 1111 fp32 18.1 us (25.2), 16384 x 2730
 // bf16 77 (109), 16000 x 4001 bf16 102 (179).
 //

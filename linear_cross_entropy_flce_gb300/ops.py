@@ -242,7 +242,7 @@ class FusedLayerNorm(torch.nn.Module):
 
 def fused_embedding(tokens, weight, *, scale: float = 1.0, ignore_index: int = -100, dtype=None):
     """scale * weight[tokens] of integer tokens [...], as `dtype` (fp32 or bf16; the weight's by
-    default); rows of ignore_index are 0. Differentiable in weight [V, D] (fp32 or bf16), whose
+    default); rows of ignore_index are 0, of other ids outside the table NaN. Differentiable in weight [V, D] (fp32 or bf16), whose
     gradient sums each id's tokens in fp32 in a fixed order."""
     return EmbeddingFunction.apply(tokens, weight, float(scale), int(ignore_index), dtype)
 
