@@ -214,6 +214,8 @@ def int32_ids(ids, ignore_index: int):
     import torch
     if ids.dtype == torch.int32:
         return ids
+    if ids.dtype == torch.uint32:
+        ids = ids.to(torch.int64)
     if ids.dtype == torch.int64:
         least, most = -2 ** 31, 2 ** 31 - 1
         if ignore_index in (least, most):

@@ -22,8 +22,10 @@ def test_ids(ignore):
 def test_other_types():
     t = torch.tensor([1, 2], dtype=torch.int32)
     assert int32_ids(t, -100) is t
-    for dtype in (torch.uint8, torch.int8, torch.int16):
+    for dtype in (torch.uint8, torch.int8, torch.int16, torch.uint32):
         assert int32_ids(torch.tensor([1, 2], dtype=dtype), -100).tolist() == [1, 2]
+    far = int32_ids(torch.tensor([2 ** 32 - 100, 2 ** 31], dtype=torch.uint32), -100)   # not -100
+    assert far.tolist() == [MOST, MOST]
 
 
 def test_ignore_index_past_32_bits_is_refused():
