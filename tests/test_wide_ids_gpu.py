@@ -50,7 +50,7 @@ def test_loss_is_that_of_ids_out_of_range():
 def test_narrow_and_wrong_types():
     W = torch.randn(10, 8)
     t = torch.tensor([[3], [9]])
-    for dtype in (torch.uint8, torch.int8, torch.int16, torch.int64):
+    for dtype in (torch.uint8, torch.int8, torch.int16, torch.uint32, torch.int64):
         y = flce.fused_embedding(t.to(dtype).to(DEV), W.to(DEV))
         assert torch.equal(y.cpu(), W.index_select(0, t.flatten()).view(2, 1, 8))
     with pytest.raises(TypeError):
